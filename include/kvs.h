@@ -448,6 +448,124 @@ kvs_status kvs_pool_export(kvs_pool* pool, const int32_t* blocks_dev, int32_t n_
 kvs_status kvs_pool_import(kvs_pool* pool, const int32_t* blocks_dev, int32_t n_blocks, const void* src_dev,
                            size_t src_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * New tokens: rotary positions, append, read-back and attention of query
+ * chunks.  The calls before this point attend with one query row per sequence
+ * to a cache that is already filled; these fill it and attend with any number
+ * of rows.  Rows of new tokens are packed over the batch:
+ * tok_off_dev   int32 [n_seq + 1], non-decreasing: sequence a owns rows
+ *               [tok_off[a], tok_off[a + 1]) of the packed tensors, none where
+ *               the two are equal.
+ * seq_len_dev   int32 [n_seq]: tokens of each sequence with the new ones, so
+ *               row j of the n rows of sequence a is its token
+ *               seq_len[a] - n + j.
+ * n_tokens      rows of the packed tensors; rows in front of tok_off[0] and
+ *               behind tok_off[n_seq] (a padded batch) belong to no sequence:
+ *               nothing is written for them.
+ * Packed tensors are bf16 [n_tokens][heads][head_dim].  Where a call takes a
+ * stride, it is the distance in elements between the rows of two tokens (at
+ * least heads * head_dim, a multiple of 8), so that queries, keys and values
+ * may lie side by side in one projection's rows.  Pointers are 16-byte
+ * aligned.
+ *
+ * Rotary positions on one to three axes (the order of a text; time, height
+ * and width of images and video).  Dimensions i and i + head_dim/2 form pair
+ * i (as in kvs_rope_rerotate); the first section[0] pairs turn with the
+ * token's position on axis 0, the next section[1] with axis 1, the next
+ * section[2] with axis 2; the sections sum to head_dim/2 (unused ones are 0).
+ *   y_i          = x_i cos(f) - x_(i+d/2) sin(f),
+ *   y_(i+d/2)    = x_(i+d/2) cos(f) + x_i sin(f),   f = pos[axis] * w_i
+ * w_i = theta^(-2i/head_dim), or with own_spectrum = 1 theta^(-j/s) for pair j
+ * of an axis' s pairs.  Every int32 position is exact to float32: the angle is
+ * reduced modulo a turn in 64-bit fixed point.  The product is taken in
+ * float32 and rounded once to bf16. */
+typedef struct {
+  float theta;          /* > 0 */
+  int32_t n_axes;       /* 1..3 */
+  int32_t section[3];   /* pairs turned by each axis */
+  int32_t own_spectrum; /* 0: one spectrum over all pairs; 1: one per axis */
+} kvs_rope_axes;
+
+/* out[t][h] = R(pos[.][t]) x[t][h] for n_heads heads of n_tokens rows, or
+ * R(-pos) with inverse != 0 (takes a rotation back).  pos_dev is int32
+ * [n_axes][n_tokens].  out may be x itself with the same stride; otherwise
+ * the two must not overlap.  head_dim 64 or 128. */
+kvs_status kvs_rope_apply(const void* x_dev, int64_t x_stride, const int32_t* pos_dev, const kvs_rope_axes* axes,
+                          int32_t inverse, void* out_dev, int64_t out_stride, int32_t n_tokens, int32_t n_heads,
+                          int32_t head_dim, cudaStream_t stream);
+
+/* Append: writes the new tokens' keys and values through the block table, the
+ * keys rotated on the way, and in the same pass rotates the queries of the
+ * same tokens:
+ *   K[blk][h][p % B] = R(pos) k_new[t][h],  V[blk][h][p % B] = v_new[t][h],
+ *   q_out[t][h] = R(pos) q[t][h],   p = seq_len[a] - n + j, blk = table[a][p/B]
+ * axes          NULL: no rotation (queries are then copied).
+ * pos_dev       int32 [n_axes][n_tokens], or NULL with one axis: p itself.
+ * q_dev, q_out_dev   both or neither; q_out is bf16 [n_tokens][n_q_heads]
+ *               [head_dim] without gaps and may be q itself when q has none.
+ * A Q4G64 pool stores what kvs_quantize_q4 makes of the same bf16 values.
+ * The written blocks belong to their sequence alone (kvs_block_write first
+ * where they are shared): two rows for one place of the pool race.  A token
+ * whose place is negative or past the table's row sets KVS_DEVERR_SEQ_LEN, a
+ * block id out of range KVS_DEVERR_BLOCK_ID; its key and value are dropped. */
+kvs_status kvs_append(kvs_pool* pool, int32_t layer, const void* k_dev, int64_t k_stride, const void* v_dev,
+                      int64_t v_stride, const void* q_dev, int64_t q_stride, int32_t n_q_heads, void* q_out_dev,
+                      const int32_t* tok_off_dev, int32_t n_tokens, const int32_t* pos_dev,
+                      const kvs_rope_axes* axes, const int32_t* block_table_dev, int32_t max_blocks,
+                      const int32_t* seq_len_dev, int32_t n_seq, cudaStream_t stream);
+
+/* Gather, the way back: k_out / v_out bf16 [n_tokens][num_kv_heads][head_dim]
+ * receive the pool's values of the tokens that kvs_append with the same
+ * tok_off and seq_len would write (the last n of the first seq_len[a]); Q4G64
+ * pools give scale * code + bias, rounded to bf16.  This is the k_cached of
+ * kvs_select_critical.  Rows whose token has no valid place (device errors as
+ * for kvs_append) are left as they were. */
+kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* tok_off_dev, int32_t n_tokens,
+                      const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev, int32_t n_seq,
+                      void* k_out_dev, void* v_out_dev, cudaStream_t stream);
+
+/* Attention of query chunks over the block tables (prompt chunks, drafted
+ * tokens, cross attention):
+ *   out[t][h] = sum_(p < lim) softmax_p(scale * <q[t][h], K_a[p]>) V_a[p]
+ * causal = 1: lim = seq_len[a] - n + j + 1 for row j of the n rows of
+ * sequence a (a row sees itself and what is before it); causal = 0: lim =
+ * seq_len[a] for every row (an encoder's states, of any length).  A row with
+ * lim <= 0 yields zeros.
+ * q_dev         bf16 [n_tokens][n_q_heads][head_dim] with row stride q_stride,
+ *               already position-encoded; out_dev bf16, without gaps, must
+ *               not overlap q.  scale is positive and finite.
+ * Requires n_q_heads % num_kv_heads == 0, a group of at most 16 query heads
+ * per KV head and a BF16 pool.  Stored keys and values of tokens below
+ * seq_len are finite; what the pool holds behind them (the rest of a block)
+ * is never used.  Bad block ids (KVS_DEVERR_BLOCK_ID) count as zero keys and
+ * values; seq_len outside [0, max_blocks * 16] (KVS_DEVERR_SEQ_LEN) is
+ * clamped; with offsets outside [0, n_tokens] or decreasing ones
+ * (KVS_DEVERR_JOB) nothing is written.
+ * Neighbouring sequences whose tables begin with the same blocks share their
+ * work: the rows of all of them go over the common part together, once.  The
+ * result is the same to rounding for every grouping, and the same to the bit
+ * for the same call.
+ * As for decoding, a plan per step serves every layer: kvs_extend_plan writes
+ * it into ws, kvs_extend_attn_planned runs a layer with it (same arguments;
+ * other shapes set KVS_DEVERR_PLAN and nothing is written), kvs_extend_attn is
+ * the one after the other.  ws: kvs_extend_workspace_size bytes, of one stream
+ * at a time. */
+kvs_status kvs_extend_workspace_size(const kvs_pool* pool, int32_t n_tokens, int32_t n_seq, int32_t max_blocks,
+                                     int32_t n_q_heads, size_t* bytes);
+kvs_status kvs_extend_plan(kvs_pool* pool, const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,
+                           const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                           int32_t n_seq, int32_t causal, void* ws, size_t ws_bytes, cudaStream_t stream);
+kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, const void* q_dev, int64_t q_stride,
+                                   const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,
+                                   const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                                   int32_t n_seq, int32_t causal, float scale, void* out_dev, void* ws,
+                                   size_t ws_bytes, cudaStream_t stream);
+kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int64_t q_stride,
+                           const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,
+                           const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                           int32_t n_seq, int32_t causal, float scale, void* out_dev, void* ws, size_t ws_bytes,
+                           cudaStream_t stream);
+
 /* Test-only switches.  KVS_TEST_STALL_ONE_STAGE: the next kvs_decode_attn /
  * kvs_decode_attn_planned launch with a query group <= 8 leaves one ring
  * stage of one warp unarmed, so that warp's bounded wait runs out (about a

@@ -1,0 +1,1193 @@
+// Attention of query chunks over the paged pool (prompt chunks, drafted
+// tokens, cross attention) on the fifth-generation tensor cores.
+//
+//   out_r = sum_p e^(x_rp) V_p / sum_p e^(x_rp),  x_rp = scale <q_r, K_p>,  p < lim_r
+//
+// in one pass over the keys: with a reference point m (a running maximum that
+// moves only when it is exceeded by more than 2^8), l = sum_p 2^(s_p - m) and
+// O = sum_p 2^(s_p - m) V_p in fp32, s = x log2 e; moving m rescales l and O.
+//
+// GB300 layout of the work:
+//  * Rows are (token, query head of a KV head): 128 / G whole tokens make the
+//    M = 128 rows of a tile.  A CTA holds two tiles, A and B, of consecutive
+//    tokens, and streams the keys in tiles of 128 through both: each K / V tile
+//    that TMA brings (block by block through the block table, 128-byte
+//    swizzle) feeds four 128 x 128 x head_dim products.
+//  * S = Q K^T lands in tensor memory; two warpgroups (one per tile, one row
+//    per thread, so the softmax needs no shuffles) turn it into P = 2^(s - m)
+//    as bf16 in the same columns, and O += P V takes P from tensor memory.
+//    While one tile's softmax runs, the tensor cores work for the other tile.
+//  * P is rounded to bf16 (relative error at most 2^-8 per weight; the output's own
+//    rounding is of that size); l sums the unrounded weights; O, m, l are fp32.
+//  * Warp 8 issues the MMAs, warp 9 the TMA copies and the work claims.
+//
+// The plan lists the work as items (row tile pair, block table, key range).
+// Long key ranges are split into pieces so that the items fill the SMs evenly;
+// runs of sequences whose tables begin with the same blocks put their rows,
+// which lie side by side in the packed batch, into common tiles over the
+// common part ("shared" items) and go on alone behind it.  Rows with more than
+// one part leave (m, l, O) in fp32, and a merge kernel joins them in a fixed
+// order.  CTAs claim items (longest first) from a counter in the plan.
+#include <algorithm>
+#include <cmath>
+
+#include <cudaTypedefs.h>
+
+#include "tcgen05.cuh"
+#include "internal.h"
+
+namespace kvs {
+
+namespace {
+
+// Two softmax warpgroups; MMA warp, TMA warp and two idle ones that complete
+// their warpgroup.  384 threads start with 168 registers each (64,512 in all);
+// the softmax threads, which hold a row's 128 scores, take 208 and the others
+// 88: 256 * 208 + 128 * 88 = 64,512.
+constexpr int kExThreads = 384;
+constexpr int kExRegsSoftmax = 208, kExRegsOther = 88;
+constexpr int kExTile = 128;             // keys of a tile, rows of a row tile
+constexpr int kExBlocks = kExTile / 16;  // pool blocks of a key tile
+constexpr int kExMagic = 0x45585431;
+// above this many (token, query head) rows a call fills the device without
+// splits or shared parts (2,048 row-tile pairs and more), and none are made:
+// the workspace's part buffers stay below about a gigabyte
+constexpr long long kExPartRows = 1ll << 19;
+constexpr int kExItemsPerSm = 4;         // pieces aimed at per SM
+constexpr int kExMinPiece = 2;           // key tiles of the shortest piece
+
+template <int D>
+__host__ __device__ constexpr int ex_tile_bytes() { return kExTile * D * 2; }
+template <int D>
+__host__ __device__ constexpr int ex_stages() { return D == 128 ? 5 : 8; }
+template <int D>
+__host__ __device__ constexpr int ex_smem() { return 1024 + ex_tile_bytes<D>() * (2 + ex_stages<D>()); }
+constexpr uint32_t kExCols = 512;        // S/P of A and B at 0 and 128, O at 256 and 256 + D
+
+// Plan header (int indices)
+enum { kHMagic, kHSeq, kHBlocks, kHGroup, kHKv, kHCausal, kHTokens, kHItems, kHCounter, kHUnits, kHParts, kHSharedUnits, kHTotal = 16 };
+
+// One item: a row-tile pair over a range of key tiles of one block table.
+struct __align__(16) ExItem {
+  int t0, n_tok;      // packed rows t0 .. t0 + n_tok
+  int seq;            // row of the block table
+  int kv0, kv1;       // key tiles
+  int lim0, step;     // keys visible to token k of the item: min(lim0 + step * k, kv_end)
+  int kv_end;         // keys of the sequence (or of the shared part)
+  int part;           // first part row, -1: the output itself
+  int pad[3];
+};
+static_assert(sizeof(ExItem) == 48, "three 16-byte loads");
+
+// One row-tile pair of the plan, as the merge reads it.
+struct __align__(16) ExUnit {
+  int t0, n_tok;
+  int part, pieces;   // first part row and pieces of its own range (part -1: written directly)
+  int sh_t0, sh_unit; // shared range: first token of the run, its first unit (-1: none)
+  int pad[2];
+};
+static_assert(sizeof(ExUnit) == 32, "two 16-byte loads");
+
+struct ExWorkspace {
+  int* hdr;
+  int4* seq;        // [n_seq] {first row, rows, keys, shareable tiles}
+  int* lcp;         // [n_seq] common leading key tiles with the next sequence
+  int4* run;        // [n_seq] by run index: {shared tiles, first sequence, sequences, rows}
+  int2* seg;        // [n_seq] by sequence: {run, first unit}
+  int2* runseg;     // [n_seq] by run: {first shared unit, shared units}
+  ExItem* items;
+  ExUnit* units;
+  float* part;      // [rows][hkv][D]
+  float2* ml;       // [rows][hkv]
+  int max_items, max_units;
+  long long part_rows;
+  size_t bytes;
+};
+
+int ex_tokens_per_unit(int g) { return 2 * (kExTile / g); }
+
+ExWorkspace ex_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks, int g, void* base) {
+  const int hkv = pool->desc.num_kv_heads, D = pool->desc.head_dim;
+  const int tu = ex_tokens_per_unit(g);
+  ExWorkspace w{};
+  const long long own = n_tokens / tu + n_seq;
+  w.max_units = (int)(2 * own);
+  // sum of pieces <= (all key tiles of all units) / piece + units, and the
+  // piece is at least the total over kExItemsPerSm * SMs / heads
+  const long long extra = (long long)kExItemsPerSm * pool->num_sms / hkv + 1;
+  w.max_items = (int)(w.max_units + extra);
+  const bool parts = (long long)n_tokens * g * hkv <= kExPartRows;
+  // rows of a unit x its pieces: every row of its own and of a shared range
+  // once, and 2 * 128 rows for each piece beyond the first
+  w.part_rows = parts ? 2ll * n_tokens * g + extra * 2 * kExTile : 0;
+  const long long tiles = ((long long)max_blocks + kExBlocks - 1) / kExBlocks + 1;
+  w.part_rows = std::min(w.part_rows, (long long)n_tokens * g * (tiles + 1));   // at most a piece per key tile
+  char* p = static_cast<char*>(base);
+  size_t o = 0;
+  auto take = [&](size_t b) {
+    const size_t at = o;
+    o += (b + 255) & ~size_t{255};
+    return p + at;
+  };
+  w.hdr = reinterpret_cast<int*>(take(kHTotal * 4));
+  w.seq = reinterpret_cast<int4*>(take((size_t)n_seq * 16));
+  w.lcp = reinterpret_cast<int*>(take((size_t)n_seq * 4));
+  w.run = reinterpret_cast<int4*>(take((size_t)n_seq * 16));
+  w.seg = reinterpret_cast<int2*>(take((size_t)n_seq * 8));
+  w.runseg = reinterpret_cast<int2*>(take((size_t)n_seq * 8));
+  w.items = reinterpret_cast<ExItem*>(take((size_t)w.max_items * sizeof(ExItem)));
+  w.units = reinterpret_cast<ExUnit*>(take((size_t)w.max_units * sizeof(ExUnit)));
+  w.part = reinterpret_cast<float*>(take((size_t)w.part_rows * hkv * D * 4));
+  w.ml = reinterpret_cast<float2*>(take((size_t)w.part_rows * hkv * 8));
+  w.bytes = o;
+  return w;
+}
+
+// ------------------------------------------------------------------- plan ---
+struct ExPlanParams {
+  ExWorkspace w;
+  const int32_t *tok_off, *seq_len, *table;
+  uint32_t* status;
+  int n_tokens, n_seq, max_blocks, capacity, g, hkv, causal, sms, share;
+};
+
+// {first row, rows (-1: bad offsets), keys, key tiles that every row of the
+// sequence sees whole}
+__device__ __forceinline__ int4 ex_seq(const ExPlanParams& p, int a, bool report) {
+  const int t0 = __ldg(p.tok_off + a), t1 = __ldg(p.tok_off + a + 1);
+  if (t0 < 0 || t1 < t0 || t1 > p.n_tokens) return make_int4(0, -1, 0, 0);
+  const long long most = (long long)p.max_blocks * 16;
+  long long n = __ldg(p.seq_len + a);
+  if (n < 0 || n > most) {
+    if (report) set_err(p.status, KVS_DEVERR_SEQ_LEN);
+    n = n < 0 ? 0 : most;
+  }
+  const int rows = t1 - t0;
+  const long long seen = p.causal ? max(n - rows + 1, 0ll) : n;
+  return make_int4(t0, rows, (int)n, rows > 0 ? (int)(min(seen, n) / kExTile) : 0);
+}
+
+// Leading key tiles that sequence a's table has in common with the next
+// one's (blocks of valid ids, equal one by one), among those every row sees.
+__global__ void __launch_bounds__(256) extend_lcp_kernel(const __grid_constant__ ExPlanParams p) {
+  pdl_enter();
+  const int a = blockIdx.x;
+  const int tiles = min(ex_seq(p, a, false).w, ex_seq(p, a + 1, false).w);
+  const int n = tiles * kExBlocks;
+  const int32_t* x = p.table + (size_t)a * p.max_blocks;
+  const int32_t* y = x + p.max_blocks;
+  __shared__ int first;
+  if (threadIdx.x == 0) first = n;
+  __syncthreads();
+  constexpr int U = 8;   // loads in flight per thread and row
+  for (int b0 = 0; b0 < n; b0 += 256 * U) {
+    int xv[U], yv[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * 256 + threadIdx.x;
+      xv[u] = b < n ? __ldg(x + b) : 0;
+      yv[u] = b < n ? __ldg(y + b) : 0;
+    }
+    int bad = n;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * 256 + threadIdx.x;
+      if (b < n && (xv[u] != yv[u] || xv[u] < 0 || xv[u] >= p.capacity)) bad = min(bad, b);
+    }
+    if (bad < n) atomicMin(&first, bad);
+    __syncthreads();
+    if (first < n) break;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) p.w.lcp[a] = first / kExBlocks;
+}
+
+constexpr int kPlanThreads = 1024;
+
+// Exclusive scan of x over the CTA's threads plus a running total.
+__device__ __forceinline__ int ex_scan(int x, int* sums, int& carry) {
+  int total;
+  const int r = block_exclusive_scan(x, sums, total) + carry;
+  carry += total;
+  return r;
+}
+
+// Key tiles of unit i of a sequence's own range, behind `skip` shared tiles.
+__device__ __forceinline__ int ex_own_tiles(const int4& s, int i, int tu, int causal, int skip) {
+  const int last = min(s.y, (i + 1) * tu) - 1;    // the unit's last row sees most
+  const int lim = causal ? min(max(s.z - s.y + last + 1, 0), s.z) : s.z;
+  return max(0, (lim + kExTile - 1) / kExTile - skip);
+}
+
+__device__ __forceinline__ int ex_pieces(int tiles, int piece) { return max(1, (tiles + piece - 1) / piece); }
+
+// Candidate i of 32 for the piece length: the longest unit in 1.18^i pieces
+// (1 to 169).
+__device__ __forceinline__ int ex_candidate(int most, int least, int i) {
+  return max(least, (int)ceilf((float)most * exp2f(-0.2388f * (float)i)));
+}
+
+// One CTA: runs of sequences, units, piece length, items sorted by length.
+__global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_constant__ ExPlanParams p) {
+  pdl_enter();
+  __shared__ int sums[32];
+  __shared__ int hist[256];
+  __shared__ float cost[32];
+  __shared__ int s_piece, s_parts, s_most;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tu = 2 * (kExTile / p.g), tt = kExTile / p.g;
+  int* hdr = p.w.hdr;
+  if (tid < 256) hist[tid] = 0;
+  if (tid == 0) {
+    s_parts = 0;
+    s_most = 1;
+  }
+  int bad = 0;
+  for (int a = tid; a < p.n_seq; a += kPlanThreads) {
+    const int4 s = ex_seq(p, a, true);
+    bad |= s.y < 0;
+    p.w.seq[a] = s;
+  }
+  // offsets that do not ascend within [0, n_tokens] give an empty plan: rows
+  // of sequences are disjoint and side by side in everything below
+  if (__syncthreads_or(bad)) {
+    if (tid == 0) {
+      set_err(p.status, KVS_DEVERR_JOB);
+      hdr[kHMagic] = 0;
+      hdr[kHItems] = hdr[kHUnits] = hdr[kHCounter] = 0;
+    }
+    return;
+  }
+  // runs: a sequence starts a new one unless its common part with the one
+  // before it is at least half of the neighbouring common parts (so that a
+  // short common part does not cut down two families of long ones)
+  auto link = [&](int a) {   // between a and a + 1
+    if (p.share <= 0 || a < 0 || a + 1 >= p.n_seq) return 0;
+    return min(p.w.lcp[a], min(p.w.seq[a].w, p.w.seq[a + 1].w));
+  };
+  int carry = 0;
+  for (int a0 = 0; a0 < p.n_seq; a0 += kPlanThreads) {
+    const int a = a0 + tid;
+    int head = 0;
+    if (a < p.n_seq) {
+      const int l = link(a - 1);
+      head = a == 0 || l == 0 || 2 * l < max(link(a - 2), link(a));
+    }
+    const int r = ex_scan(head, sums, carry) + head - 1;
+    if (a < p.n_seq) {
+      p.w.seg[a].x = r;
+      if (head) p.w.run[r] = make_int4(0x7fffffff, a, 0, 0);
+    }
+  }
+  const int n_runs = carry;
+  __syncthreads();
+  for (int a = tid; a < p.n_seq; a += kPlanThreads) {
+    const int r = p.w.seg[a].x;
+    const int4 s = p.w.seq[a];
+    atomicAdd(&p.w.run[r].z, 1);
+    atomicAdd(&p.w.run[r].w, s.y);
+    if (a != p.w.run[r].y) atomicMin(&p.w.run[r].x, link(a - 1));
+  }
+  __syncthreads();
+  // a run shares when its rows fill at most three quarters of the row tiles
+  // that its sequences would fill one by one
+  for (int r = warp; r < n_runs; r += 32) {
+    const int4 v = p.w.run[r];
+    int sep = 0;
+    for (int a = v.y + lane; a < v.y + v.z; a += 32) sep += (p.w.seq[a].y + tt - 1) / tt;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sep += __shfl_xor_sync(0xffffffffu, sep, o);
+    const int joint = (v.w + tt - 1) / tt;
+    if (lane == 0) p.w.run[r].x = v.z >= 2 && 4 * joint <= 3 * sep ? v.x : 0;
+  }
+  __syncthreads();
+  // units: the sequences' own first, then the runs'
+  carry = 0;
+  for (int a0 = 0; a0 < p.n_seq; a0 += kPlanThreads) {
+    const int a = a0 + tid;
+    const int n = a < p.n_seq ? (p.w.seq[a].y + tu - 1) / tu : 0;
+    const int at = ex_scan(n, sums, carry);
+    if (a < p.n_seq) p.w.seg[a].y = at;
+  }
+  const int own_units = carry;
+  for (int r0 = 0; r0 < n_runs; r0 += kPlanThreads) {
+    const int r = r0 + tid;
+    const int n = r < n_runs && p.w.run[r].x > 0 ? (p.w.run[r].w + tu - 1) / tu : 0;
+    const int at = ex_scan(n, sums, carry);
+    if (r < n_runs) p.w.runseg[r] = make_int2(at, n);
+  }
+  const int n_units = carry;
+  __syncthreads();
+  // visits every unit: f(unit, tiles, own, index in its sequence or run, sequence or run)
+  auto each = [&](int w0, int nw, auto f) {
+    for (int a = w0; a < p.n_seq; a += nw) {
+      const int4 s = p.w.seq[a];
+      const int2 sg = p.w.seg[a];
+      const int skip = p.w.run[sg.x].x;
+      const int n = (s.y + tu - 1) / tu;
+      for (int i = lane; i < n; i += 32) f(sg.y + i, ex_own_tiles(s, i, tu, p.causal, skip), true, i, a, skip);
+    }
+    for (int r = w0; r < n_runs; r += nw) {
+      const int2 rs = p.w.runseg[r];
+      const int sh = p.w.run[r].x;
+      for (int i = lane; i < rs.y; i += 32) f(rs.x + i, sh, false, i, r, 0);
+    }
+  };
+  // piece length: of 32 candidates the one with the least estimated time
+  // (rounds over the SMs x mean piece, each piece with the cost of about one
+  // more tile); no splits in calls too large for part buffers
+  {
+    int most = 1;
+    long long sum = 0;
+    each(warp, 32, [&](int, int tiles, bool, int, int, int) {
+      most = max(most, tiles);
+    });
+#pragma unroll
+    for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if (lane == 0) atomicMax(&s_most, most);
+    __syncthreads();
+    most = s_most;
+    // all tiles of all units (every warp for itself)
+    for (int a = lane; a < p.n_seq; a += 32) {
+      const int4 s = p.w.seq[a];
+      const int skip = p.w.run[p.w.seg[a].x].x;
+      for (int i = 0; i * tu < s.y; ++i) sum += ex_own_tiles(s, i, tu, p.causal, skip);
+    }
+    for (int r = lane; r < n_runs; r += 32) sum += (long long)p.w.run[r].x * p.w.runseg[r].y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const long long all = sum * p.hkv;
+    const int least = (int)max((long long)kExMinPiece, (all + (long long)kExItemsPerSm * p.sms - 1) / ((long long)kExItemsPerSm * p.sms));
+    const bool split = p.share >= 0 && (long long)n_units * p.hkv < 4ll * p.sms;
+    const int cand = !split ? most : ex_candidate(most, least, warp);
+    long long n = 0;
+    for (int a = lane; a < p.n_seq; a += 32) {
+      const int4 s = p.w.seq[a];
+      const int skip = p.w.run[p.w.seg[a].x].x;
+      for (int i = 0; i * tu < s.y; ++i) n += ex_pieces(ex_own_tiles(s, i, tu, p.causal, skip), cand);
+    }
+    for (int r = lane; r < n_runs; r += 32) n += (long long)ex_pieces(p.w.run[r].x, cand) * p.w.runseg[r].y;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+    if (lane == 0) {
+      const float items = (float)(n * p.hkv), sms = (float)p.sms;
+      const float mean = (float)all / fmaxf(items, 1.f) + 1.5f;
+      const float rounds = items < 3.f * sms ? ceilf(items / sms) : items / sms + 0.5f;
+      cost[warp] = fmaxf(rounds * mean, fminf((float)cand, (float)most) + 1.5f);
+    }
+    __syncthreads();
+    if (tid == 0) {
+      int best = 0;
+      for (int i = 1; i < 32; ++i)
+        if (cost[i] < cost[best]) best = i;
+      s_piece = !split ? most : ex_candidate(most, least, best);
+    }
+    __syncthreads();
+  }
+  const int piece = s_piece, most = s_most;
+  auto pieces_of = [&](int tiles, bool own, int skip) { return own && tiles == 0 && skip > 0 ? 0 : ex_pieces(tiles, piece); };
+  // items by length, longest first (256 classes; their order inside a class
+  // changes no result)
+  auto klass = [&](int len) { return 255 - (int)((long long)len * 255 / max(most, 1)); };
+  each(warp, 32, [&](int, int tiles, bool own, int, int, int skip) {
+    const int np = pieces_of(tiles, own, skip);
+    for (int k = 0; k < np; ++k)
+      atomicAdd(&hist[klass((int)((long long)tiles * (k + 1) / np) - (int)((long long)tiles * k / np))], 1);
+  });
+  __syncthreads();
+  carry = 0;
+  const int h = tid < 256 ? hist[tid] : 0;
+  const int at0 = ex_scan(h, sums, carry);
+  const int n_items = carry;
+  if (tid < 256) hist[tid] = at0;
+  __syncthreads();
+  each(warp, 32, [&](int unit, int tiles, bool own, int i, int who, int skip) {
+    const int np = pieces_of(tiles, own, skip);
+    const bool parts = own ? (np > 1 || skip > 0) : true;
+    ExUnit u{};
+    ExItem it{};
+    if (own) {
+      const int4 s = p.w.seq[who];
+      const int2 sg = p.w.seg[who];
+      u.t0 = s.x + i * tu;
+      u.n_tok = min(tu, s.y - i * tu);
+      u.sh_unit = skip > 0 ? p.w.runseg[sg.x].x : -1;
+      u.sh_t0 = p.w.seq[p.w.run[sg.x].y].x;
+      it.seq = who;
+      it.lim0 = p.causal ? s.z - s.y + i * tu + 1 : s.z;
+      it.step = p.causal;
+      it.kv_end = s.z;
+    } else {
+      const int4 v = p.w.run[who];
+      u.t0 = p.w.seq[v.y].x + i * tu;
+      u.n_tok = min(tu, v.w - i * tu);
+      u.sh_unit = -1;
+      it.seq = v.y;
+      it.lim0 = it.kv_end = v.x * kExTile;
+    }
+    u.pieces = np;
+    u.part = -1;
+    if (parts && np > 0) {
+      const int rows = u.n_tok * p.g * np;
+      u.part = atomicAdd(&s_parts, rows);
+      if ((long long)u.part + rows > p.w.part_rows) {   // the sizes exclude it: drop the rows
+        set_err(p.status, KVS_DEVERR_PLAN);
+        u.part = 0;
+        u.n_tok = 0;
+      }
+    }
+    if (unit < p.w.max_units) p.w.units[unit] = u;
+    it.t0 = u.t0;
+    it.n_tok = u.n_tok;
+    for (int k = 0; k < np; ++k) {
+      it.kv0 = skip + (int)((long long)tiles * k / np);
+      it.kv1 = skip + (int)((long long)tiles * (k + 1) / np);
+      it.part = u.part < 0 ? -1 : u.part + k * u.n_tok * p.g;
+      const int slot = atomicAdd(&hist[klass(it.kv1 - it.kv0)], 1);
+      if (slot < p.w.max_items) p.w.items[slot] = it;
+    }
+  });
+  if (tid == 0) {
+    hdr[kHSeq] = p.n_seq;
+    hdr[kHBlocks] = p.max_blocks;
+    hdr[kHGroup] = p.g;
+    hdr[kHKv] = p.hkv;
+    hdr[kHCausal] = p.causal;
+    hdr[kHTokens] = p.n_tokens;
+    hdr[kHItems] = min(n_items, p.w.max_items);
+    hdr[kHCounter] = 0;
+    hdr[kHUnits] = min(own_units, p.w.max_units);
+    hdr[kHMagic] = kExMagic;
+  }
+}
+
+// -------------------------------------------------------------- attention ---
+struct ExParams {
+  ExWorkspace w;
+  const int32_t* table;
+  uint16_t* out;
+  uint32_t* status;
+  int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows;
+  float scale_log2;
+};
+
+__device__ __forceinline__ bool ex_plan_ok(const int* hdr, int n_seq, int max_blocks, int g, int hkv, int causal, int n_tokens) {
+  const int4* h4 = reinterpret_cast<const int4*>(hdr);
+  const int4 a = h4[0], b = h4[1];
+  return (a.x == kExMagic) & (a.y == n_seq) & (a.z == max_blocks) & (a.w == g) & (b.x == hkv) & (b.y == causal) & (b.z == n_tokens);
+}
+
+struct ExBars {
+  uint64_t full[8], empty[8];            // K / V ring
+  uint64_t q_full, q_empty;
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t it_full[2], it_empty[2];      // item slots
+  uint64_t fin;
+};
+
+// The item as the CTA's roles see it, with the key tiles of each row tile.
+struct ExWork {
+  ExItem it;
+  int head;
+  int done;
+};
+
+// Key tiles that tile x (0: A, 1: B) of an item takes.
+__device__ __forceinline__ int ex_tiles(const ExItem& it, int x, int tt) {
+  const int first = x * tt;
+  if (first >= it.n_tok) return 0;
+  const int last = min(it.n_tok, first + tt) - 1;
+  const int lim = min(it.lim0 + it.step * last, it.kv_end);
+  return max(0, min((lim + kExTile - 1) / kExTile, it.kv1) - it.kv0);
+}
+
+__device__ __forceinline__ void tmem_ld64_issue(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
+      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
+      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
+        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
+        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
+        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
+        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
+        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
+        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Completes the loads issued before; the registers pass through the statement
+// so that nothing computed from them can move in front of it.
+__device__ __forceinline__ void tmem_ld64_wait(uint32_t* r) {
+  asm volatile(
+      "tcgen05.wait::ld.sync.aligned;"
+      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
+        "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
+        "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
+        "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
+        "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+      :
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+      : "memory");
+}
+
+template <int D>
+__global__ void __launch_bounds__(kExThreads, 1)
+extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ CUtensorMap tq,
+                   const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  constexpr int HF = D / 64;                  // 64-column halves
+  constexpr int ST = ex_stages<D>();
+  constexpr int kTile = ex_tile_bytes<D>();
+  constexpr int kHalf = kExTile * 128;        // one [128][64] bf16 half, bytes
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ ExBars bars;
+  __shared__ __align__(16) ExWork work[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 1);
+    }
+    mbar_init(&bars.q_full, 1);
+    mbar_init(&bars.q_empty, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.s_full[i], 1);
+      mbar_init(&bars.p_full[i], 128);
+      mbar_init(&bars.pv_done[i], 1);
+      mbar_init(&bars.it_full[i], 1);
+      mbar_init(&bars.it_empty[i], 9);   // eight softmax warps and the MMA warp
+    }
+    mbar_init(&bars.fin, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, kExCols);
+    tmem_relinquish();
+  }
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  auto sQ = [&](int x) { return base + kTile * x; };
+  auto ring = [&](int i) { return base + kTile * (2 + i); };
+  // rows of a query tile behind its last whole token are never copied to
+  for (int i = threadIdx.x; i < 2 * kTile / 16; i += kExThreads) reinterpret_cast<uint4*>(base)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tt = kExTile / p.g;
+  const bool plan_ok = ex_plan_ok(p.w.hdr, p.n_seq, p.max_blocks, p.g, p.hkv, p.causal, p.n_tokens);
+  if (!plan_ok && threadIdx.x == 0) set_err(p.status, KVS_DEVERR_PLAN);
+  const int n_claims = plan_ok ? min(p.w.hdr[kHItems], p.w.max_items) * p.hkv : 0;
+  auto stop = [&]() { return __any_sync(0xffffffffu, s_abort != 0); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_wait_bounded(bar, parity, p.status);
+    return __all_sync(0xffffffffu, ok);
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kExRegsOther));
+  if (warp == 9) {
+    // ------------------------------------------- claims and TMA copies
+    int n = 0, nq = 0, ni = 0;      // ring uses, query loads, items
+    int armed = -1, q_armed = 0;
+    int claim = blockIdx.x;
+    bool ok = true;
+    auto copy = [&](const CUtensorMap* map, int id, int head) {
+      // stage n: lanes k < 8 copy block k of the tile; a block without an id
+      // lies behind the slab's last row and arrives as zeros
+      const int s = n % ST;
+      if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&bars.full[s], kTile);
+      __syncwarp();
+      if (lane < kExBlocks) {
+        const int row = id >= 0 ? (id * p.hkv + head) * 16 : p.slab_rows;
+#pragma unroll
+        for (int hf = 0; hf < HF; ++hf) tma_load_3d(ring(s) + hf * kHalf + lane * 2048, map, 0, row, hf, &bars.full[s]);
+      }
+      __syncwarp();
+      armed = n++;
+      return true;
+    };
+    while (ok) {
+      if (stop()) { ok = false; break; }
+      const int slot = ni & 1;
+      if (ni >= 2 && !wait(&bars.it_empty[slot], ((ni - 2) >> 1) & 1)) { ok = false; break; }
+      const bool end = claim >= n_claims;
+      ExItem it{};
+      int head = 0, next = 0;
+      if (!end) {
+        const int item = claim / p.hkv;
+        head = claim - item * p.hkv;
+        const int4* src = reinterpret_cast<const int4*>(p.w.items + item);
+        int4* dst = reinterpret_cast<int4*>(&it);
+        dst[0] = __ldg(src);
+        dst[1] = __ldg(src + 1);
+        dst[2] = __ldg(src + 2);
+        if (lane == 0) next = (int)gridDim.x + atomicAdd(p.w.hdr + kHCounter, 1);
+      }
+      if (lane == 0) {
+        work[slot].it = it;
+        work[slot].head = head;
+        work[slot].done = end;
+        mbar_arrive(&bars.it_full[slot]);
+      }
+      __syncwarp();
+      ++ni;
+      if (end) break;
+      const int na = ex_tiles(it, 0, tt), nb = ex_tiles(it, 1, tt), nt = max(na, nb);
+      const int32_t* row = p.table + (size_t)it.seq * p.max_blocks;
+      const int nblk = (it.kv_end + 15) / 16;
+      auto block = [&](int j) {
+        const int b = (it.kv0 + j) * kExBlocks + lane;
+        int id = -1;
+        if (lane < kExBlocks && j < nt && b < nblk) {
+          id = __ldg(row + b);
+          if (id < 0 || id >= p.capacity) {
+            set_err(p.status, KVS_DEVERR_BLOCK_ID);
+            id = -1;
+          }
+        }
+        return id;
+      };
+      int id = block(0);
+      for (int j = 0; j < nt; ++j) {
+        const int id_next = block(j + 1);
+        if (!copy(&tk, id, head)) { ok = false; break; }
+        if (j == 0) {
+          // the query tiles, once the last S of the item before has read them
+          if (nq >= 1 && !wait(&bars.q_empty, (nq - 1) & 1)) { ok = false; break; }
+          if (lane == 0) {
+            const int tiles = nb > 0 ? 2 : 1;
+            mbar_arrive_expect_tx(&bars.q_full, (uint32_t)(tiles * HF * tt * p.g * 128));
+            for (int x = 0; x < tiles; ++x)
+              for (int hf = 0; hf < HF; ++hf)
+                tma_load_5d(sQ(x) + hf * kHalf, &tq, 0, 0, it.t0 + x * tt, head, hf, &bars.q_full);
+          }
+          __syncwarp();
+          q_armed = ++nq;
+        }
+        if (!copy(&tv, id, head)) { ok = false; break; }
+        id = id_next;
+      }
+      claim = __shfl_sync(0xffffffffu, next, 0);
+    }
+    if (!ok) {
+      s_abort = 1;
+      // copies in flight land before the shared memory goes away
+      for (int m = max(0, armed - ST + 1); m <= armed; ++m) mbar_drain(&bars.full[m % ST], (m / ST) & 1);
+      if (q_armed) mbar_drain(&bars.q_full, (q_armed - 1) & 1);
+    }
+  } else if (warp == 8) {
+    // ------------------------------------------------------- MMA issue
+    constexpr uint32_t idS = umma_idesc_bf16(128, 128, false, false);
+    constexpr uint32_t idO = umma_idesc_bf16(128, D, false, true);
+    int n = 0, nq = 0, np[2] = {0, 0};    // ring position, query loads, P uses
+    bool ok = true;
+    auto issue_s = [&](int x, int m) {    // S_x = Q_x K^T, K in ring use m
+      if (lane == 0) {
+        const uint32_t a0 = smem_u32(sQ(x)), b0 = smem_u32(ring(m % ST));
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
+          umma_ss(tmem + 128u * x, umma_desc_sw128(a0 + o, 16, 1024), umma_desc_sw128(b0 + o, 16, 1024), idS, kk > 0);
+        }
+        umma_commit(&bars.s_full[x]);
+      }
+    };
+    auto issue_pv = [&](int x, int m, bool acc) {   // O_x (+)= P_x V, V in ring use m
+      if (lane == 0) {
+        const uint32_t b0 = smem_u32(ring(m % ST));
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          umma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * kk,
+                  umma_desc_sw128(b0 + kk * 2048, kHalf, 1024), idO, acc || kk > 0);
+        umma_commit(&bars.pv_done[x]);
+      }
+    };
+    for (int ni = 0;; ++ni) {
+      const int slot = ni & 1;
+      if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+      const ExItem it = work[slot].it;
+      const int done = work[slot].done;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+      if (done) break;
+      const int nx[2] = {ex_tiles(it, 0, tt), ex_tiles(it, 1, tt)};
+      const int nt = max(nx[0], nx[1]);
+      if (nt == 0) continue;
+      // rows of the last tile's V behind the sequence's end hold anything:
+      // zero them up to the block's end (P is zero there, and 0 * NaN is not)
+      const int tail = it.kv_end - (it.kv0 + nt - 1) * kExTile;
+      if (!wait(&bars.full[n % ST], (n / ST) & 1) || !wait(&bars.q_full, nq++ & 1)) { ok = false; break; }
+      tc_fence_after();
+#pragma unroll
+      for (int x = 0; x < 2; ++x)
+        if (nx[x] > 0) {
+          // P of the item before has been read (its last P V is complete)
+          if (np[x] > 0 && !wait(&bars.pv_done[x], (np[x] - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          issue_s(x, n);
+        }
+      if (!ok) break;
+      if (lane == 0) {
+        umma_commit(&bars.empty[n % ST]);
+        if (nt == 1) umma_commit(&bars.q_empty);
+      }
+      for (int j = 0; j < nt && ok; ++j) {
+        const int mv = n + 2 * j + 1, mk = n + 2 * j + 2;   // ring uses of V(j) and K(j + 1)
+        if (!wait(&bars.full[mv % ST], (mv / ST) & 1)) { ok = false; break; }
+        if (j == nt - 1 && tail < kExTile && (tail & 15)) {
+          const int r0 = tail, r1 = (tail + 15) & ~15;
+          for (int i = lane; i < (r1 - r0) * HF * 8; i += 32) {
+            const int c = i & 7, hf = (i >> 3) % HF, r = r0 + (i >> 3) / HF;
+            *reinterpret_cast<uint4*>(ring(mv % ST) + hf * kHalf + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+        const bool more = j + 1 < nt;
+        if (more && !wait(&bars.full[mk % ST], (mk / ST) & 1)) { ok = false; break; }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          if (j >= nx[x]) continue;
+          if (!wait(&bars.p_full[x], np[x] & 1)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv(x, mv, j > 0);
+          const int mine = np[x]++;
+          if (j + 1 < nx[x]) {
+            if (!wait(&bars.pv_done[x], mine & 1)) { ok = false; break; }   // S goes where P was
+            tc_fence_after();
+            issue_s(x, mk);
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          umma_commit(&bars.empty[mv % ST]);
+          if (more) umma_commit(&bars.empty[mk % ST]);
+          if (j + 2 == nt) umma_commit(&bars.q_empty);
+        }
+        __syncwarp();
+      }
+      if (!ok) break;
+      n += 2 * nt;
+    }
+    if (!ok) s_abort = 1;
+    // every MMA issued has completed before the tensor memory is released
+    if (lane == 0) umma_commit(&bars.fin);
+    __syncwarp();
+    mbar_wait_bounded(&bars.fin, 0, p.status);
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kExRegsSoftmax));
+    // ---------------------------------------------------------- softmax
+    const int x = warp >> 2, r = (warp & 3) * 32 + lane;   // row tile, row = TMEM lane
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + 128u * x, tO = tmem + lanes + 256u + (uint32_t)D * x;
+    const int rt = r / p.g, rg = r - rt * p.g;             // token and head of the row
+    const float sl2 = p.scale_log2;
+    int ns = 0;      // S uses of this tile
+    bool ok = true;
+    for (int ni = 0;; ++ni) {
+      const int slot = ni & 1;
+      if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+      const ExItem it = work[slot].it;
+      const int head = work[slot].head, done = work[slot].done;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+      if (done) break;
+      const int nt = ex_tiles(it, x, tt);
+      const int tok = x * tt + rt;
+      const bool live = rt < tt && tok < it.n_tok;
+      const int lim = min(it.lim0 + it.step * tok, it.kv_end);   // keys this row sees
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < nt; ++j) {
+        if (!wait(&bars.s_full[x], ns & 1)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t s0[64], s1[64];
+        tmem_ld64_issue(tS, s0);
+        tmem_ld64_wait(s0);
+        tmem_ld64_issue(tS + 64, s1);
+        const int rem = lim - (it.kv0 + j) * kExTile;   // visible keys of this tile
+        const bool masked = !__all_sync(0xffffffffu, rem >= kExTile || !live);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i >= rem) s0[i] = 0xff800000u;
+        }
+        float mx0 = -INFINITY, mx1 = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          mx0 = fmaxf(mx0, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s0[i + 1])));
+          mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s0[i + 2]), __uint_as_float(s0[i + 3])));
+        }
+        tmem_ld64_wait(s1);
+        if (masked) {
+#pragma unroll
+          for (int i = 0; i < 64; ++i)
+            if (i + 64 >= rem) s1[i] = 0xff800000u;
+        }
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          mx0 = fmaxf(mx0, fmaxf(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])));
+          mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s1[i + 2]), __uint_as_float(s1[i + 3])));
+        }
+        const float mx = fmaxf(mx0, mx1) * sl2;
+        const float mn = (m == -INFINITY || mx > m + 8.f) ? fmaxf(m, mx) : m;
+        const float ref = mn == -INFINITY ? 0.f : mn;   // nothing visible yet: 2^(-inf - 0) = 0
+        // a row whose reference moved rescales its O once the P V before is done
+        const bool move = m != -INFINITY && mn > m;
+        if (__any_sync(0xffffffffu, move)) {
+          const float f = move ? fast_exp2(m - mn) : 1.f;
+          if (!wait(&bars.pv_done[x], (ns - 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t v[32];
+            tmem_ld32(tO + 32 * q, v);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+            tmem_st32(tO + 32 * q, v);
+          }
+          l *= f;
+        }
+        m = mn;
+        const float2 sc2 = make_float2(sl2, sl2), rf2 = make_float2(-ref, -ref);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        auto half = [&](uint32_t* s, uint32_t col) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            float2 a = __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, rf2);
+            float2 b = __ffma2_rn(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), sc2, rf2);
+            a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+            b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
+            sum0 = __fadd2_rn(sum0, a);
+            sum1 = __fadd2_rn(sum1, b);
+            s[i / 2] = pack_bf16(a.x, a.y);
+            s[i / 2 + 1] = pack_bf16(b.x, b.y);
+          }
+          tmem_st32(col, s);
+        };
+        half(s0, tS);
+        half(s1, tS + 32);
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bars.p_full[x]);
+        ++ns;
+      }
+      if (!ok) break;
+      // the rows' results
+      if (nt > 0) {
+        if (!wait(&bars.pv_done[x], (ns - 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+      }
+      const bool some = live && !(l == 0.f);
+      const size_t prow = ((size_t)(it.part + tok * p.g + rg)) * p.hkv + head;
+      const float inv = some ? 1.f / l : 0.f;
+      if (x == 1 && it.n_tok <= tt) continue;   // no tile B
+#pragma unroll 1
+      for (int q = 0; q < D / 32; ++q) {
+        uint32_t v[32];
+        if (nt > 0) tmem_ld32(tO + 32 * q, v);
+        if (live && it.part >= 0) {
+          uint4* dst = reinterpret_cast<uint4*>(p.w.part + prow * D + 32 * q);
+#pragma unroll
+          for (int e = 0; e < 8; ++e)
+            dst[e] = some ? make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]) : make_uint4(0u, 0u, 0u, 0u);
+        } else if (live) {
+          uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)(it.t0 + tok) * p.hq + head * p.g + rg) * D + 32 * q);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint32_t o[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              o[i] = some ? pack_bf16(__uint_as_float(v[8 * e + 2 * i]) * inv, __uint_as_float(v[8 * e + 2 * i + 1]) * inv) : 0u;
+            dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
+          }
+        }
+        __syncwarp();
+      }
+      if (live && it.part >= 0) p.w.ml[prow] = make_float2(some ? m : -INFINITY, some ? l : 0.f);
+    }
+    if (!ok) s_abort = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kExCols);
+  }
+}
+
+// ------------------------------------------------------------------ merge ---
+// Joins the parts of the rows that have several: a CTA takes one unit and KV
+// head, a warp one row at a time, the parts in the order shared range, own
+// range, each by its pieces.
+template <int D>
+__global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExParams p) {
+  pdl_enter();
+  constexpr int E = D / 32;   // elements per lane
+  const bool plan_ok = ex_plan_ok(p.w.hdr, p.n_seq, p.max_blocks, p.g, p.hkv, p.causal, p.n_tokens);
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && plan_ok) p.w.hdr[kHCounter] = 0;   // for the next layer
+  if (!plan_ok) return;
+  const int n_units = p.w.hdr[kHUnits], head = blockIdx.y;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tu = 2 * (kExTile / p.g);
+  for (int i = blockIdx.x; i < n_units; i += gridDim.x) {
+    const ExUnit u = p.w.units[i];
+    if (u.part < 0 && u.sh_unit < 0) continue;   // written by the attention itself
+    for (int r = warp; r < u.n_tok * p.g; r += 8) {
+      const int t = u.t0 + r / p.g;
+      ExUnit sh{};
+      if (u.sh_unit >= 0) sh = p.w.units[u.sh_unit + (t - u.sh_t0) / tu];
+      const int n_sh = u.sh_unit >= 0 ? sh.pieces : 0, n = n_sh + (u.part >= 0 ? u.pieces : 0);
+      const int sh_row = (t - sh.t0) * p.g + r % p.g;
+      auto at = [&](int k) {
+        const long long row = k < n_sh ? (long long)sh.part + (long long)k * sh.n_tok * p.g + sh_row
+                                       : (long long)u.part + (long long)(k - n_sh) * u.n_tok * p.g + r;
+        return (size_t)row * p.hkv + head;
+      };
+      float mx = -INFINITY;
+      for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.w.ml[at(k)].x);
+#pragma unroll
+      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+      float acc[E], l = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) acc[e] = 0.f;
+      if (mx != -INFINITY) {
+        for (int k = 0; k < n; ++k) {
+          const size_t row = at(k);
+          const float2 ml = p.w.ml[row];
+          const float f = fast_exp2(ml.x - mx);
+          l += f * ml.y;
+          float v[E];
+          if constexpr (E == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(p.w.part + row * D + lane * 4);
+            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(p.w.part + row * D + lane * 2);
+            v[0] = x.x; v[1] = x.y;
+          }
+#pragma unroll
+          for (int e = 0; e < E; ++e) acc[e] += f * v[e];
+        }
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((size_t)t * p.hq + head * p.g + r % p.g) * D + lane * E);
+#pragma unroll
+      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+    }
+  }
+}
+
+// ------------------------------------------------------------------- host ---
+PFN_cuTensorMapEncodeTiled_v12000 ex_encoder() {
+  static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+  }();
+  return fn;
+}
+
+// Queries [tokens][hkv][G][D] as {64 elements, G heads, tokens, KV heads, D/64
+// halves}: a box {64, G, 128/G, 1, 1} is one half of a row tile, row = token *
+// G + head.  Tokens behind the last one arrive as zeros.
+bool ex_query_map(CUtensorMap* m, const void* q, int n_tokens, int g, int hkv, int d, long long stride) {
+  auto enc = ex_encoder();
+  if (!enc) return false;
+  cuuint64_t dims[5] = {64, (cuuint64_t)g, (cuuint64_t)n_tokens, (cuuint64_t)hkv, (cuuint64_t)(d / 64)};
+  cuuint64_t strides[4] = {(cuuint64_t)d * 2, (cuuint64_t)stride * 2, (cuuint64_t)g * d * 2, 128};
+  cuuint32_t box[5] = {64, (cuuint32_t)g, (cuuint32_t)(kExTile / g), 1, 1};
+  cuuint32_t es[5] = {1, 1, 1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(q), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+kvs_status ex_check(const kvs_pool* pool, const char* what, int n_tokens, int n_seq, int max_blocks, int n_q_heads) {
+  if (!pool) return fail(KVS_ERR_INVALID_ARG, std::string(what) + ": null pool");
+  const kvs_pool_desc& d = pool->desc;
+  if (d.dtype != KVS_DTYPE_BF16) return fail(KVS_ERR_UNSUPPORTED, std::string(what) + ": bf16 pools only");
+  if (n_tokens < 0 || n_seq < 0 || max_blocks < 1) return fail(KVS_ERR_INVALID_ARG, std::string(what) + ": bad sizes");
+  if (n_seq > d.max_seqs) return fail(KVS_ERR_CAPACITY, std::string(what) + ": n_seq exceeds the pool's max_seqs");
+  if (n_q_heads < 1 || n_q_heads % d.num_kv_heads)
+    return fail(KVS_ERR_INVALID_ARG, std::string(what) + ": n_q_heads must be a multiple of num_kv_heads");
+  if (n_q_heads / d.num_kv_heads > 16) return fail(KVS_ERR_UNSUPPORTED, std::string(what) + ": more than 16 query heads per KV head");
+  // key tiles, part rows and units are counted in 32 bits
+  if ((long long)max_blocks * 16 > (1ll << 30) || (long long)n_tokens * n_q_heads > (1ll << 30))
+    return fail(KVS_ERR_CAPACITY, std::string(what) + ": too many tokens");
+  return KVS_OK;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t ex_launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D>
+kvs_status ex_run(kvs_pool* pool, int layer, const ExParams& p, const CUtensorMap& tq, long long max_claims, cudaStream_t stream) {
+  if (!smem_limit_once<extend_attn_kernel<D>>(ex_smem<D>(), pool->device))
+    return fail(KVS_ERR_CUDA, "extend_attn: cannot raise the shared-memory limit");
+  const unsigned grid = (unsigned)std::min<long long>(pool->num_sms, max_claims);
+  const CUtensorMap& tk = D == 128 ? pool->tk1[layer] : pool->tk[layer];
+  const CUtensorMap& tv = D == 128 ? pool->tv1[layer] : pool->tv[layer];
+  if (ex_launch(extend_attn_kernel<D>, dim3(grid), dim3(kExThreads), ex_smem<D>(), stream, p, tq, tk, tv) != cudaSuccess)
+    return fail(KVS_ERR_CUDA, std::string("extend_attn: ") + cudaGetErrorString(cudaGetLastError()));
+  count_launch();
+  const unsigned units = (unsigned)std::min(p.w.max_units / 2, 4096);
+  if (ex_launch(extend_merge_kernel<D>, dim3(units, (unsigned)p.hkv), dim3(256), 0, stream, p) != cudaSuccess)
+    return fail(KVS_ERR_CUDA, std::string("extend_attn merge: ") + cudaGetErrorString(cudaGetLastError()));
+  count_launch();
+  return check_launch("extend_attn");
+}
+
+}  // namespace
+
+}  // namespace kvs
+
+using namespace kvs;
+
+extern "C" kvs_status kvs_extend_workspace_size(const kvs_pool* pool, int32_t n_tokens, int32_t n_seq, int32_t max_blocks,
+                                                int32_t n_q_heads, size_t* bytes) {
+  if (!bytes) return fail(KVS_ERR_INVALID_ARG, "extend_workspace_size: null pointer");
+  if (kvs_status st = ex_check(pool, "extend_workspace_size", n_tokens, n_seq, max_blocks, n_q_heads); st != KVS_OK) return st;
+  *bytes = ex_layout(pool, n_tokens, n_seq, max_blocks, n_q_heads / pool->desc.num_kv_heads, nullptr).bytes;
+  return KVS_OK;
+}
+
+extern "C" kvs_status kvs_extend_plan(kvs_pool* pool, const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,
+                                      const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                                      int32_t n_seq, int32_t causal, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (kvs_status st = ex_check(pool, "extend_plan", n_tokens, n_seq, max_blocks, n_q_heads); st != KVS_OK) return st;
+  if (causal != 0 && causal != 1) return fail(KVS_ERR_INVALID_ARG, "extend_plan: causal is 0 or 1");
+  if (n_tokens == 0 || n_seq == 0) return KVS_OK;
+  if (!tok_off_dev || !block_table_dev || !seq_len_dev || !ws) return fail(KVS_ERR_INVALID_ARG, "extend_plan: null pointer");
+  if (!aligned16(ws)) return fail(KVS_ERR_INVALID_ARG, "extend_plan: ws must be 16-byte aligned");
+  const int hkv = pool->desc.num_kv_heads, g = n_q_heads / hkv;
+  ExPlanParams p{};
+  p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
+  if (ws_bytes < p.w.bytes) return fail(KVS_ERR_CAPACITY, "extend_plan: workspace too small");
+  if (kvs_status st = check_pool_device(pool, "extend_plan"); st != KVS_OK) return st;
+  p.tok_off = tok_off_dev;
+  p.seq_len = seq_len_dev;
+  p.table = block_table_dev;
+  p.status = pool->status;
+  p.n_tokens = n_tokens;
+  p.n_seq = n_seq;
+  p.max_blocks = max_blocks;
+  p.capacity = pool->desc.capacity_blocks;
+  p.g = g;
+  p.hkv = hkv;
+  p.causal = causal;
+  p.sms = pool->num_sms;
+  const bool parts = (long long)n_tokens * n_q_heads <= kExPartRows;
+  p.share = !parts ? -1 : n_seq > 1 ? 1 : 0;
+  if (p.share == 1) {
+    if (launch_pdl(extend_lcp_kernel, dim3((unsigned)(n_seq - 1)), dim3(256), stream, p) != cudaSuccess)
+      return fail(KVS_ERR_CUDA, std::string("extend_plan: ") + cudaGetErrorString(cudaGetLastError()));
+    count_launch();
+  }
+  if (launch_pdl(extend_plan_kernel, dim3(1), dim3(kPlanThreads), stream, p) != cudaSuccess)
+    return fail(KVS_ERR_CUDA, std::string("extend_plan: ") + cudaGetErrorString(cudaGetLastError()));
+  count_launch();
+  return check_launch("extend_plan");
+}
+
+extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, const void* q_dev, int64_t q_stride,
+                                              const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,
+                                              const int32_t* block_table_dev, int32_t max_blocks,
+                                              const int32_t* seq_len_dev, int32_t n_seq, int32_t causal, float scale,
+                                              void* out_dev, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (kvs_status st = ex_check(pool, "extend_attn", n_tokens, n_seq, max_blocks, n_q_heads); st != KVS_OK) return st;
+  const kvs_pool_desc& d = pool->desc;
+  if (layer < 0 || layer >= d.num_layers) return fail(KVS_ERR_INVALID_ARG, "extend_attn: layer out of range");
+  if (causal != 0 && causal != 1) return fail(KVS_ERR_INVALID_ARG, "extend_attn: causal is 0 or 1");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: scale must be positive and finite");
+  const long long row = (long long)n_q_heads * d.head_dim;
+  if (q_stride < row || (q_stride & 7)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: q_stride must hold n_q_heads * head_dim elements and be a multiple of 8");
+  if (n_tokens == 0 || n_seq == 0) return KVS_OK;
+  if (!q_dev || !tok_off_dev || !block_table_dev || !seq_len_dev || !out_dev || !ws)
+    return fail(KVS_ERR_INVALID_ARG, "extend_attn: null pointer");
+  if (!aligned16(q_dev) || !aligned16(out_dev) || !aligned16(ws))
+    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q, out and ws must be 16-byte aligned");
+  const int g = n_q_heads / d.num_kv_heads;
+  ExParams p{};
+  p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
+  if (ws_bytes < p.w.bytes) return fail(KVS_ERR_CAPACITY, "extend_attn: workspace too small");
+  if (kvs_status st = check_pool_device(pool, "extend_attn"); st != KVS_OK) return st;
+  p.table = block_table_dev;
+  p.out = static_cast<uint16_t*>(out_dev);
+  p.status = pool->status;
+  p.n_tokens = n_tokens;
+  p.n_seq = n_seq;
+  p.max_blocks = max_blocks;
+  p.capacity = d.capacity_blocks;
+  p.g = g;
+  p.hkv = d.num_kv_heads;
+  p.hq = n_q_heads;
+  p.causal = causal;
+  p.slab_rows = d.capacity_blocks * d.num_kv_heads * d.block_tokens;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  CUtensorMap tq;
+  if (!ex_query_map(&tq, q_dev, n_tokens, g, d.num_kv_heads, d.head_dim, q_stride))
+    return fail(KVS_ERR_CUDA, "extend_attn: cuTensorMapEncodeTiled failed for q");
+  const long long max_claims = (long long)p.w.max_items * d.num_kv_heads;
+  return d.head_dim == 128 ? ex_run<128>(pool, layer, p, tq, max_claims, stream)
+                           : ex_run<64>(pool, layer, p, tq, max_claims, stream);
+}
+
+extern "C" kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int64_t q_stride,
+                                      const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,
+                                      const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                                      int32_t n_seq, int32_t causal, float scale, void* out_dev, void* ws,
+                                      size_t ws_bytes, cudaStream_t stream) {
+  // the layer's own arguments are checked before the plan is enqueued
+  if (!pool) return fail(KVS_ERR_INVALID_ARG, "extend_attn: null pool");
+  if (layer < 0 || layer >= pool->desc.num_layers) return fail(KVS_ERR_INVALID_ARG, "extend_attn: layer out of range");
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: scale must be positive and finite");
+  if (n_tokens > 0 && n_seq > 0 && (!q_dev || !out_dev || !aligned16(q_dev) || !aligned16(out_dev)))
+    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q and out must be set and 16-byte aligned");
+  if (q_stride < (long long)n_q_heads * pool->desc.head_dim || (q_stride & 7))
+    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q_stride must hold n_q_heads * head_dim elements and be a multiple of 8");
+  kvs_status st = kvs_extend_plan(pool, tok_off_dev, n_tokens, n_q_heads, block_table_dev, max_blocks, seq_len_dev, n_seq,
+                                  causal, ws, ws_bytes, stream);
+  if (st != KVS_OK) return st;
+  return kvs_extend_attn_planned(pool, layer, q_dev, q_stride, tok_off_dev, n_tokens, n_q_heads, block_table_dev,
+                                 max_blocks, seq_len_dev, n_seq, causal, scale, out_dev, ws, ws_bytes, stream);
+}

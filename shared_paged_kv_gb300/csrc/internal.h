@@ -125,6 +125,9 @@ __device__ __forceinline__ PlanHdr load_plan_hdr(const int* hdr) {
   return PlanHdr{{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w, c.x, c.y, c.z, c.w}};
 }
 
+// OK when the pool lives on the current device (append.cu).
+kvs_status check_pool_device(const kvs_pool* pool, const char* what);
+
 // CTAs of the wide tile's grid for rotation calls (attn_tm.cu)
 int runs_wide_ctas(const kvs_pool* pool);
 kvs_status launch_wide_tile(const WideParams& p, const kvs_pool* pool, int layer, int max_claims,

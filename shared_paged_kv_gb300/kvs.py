@@ -50,7 +50,8 @@ EXPORTED = [
     "kvs_blocks_init_free", "kvs_block_write", "kvs_seq_release", "kvs_evict_score",
     "kvs_pool_block_bytes", "kvs_pool_export", "kvs_pool_import", "kvs_pool_set_test_flags",
     "kvs_workspace_size", "kvs_pool_check", "kvs_pool_stats", "kvs_last_error_string",
-    "kvs_launch_count",
+    "kvs_launch_count", "kvs_rope_apply", "kvs_append", "kvs_gather", "kvs_extend_workspace_size",
+    "kvs_extend_plan", "kvs_extend_attn_planned", "kvs_extend_attn",
 ]
 
 
@@ -64,6 +65,19 @@ class PoolDesc(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "num_layers", "num_kv_heads", "head_dim", "block_tokens", "dtype",
         "capacity_blocks", "diff_capacity_blocks", "max_seqs")]
+
+
+class RopeAxes(ctypes.Structure):
+    """kvs_rope_axes: theta, the pairs that each of one to three position axes
+    turns (they sum to head_dim / 2), and whether the axes share one spectrum."""
+    _fields_ = [("theta", ctypes.c_float), ("n_axes", ctypes.c_int32), ("section", ctypes.c_int32 * 3),
+                ("own_spectrum", ctypes.c_int32)]
+
+    def __init__(self, theta, sections, own_spectrum=False):
+        sections = tuple(int(x) for x in sections)
+        if not 1 <= len(sections) <= 3:
+            raise ValueError("1 to 3 position axes")
+        super().__init__(theta, len(sections), (ctypes.c_int32 * 3)(*sections), int(own_spectrum))
 
 
 class Stats(ctypes.Structure):
@@ -106,6 +120,13 @@ def load(path: str = LIB_PATH):
         "kvs_decode_attn_q4": [P, I32, P, I32, P, I32, P, I32, P, F32, P, P, SZ, P],
         "kvs_quantize_q4": [P, I32, P, P, P, I32, P],
         "kvs_workspace_size": [P, I32, I32, I32, I32, ctypes.POINTER(SZ)],
+        "kvs_rope_apply": [P, I64, P, P, I32, P, I64, I32, I32, I32, P],
+        "kvs_append": [P, I32, P, I64, P, I64, P, I64, I32, P, P, I32, P, P, P, I32, P, I32, P],
+        "kvs_gather": [P, I32, P, I32, P, I32, P, I32, P, P, P],
+        "kvs_extend_workspace_size": [P, I32, I32, I32, I32, ctypes.POINTER(SZ)],
+        "kvs_extend_plan": [P, P, I32, I32, P, I32, P, I32, I32, P, SZ, P],
+        "kvs_extend_attn_planned": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, P, SZ, P],
+        "kvs_extend_attn": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, P, SZ, P],
         "kvs_pool_check": [P, P, ctypes.POINTER(U32)],
         "kvs_pool_stats": [P, P, P, P, ctypes.POINTER(Stats)],
     }
@@ -333,6 +354,111 @@ def kvs_decode_attn_q4(pool: Pool, layer, q, n_q_heads, block_table, max_blocks,
 def kvs_quantize_q4(pool: Pool, layer, k_src, v_src, dst_blocks, n_blocks, stream=None):
     _check(load().kvs_quantize_q4(pool.handle, layer, _ptr(k_src), _ptr(v_src), _ptr(dst_blocks),
                                   n_blocks, _stream(stream)))
+
+
+def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str):
+    """(pointer, elements between two tokens) of packed rows [n_tokens][heads]
+    [head_dim] of 16-bit elements; the tokens may lie apart."""
+    if t.element_size() != 2 or t.dtype == torch.float16:
+        raise ValueError(f"{what}: bf16 rows (torch.bfloat16, or their bits as int16) are wanted, got {t.dtype}")
+    if t.dim() != 3 or t.shape[0] < n_tokens or t.shape[1] != n_heads or t.shape[2] != head_dim:
+        raise ValueError(f"{what}: shape {tuple(t.shape)} is not [>= {n_tokens}][{n_heads}][{head_dim}]")
+    st = t.stride()
+    if st[2] != 1 or (n_heads > 1 and st[1] != head_dim):
+        raise ValueError(f"{what}: the heads of a token must lie side by side")
+    return t.data_ptr(), (st[0] if t.shape[0] > 1 else n_heads * head_dim)
+
+
+def _ints(t, n: int, what: str):
+    if t is None:
+        return None
+    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} values is wanted")
+    return t.data_ptr()
+
+
+def kvs_rope_apply(x, pos, rope: RopeAxes, out, n_tokens, n_heads, head_dim, inverse=False, stream=None):
+    """out[t][h] = x[t][h] rotated by its positions pos int32 [axes][n_tokens]
+    (taken back with inverse); x and out may be views into wider rows."""
+    xp, xs = _rows(x, n_tokens, n_heads, head_dim, "x")
+    op, os_ = _rows(out, n_tokens, n_heads, head_dim, "out")
+    _check(load().kvs_rope_apply(xp, xs, _ints(pos, rope.n_axes * n_tokens, "pos"), ctypes.byref(rope), int(inverse), op,
+                                 os_, n_tokens, n_heads, head_dim, _stream(stream)))
+
+
+def kvs_append(pool: Pool, layer, k_new, v_new, n_tokens, tok_off, block_table, max_blocks, seq_len, n_seq, pos=None,
+               rope: Optional[RopeAxes] = None, q=None, n_q_heads=0, q_out=None, stream=None):
+    """Write packed new rows k_new / v_new through the block table, keys
+    rotated; rotate q into q_out (without gaps) in the same pass."""
+    d = pool.desc
+    kp, ks = _rows(k_new, n_tokens, d.num_kv_heads, d.head_dim, "k_new")
+    vp, vs = _rows(v_new, n_tokens, d.num_kv_heads, d.head_dim, "v_new")
+    qp = qs = op = 0
+    if q is not None:
+        qp, qs = _rows(q, n_tokens, n_q_heads, d.head_dim, "q")
+    if q_out is not None:
+        op, os_ = _rows(q_out, n_tokens, n_q_heads, d.head_dim, "q_out")
+        if os_ != n_q_heads * d.head_dim:
+            raise ValueError("q_out: rows without gaps are wanted")
+    _check(load().kvs_append(
+        pool.handle, layer, kp, ks, vp, vs, qp, qs, n_q_heads, op, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens,
+        _ints(pos, (rope.n_axes if rope is not None else 1) * n_tokens, "pos"),
+        ctypes.byref(rope) if rope is not None else None, _ints(block_table, n_seq * max_blocks, "block_table"),
+        max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq, _stream(stream)))
+
+
+def kvs_gather(pool: Pool, layer, n_tokens, tok_off, block_table, max_blocks, seq_len, n_seq, k_out, v_out, stream=None):
+    """Read the rows that kvs_append with the same arguments would write, as
+    bf16 [n_tokens][num_kv_heads][head_dim]."""
+    d = pool.desc
+    gap = d.num_kv_heads * d.head_dim
+    kp, ks = _rows(k_out, n_tokens, d.num_kv_heads, d.head_dim, "k_out")
+    vp, vs = _rows(v_out, n_tokens, d.num_kv_heads, d.head_dim, "v_out")
+    if ks != gap or vs != gap:
+        raise ValueError("k_out, v_out: rows without gaps are wanted")
+    _check(load().kvs_gather(pool.handle, layer, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens,
+                             _ints(block_table, n_seq * max_blocks, "block_table"), max_blocks,
+                             _ints(seq_len, n_seq, "seq_len"), n_seq, kp, vp, _stream(stream)))
+
+
+def kvs_extend_workspace_size(pool: Pool, n_tokens: int, n_seq: int, max_blocks: int, n_q_heads: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().kvs_extend_workspace_size(pool.handle, n_tokens, n_seq, max_blocks, n_q_heads, ctypes.byref(out)))
+    return out.value
+
+
+def kvs_extend_plan(pool: Pool, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq, causal, ws,
+                    stream=None):
+    """The work plan of a batch of query chunks, for every layer of a step."""
+    _check(load().kvs_extend_plan(pool.handle, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens, n_q_heads,
+                                  _ints(block_table, n_seq * max_blocks, "block_table"), max_blocks,
+                                  _ints(seq_len, n_seq, "seq_len"), n_seq, int(causal), _ptr(ws),
+                                  ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def _extend(fn, pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq, causal, scale, out,
+            ws, stream):
+    d = pool.desc
+    qp, qs = _rows(q, n_tokens, n_q_heads, d.head_dim, "q")
+    op, os_ = _rows(out, n_tokens, n_q_heads, d.head_dim, "out")
+    if os_ != n_q_heads * d.head_dim:
+        raise ValueError("out: rows without gaps are wanted")
+    _check(fn(pool.handle, layer, qp, qs, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens, n_q_heads,
+              _ints(block_table, n_seq * max_blocks, "block_table"), max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq,
+              int(causal), scale, op, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+
+
+def kvs_extend_attn_planned(pool: Pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq,
+                            causal, scale, out, ws, stream=None):
+    _extend(load().kvs_extend_attn_planned, pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len,
+            n_seq, causal, scale, out, ws, stream)
+
+
+def kvs_extend_attn(pool: Pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq, causal,
+                    scale, out, ws, stream=None):
+    """Attention of packed query chunks (bf16 out); see include/kvs.h."""
+    _extend(load().kvs_extend_attn, pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq,
+            causal, scale, out, ws, stream)
 
 
 def kvs_pool_check(pool: Pool, stream=None) -> int:
