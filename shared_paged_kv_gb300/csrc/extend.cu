@@ -203,6 +203,8 @@ __global__ void __launch_bounds__(256) extend_lcp_kernel(const __grid_constant__
 }
 
 constexpr int kPlanThreads = 1024;
+constexpr int kPlanSeqs = 512;     // up to this many sequences the plan's arrays stay in shared memory
+constexpr int kPlanUnits = 640;    // more units than calls that are split have (4 per SM)
 
 // Exclusive scan of x over the CTA's threads plus a running total.
 __device__ __forceinline__ int ex_scan(int x, int* sums, int& carry) {
@@ -234,6 +236,16 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   __shared__ int hist[256];
   __shared__ float cost[32];
   __shared__ int s_piece, s_parts, s_most;
+  __shared__ int tiles_of[kPlanUnits];
+  __shared__ int4 sm_seq[kPlanSeqs], sm_run[kPlanSeqs];
+  __shared__ int2 sm_seg[kPlanSeqs], sm_runseg[kPlanSeqs];
+  __shared__ int sm_lcp[kPlanSeqs];
+  const bool small = p.n_seq <= kPlanSeqs;
+  int4* const seq = small ? sm_seq : p.w.seq;
+  int4* const run = small ? sm_run : p.w.run;
+  int2* const seg = small ? sm_seg : p.w.seg;
+  int2* const runseg = small ? sm_runseg : p.w.runseg;
+  const int* const lcp = small ? sm_lcp : p.w.lcp;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tu = 2 * (kExTile / p.g), tt = kExTile / p.g;
   int* hdr = p.w.hdr;
@@ -244,9 +256,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   }
   int bad = 0;
   for (int a = tid; a < p.n_seq; a += kPlanThreads) {
+    if (small && p.share > 0) sm_lcp[a] = a + 1 < p.n_seq ? p.w.lcp[a] : 0;
     const int4 s = ex_seq(p, a, true);
     bad |= s.y < 0;
-    p.w.seq[a] = s;
+    seq[a] = s;
   }
   // offsets that do not ascend within [0, n_tokens] give an empty plan: rows
   // of sequences are disjoint and side by side in everything below
@@ -263,7 +276,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   // short common part does not cut down two families of long ones)
   auto link = [&](int a) {   // between a and a + 1
     if (p.share <= 0 || a < 0 || a + 1 >= p.n_seq) return 0;
-    return min(p.w.lcp[a], min(p.w.seq[a].w, p.w.seq[a + 1].w));
+    return min(lcp[a], min(seq[a].w, seq[a + 1].w));
   };
   int carry = 0;
   for (int a0 = 0; a0 < p.n_seq; a0 += kPlanThreads) {
@@ -275,112 +288,114 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     }
     const int r = ex_scan(head, sums, carry) + head - 1;
     if (a < p.n_seq) {
-      p.w.seg[a].x = r;
-      if (head) p.w.run[r] = make_int4(0x7fffffff, a, 0, 0);
+      seg[a].x = r;
+      if (head) run[r] = make_int4(0x7fffffff, a, 0, 0);
     }
   }
   const int n_runs = carry;
   __syncthreads();
   for (int a = tid; a < p.n_seq; a += kPlanThreads) {
-    const int r = p.w.seg[a].x;
-    const int4 s = p.w.seq[a];
-    atomicAdd(&p.w.run[r].z, 1);
-    atomicAdd(&p.w.run[r].w, s.y);
-    if (a != p.w.run[r].y) atomicMin(&p.w.run[r].x, link(a - 1));
+    const int r = seg[a].x;
+    const int4 s = seq[a];
+    atomicAdd(&run[r].z, 1);
+    atomicAdd(&run[r].w, s.y);
+    if (a != run[r].y) atomicMin(&run[r].x, link(a - 1));
   }
   __syncthreads();
   // a run shares when its rows fill at most three quarters of the row tiles
   // that its sequences would fill one by one
   for (int r = warp; r < n_runs; r += 32) {
-    const int4 v = p.w.run[r];
+    const int4 v = run[r];
     int sep = 0;
-    for (int a = v.y + lane; a < v.y + v.z; a += 32) sep += (p.w.seq[a].y + tt - 1) / tt;
+    for (int a = v.y + lane; a < v.y + v.z; a += 32) sep += (seq[a].y + tt - 1) / tt;
 #pragma unroll
     for (int o = 16; o; o >>= 1) sep += __shfl_xor_sync(0xffffffffu, sep, o);
     const int joint = (v.w + tt - 1) / tt;
-    if (lane == 0) p.w.run[r].x = v.z >= 2 && 4 * joint <= 3 * sep ? v.x : 0;
+    if (lane == 0) run[r].x = v.z >= 2 && 4 * joint <= 3 * sep ? v.x : 0;
   }
   __syncthreads();
   // units: the sequences' own first, then the runs'
   carry = 0;
   for (int a0 = 0; a0 < p.n_seq; a0 += kPlanThreads) {
     const int a = a0 + tid;
-    const int n = a < p.n_seq ? (p.w.seq[a].y + tu - 1) / tu : 0;
+    const int n = a < p.n_seq ? (seq[a].y + tu - 1) / tu : 0;
     const int at = ex_scan(n, sums, carry);
-    if (a < p.n_seq) p.w.seg[a].y = at;
+    if (a < p.n_seq) seg[a].y = at;
   }
   const int own_units = carry;
   for (int r0 = 0; r0 < n_runs; r0 += kPlanThreads) {
     const int r = r0 + tid;
-    const int n = r < n_runs && p.w.run[r].x > 0 ? (p.w.run[r].w + tu - 1) / tu : 0;
+    const int n = r < n_runs && run[r].x > 0 ? (run[r].w + tu - 1) / tu : 0;
     const int at = ex_scan(n, sums, carry);
-    if (r < n_runs) p.w.runseg[r] = make_int2(at, n);
+    if (r < n_runs) runseg[r] = make_int2(at, n);
   }
   const int n_units = carry;
   __syncthreads();
   // visits every unit: f(unit, tiles, own, index in its sequence or run, sequence or run)
   auto each = [&](int w0, int nw, auto f) {
     for (int a = w0; a < p.n_seq; a += nw) {
-      const int4 s = p.w.seq[a];
-      const int2 sg = p.w.seg[a];
-      const int skip = p.w.run[sg.x].x;
+      const int4 s = seq[a];
+      const int2 sg = seg[a];
+      const int skip = run[sg.x].x;
       const int n = (s.y + tu - 1) / tu;
       for (int i = lane; i < n; i += 32) f(sg.y + i, ex_own_tiles(s, i, tu, p.causal, skip), true, i, a, skip);
     }
     for (int r = w0; r < n_runs; r += nw) {
-      const int2 rs = p.w.runseg[r];
-      const int sh = p.w.run[r].x;
+      const int2 rs = runseg[r];
+      const int sh = run[r].x;
       for (int i = lane; i < rs.y; i += 32) f(rs.x + i, sh, false, i, r, 0);
     }
   };
   // piece length: of 32 candidates the one with the least estimated time
   // (rounds over the SMs x mean piece, each piece with the cost of about one
-  // more tile); no splits in calls too large for part buffers
+  // more tile); no splits in calls that fill the device, or are too large for
+  // part buffers
+  const bool split = p.share >= 0 && (long long)n_units * p.hkv < 4ll * p.sms && n_units <= kPlanUnits;
   {
     int most = 1;
-    long long sum = 0;
-    each(warp, 32, [&](int, int tiles, bool, int, int, int) {
+    each(warp, 32, [&](int unit, int tiles, bool, int, int, int) {
       most = max(most, tiles);
+      if (split) tiles_of[unit] = tiles;
     });
 #pragma unroll
     for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
     if (lane == 0) atomicMax(&s_most, most);
     __syncthreads();
     most = s_most;
-    // all tiles of all units (every warp for itself)
-    for (int a = lane; a < p.n_seq; a += 32) {
-      const int4 s = p.w.seq[a];
-      const int skip = p.w.run[p.w.seg[a].x].x;
-      for (int i = 0; i * tu < s.y; ++i) sum += ex_own_tiles(s, i, tu, p.causal, skip);
-    }
-    for (int r = lane; r < n_runs; r += 32) sum += (long long)p.w.run[r].x * p.w.runseg[r].y;
+    if (split) {   // a candidate per warp; every warp sums all units
+      int sum = 0, n = 0;
+      for (int u = lane; u < n_units; u += 32) sum += tiles_of[u];
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    const long long all = sum * p.hkv;
-    const int least = (int)max((long long)kExMinPiece, (all + (long long)kExItemsPerSm * p.sms - 1) / ((long long)kExItemsPerSm * p.sms));
-    const bool split = p.share >= 0 && (long long)n_units * p.hkv < 4ll * p.sms;
-    const int cand = !split ? most : ex_candidate(most, least, warp);
-    long long n = 0;
-    for (int a = lane; a < p.n_seq; a += 32) {
-      const int4 s = p.w.seq[a];
-      const int skip = p.w.run[p.w.seg[a].x].x;
-      for (int i = 0; i * tu < s.y; ++i) n += ex_pieces(ex_own_tiles(s, i, tu, p.causal, skip), cand);
-    }
-    for (int r = lane; r < n_runs; r += 32) n += (long long)ex_pieces(p.w.run[r].x, cand) * p.w.runseg[r].y;
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const float all = (float)sum * (float)p.hkv, sms = (float)p.sms;
+      const int least = max(kExMinPiece, (int)ceilf(all / (kExItemsPerSm * sms)));
+      const int cand = ex_candidate(most, least, warp);
+      for (int u = lane; u < n_units; u += 32) n += ex_pieces(tiles_of[u], cand);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-    if (lane == 0) {
-      const float items = (float)(n * p.hkv), sms = (float)p.sms;
-      const float mean = (float)all / fmaxf(items, 1.f) + 1.5f;
-      const float rounds = items < 3.f * sms ? ceilf(items / sms) : items / sms + 0.5f;
-      cost[warp] = fmaxf(rounds * mean, fminf((float)cand, (float)most) + 1.5f);
-    }
-    __syncthreads();
-    if (tid == 0) {
-      int best = 0;
-      for (int i = 1; i < 32; ++i)
-        if (cost[i] < cost[best]) best = i;
-      s_piece = !split ? most : ex_candidate(most, least, best);
+      for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      if (lane == 0) {
+        const float items = (float)n * (float)p.hkv;
+        const float mean = all / fmaxf(items, 1.f) + 1.5f;
+        const float rounds = items < 3.f * sms ? ceilf(items / sms) : items / sms + 0.5f;
+        cost[warp] = fmaxf(rounds * mean, (float)min(cand, most) + 1.5f);
+      }
+      __syncthreads();
+      if (warp == 0) {   // the least cost, the longest piece on a tie
+        float c = cost[lane];
+        int best = lane;
+#pragma unroll
+        for (int o = 16; o; o >>= 1) {
+          const float c2 = __shfl_xor_sync(0xffffffffu, c, o);
+          const int b2 = __shfl_xor_sync(0xffffffffu, best, o);
+          if (c2 < c || (c2 == c && b2 < best)) {
+            c = c2;
+            best = b2;
+          }
+        }
+        if (lane == 0) s_piece = ex_candidate(most, least, best);
+      }
+    } else if (tid == 0) {
+      s_piece = most;
     }
     __syncthreads();
   }
@@ -407,19 +422,19 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     ExUnit u{};
     ExItem it{};
     if (own) {
-      const int4 s = p.w.seq[who];
-      const int2 sg = p.w.seg[who];
+      const int4 s = seq[who];
+      const int2 sg = seg[who];
       u.t0 = s.x + i * tu;
       u.n_tok = min(tu, s.y - i * tu);
-      u.sh_unit = skip > 0 ? p.w.runseg[sg.x].x : -1;
-      u.sh_t0 = p.w.seq[p.w.run[sg.x].y].x;
+      u.sh_unit = skip > 0 ? runseg[sg.x].x : -1;
+      u.sh_t0 = seq[run[sg.x].y].x;
       it.seq = who;
       it.lim0 = p.causal ? s.z - s.y + i * tu + 1 : s.z;
       it.step = p.causal;
       it.kv_end = s.z;
     } else {
-      const int4 v = p.w.run[who];
-      u.t0 = p.w.seq[v.y].x + i * tu;
+      const int4 v = run[who];
+      u.t0 = seq[v.y].x + i * tu;
       u.n_tok = min(tu, v.w - i * tu);
       u.sh_unit = -1;
       it.seq = v.y;
@@ -480,7 +495,7 @@ __device__ __forceinline__ bool ex_plan_ok(const int* hdr, int n_seq, int max_bl
 struct ExBars {
   uint64_t full[8], empty[8];            // K / V ring
   uint64_t q_full, q_empty;
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_half[2], p_full[2], pv_done[2];
   uint64_t it_full[2], it_empty[2];      // item slots
   uint64_t fin;
 };
@@ -536,6 +551,45 @@ __device__ __forceinline__ void tmem_ld64_wait(uint32_t* r) {
       : "memory");
 }
 
+// MMA issue with descriptors built from a variable low word (address and
+// leading offset) and a constant high word.  The issuing warp stays converged
+// and elects the thread, so that the operands live in uniform registers and an
+// MMA costs a few instructions: with a branch on the lane and 64-bit
+// descriptors the issue alone took 3,300 cycles per tile pair, more than the
+// products themselves.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+__host__ __device__ constexpr uint32_t ex_desc_hi(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+__device__ __forceinline__ uint32_t ex_desc_lo(uint32_t saddr, uint32_t lbo) { return (saddr >> 4) | ((lbo >> 4) << 16); }
+
+__device__ __forceinline__ void ex_mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tmov.b64 da, {%1, %3};\n\tmov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void ex_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
+      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, int c4,
                                             uint64_t* bar) {
   asm volatile(
@@ -571,10 +625,11 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
     mbar_init(&bars.q_empty, 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars.s_full[i], 1);
-      mbar_init(&bars.p_full[i], 128);
+      mbar_init(&bars.p_half[i], 4);
+      mbar_init(&bars.p_full[i], 4);
       mbar_init(&bars.pv_done[i], 1);
       mbar_init(&bars.it_full[i], 1);
-      mbar_init(&bars.it_empty[i], 9);   // eight softmax warps and the MMA warp
+      mbar_init(&bars.it_empty[i], 9);   // eight softmax warps and the MMA thread
     }
     mbar_init(&bars.fin, 1);
     s_abort = 0;
@@ -703,100 +758,109 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
     // ------------------------------------------------------- MMA issue
     constexpr uint32_t idS = umma_idesc_bf16(128, 128, false, false);
     constexpr uint32_t idO = umma_idesc_bf16(128, D, false, true);
-    int n = 0, nq = 0, np[2] = {0, 0};    // ring position, query loads, P uses
+    constexpr uint32_t kHi = ex_desc_hi(1024);
+    const uint32_t q_lo = ex_desc_lo(smem_u32(base), 16);
+    const uint32_t k_lo = ex_desc_lo(smem_u32(ring(0)), 16), v_lo = ex_desc_lo(smem_u32(ring(0)), kHalf);
+    struct Pos {   // a use of the ring
+      int s;
+      uint32_t par;
+      __device__ __forceinline__ void next() {
+        if (++s == ST) {
+          s = 0;
+          par ^= 1u;
+        }
+      }
+    };
+    Pos at{0, 0};                         // K of the tile to come
+    uint32_t q_par = 0, np[2] = {0, 0};   // query loads, P uses
     bool ok = true;
-    auto issue_s = [&](int x, int m) {    // S_x = Q_x K^T, K in ring use m
-      if (lane == 0) {
-        const uint32_t a0 = smem_u32(sQ(x)), b0 = smem_u32(ring(m % ST));
+    auto issue_s = [&](int x, const Pos& k) {    // S_x = Q_x K^T
+      if (elect_one()) {
+        const uint32_t a = q_lo + x * (kTile / 16), b = k_lo + k.s * (kTile / 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t o = (kk >> 2) * kHalf + (kk & 3) * 32;
-          umma_ss(tmem + 128u * x, umma_desc_sw128(a0 + o, 16, 1024), umma_desc_sw128(b0 + o, 16, 1024), idS, kk > 0);
+          const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) / 16;
+          ex_mma_ss(tmem + 128u * x, a + o, b + o, kHi, idS, kk > 0);
         }
         umma_commit(&bars.s_full[x]);
       }
+      __syncwarp();
     };
-    auto issue_pv = [&](int x, int m, bool acc) {   // O_x (+)= P_x V, V in ring use m
-      if (lane == 0) {
-        const uint32_t b0 = smem_u32(ring(m % ST));
+    auto issue_pv = [&](int x, const Pos& v, int k0, bool acc) {   // O_x (+)= P_x V over keys 16 k0 .. 16 k0 + 63
+      if (elect_one()) {
+        const uint32_t b = v_lo + v.s * (kTile / 16);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          umma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * kk,
-                  umma_desc_sw128(b0 + kk * 2048, kHalf, 1024), idO, acc || kk > 0);
-        umma_commit(&bars.pv_done[x]);
+        for (int kk = 0; kk < 4; ++kk)
+          ex_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * (k0 + kk), b + (k0 + kk) * (2048 / 16), kHi, idO,
+                    acc || kk > 0);
+        if (k0) umma_commit(&bars.pv_done[x]);
       }
+      __syncwarp();
+    };
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) umma_commit(bar);
+      __syncwarp();
     };
     for (int ni = 0;; ++ni) {
       const int slot = ni & 1;
       if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
-      const ExItem it = work[slot].it;
-      const int done = work[slot].done;
-      __syncwarp();
+      const int na = __shfl_sync(0xffffffffu, ex_tiles(work[slot].it, 0, tt), 0);
+      const int nb = __shfl_sync(0xffffffffu, ex_tiles(work[slot].it, 1, tt), 0);
+      const int done = __shfl_sync(0xffffffffu, work[slot].done, 0);
       if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+      __syncwarp();
       if (done) break;
-      const int nx[2] = {ex_tiles(it, 0, tt), ex_tiles(it, 1, tt)};
-      const int nt = max(nx[0], nx[1]);
+      const int nt = max(na, nb);
       if (nt == 0) continue;
-      // rows of the last tile's V behind the sequence's end hold anything:
-      // zero them up to the block's end (P is zero there, and 0 * NaN is not)
-      const int tail = it.kv_end - (it.kv0 + nt - 1) * kExTile;
-      if (!wait(&bars.full[n % ST], (n / ST) & 1) || !wait(&bars.q_full, nq++ & 1)) { ok = false; break; }
-      tc_fence_after();
+      if (!wait(&bars.full[at.s], at.par) || !wait(&bars.q_full, q_par)) { ok = false; break; }
+      q_par ^= 1u;
 #pragma unroll
-      for (int x = 0; x < 2; ++x)
-        if (nx[x] > 0) {
-          // P of the item before has been read (its last P V is complete)
-          if (np[x] > 0 && !wait(&bars.pv_done[x], (np[x] - 1) & 1)) { ok = false; break; }
-          tc_fence_after();
-          issue_s(x, n);
-        }
-      if (!ok) break;
-      if (lane == 0) {
-        umma_commit(&bars.empty[n % ST]);
-        if (nt == 1) umma_commit(&bars.q_empty);
+      for (int x = 0; x < 2; ++x) {
+        if ((x ? nb : na) == 0) continue;
+        // P of the item before has been read (its last P V is complete)
+        if (np[x] > 0 && !wait(&bars.pv_done[x], (np[x] - 1) & 1)) { ok = false; break; }
+        tc_fence_after();
+        issue_s(x, at);
       }
-      for (int j = 0; j < nt && ok; ++j) {
-        const int mv = n + 2 * j + 1, mk = n + 2 * j + 2;   // ring uses of V(j) and K(j + 1)
-        if (!wait(&bars.full[mv % ST], (mv / ST) & 1)) { ok = false; break; }
-        if (j == nt - 1 && tail < kExTile && (tail & 15)) {
-          const int r0 = tail, r1 = (tail + 15) & ~15;
-          for (int i = lane; i < (r1 - r0) * HF * 8; i += 32) {
-            const int c = i & 7, hf = (i >> 3) % HF, r = r0 + (i >> 3) / HF;
-            *reinterpret_cast<uint4*>(ring(mv % ST) + hf * kHalf + r * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
-          }
-          fence_proxy_async_smem();
-          __syncwarp();
-        }
+      if (!ok) break;
+      commit(&bars.empty[at.s]);
+      if (nt == 1) commit(&bars.q_empty);
+      at.next();
+      for (int j = 0; j < nt; ++j) {
+        const Pos v = at;
+        at.next();
+        const Pos k = at;     // K(j + 1)
         const bool more = j + 1 < nt;
-        if (more && !wait(&bars.full[mk % ST], (mk / ST) & 1)) { ok = false; break; }
+        if (more) at.next();
+        if (!wait(&bars.full[v.s], v.par)) { ok = false; break; }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          if (j >= nx[x]) continue;
-          if (!wait(&bars.p_full[x], np[x] & 1)) { ok = false; break; }
+          const int nx = x ? nb : na;
+          if (j >= nx) continue;
+          const uint32_t par = np[x] & 1;
+          ++np[x];
+          if (!wait(&bars.p_half[x], par)) { ok = false; break; }
           tc_fence_after();
-          issue_pv(x, mv, j > 0);
-          const int mine = np[x]++;
-          if (j + 1 < nx[x]) {
-            if (!wait(&bars.pv_done[x], mine & 1)) { ok = false; break; }   // S goes where P was
+          issue_pv(x, v, 0, j > 0);
+          if (!wait(&bars.p_full[x], par)) { ok = false; break; }
+          tc_fence_after();
+          issue_pv(x, v, 4, true);
+          if (j + 1 < nx) {
+            if (!wait(&bars.full[k.s], k.par) || !wait(&bars.pv_done[x], par)) { ok = false; break; }   // S goes where P was
             tc_fence_after();
-            issue_s(x, mk);
+            issue_s(x, k);
           }
         }
         if (!ok) break;
-        if (lane == 0) {
-          umma_commit(&bars.empty[mv % ST]);
-          if (more) umma_commit(&bars.empty[mk % ST]);
-          if (j + 2 == nt) umma_commit(&bars.q_empty);
-        }
-        __syncwarp();
+        commit(&bars.empty[v.s]);
+        if (more) commit(&bars.empty[k.s]);
+        if (j + 2 == nt) commit(&bars.q_empty);
       }
       if (!ok) break;
-      n += 2 * nt;
     }
     if (!ok) s_abort = 1;
     // every MMA issued has completed before the tensor memory is released
-    if (lane == 0) umma_commit(&bars.fin);
-    __syncwarp();
+    commit(&bars.fin);
     mbar_wait_bounded(&bars.fin, 0, p.status);
   }
   } else {
@@ -807,7 +871,7 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
     const uint32_t tS = tmem + lanes + 128u * x, tO = tmem + lanes + 256u + (uint32_t)D * x;
     const int rt = r / p.g, rg = r - rt * p.g;             // token and head of the row
     const float sl2 = p.scale_log2;
-    int ns = 0;      // S uses of this tile
+    int ns = 0, n = 0;      // S uses of this tile, ring position
     bool ok = true;
     for (int ni = 0;; ++ni) {
       const int slot = ni & 1;
@@ -817,11 +881,50 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
       __syncwarp();
       if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
       if (done) break;
-      const int nt = ex_tiles(it, x, tt);
+      const int nt = ex_tiles(it, x, tt), nt_other = ex_tiles(it, x ^ 1, tt), nt_all = max(nt, nt_other);
       const int tok = x * tt + rt;
       const bool live = rt < tt && tok < it.n_tok;
       const int lim = min(it.lim0 + it.step * tok, it.kv_end);   // keys this row sees
-      float m = -INFINITY, l = 0.f;
+      // rows of the last V tile behind the sequence's end hold anything: the
+      // first tile that takes it zeroes them up to the block's end (P is zero
+      // there, but 0 * NaN is not)
+      const int tail = it.kv_end - (it.kv0 + nt_all - 1) * kExTile;
+      const bool fix_tail = nt == nt_all && (x == 0 || nt_other < nt_all) && tail < kExTile && (tail & 15);
+      // m: reference point of l and O; next: where it moves with the next tile
+      float m = -INFINITY, next = -INFINITY, l = 0.f;
+      const float2 sc2 = make_float2(sl2, sl2);
+      float2 sum0, sum1;
+      // s[0..31] = 2^(s - ref) of the 64 scores, packed in place; returns
+      // their maximum
+      auto half = [&](uint32_t* s, float ref) {
+        const float2 rf2 = make_float2(-ref, -ref);
+        float ma = -INFINITY, mb = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          float2 a = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
+          float2 b = make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
+          ma = fmaxf(ma, fmaxf(a.x, a.y));
+          mb = fmaxf(mb, fmaxf(b.x, b.y));
+          a = __ffma2_rn(a, sc2, rf2);
+          b = __ffma2_rn(b, sc2, rf2);
+          a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
+          b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
+          sum0 = __fadd2_rn(sum0, a);
+          sum1 = __fadd2_rn(sum1, b);
+          s[i / 2] = pack_bf16(a.x, a.y);
+          s[i / 2 + 1] = pack_bf16(b.x, b.y);
+        }
+        return fmaxf(ma, mb);
+      };
+      auto most = [&](const uint32_t* s) {
+        float a = -INFINITY, b = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 64; i += 4) {
+          a = fmaxf(a, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
+          b = fmaxf(b, fmaxf(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])));
+        }
+        return fmaxf(a, b);
+      };
       for (int j = 0; j < nt; ++j) {
         if (!wait(&bars.s_full[x], ns & 1)) { ok = false; break; }
         tc_fence_after();
@@ -830,73 +933,79 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
         tmem_ld64_wait(s0);
         tmem_ld64_issue(tS + 64, s1);
         const int rem = lim - (it.kv0 + j) * kExTile;   // visible keys of this tile
-        const bool masked = !__all_sync(0xffffffffu, rem >= kExTile || !live);
-        if (masked) {
-#pragma unroll
-          for (int i = 0; i < 64; ++i)
-            if (i >= rem) s0[i] = 0xff800000u;
-        }
-        float mx0 = -INFINITY, mx1 = -INFINITY;
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          mx0 = fmaxf(mx0, fmaxf(__uint_as_float(s0[i]), __uint_as_float(s0[i + 1])));
-          mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s0[i + 2]), __uint_as_float(s0[i + 3])));
-        }
+        const bool masked = __any_sync(0xffffffffu, rem < kExTile && live);
+        // The weights are taken against the reference of the tiles before
+        // (exact for any reference), so the first half's exponentials do not
+        // wait for this tile's maximum; only a tile that exceeds it by 2^32,
+        // the first one and masked ones move it before they start.
+        const bool fresh = __any_sync(0xffffffffu, next == -INFINITY) || masked;
+        sum0 = sum1 = make_float2(0.f, 0.f);
+        float ref = next;
+        float mx = -INFINITY;
+        if (!fresh) mx = half(s0, ref);
         tmem_ld64_wait(s1);
         if (masked) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i)
+          for (int i = 0; i < 64; ++i) {
+            if (i >= rem) s0[i] = 0xff800000u;
             if (i + 64 >= rem) s1[i] = 0xff800000u;
+          }
         }
-#pragma unroll
-        for (int i = 0; i < 64; i += 4) {
-          mx0 = fmaxf(mx0, fmaxf(__uint_as_float(s1[i]), __uint_as_float(s1[i + 1])));
-          mx1 = fmaxf(mx1, fmaxf(__uint_as_float(s1[i + 2]), __uint_as_float(s1[i + 3])));
+        if (fresh) mx = most(s0);
+        mx = fmaxf(mx, most(s1)) * sl2;
+        if (fresh || __any_sync(0xffffffffu, mx > ref + 32.f)) {
+          if (!fresh) {
+            tmem_ld64_issue(tS, s0);
+            tmem_ld64_wait(s0);
+          }
+          if (next == -INFINITY || mx > next + 8.f) next = fmaxf(next, mx);
+          ref = next == -INFINITY ? 0.f : next;   // nothing visible yet: 2^(-inf - 0) = 0
+          sum0 = sum1 = make_float2(0.f, 0.f);
+          half(s0, ref);
         }
-        const float mx = fmaxf(mx0, mx1) * sl2;
-        const float mn = (m == -INFINITY || mx > m + 8.f) ? fmaxf(m, mx) : m;
-        const float ref = mn == -INFINITY ? 0.f : mn;   // nothing visible yet: 2^(-inf - 0) = 0
         // a row whose reference moved rescales its O once the P V before is done
-        const bool move = m != -INFINITY && mn > m;
+        const bool move = m != -INFINITY && next > m;
         if (__any_sync(0xffffffffu, move)) {
-          const float f = move ? fast_exp2(m - mn) : 1.f;
+          const float f = move ? fast_exp2(m - next) : 1.f;
           if (!wait(&bars.pv_done[x], (ns - 1) & 1)) { ok = false; break; }
           tc_fence_after();
 #pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t v[32];
-            tmem_ld32(tO + 32 * q, v);
+          for (int q = 0; q < D / 16; ++q) {
+            uint32_t v[16];
+            tmem_ld16(tO + 16 * q, v);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
-            tmem_st32(tO + 32 * q, v);
+            for (int e = 0; e < 16; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * f);
+            tmem_st16(tO + 16 * q, v);
           }
           l *= f;
         }
-        m = mn;
-        const float2 sc2 = make_float2(sl2, sl2), rf2 = make_float2(-ref, -ref);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-        auto half = [&](uint32_t* s, uint32_t col) {
-#pragma unroll
-          for (int i = 0; i < 64; i += 4) {
-            float2 a = __ffma2_rn(make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1])), sc2, rf2);
-            float2 b = __ffma2_rn(make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])), sc2, rf2);
-            a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
-            b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
-            sum0 = __fadd2_rn(sum0, a);
-            sum1 = __fadd2_rn(sum1, b);
-            s[i / 2] = pack_bf16(a.x, a.y);
-            s[i / 2 + 1] = pack_bf16(b.x, b.y);
+        m = next;
+        tmem_st32(tS, s0);
+        if (j == nt - 1 && fix_tail) {
+          const int mv = n + 2 * j + 1;
+          if (!wait(&bars.full[mv % ST], (mv / ST) & 1)) { ok = false; break; }
+          const int rows = ((tail + 15) & ~15) - tail;
+          for (int i = threadIdx.x & 127; i < rows * HF * 8; i += 128) {
+            const int c = i & 7, hf = (i >> 3) % HF, rr = tail + (i >> 3) / HF;
+            *reinterpret_cast<uint4*>(ring(mv % ST) + hf * kHalf + rr * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
-          tmem_st32(col, s);
-        };
-        half(s0, tS);
-        half(s1, tS + 32);
-        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          fence_proxy_async_smem();
+        }
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bars.p_full[x]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_half[x]);
+        half(s1, ref);
+        l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+        tmem_st32(tS + 32, s1);
+        if (mx > m + 8.f) next = mx;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.p_full[x]);
         ++ns;
       }
+      n += 2 * nt_all;
       if (!ok) break;
       // the rows' results
       if (nt > 0) {
@@ -942,33 +1051,35 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
 }
 
 // ------------------------------------------------------------------ merge ---
-// Joins the parts of the rows that have several: a CTA takes one unit and KV
-// head, a warp one row at a time, the parts in the order shared range, own
-// range, each by its pieces.
+// Joins the parts of the rows that have several, in the order shared range,
+// own range, each by its pieces.  A CTA takes one unit and KV head and every
+// gridDim.z-th eight rows of it, a warp one row at a time; four parts' loads
+// are in flight together (the parts lie in L2: the chain of loads bounds it).
 template <int D>
 __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExParams p) {
   pdl_enter();
   constexpr int E = D / 32;   // elements per lane
+  constexpr int U = 4;
   const bool plan_ok = ex_plan_ok(p.w.hdr, p.n_seq, p.max_blocks, p.g, p.hkv, p.causal, p.n_tokens);
-  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0 && plan_ok) p.w.hdr[kHCounter] = 0;   // for the next layer
   if (!plan_ok) return;
+  if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) p.w.hdr[kHCounter] = 0;   // for the next layer
   const int n_units = p.w.hdr[kHUnits], head = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tu = 2 * (kExTile / p.g);
   for (int i = blockIdx.x; i < n_units; i += gridDim.x) {
     const ExUnit u = p.w.units[i];
     if (u.part < 0 && u.sh_unit < 0) continue;   // written by the attention itself
-    for (int r = warp; r < u.n_tok * p.g; r += 8) {
+    for (int r = blockIdx.z * 8 + warp; r < u.n_tok * p.g; r += 8 * gridDim.z) {
       const int t = u.t0 + r / p.g;
       ExUnit sh{};
       if (u.sh_unit >= 0) sh = p.w.units[u.sh_unit + (t - u.sh_t0) / tu];
       const int n_sh = u.sh_unit >= 0 ? sh.pieces : 0, n = n_sh + (u.part >= 0 ? u.pieces : 0);
       const int sh_row = (t - sh.t0) * p.g + r % p.g;
       auto at = [&](int k) {
-        const long long row = k < n_sh ? (long long)sh.part + (long long)k * sh.n_tok * p.g + sh_row
-                                       : (long long)u.part + (long long)(k - n_sh) * u.n_tok * p.g + r;
+        const int row = k < n_sh ? sh.part + k * sh.n_tok * p.g + sh_row : u.part + (k - n_sh) * u.n_tok * p.g + r;
         return (size_t)row * p.hkv + head;
       };
+      // lane k holds part k's factor 2^(m_k - max) and row; further parts in rounds of 32
       float mx = -INFINITY;
       for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.w.ml[at(k)].x);
 #pragma unroll
@@ -977,22 +1088,39 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
 #pragma unroll
       for (int e = 0; e < E; ++e) acc[e] = 0.f;
       if (mx != -INFINITY) {
-        for (int k = 0; k < n; ++k) {
-          const size_t row = at(k);
-          const float2 ml = p.w.ml[row];
-          const float f = fast_exp2(ml.x - mx);
-          l += f * ml.y;
-          float v[E];
-          if constexpr (E == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(p.w.part + row * D + lane * 4);
-            v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(p.w.part + row * D + lane * 2);
-            v[0] = x.x; v[1] = x.y;
+        for (int k0 = 0; k0 < n; k0 += 32) {
+          float f = 0.f;
+          if (k0 + lane < n) {
+            const float2 ml = p.w.ml[at(k0 + lane)];
+            f = fast_exp2(ml.x - mx);
+            l += f * ml.y;
           }
+          const int m = min(32, n - k0);
+          for (int k = 0; k < m; k += U) {
+            float v[U][E];
 #pragma unroll
-          for (int e = 0; e < E; ++e) acc[e] += f * v[e];
+            for (int j = 0; j < U; ++j) {
+              if (k + j >= m) {
+#pragma unroll
+                for (int e = 0; e < E; ++e) v[j][e] = 0.f;
+              } else if constexpr (E == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(p.w.part + at(k0 + k + j) * D + lane * 4);
+                v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
+              } else {
+                const float2 x = *reinterpret_cast<const float2*>(p.w.part + at(k0 + k + j) * D + lane * 2);
+                v[j][0] = x.x; v[j][1] = x.y;
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+              const float fj = __shfl_sync(0xffffffffu, f, min(k + j, 31));
+#pragma unroll
+              for (int e = 0; e < E; ++e) acc[e] += fj * v[j][e];
+            }
+          }
         }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
       }
       const float inv = l == 0.f ? 0.f : 1.f / l;
       uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((size_t)t * p.hq + head * p.g + r % p.g) * D + lane * E);
@@ -1070,8 +1198,11 @@ kvs_status ex_run(kvs_pool* pool, int layer, const ExParams& p, const CUtensorMa
   if (ex_launch(extend_attn_kernel<D>, dim3(grid), dim3(kExThreads), ex_smem<D>(), stream, p, tq, tk, tv) != cudaSuccess)
     return fail(KVS_ERR_CUDA, std::string("extend_attn: ") + cudaGetErrorString(cudaGetLastError()));
   count_launch();
+  // about 16 CTAs per SM over units, heads and blocks of eight rows
   const unsigned units = (unsigned)std::min(p.w.max_units / 2, 4096);
-  if (ex_launch(extend_merge_kernel<D>, dim3(units, (unsigned)p.hkv), dim3(256), 0, stream, p) != cudaSuccess)
+  const long long most = std::min<long long>(32, ((long long)p.n_tokens * p.g + 7) / 8);
+  const unsigned z = (unsigned)std::clamp<long long>(16ll * pool->num_sms / ((long long)units * p.hkv), 1, most);
+  if (ex_launch(extend_merge_kernel<D>, dim3(units, (unsigned)p.hkv, z), dim3(256), 0, stream, p) != cudaSuccess)
     return fail(KVS_ERR_CUDA, std::string("extend_attn merge: ") + cudaGetErrorString(cudaGetLastError()));
   count_launch();
   return check_launch("extend_attn");
