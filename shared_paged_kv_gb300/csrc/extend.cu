@@ -346,16 +346,19 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
       for (int i = lane; i < rs.y; i += 32) f(rs.x + i, sh, false, i, r, 0);
     }
   };
+  // whether a unit fills more than one row tile
+  auto two_tiles = [&](bool own, int i, int who) { return (own ? seq[who].y : run[who].w) - i * tu > tt; };
   // piece length: of 32 candidates the one with the least estimated time
-  // (rounds over the SMs x mean piece, each piece with the cost of about one
-  // more tile); no splits in calls that fill the device, or are too large for
+  // (the mean load of an SM, or the rounds that the larger half of the pieces
+  // takes; a piece costs its tiles and about 1.5 more, with one row tile 0.6
+  // of that); no splits in calls that fill the device, or are too large for
   // part buffers
   const bool split = p.share >= 0 && (long long)n_units * p.hkv < 4ll * p.sms && n_units <= kPlanUnits;
   {
     int most = 1;
-    each(warp, 32, [&](int unit, int tiles, bool, int, int, int) {
+    each(warp, 32, [&](int unit, int tiles, bool own, int i, int who, int) {
       most = max(most, tiles);
-      if (split) tiles_of[unit] = tiles;
+      if (split) tiles_of[unit] = tiles | (two_tiles(own, i, who) ? 1 << 30 : 0);
     });
 #pragma unroll
     for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -363,22 +366,38 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     __syncthreads();
     most = s_most;
     if (split) {   // a candidate per warp; every warp sums all units
-      int sum = 0, n = 0;
-      for (int u = lane; u < n_units; u += 32) sum += tiles_of[u];
+      int sum = 0;
+      for (int u = lane; u < n_units; u += 32) sum += tiles_of[u] & ~(1 << 30);
 #pragma unroll
       for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float all = (float)sum * (float)p.hkv, sms = (float)p.sms;
-      const int least = max(kExMinPiece, (int)ceilf(all / (kExItemsPerSm * sms)));
+      const float heads = (float)p.hkv, sms = (float)p.sms;
+      const int least = max(kExMinPiece, (int)ceilf((float)sum * heads / (kExItemsPerSm * sms)));
       const int cand = ex_candidate(most, least, warp);
-      for (int u = lane; u < n_units; u += 32) n += ex_pieces(tiles_of[u], cand);
+      auto piece_cost = [&](int u, int& np) {
+        const int tiles = tiles_of[u] & ~(1 << 30);
+        np = ex_pieces(tiles, cand);
+        return (tiles_of[u] >> 30 ? 1.f : 0.6f) * ((float)tiles / (float)np + 1.5f);
+      };
+      float load = 0.f, big = 0.f, n_big = 0.f, top = 0.f;
+      int np;
+      for (int u = lane; u < n_units; u += 32) top = fmaxf(top, piece_cost(u, np));
 #pragma unroll
-      for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-      if (lane == 0) {
-        const float items = (float)n * (float)p.hkv;
-        const float mean = all / fmaxf(items, 1.f) + 1.5f;
-        const float rounds = items < 3.f * sms ? ceilf(items / sms) : items / sms + 0.5f;
-        cost[warp] = fmaxf(rounds * mean, (float)min(cand, most) + 1.5f);
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      for (int u = lane; u < n_units; u += 32) {
+        const float one = piece_cost(u, np);
+        load += one * (float)np;
+        if (2.f * one > top) {
+          big += one * (float)np;
+          n_big += (float)np;
+        }
       }
+#pragma unroll
+      for (int o = 16; o; o >>= 1) {
+        load += __shfl_xor_sync(0xffffffffu, load, o);
+        big += __shfl_xor_sync(0xffffffffu, big, o);
+        n_big += __shfl_xor_sync(0xffffffffu, n_big, o);
+      }
+      if (lane == 0) cost[warp] = fmaxf(load * heads / sms, ceilf(n_big * heads / sms) * big / fmaxf(n_big, 1.f));
       __syncthreads();
       if (warp == 0) {   // the least cost, the longest piece on a tie
         float c = cost[lane];
@@ -401,13 +420,18 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   }
   const int piece = s_piece, most = s_most;
   auto pieces_of = [&](int tiles, bool own, int skip) { return own && tiles == 0 && skip > 0 ? 0 : ex_pieces(tiles, piece); };
-  // items by length, longest first (256 classes; their order inside a class
-  // changes no result)
-  auto klass = [&](int len) { return 255 - (int)((long long)len * 255 / max(most, 1)); };
-  each(warp, 32, [&](int, int tiles, bool own, int, int, int skip) {
+  // items by cost (key tiles x row tiles), largest first: 256 classes; the
+  // order inside a class changes no result.  The pieces of a unit are equal
+  // to one tile, so they fall into two classes.
+  const float per_class = 255.f / (float)(2 * most);
+  auto klass = [&](int len, bool two) { return 255 - (int)((float)(two ? 2 * len : len) * per_class); };
+  each(warp, 32, [&](int, int tiles, bool own, int i, int who, int skip) {
     const int np = pieces_of(tiles, own, skip);
-    for (int k = 0; k < np; ++k)
-      atomicAdd(&hist[klass((int)((long long)tiles * (k + 1) / np) - (int)((long long)tiles * k / np))], 1);
+    if (np == 0) return;
+    const int len = tiles / np, longer = tiles - len * np;
+    const bool two = two_tiles(own, i, who);
+    atomicAdd(&hist[klass(len, two)], np - longer);
+    if (longer) atomicAdd(&hist[klass(len + 1, two)], longer);
   });
   __syncthreads();
   carry = 0;
@@ -454,12 +478,18 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     if (unit < p.w.max_units) p.w.units[unit] = u;
     it.t0 = u.t0;
     it.n_tok = u.n_tok;
+    if (np == 0) return;
+    const int len = tiles / np, longer = tiles - len * np;
+    const bool two = two_tiles(own, i, who);
+    const int at = atomicAdd(&hist[klass(len, two)], np - longer);
+    const int at_longer = longer ? atomicAdd(&hist[klass(len + 1, two)], longer) : 0;
+    it.kv0 = skip;
     for (int k = 0; k < np; ++k) {
-      it.kv0 = skip + (int)((long long)tiles * k / np);
-      it.kv1 = skip + (int)((long long)tiles * (k + 1) / np);
+      it.kv1 = it.kv0 + len + (k < longer ? 1 : 0);
       it.part = u.part < 0 ? -1 : u.part + k * u.n_tok * p.g;
-      const int slot = atomicAdd(&hist[klass(it.kv1 - it.kv0)], 1);
+      const int slot = k < longer ? at_longer + k : at + k - longer;
       if (slot < p.w.max_items) p.w.items[slot] = it;
+      it.kv0 = it.kv1;
     }
   });
   if (tid == 0) {
