@@ -19,6 +19,7 @@
 // int32 position (error below 2^-53 * f * |pos| turns), its top 32 bits the
 // reduced angle of sincospif.
 #include <cmath>
+#include <cstring>
 
 #include "common.cuh"
 #include "internal.h"
@@ -336,7 +337,22 @@ const char* axes_error(const kvs_rope_axes* a, int head_dim) {
   return sum == head_dim / 2 ? "" : "the axis sections must sum to head_dim / 2";
 }
 
+// The frequency table is a function of the description alone: a thread keeps
+// the last one (64 powers take longer than the rest of a call).
 void axes_turns(const kvs_rope_axes* a, int head_dim, AppendParams& p) {
+  struct Last {
+    kvs_rope_axes axes;
+    int head_dim = 0;
+    unsigned long long turn[64];
+  };
+  static thread_local Last last;
+  p.rotate = 1;
+  p.s0 = a->section[0];
+  p.s1 = a->section[0] + a->section[1];
+  if (last.head_dim == head_dim && std::memcmp(&last.axes, a, sizeof *a) == 0) {
+    std::memcpy(p.turn, last.turn, sizeof p.turn);
+    return;
+  }
   const double two_pi = 6.283185307179586476925286766559;
   int axis = 0, j = 0;
   for (int i = 0; i < head_dim / 2; ++i, ++j) {
@@ -348,9 +364,9 @@ void axes_turns(const kvs_rope_axes* a, int head_dim, AppendParams& p) {
     const double f = std::pow((double)a->theta, e) / two_pi;
     p.turn[i] = static_cast<unsigned long long>(std::ldexp(f - std::floor(f), 64));
   }
-  p.rotate = 1;
-  p.s0 = a->section[0];
-  p.s1 = a->section[0] + a->section[1];
+  last.axes = *a;
+  last.head_dim = head_dim;
+  std::memcpy(last.turn, p.turn, sizeof p.turn);
 }
 
 bool bad_stride(long long stride, long long row) { return stride < row || (stride & 7); }

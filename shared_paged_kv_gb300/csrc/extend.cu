@@ -202,17 +202,37 @@ __global__ void __launch_bounds__(256) extend_lcp_kernel(const __grid_constant__
   if (threadIdx.x == 0) p.w.lcp[a] = first / kExBlocks;
 }
 
-constexpr int kPlanThreads = 1024;
+constexpr int kPlanThreads = 256;
 constexpr int kPlanSeqs = 512;     // up to this many sequences the plan's arrays stay in shared memory
 constexpr int kPlanUnits = 640;    // more units than calls that are split have (4 per SM)
+constexpr int kPlanCands = 16;     // piece lengths that are tried
 
-// Exclusive scan of x over the CTA's threads plus a running total.
-__device__ __forceinline__ int ex_scan(int x, int* sums, int& carry) {
-  int total;
-  const int r = block_exclusive_scan(x, sums, total) + carry;
-  carry += total;
-  return r;
-}
+// Exclusive scan over the CTA plus a running total, one barrier per call:
+// calls alternate between two rows of warp sums.
+struct ExScan {
+  int (*sums)[kPlanThreads / 32];
+  int carry = 0, turn = 0;
+  __device__ __forceinline__ int operator()(int x) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int incl = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) sums[turn][warp] = incl;
+    __syncthreads();
+    int before = carry;
+#pragma unroll
+    for (int w = 0; w < kPlanThreads / 32; ++w) {
+      const int v = sums[turn][w];
+      before += w < warp ? v : 0;
+      carry += v;
+    }
+    turn ^= 1;
+    return before + incl - x;
+  }
+};
 
 // Key tiles of unit i of a sequence's own range, behind `skip` shared tiles.
 __device__ __forceinline__ int ex_own_tiles(const int4& s, int i, int tu, int causal, int skip) {
@@ -223,37 +243,40 @@ __device__ __forceinline__ int ex_own_tiles(const int4& s, int i, int tu, int ca
 
 __device__ __forceinline__ int ex_pieces(int tiles, int piece) { return max(1, (tiles + piece - 1) / piece); }
 
-// Candidate i of 32 for the piece length: the longest unit in 1.18^i pieces
-// (1 to 169).
+// Candidate i of kPlanCands for the piece length: the longest unit in 1.41^i
+// pieces (1 to 181).
 __device__ __forceinline__ int ex_candidate(int most, int least, int i) {
-  return max(least, (int)ceilf((float)most * exp2f(-0.2388f * (float)i)));
+  return max(least, (int)ceilf((float)most * exp2f(-0.5f * (float)i)));
 }
 
-// One CTA: runs of sequences, units, piece length, items sorted by length.
+// One CTA: runs of sequences, units, piece length, items sorted by cost.  A
+// chain of short dependent steps bounds it (6 to 9 us with 1,024 threads and
+// a piece per loop step, 3 to 5 us so).
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_constant__ ExPlanParams p) {
-  pdl_enter();
-  __shared__ int sums[32];
+  __shared__ int sums[2][kPlanThreads / 32];
   __shared__ int hist[256];
-  __shared__ float cost[32];
-  __shared__ int s_piece, s_parts, s_most;
+  __shared__ float cost[kPlanCands];
+  __shared__ int s_parts, s_most, s_sum;
   __shared__ int tiles_of[kPlanUnits];
+  __shared__ int2 src_of[kPlanUnits];   // {sequence, or ~run, index in it}
   __shared__ int4 sm_seq[kPlanSeqs], sm_run[kPlanSeqs];
   __shared__ int2 sm_seg[kPlanSeqs], sm_runseg[kPlanSeqs];
   __shared__ int sm_lcp[kPlanSeqs];
   const bool small = p.n_seq <= kPlanSeqs;
-  int4* const seq = small ? sm_seq : p.w.seq;
-  int4* const run = small ? sm_run : p.w.run;
-  int2* const seg = small ? sm_seg : p.w.seg;
-  int2* const runseg = small ? sm_runseg : p.w.runseg;
+  int4* const seq = small ? sm_seq : p.w.seq;          // {first row, rows, keys, shareable tiles}
+  int4* const run = small ? sm_run : p.w.run;          // {shared tiles, first sequence, sequences, rows}
+  int2* const seg = small ? sm_seg : p.w.seg;          // {run, first unit} of a sequence
+  int2* const runseg = small ? sm_runseg : p.w.runseg; // {first shared unit, shared units} of a run
   const int* const lcp = small ? sm_lcp : p.w.lcp;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tu = 2 * (kExTile / p.g), tt = kExTile / p.g;
   int* hdr = p.w.hdr;
-  if (tid < 256) hist[tid] = 0;
+  hist[tid] = 0;
   if (tid == 0) {
-    s_parts = 0;
+    s_parts = s_sum = 0;
     s_most = 1;
   }
+  pdl_enter();
   int bad = 0;
   for (int a = tid; a < p.n_seq; a += kPlanThreads) {
     if (small && p.share > 0) sm_lcp[a] = a + 1 < p.n_seq ? p.w.lcp[a] : 0;
@@ -273,225 +296,241 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   }
   // runs: a sequence starts a new one unless its common part with the one
   // before it is at least half of the neighbouring common parts (so that a
-  // short common part does not cut down two families of long ones)
+  // short common part does not cut down two families of long ones); in the
+  // same pass every sequence's own units
   auto link = [&](int a) {   // between a and a + 1
     if (p.share <= 0 || a < 0 || a + 1 >= p.n_seq) return 0;
     return min(lcp[a], min(seq[a].w, seq[a + 1].w));
   };
-  int carry = 0;
+  ExScan runs{sums}, units{sums};
   for (int a0 = 0; a0 < p.n_seq; a0 += kPlanThreads) {
     const int a = a0 + tid;
-    int head = 0;
+    int head = 0, n = 0;
     if (a < p.n_seq) {
       const int l = link(a - 1);
       head = a == 0 || l == 0 || 2 * l < max(link(a - 2), link(a));
+      n = (seq[a].y + tu - 1) / tu;
     }
-    const int r = ex_scan(head, sums, carry) + head - 1;
+    const int r = runs(head) + head - 1;
+    units.turn = runs.turn;
+    const int at = units(n);
+    runs.turn = units.turn;
     if (a < p.n_seq) {
-      seg[a].x = r;
+      seg[a] = make_int2(r, at);
       if (head) run[r] = make_int4(0x7fffffff, a, 0, 0);
     }
   }
-  const int n_runs = carry;
+  const int n_runs = runs.carry, own_units = units.carry;
+  int n_units = own_units;
   __syncthreads();
-  for (int a = tid; a < p.n_seq; a += kPlanThreads) {
-    const int r = seg[a].x;
-    const int4 s = seq[a];
-    atomicAdd(&run[r].z, 1);
-    atomicAdd(&run[r].w, s.y);
-    if (a != run[r].y) atomicMin(&run[r].x, link(a - 1));
-  }
-  __syncthreads();
-  // a run shares when its rows fill at most three quarters of the row tiles
-  // that its sequences would fill one by one
-  for (int r = warp; r < n_runs; r += 32) {
-    const int4 v = run[r];
-    int sep = 0;
-    for (int a = v.y + lane; a < v.y + v.z; a += 32) sep += (seq[a].y + tt - 1) / tt;
+  if (p.share > 0) {
+    for (int a = tid; a < p.n_seq; a += kPlanThreads) {
+      const int r = seg[a].x;
+      atomicAdd(&run[r].z, 1);
+      atomicAdd(&run[r].w, seq[a].y);
+      if (a != run[r].y) atomicMin(&run[r].x, link(a - 1));
+    }
+    __syncthreads();
+    // a run shares when its rows fill at most three quarters of the row tiles
+    // that its sequences would fill one by one; its units follow the others
+    for (int r = warp; r < n_runs; r += kPlanThreads / 32) {
+      const int4 v = run[r];
+      int sep = 0;
+      if (v.z >= 2)
+        for (int a = v.y + lane; a < v.y + v.z; a += 32) sep += (seq[a].y + tt - 1) / tt;
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sep += __shfl_xor_sync(0xffffffffu, sep, o);
-    const int joint = (v.w + tt - 1) / tt;
-    if (lane == 0) run[r].x = v.z >= 2 && 4 * joint <= 3 * sep ? v.x : 0;
+      for (int o = 16; o; o >>= 1) sep += __shfl_xor_sync(0xffffffffu, sep, o);
+      const int joint = (v.w + tt - 1) / tt;
+      if (lane == 0) run[r].x = v.z >= 2 && 4 * joint <= 3 * sep ? v.x : 0;
+    }
+    __syncthreads();
+    for (int r0 = 0; r0 < n_runs; r0 += kPlanThreads) {
+      const int r = r0 + tid;
+      const int n = r < n_runs && run[r].x > 0 ? (run[r].w + tu - 1) / tu : 0;
+      const int at = units(n);
+      if (r < n_runs) runseg[r] = make_int2(at, n);
+    }
+    n_units = units.carry;
+  } else {
+    for (int r = tid; r < n_runs; r += kPlanThreads) {   // one sequence each
+      run[r].x = 0;
+      runseg[r] = make_int2(0, 0);
+    }
   }
   __syncthreads();
-  // units: the sequences' own first, then the runs'
-  carry = 0;
-  for (int a0 = 0; a0 < p.n_seq; a0 += kPlanThreads) {
-    const int a = a0 + tid;
-    const int n = a < p.n_seq ? (seq[a].y + tu - 1) / tu : 0;
-    const int at = ex_scan(n, sums, carry);
-    if (a < p.n_seq) seg[a].y = at;
-  }
-  const int own_units = carry;
-  for (int r0 = 0; r0 < n_runs; r0 += kPlanThreads) {
-    const int r = r0 + tid;
-    const int n = r < n_runs && run[r].x > 0 ? (run[r].w + tu - 1) / tu : 0;
-    const int at = ex_scan(n, sums, carry);
-    if (r < n_runs) runseg[r] = make_int2(at, n);
-  }
-  const int n_units = carry;
-  __syncthreads();
-  // visits every unit: f(unit, tiles, own, index in its sequence or run, sequence or run)
-  auto each = [&](int w0, int nw, auto f) {
-    for (int a = w0; a < p.n_seq; a += nw) {
+  // visits every unit: f(unit, tiles, {sequence or ~run, index}, shared tiles
+  // in front of it); units of a sequence or run go over a warp's lanes
+  const bool split = p.share >= 0 && (long long)n_units * p.hkv < 4ll * p.sms && n_units <= kPlanUnits;
+  auto walk = [&](auto f) {
+    for (int a = warp; a < p.n_seq; a += kPlanThreads / 32) {
       const int4 s = seq[a];
       const int2 sg = seg[a];
-      const int skip = run[sg.x].x;
-      const int n = (s.y + tu - 1) / tu;
-      for (int i = lane; i < n; i += 32) f(sg.y + i, ex_own_tiles(s, i, tu, p.causal, skip), true, i, a, skip);
+      const int skip = run[sg.x].x, n = (s.y + tu - 1) / tu;
+      for (int i = lane; i < n; i += 32) f(sg.y + i, ex_own_tiles(s, i, tu, p.causal, skip), make_int2(a, i), skip);
     }
-    for (int r = w0; r < n_runs; r += nw) {
+    for (int r = warp; r < n_runs; r += kPlanThreads / 32) {
       const int2 rs = runseg[r];
       const int sh = run[r].x;
-      for (int i = lane; i < rs.y; i += 32) f(rs.x + i, sh, false, i, r, 0);
+      for (int i = lane; i < rs.y; i += 32) f(rs.x + i, sh, make_int2(~r, i), 0);
     }
   };
   // whether a unit fills more than one row tile
-  auto two_tiles = [&](bool own, int i, int who) { return (own ? seq[who].y : run[who].w) - i * tu > tt; };
-  // piece length: of 32 candidates the one with the least estimated time
-  // (the mean load of an SM, or the rounds that the larger half of the pieces
-  // takes; a piece costs its tiles and about 1.5 more, with one row tile 0.6
-  // of that); no splits in calls that fill the device, or are too large for
-  // part buffers
-  const bool split = p.share >= 0 && (long long)n_units * p.hkv < 4ll * p.sms && n_units <= kPlanUnits;
+  auto two_tiles = [&](int2 src) { return (src.x >= 0 ? seq[src.x].y : run[~src.x].w) - src.y * tu > tt; };
   {
-    int most = 1;
-    each(warp, 32, [&](int unit, int tiles, bool own, int i, int who, int) {
+    int most = 1, sum = 0;
+    walk([&](int unit, int tiles, int2 src, int) {
       most = max(most, tiles);
-      if (split) tiles_of[unit] = tiles | (two_tiles(own, i, who) ? 1 << 30 : 0);
+      sum += tiles;
+      if (split) {
+        tiles_of[unit] = tiles | (two_tiles(src) ? 1 << 30 : 0);
+        src_of[unit] = src;
+      }
     });
 #pragma unroll
-    for (int o = 16; o; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    if (lane == 0) atomicMax(&s_most, most);
-    __syncthreads();
-    most = s_most;
-    if (split) {   // a candidate per warp; every warp sums all units
-      int sum = 0;
-      for (int u = lane; u < n_units; u += 32) sum += tiles_of[u] & ~(1 << 30);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-      const float heads = (float)p.hkv, sms = (float)p.sms;
-      const int least = max(kExMinPiece, (int)ceilf((float)sum * heads / (kExItemsPerSm * sms)));
-      const int cand = ex_candidate(most, least, warp);
-      auto piece_cost = [&](int u, int& np) {
-        const int tiles = tiles_of[u] & ~(1 << 30);
-        np = ex_pieces(tiles, cand);
-        return (tiles_of[u] >> 30 ? 1.f : 0.6f) * ((float)tiles / (float)np + 1.5f);
-      };
-      float load = 0.f, big = 0.f, n_big = 0.f, top = 0.f;
-      int np;
-      for (int u = lane; u < n_units; u += 32) top = fmaxf(top, piece_cost(u, np));
-#pragma unroll
-      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      for (int u = lane; u < n_units; u += 32) {
-        const float one = piece_cost(u, np);
-        load += one * (float)np;
-        if (2.f * one > top) {
-          big += one * (float)np;
-          n_big += (float)np;
-        }
-      }
-#pragma unroll
-      for (int o = 16; o; o >>= 1) {
-        load += __shfl_xor_sync(0xffffffffu, load, o);
-        big += __shfl_xor_sync(0xffffffffu, big, o);
-        n_big += __shfl_xor_sync(0xffffffffu, n_big, o);
-      }
-      if (lane == 0) cost[warp] = fmaxf(load * heads / sms, ceilf(n_big * heads / sms) * big / fmaxf(n_big, 1.f));
-      __syncthreads();
-      if (warp == 0) {   // the least cost, the longest piece on a tie
-        float c = cost[lane];
-        int best = lane;
-#pragma unroll
-        for (int o = 16; o; o >>= 1) {
-          const float c2 = __shfl_xor_sync(0xffffffffu, c, o);
-          const int b2 = __shfl_xor_sync(0xffffffffu, best, o);
-          if (c2 < c || (c2 == c && b2 < best)) {
-            c = c2;
-            best = b2;
-          }
-        }
-        if (lane == 0) s_piece = ex_candidate(most, least, best);
-      }
-    } else if (tid == 0) {
-      s_piece = most;
+    for (int o = 16; o; o >>= 1) {
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+      sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (lane == 0) {
+      atomicMax(&s_most, most);
+      atomicAdd(&s_sum, sum);
     }
     __syncthreads();
   }
-  const int piece = s_piece, most = s_most;
-  auto pieces_of = [&](int tiles, bool own, int skip) { return own && tiles == 0 && skip > 0 ? 0 : ex_pieces(tiles, piece); };
+  const int most = s_most;
+  int piece = most;
+  // piece length: of 16 candidates the one with the least estimated time (the
+  // mean load of an SM, or the rounds that the larger half of the pieces
+  // takes; a piece costs its tiles and about 1.5 more, with one row tile 0.6
+  // of that); no splits in calls that fill the device, or are too large for
+  // part buffers.  Sixteen lanes work on a candidate.
+  if (split) {
+    const float heads = (float)p.hkv, sms = (float)p.sms;
+    const int least = max(kExMinPiece, (int)ceilf((float)s_sum * heads / (kExItemsPerSm * sms)));
+    const int c = tid >> 4, cand = ex_candidate(most, least, c);
+    const float inv = __frcp_rn((float)cand);
+    auto piece_cost = [&](int u, float& np) {
+      const float tiles = (float)(tiles_of[u] & ~(1 << 30));
+      np = fmaxf(1.f, ceilf(tiles * inv - 1e-4f));
+      return (tiles_of[u] >> 30 ? 1.f : 0.6f) * (__fdividef(tiles, np) + 1.5f);
+    };
+    float load = 0.f, big = 0.f, n_big = 0.f, top = 0.f, np;
+    for (int u = tid & 15; u < n_units; u += 16) top = fmaxf(top, piece_cost(u, np));
+#pragma unroll
+    for (int o = 8; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int u = tid & 15; u < n_units; u += 16) {
+      const float one = piece_cost(u, np);
+      load += one * np;
+      if (2.f * one > top) {
+        big += one * np;
+        n_big += np;
+      }
+    }
+#pragma unroll
+    for (int o = 8; o; o >>= 1) {
+      load += __shfl_xor_sync(0xffffffffu, load, o);
+      big += __shfl_xor_sync(0xffffffffu, big, o);
+      n_big += __shfl_xor_sync(0xffffffffu, n_big, o);
+    }
+    if ((tid & 15) == 0) cost[c] = fmaxf(load * heads / sms, ceilf(n_big * heads / sms) * big / fmaxf(n_big, 1.f));
+    __syncthreads();
+    int best = 0;   // the longest piece on a tie
+#pragma unroll
+    for (int i = 1; i < kPlanCands; ++i)
+      if (cost[i] < cost[best]) best = i;
+    piece = ex_candidate(most, least, best);
+  }
   // items by cost (key tiles x row tiles), largest first: 256 classes; the
   // order inside a class changes no result.  The pieces of a unit are equal
   // to one tile, so they fall into two classes.
+  auto pieces_of = [&](int tiles, int skip) { return tiles == 0 && skip > 0 ? 0 : ex_pieces(tiles, piece); };
   const float per_class = 255.f / (float)(2 * most);
   auto klass = [&](int len, bool two) { return 255 - (int)((float)(two ? 2 * len : len) * per_class); };
-  each(warp, 32, [&](int, int tiles, bool own, int i, int who, int skip) {
-    const int np = pieces_of(tiles, own, skip);
+  auto skip_of = [&](int2 src) { return src.x >= 0 ? run[seg[src.x].x].x : 0; };
+  auto count = [&](int, int tiles, int2 src, int skip) {
+    const int np = pieces_of(tiles, skip);
     if (np == 0) return;
     const int len = tiles / np, longer = tiles - len * np;
-    const bool two = two_tiles(own, i, who);
+    const bool two = two_tiles(src);
     atomicAdd(&hist[klass(len, two)], np - longer);
     if (longer) atomicAdd(&hist[klass(len + 1, two)], longer);
-  });
+  };
+  if (split) {
+    for (int u = tid; u < n_units; u += kPlanThreads) count(u, tiles_of[u] & ~(1 << 30), src_of[u], skip_of(src_of[u]));
+  } else {
+    walk(count);
+  }
   __syncthreads();
-  carry = 0;
-  const int h = tid < 256 ? hist[tid] : 0;
-  const int at0 = ex_scan(h, sums, carry);
-  const int n_items = carry;
-  if (tid < 256) hist[tid] = at0;
+  ExScan items{sums};
+  items.turn = units.turn;
+  hist[tid] = items(hist[tid]);
+  const int n_items = items.carry;
   __syncthreads();
-  each(warp, 32, [&](int unit, int tiles, bool own, int i, int who, int skip) {
-    const int np = pieces_of(tiles, own, skip);
-    const bool parts = own ? (np > 1 || skip > 0) : true;
+  // writes a unit and the items k = k0, k0 + step, ... of it; with step 16
+  // the sixteen lanes of a group share the unit, the first one reserves
+  auto emit = [&](int unit, int tiles, int2 src, int skip, int k0, int step) {
+    const int np = pieces_of(tiles, skip);
+    const bool own = src.x >= 0, parts = !own || np > 1 || skip > 0;
+    const int i = src.y;
     ExUnit u{};
     ExItem it{};
     if (own) {
-      const int4 s = seq[who];
-      const int2 sg = seg[who];
+      const int4 s = seq[src.x];
+      const int r = seg[src.x].x;
       u.t0 = s.x + i * tu;
       u.n_tok = min(tu, s.y - i * tu);
-      u.sh_unit = skip > 0 ? runseg[sg.x].x : -1;
-      u.sh_t0 = seq[run[sg.x].y].x;
-      it.seq = who;
+      u.sh_unit = skip > 0 ? runseg[r].x : -1;
+      u.sh_t0 = seq[run[r].y].x;
+      it.seq = src.x;
       it.lim0 = p.causal ? s.z - s.y + i * tu + 1 : s.z;
       it.step = p.causal;
       it.kv_end = s.z;
     } else {
-      const int4 v = run[who];
+      const int4 v = run[~src.x];
       u.t0 = seq[v.y].x + i * tu;
       u.n_tok = min(tu, v.w - i * tu);
       u.sh_unit = -1;
       it.seq = v.y;
       it.lim0 = it.kv_end = v.x * kExTile;
     }
+    const int len = np ? tiles / np : 0, longer = np ? tiles - len * np : 0;
+    const bool two = two_tiles(src);
     u.pieces = np;
     u.part = -1;
-    if (parts && np > 0) {
-      const int rows = u.n_tok * p.g * np;
-      u.part = atomicAdd(&s_parts, rows);
-      if ((long long)u.part + rows > p.w.part_rows) {   // the sizes exclude it: drop the rows
-        set_err(p.status, KVS_DEVERR_PLAN);
-        u.part = 0;
-        u.n_tok = 0;
-      }
+    int at = 0, at_longer = 0;
+    if (k0 == 0 && np > 0) {
+      if (parts) u.part = atomicAdd(&s_parts, u.n_tok * p.g * np);
+      at = atomicAdd(&hist[klass(len, two)], np - longer);
+      if (longer) at_longer = atomicAdd(&hist[klass(len + 1, two)], longer);
     }
-    if (unit < p.w.max_units) p.w.units[unit] = u;
+    if (step > 1) {
+      const uint32_t group = 0xffffu << (lane & 16);
+      u.part = __shfl_sync(group, u.part, 0, 16);
+      at = __shfl_sync(group, at, 0, 16);
+      at_longer = __shfl_sync(group, at_longer, 0, 16);
+    }
+    if (u.part >= 0 && (long long)u.part + u.n_tok * p.g * np > p.w.part_rows) {   // the sizes exclude it: drop the rows
+      set_err(p.status, KVS_DEVERR_PLAN);
+      u.part = 0;
+      u.n_tok = 0;
+    }
+    if (k0 == 0 && unit < p.w.max_units) p.w.units[unit] = u;
     it.t0 = u.t0;
     it.n_tok = u.n_tok;
-    if (np == 0) return;
-    const int len = tiles / np, longer = tiles - len * np;
-    const bool two = two_tiles(own, i, who);
-    const int at = atomicAdd(&hist[klass(len, two)], np - longer);
-    const int at_longer = longer ? atomicAdd(&hist[klass(len + 1, two)], longer) : 0;
-    it.kv0 = skip;
-    for (int k = 0; k < np; ++k) {
+    for (int k = k0; k < np; k += step) {
+      it.kv0 = skip + k * len + min(k, longer);
       it.kv1 = it.kv0 + len + (k < longer ? 1 : 0);
       it.part = u.part < 0 ? -1 : u.part + k * u.n_tok * p.g;
       const int slot = k < longer ? at_longer + k : at + k - longer;
       if (slot < p.w.max_items) p.w.items[slot] = it;
-      it.kv0 = it.kv1;
     }
-  });
+  };
+  if (split) {
+    for (int u = tid >> 4; u < n_units; u += kPlanThreads / 16)
+      emit(u, tiles_of[u] & ~(1 << 30), src_of[u], skip_of(src_of[u]), tid & 15, 16);
+  } else {
+    walk([&](int unit, int tiles, int2 src, int skip) { emit(unit, tiles, src, skip, 0, 1); });
+  }
   if (tid == 0) {
     hdr[kHSeq] = p.n_seq;
     hdr[kHBlocks] = p.max_blocks;

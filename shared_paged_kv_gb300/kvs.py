@@ -356,23 +356,30 @@ def kvs_quantize_q4(pool: Pool, layer, k_src, v_src, dst_blocks, n_blocks, strea
                                   n_blocks, _stream(stream)))
 
 
+_BF16, _I16, _I32 = torch.bfloat16, torch.int16, torch.int32
+
+
 def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str):
     """(pointer, elements between two tokens) of packed rows [n_tokens][heads]
     [head_dim] of 16-bit elements; the tokens may lie apart."""
-    if t.element_size() != 2 or t.dtype == torch.float16:
-        raise ValueError(f"{what}: bf16 rows (torch.bfloat16, or their bits as int16) are wanted, got {t.dtype}")
-    if t.dim() != 3 or t.shape[0] < n_tokens or t.shape[1] != n_heads or t.shape[2] != head_dim:
-        raise ValueError(f"{what}: shape {tuple(t.shape)} is not [>= {n_tokens}][{n_heads}][{head_dim}]")
+    dt = t.dtype
+    if dt is not _BF16 and dt is not _I16:
+        raise ValueError(f"{what}: bf16 rows (torch.bfloat16, or their bits as int16) are wanted, got {dt}")
+    shape = t.shape
+    if len(shape) != 3 or shape[0] < n_tokens or shape[1] != n_heads or shape[2] != head_dim:
+        raise ValueError(f"{what}: shape {tuple(shape)} is not [>= {n_tokens}][{n_heads}][{head_dim}]")
+    if t.is_contiguous():
+        return t.data_ptr(), n_heads * head_dim
     st = t.stride()
     if st[2] != 1 or (n_heads > 1 and st[1] != head_dim):
         raise ValueError(f"{what}: the heads of a token must lie side by side")
-    return t.data_ptr(), (st[0] if t.shape[0] > 1 else n_heads * head_dim)
+    return t.data_ptr(), st[0]
 
 
 def _ints(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype != torch.int32 or not t.is_contiguous() or t.numel() < n:
+    if t.dtype is not _I32 or not t.is_contiguous() or t.numel() < n:
         raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} values is wanted")
     return t.data_ptr()
 
