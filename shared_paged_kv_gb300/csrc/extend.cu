@@ -649,6 +649,13 @@ __device__ __forceinline__ void ex_mma_ts(uint32_t d, uint32_t a, uint32_t b, ui
       : "memory");
 }
 
+// A 32-byte store: a thread's columns of a row fill whole sectors.
+__device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+               "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t* r) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n\t"
@@ -1090,20 +1097,21 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
         uint32_t v[32];
         if (nt > 0) tmem_ld32(tO + 32 * q, v);
         if (live && it.part >= 0) {
-          uint4* dst = reinterpret_cast<uint4*>(p.w.part + prow * D + 32 * q);
+          float* dst = p.w.part + prow * D + 32 * q;
+          if (!some) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            dst[e] = some ? make_uint4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]) : make_uint4(0u, 0u, 0u, 0u);
-        } else if (live) {
-          uint4* dst = reinterpret_cast<uint4*>(p.out + ((size_t)(it.t0 + tok) * p.hq + head * p.g + rg) * D + 32 * q);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t o[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              o[i] = some ? pack_bf16(__uint_as_float(v[8 * e + 2 * i]) * inv, __uint_as_float(v[8 * e + 2 * i + 1]) * inv) : 0u;
-            dst[e] = make_uint4(o[0], o[1], o[2], o[3]);
+            for (int e = 0; e < 32; ++e) v[e] = 0u;
           }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) st_global_v8(dst + 8 * e, v + 8 * e);
+        } else if (live) {
+          uint16_t* dst = p.out + ((size_t)(it.t0 + tok) * p.hq + head * p.g + rg) * D + 32 * q;
+          uint32_t o[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e)
+            o[e] = some ? pack_bf16(__uint_as_float(v[2 * e]) * inv, __uint_as_float(v[2 * e + 1]) * inv) : 0u;
+          st_global_v8(dst, o);
+          st_global_v8(dst + 16, o + 8);
         }
         __syncwarp();
       }
@@ -1200,6 +1208,8 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
 }
 
 // ------------------------------------------------------------------- host ---
+bool aligned32(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
+
 PFN_cuTensorMapEncodeTiled_v12000 ex_encoder() {
   static const PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* f = nullptr;
@@ -1298,7 +1308,7 @@ extern "C" kvs_status kvs_extend_plan(kvs_pool* pool, const int32_t* tok_off_dev
   if (causal != 0 && causal != 1) return fail(KVS_ERR_INVALID_ARG, "extend_plan: causal is 0 or 1");
   if (n_tokens == 0 || n_seq == 0) return KVS_OK;
   if (!tok_off_dev || !block_table_dev || !seq_len_dev || !ws) return fail(KVS_ERR_INVALID_ARG, "extend_plan: null pointer");
-  if (!aligned16(ws)) return fail(KVS_ERR_INVALID_ARG, "extend_plan: ws must be 16-byte aligned");
+  if (!aligned32(ws)) return fail(KVS_ERR_INVALID_ARG, "extend_plan: ws must be 32-byte aligned");
   const int hkv = pool->desc.num_kv_heads, g = n_q_heads / hkv;
   ExPlanParams p{};
   p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
@@ -1344,8 +1354,8 @@ extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, con
   if (n_tokens == 0 || n_seq == 0) return KVS_OK;
   if (!q_dev || !tok_off_dev || !block_table_dev || !seq_len_dev || !out_dev || !ws)
     return fail(KVS_ERR_INVALID_ARG, "extend_attn: null pointer");
-  if (!aligned16(q_dev) || !aligned16(out_dev) || !aligned16(ws))
-    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q, out and ws must be 16-byte aligned");
+  if (!aligned16(q_dev) || !aligned32(out_dev) || !aligned32(ws))
+    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q must be 16-byte, out and ws 32-byte aligned");
   const int g = n_q_heads / d.num_kv_heads;
   ExParams p{};
   p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
@@ -1381,8 +1391,8 @@ extern "C" kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void*
   if (!pool) return fail(KVS_ERR_INVALID_ARG, "extend_attn: null pool");
   if (layer < 0 || layer >= pool->desc.num_layers) return fail(KVS_ERR_INVALID_ARG, "extend_attn: layer out of range");
   if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: scale must be positive and finite");
-  if (n_tokens > 0 && n_seq > 0 && (!q_dev || !out_dev || !aligned16(q_dev) || !aligned16(out_dev)))
-    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q and out must be set and 16-byte aligned");
+  if (n_tokens > 0 && n_seq > 0 && (!q_dev || !out_dev || !aligned16(q_dev) || !aligned32(out_dev)))
+    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q must be set and 16-byte, out set and 32-byte aligned");
   if (q_stride < (long long)n_q_heads * pool->desc.head_dim || (q_stride & 7))
     return fail(KVS_ERR_INVALID_ARG, "extend_attn: q_stride must hold n_q_heads * head_dim elements and be a multiple of 8");
   kvs_status st = kvs_extend_plan(pool, tok_off_dev, n_tokens, n_q_heads, block_table_dev, max_blocks, seq_len_dev, n_seq,
