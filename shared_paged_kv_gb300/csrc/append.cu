@@ -6,13 +6,12 @@
 // token's place: its sequence (a search of tok_off), the sequence's length,
 // the block table's entry (single-token calls).
 //
-// Split: a CTA takes 1 or 8 tokens.  Its first step finds each token's place
+// Split: a CTA takes 1 or 4 tokens.  Its first step finds each token's place
 // and computes cos / sin once for all heads of a token (head_dim / 2 angles,
 // one per thread, into shared memory).  Then a row (one head of K, V or Q) is
 // taken by head_dim / 16 lanes; a lane holds elements [8v, 8v + 8) and their
 // partners [d/2 + 8v, d/2 + 8v + 8), so that a rotation needs no exchange and
-// every access is 16 bytes wide.  A lane loads kApBatch rows before it stores
-// any.
+// every access is 16 bytes wide.
 //
 // Angles: turns per position f = w / 2 pi as a 64-bit fixed-point fraction F;
 // pos * F modulo 2^64 is the exact phase of the rounded frequency for every
@@ -30,8 +29,14 @@ namespace {
 
 constexpr int kApThreads = 256;
 constexpr int kApWarps = kApThreads / 32;
-constexpr int kApTokens = 8;   // tokens of a CTA in large calls (one warp each)
-constexpr int kApBatch = 4;    // rows a lane loads before it stores any
+constexpr int kApTokens = 4;   // tokens of a CTA in large calls (two warps each)
+// Rows a lane loads before it stores any, and CTAs per SM.  Measured for 7,700
+// tokens into a 4-bit pool (8 KV heads, 32 query heads) / 11,600 tokens of 32
+// KV and 32 query heads into a bf16 pool: 8 tokens, 4 rows 50 / 90.5 us; 4
+// tokens, 4 rows 48 / 87.6; 4 tokens, 2 rows, 5 CTAs 42.7 / 88.6; 2 tokens or
+// 6 CTAs slower on both.
+constexpr int kApBatch = 2, kGaBatch = 2;
+constexpr int kApCtas = 5;
 
 struct Place {
   int phys, at, pos, ok;   // physical block (-1: none), row inside it, logical position; ok: the row belongs to a sequence
@@ -129,9 +134,12 @@ __device__ __forceinline__ uint32_t q4_codes(const float* x, __half2& sb) {
   bool clear = true;
 #pragma unroll
   for (int e = 0; e < 8; ++e) {
-    const float q = __fmul_rn(__fsub_rn(x[e], b), inv), n = rintf(q);
-    clear &= fabsf(q - n) < 0.4999f;
-    w |= (static_cast<uint32_t>(fminf(fmaxf(n, 0.f), 15.f)) & 15u) << (4 * e);
+    // rint by the addition of 1.5 * 2^23, whose last place is 1; a quotient
+    // outside [0, 15] has the code of its bound either way
+    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[e], b), inv), 0.f), 15.f);
+    const float t = __fadd_rn(q, 12582912.f);
+    clear &= fabsf(__fsub_rn(q, __fsub_rn(t, 12582912.f))) < 0.4999f;
+    w |= (__float_as_uint(t) & 15u) << (4 * e);
   }
   if (!clear) {
     w = 0;
@@ -145,7 +153,7 @@ __device__ __forceinline__ uint32_t q4_codes(const float* x, __half2& sb) {
 enum { kApBf16 = 0, kApQ4 = 1, kApRows = 2 };   // pool type, or rows only (kvs_rope_apply)
 
 template <int D, int MODE>
-__global__ void __launch_bounds__(kApThreads) append_kernel(const __grid_constant__ AppendParams p, int tokens_per_cta) {
+__global__ void __launch_bounds__(kApThreads, kApCtas) append_kernel(const __grid_constant__ AppendParams p, int tokens_per_cta) {
   constexpr int NV = D / 16;         // lanes per row
   constexpr int RPW = 32 / NV;       // rows of a warp step
   constexpr int H = D / 2;
@@ -296,12 +304,12 @@ __global__ void __launch_bounds__(kApThreads) gather_kernel(const __grid_constan
   const Place w = where[slot];
   if (w.phys < 0) return;
   const int v = lane % NV, rows = 2 * p.hkv, rstep = wpt * RPW;
-  for (int rb = (warp % wpt) * RPW + lane / NV; rb < rows; rb += kApBatch * rstep) {
-    uint4 x[kApBatch][2];
-    uint2 code[kApBatch];
-    float2 sb[kApBatch];
+  for (int rb = (warp % wpt) * RPW + lane / NV; rb < rows; rb += kGaBatch * rstep) {
+    uint4 x[kGaBatch][2];
+    uint2 code[kGaBatch];
+    float2 sb[kGaBatch];
 #pragma unroll
-    for (int i = 0; i < kApBatch; ++i) {
+    for (int i = 0; i < kGaBatch; ++i) {
       const int r = rb + i * rstep;
       if (r >= rows) continue;
       const bool is_v = r >= p.hkv;
@@ -316,7 +324,7 @@ __global__ void __launch_bounds__(kApThreads) gather_kernel(const __grid_constan
       }
     }
 #pragma unroll
-    for (int i = 0; i < kApBatch; ++i) {
+    for (int i = 0; i < kGaBatch; ++i) {
       const int r = rb + i * rstep;
       if (r >= rows) continue;
       const bool is_v = r >= p.hkv;
@@ -339,8 +347,8 @@ __global__ void __launch_bounds__(kApThreads) gather_kernel(const __grid_constan
 }
 
 // Single-token steps spread a token over a CTA's eight warps, so that its
-// rows are loaded at once; once the grid fills the device twice over, a warp
-// per token shares a CTA's look-ups and angles.
+// rows are loaded at once; once the grid fills the device twice over, tokens
+// share a CTA's look-ups and angles.
 int append_tokens_per_cta(int n_tokens, int num_sms) { return n_tokens <= 2 * num_sms ? 1 : kApTokens; }
 
 // "" or what is wrong with the description
