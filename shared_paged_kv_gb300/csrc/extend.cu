@@ -317,31 +317,42 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     runs.turn = units.turn;
     if (a < p.n_seq) {
       seg[a] = make_int2(r, at);
-      if (head) run[r] = make_int4(0x7fffffff, a, 0, 0);
+      if (head) run[r] = make_int4(0, a, 0, 0);
     }
   }
   const int n_runs = runs.carry, own_units = units.carry;
   int n_units = own_units;
   __syncthreads();
   if (p.share > 0) {
-    for (int a = tid; a < p.n_seq; a += kPlanThreads) {
-      const int r = seg[a].x;
-      atomicAdd(&run[r].z, 1);
-      atomicAdd(&run[r].w, seq[a].y);
-      if (a != run[r].y) atomicMin(&run[r].x, link(a - 1));
-    }
-    __syncthreads();
     // a run shares when its rows fill at most three quarters of the row tiles
-    // that its sequences would fill one by one; its units follow the others
+    // that its sequences would fill one by one; its units follow the others.
+    // A warp takes a run; runs of one sequence share nothing.
     for (int r = warp; r < n_runs; r += kPlanThreads / 32) {
-      const int4 v = run[r];
-      int sep = 0;
-      if (v.z >= 2)
-        for (int a = v.y + lane; a < v.y + v.z; a += 32) sep += (seq[a].y + tt - 1) / tt;
+      const int first = run[r].y, count = (r + 1 < n_runs ? run[r + 1].y : p.n_seq) - first;
+      int sh = 0, rows = seq[first].y;
+      if (count > 1) {
+        int sep = 0;
+        sh = 0x7fffffff;
+        rows = 0;
+        for (int a = first + lane; a < first + count; a += 32) {
+          rows += seq[a].y;
+          sep += (seq[a].y + tt - 1) / tt;
+          if (a > first) sh = min(sh, link(a - 1));
+        }
 #pragma unroll
-      for (int o = 16; o; o >>= 1) sep += __shfl_xor_sync(0xffffffffu, sep, o);
-      const int joint = (v.w + tt - 1) / tt;
-      if (lane == 0) run[r].x = v.z >= 2 && 4 * joint <= 3 * sep ? v.x : 0;
+        for (int o = 16; o; o >>= 1) {
+          rows += __shfl_xor_sync(0xffffffffu, rows, o);
+          sep += __shfl_xor_sync(0xffffffffu, sep, o);
+          sh = min(sh, __shfl_xor_sync(0xffffffffu, sh, o));
+        }
+        if (4 * ((rows + tt - 1) / tt) > 3 * sep) sh = 0;
+      }
+      __syncwarp();
+      if (lane == 0) {
+        run[r].x = sh;
+        run[r].z = count;
+        run[r].w = rows;
+      }
     }
     __syncthreads();
     for (int r0 = 0; r0 < n_runs; r0 += kPlanThreads) {
@@ -352,10 +363,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     }
     n_units = units.carry;
   } else {
-    for (int r = tid; r < n_runs; r += kPlanThreads) {   // one sequence each
-      run[r].x = 0;
-      runseg[r] = make_int2(0, 0);
-    }
+    for (int r = tid; r < n_runs; r += kPlanThreads) runseg[r] = make_int2(0, 0);   // one sequence each
   }
   __syncthreads();
   // visits every unit: f(unit, tiles, {sequence or ~run, index}, shared tiles
@@ -378,14 +386,37 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   auto two_tiles = [&](int2 src) { return (src.x >= 0 ? seq[src.x].y : run[~src.x].w) - src.y * tu > tt; };
   {
     int most = 1, sum = 0;
-    walk([&](int unit, int tiles, int2 src, int) {
-      most = max(most, tiles);
-      sum += tiles;
-      if (split) {
-        tiles_of[unit] = tiles | (two_tiles(src) ? 1 << 30 : 0);
-        src_of[unit] = src;
+    if (split) {   // few units: a thread each, its sequence or run found by bisection
+      for (int u = tid; u < n_units; u += kPlanThreads) {
+        const bool own = u < own_units;
+        const int2* first = own ? seg : runseg;   // .y of a sequence, .x of a run: its first unit
+        int lo = 0, n = own ? p.n_seq : n_runs;
+        while (n > 1) {   // the last one whose first unit is at most u
+          const int h = n >> 1;
+          const int f = own ? first[lo + h].y : first[lo + h].x;
+          lo = f <= u ? lo + h : lo;
+          n = f <= u ? n - h : h;
+        }
+        int2 src;
+        int tiles;
+        if (own) {
+          src = make_int2(lo, u - seg[lo].y);
+          tiles = ex_own_tiles(seq[lo], src.y, tu, p.causal, run[seg[lo].x].x);
+        } else {
+          src = make_int2(~lo, u - runseg[lo].x);
+          tiles = run[lo].x;
+        }
+        most = max(most, tiles);
+        sum += tiles;
+        tiles_of[u] = tiles | (two_tiles(src) ? 1 << 30 : 0);
+        src_of[u] = src;
       }
-    });
+    } else {
+      walk([&](int, int tiles, int2, int) {
+        most = max(most, tiles);
+        sum += tiles;
+      });
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
       most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
@@ -434,10 +465,17 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     }
     if ((tid & 15) == 0) cost[c] = fmaxf(load * heads / sms, ceilf(n_big * heads / sms) * big / fmaxf(n_big, 1.f));
     __syncthreads();
-    int best = 0;   // the longest piece on a tie
+    float low = cost[tid & 15];   // the longest piece on a tie
+    int best = tid & 15;
 #pragma unroll
-    for (int i = 1; i < kPlanCands; ++i)
-      if (cost[i] < cost[best]) best = i;
+    for (int o = 8; o; o >>= 1) {
+      const float low2 = __shfl_xor_sync(0xffffffffu, low, o);
+      const int best2 = __shfl_xor_sync(0xffffffffu, best, o);
+      if (low2 < low || (low2 == low && best2 < best)) {
+        low = low2;
+        best = best2;
+      }
+    }
     piece = ex_candidate(most, least, best);
   }
   // items by cost (key tiles x row tiles), largest first: 256 classes; the
@@ -468,8 +506,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   __syncthreads();
   // writes a unit and the items k = k0, k0 + step, ... of it; with step 16
   // the sixteen lanes of a group share the unit, the first one reserves
-  auto emit = [&](int unit, int tiles, int2 src, int skip, int k0, int step) {
-    const int np = pieces_of(tiles, skip);
+  auto emit = [&](int unit, int tiles, int2 src, int skip, int k0, int step, bool valid) {
+    const int np = valid ? pieces_of(tiles, skip) : 0;
     const bool own = src.x >= 0, parts = !own || np > 1 || skip > 0;
     const int i = src.y;
     ExUnit u{};
@@ -504,17 +542,16 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
       if (longer) at_longer = atomicAdd(&hist[klass(len + 1, two)], longer);
     }
     if (step > 1) {
-      const uint32_t group = 0xffffu << (lane & 16);
-      u.part = __shfl_sync(group, u.part, 0, 16);
-      at = __shfl_sync(group, at, 0, 16);
-      at_longer = __shfl_sync(group, at_longer, 0, 16);
+      u.part = __shfl_sync(0xffffffffu, u.part, 0, 16);
+      at = __shfl_sync(0xffffffffu, at, 0, 16);
+      at_longer = __shfl_sync(0xffffffffu, at_longer, 0, 16);
     }
     if (u.part >= 0 && (long long)u.part + u.n_tok * p.g * np > p.w.part_rows) {   // the sizes exclude it: drop the rows
       set_err(p.status, KVS_DEVERR_PLAN);
       u.part = 0;
       u.n_tok = 0;
     }
-    if (k0 == 0 && unit < p.w.max_units) p.w.units[unit] = u;
+    if (valid && k0 == 0 && unit < p.w.max_units) p.w.units[unit] = u;
     it.t0 = u.t0;
     it.n_tok = u.n_tok;
     for (int k = k0; k < np; k += step) {
@@ -526,10 +563,12 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     }
   };
   if (split) {
-    for (int u = tid >> 4; u < n_units; u += kPlanThreads / 16)
-      emit(u, tiles_of[u] & ~(1 << 30), src_of[u], skip_of(src_of[u]), tid & 15, 16);
+    for (int u0 = 0; u0 < n_units; u0 += kPlanThreads / 16) {   // whole warps take part in the exchanges
+      const int u = u0 + (tid >> 4), at = min(u, n_units - 1);
+      emit(u, tiles_of[at] & ~(1 << 30), src_of[at], skip_of(src_of[at]), tid & 15, 16, u < n_units);
+    }
   } else {
-    walk([&](int unit, int tiles, int2 src, int skip) { emit(unit, tiles, src, skip, 0, 1); });
+    walk([&](int unit, int tiles, int2 src, int skip) { emit(unit, tiles, src, skip, 0, 1, true); });
   }
   if (tid == 0) {
     hdr[kHSeq] = p.n_seq;
