@@ -53,6 +53,7 @@ constexpr int kExMagic = 0x45585431;
 // splits or shared parts (2,048 row-tile pairs and more), and none are made:
 // the workspace's part buffers stay below about a gigabyte
 constexpr long long kExPartRows = 1ll << 19;
+constexpr int kExMergeRows = 2;          // rows a warp of the merge joins at a time
 constexpr int kExItemsPerSm = 4;         // pieces aimed at per SM
 constexpr int kExMinPiece = 2;           // key tiles of the shortest piece
 
@@ -722,6 +723,7 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
   constexpr int ST = ex_stages<D>();
   constexpr int kTile = ex_tile_bytes<D>();
   constexpr int kHalf = kExTile * 128;        // one [128][64] bf16 half, bytes
+  constexpr int kBlock = 16 * D * 2;          // one block of a KV head
   extern __shared__ uint8_t smem_raw[];
   __shared__ ExBars bars;
   __shared__ __align__(16) ExWork work[2];
@@ -784,7 +786,7 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
     int armed = -1, q_armed = 0;
     int claim = blockIdx.x;
     bool ok = true;
-    auto copy = [&](const CUtensorMap* map, int id, int head) {
+    auto copy = [&](const CUtensorMap* map, bool is_v, int id, int head) {
       // stage n: lanes k < 8 copy block k of the tile; a block without an id
       // lies behind the slab's last row and arrives as zeros
       const int s = n % ST;
@@ -793,8 +795,12 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
       __syncwarp();
       if (lane < kExBlocks) {
         const int row = id >= 0 ? (id * p.hkv + head) * 16 : p.slab_rows;
+        if (is_v) {   // V: the whole block, [block][half][16 tokens][64]
+          tma_load_3d(ring(s) + lane * kBlock, map, 0, row, 0, &bars.full[s]);
+        } else {      // K: [half][128 tokens][64]
 #pragma unroll
-        for (int hf = 0; hf < HF; ++hf) tma_load_3d(ring(s) + hf * kHalf + lane * 2048, map, 0, row, hf, &bars.full[s]);
+          for (int hf = 0; hf < HF; ++hf) tma_load_3d(ring(s) + hf * kHalf + lane * 2048, map, 0, row, hf, &bars.full[s]);
+        }
       }
       __syncwarp();
       armed = n++;
@@ -844,7 +850,7 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
       int id = block(0);
       for (int j = 0; j < nt; ++j) {
         const int id_next = block(j + 1);
-        if (!copy(&tk, id, head)) { ok = false; break; }
+        if (!copy(&tk, false, id, head)) { ok = false; break; }
         if (j == 0) {
           // the query tiles, once the last S of the item before has read them
           if (nq >= 1 && !wait(&bars.q_empty, (nq - 1) & 1)) { ok = false; break; }
@@ -858,7 +864,7 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
           __syncwarp();
           q_armed = ++nq;
         }
-        if (!copy(&tv, id, head)) { ok = false; break; }
+        if (!copy(&tv, true, id, head)) { ok = false; break; }
         id = id_next;
       }
       claim = __shfl_sync(0xffffffffu, next, 0);
@@ -875,7 +881,7 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
     constexpr uint32_t idO = umma_idesc_bf16(128, D, false, true);
     constexpr uint32_t kHi = ex_desc_hi(1024);
     const uint32_t q_lo = ex_desc_lo(smem_u32(base), 16);
-    const uint32_t k_lo = ex_desc_lo(smem_u32(ring(0)), 16), v_lo = ex_desc_lo(smem_u32(ring(0)), kHalf);
+    const uint32_t k_lo = ex_desc_lo(smem_u32(ring(0)), 16), v_lo = ex_desc_lo(smem_u32(ring(0)), 2048);
     struct Pos {   // a use of the ring
       int s;
       uint32_t par;
@@ -906,7 +912,7 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
         const uint32_t b = v_lo + v.s * (kTile / 16);
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk)
-          ex_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * (k0 + kk), b + (k0 + kk) * (2048 / 16), kHi, idO,
+          ex_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * (k0 + kk), b + (k0 + kk) * (kBlock / 16), kHi, idO,
                     acc || kk > 0);
         if (k0) umma_commit(&bars.pv_done[x]);
       }
@@ -1102,7 +1108,7 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
           const int rows = ((tail + 15) & ~15) - tail;
           for (int i = threadIdx.x & 127; i < rows * HF * 8; i += 128) {
             const int c = i & 7, hf = (i >> 3) % HF, rr = tail + (i >> 3) / HF;
-            *reinterpret_cast<uint4*>(ring(mv % ST) + hf * kHalf + rr * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint4*>(ring(mv % ST) + (rr >> 4) * kBlock + hf * 2048 + (rr & 15) * 128 + c * 16) = make_uint4(0u, 0u, 0u, 0u);
           }
           fence_proxy_async_smem();
         }
@@ -1169,79 +1175,134 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
 // ------------------------------------------------------------------ merge ---
 // Joins the parts of the rows that have several, in the order shared range,
 // own range, each by its pieces.  A CTA takes one unit and KV head and every
-// gridDim.z-th eight rows of it, a warp one row at a time; four parts' loads
-// are in flight together (the parts lie in L2: the chain of loads bounds it).
+// gridDim.z-th sixteen rows of it, a warp two rows at a time.  The parts lie
+// in L2 and the chain of loads bounds it: up to four parts of both rows are
+// loaded at once; with more, 32 lanes take the factors of 32 parts and four
+// parts are in flight.
 template <int D>
 __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExParams p) {
   pdl_enter();
   constexpr int E = D / 32;   // elements per lane
-  constexpr int U = 4;
+  constexpr int U = 4, R = kExMergeRows;
   const bool plan_ok = ex_plan_ok(p.w.hdr, p.n_seq, p.max_blocks, p.g, p.hkv, p.causal, p.n_tokens);
   if (!plan_ok) return;
   if (blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && threadIdx.x == 0) p.w.hdr[kHCounter] = 0;   // for the next layer
   const int n_units = p.w.hdr[kHUnits], head = blockIdx.y;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tu = 2 * (kExTile / p.g);
+  struct Vec {
+    float v[E];
+  };
+  auto load = [&](size_t row) {
+    Vec x;
+    if constexpr (E == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(p.w.part + row * D + lane * 4);
+      x.v[0] = y.x; x.v[1] = y.y; x.v[2] = y.z; x.v[3] = y.w;
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(p.w.part + row * D + lane * 2);
+      x.v[0] = y.x; x.v[1] = y.y;
+    }
+    return x;
+  };
   for (int i = blockIdx.x; i < n_units; i += gridDim.x) {
     const ExUnit u = p.w.units[i];
     if (u.part < 0 && u.sh_unit < 0) continue;   // written by the attention itself
-    for (int r = blockIdx.z * 8 + warp; r < u.n_tok * p.g; r += 8 * gridDim.z) {
-      const int t = u.t0 + r / p.g;
-      ExUnit sh{};
-      if (u.sh_unit >= 0) sh = p.w.units[u.sh_unit + (t - u.sh_t0) / tu];
-      const int n_sh = u.sh_unit >= 0 ? sh.pieces : 0, n = n_sh + (u.part >= 0 ? u.pieces : 0);
-      const int sh_row = (t - sh.t0) * p.g + r % p.g;
-      auto at = [&](int k) {
-        const int row = k < n_sh ? sh.part + k * sh.n_tok * p.g + sh_row : u.part + (k - n_sh) * u.n_tok * p.g + r;
-        return (size_t)row * p.hkv + head;
+    const int rows = u.n_tok * p.g, n_own = u.part >= 0 ? u.pieces : 0;
+    for (int r0 = (blockIdx.z * 8 + warp) * R; r0 < rows; r0 += 8 * R * gridDim.z) {
+      // a row's parts: n_sh of the shared range from sh_at on, sh_step rows
+      // apart (every unit of a shared range has as many), then its own
+      int row[R], sh_at[R], sh_step[R], n_sh = 0;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        row[j] = min(r0 + j, rows - 1);
+        sh_at[j] = sh_step[j] = 0;
+        if (u.sh_unit >= 0) {
+          const int t = u.t0 + row[j] / p.g;
+          const ExUnit sh = p.w.units[u.sh_unit + (t - u.sh_t0) / tu];
+          n_sh = sh.pieces;
+          sh_step[j] = sh.n_tok * p.g;
+          sh_at[j] = sh.part + (t - sh.t0) * p.g + row[j] % p.g;
+        }
+      }
+      const int n = n_sh + n_own;
+      auto at = [&](int j, int k) {
+        const int r = k < n_sh ? sh_at[j] + k * sh_step[j] : u.part + (k - n_sh) * rows + row[j];
+        return (size_t)r * p.hkv + head;
       };
-      // lane k holds part k's factor 2^(m_k - max) and row; further parts in rounds of 32
-      float mx = -INFINITY;
-      for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.w.ml[at(k)].x);
+      Vec acc[R];
+      float l[R];
+      if (n <= U) {
+        float2 ml[R][U];
+        Vec x[R][U];
 #pragma unroll
-      for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      float acc[E], l = 0.f;
+        for (int j = 0; j < R; ++j)
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = 0.f;
-      if (mx != -INFINITY) {
-        for (int k0 = 0; k0 < n; k0 += 32) {
-          float f = 0.f;
-          if (k0 + lane < n) {
-            const float2 ml = p.w.ml[at(k0 + lane)];
-            f = fast_exp2(ml.x - mx);
-            l += f * ml.y;
+          for (int k = 0; k < U; ++k) {
+            ml[j][k] = make_float2(-INFINITY, 0.f);
+            x[j][k] = Vec{};
+            if (k < n) {
+              ml[j][k] = p.w.ml[at(j, k)];
+              x[j][k] = load(at(j, k));
+            }
           }
-          const int m = min(32, n - k0);
-          for (int k = 0; k < m; k += U) {
-            float v[U][E];
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-              if (k + j >= m) {
+        for (int j = 0; j < R; ++j) {
+          const float mx = fmaxf(fmaxf(ml[j][0].x, ml[j][1].x), fmaxf(ml[j][2].x, ml[j][3].x));
+          const float ref = mx == -INFINITY ? 0.f : mx;   // no part saw a key: factors 0
+          acc[j] = Vec{};
+          l[j] = 0.f;
 #pragma unroll
-                for (int e = 0; e < E; ++e) v[j][e] = 0.f;
-              } else if constexpr (E == 4) {
-                const float4 x = *reinterpret_cast<const float4*>(p.w.part + at(k0 + k + j) * D + lane * 4);
-                v[j][0] = x.x; v[j][1] = x.y; v[j][2] = x.z; v[j][3] = x.w;
-              } else {
-                const float2 x = *reinterpret_cast<const float2*>(p.w.part + at(k0 + k + j) * D + lane * 2);
-                v[j][0] = x.x; v[j][1] = x.y;
-              }
-            }
+          for (int k = 0; k < U; ++k) {
+            const float f = fast_exp2(ml[j][k].x - ref);
+            l[j] += f * ml[j][k].y;
 #pragma unroll
-            for (int j = 0; j < U; ++j) {
-              const float fj = __shfl_sync(0xffffffffu, f, min(k + j, 31));
-#pragma unroll
-              for (int e = 0; e < E; ++e) acc[e] += fj * v[j][e];
-            }
+            for (int e = 0; e < E; ++e) acc[j].v[e] += f * x[j][k].v[e];
           }
         }
+      } else {
 #pragma unroll
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        for (int j = 0; j < R; ++j) {
+          float mx = -INFINITY, lj = 0.f;
+          Vec a{};
+          for (int k = lane; k < n; k += 32) mx = fmaxf(mx, p.w.ml[at(j, k)].x);
+#pragma unroll
+          for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const float ref = mx == -INFINITY ? 0.f : mx;
+          for (int k0 = 0; k0 < n; k0 += 32) {
+            float f = 0.f;
+            if (k0 + lane < n) {
+              const float2 ml = p.w.ml[at(j, k0 + lane)];
+              f = fast_exp2(ml.x - ref);
+              lj += f * ml.y;
+            }
+            const int m = min(32, n - k0);
+            for (int k = 0; k < m; k += U) {
+              Vec x[U];
+#pragma unroll
+              for (int q = 0; q < U; ++q) x[q] = k + q < m ? load(at(j, k0 + k + q)) : Vec{};
+#pragma unroll
+              for (int q = 0; q < U; ++q) {
+                const float fq = __shfl_sync(0xffffffffu, f, min(k + q, 31));
+#pragma unroll
+                for (int e = 0; e < E; ++e) a.v[e] += fq * x[q].v[e];
+              }
+            }
+          }
+#pragma unroll
+          for (int o = 16; o; o >>= 1) lj += __shfl_xor_sync(0xffffffffu, lj, o);
+          acc[j] = a;
+          l[j] = lj;
+        }
       }
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + ((size_t)t * p.hq + head * p.g + r % p.g) * D + lane * E);
 #pragma unroll
-      for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[e] * inv, acc[e + 1] * inv);
+      for (int j = 0; j < R; ++j) {
+        if (r0 + j >= rows) break;
+        const float inv = l[j] == 0.f ? 0.f : 1.f / l[j];
+        uint32_t* dst = reinterpret_cast<uint32_t*>(
+            p.out + ((size_t)(u.t0 + row[j] / p.g) * p.hq + head * p.g + row[j] % p.g) * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) dst[e / 2] = pack_bf16(acc[j].v[e] * inv, acc[j].v[e + 1] * inv);
+      }
     }
   }
 }
@@ -1312,13 +1373,13 @@ kvs_status ex_run(kvs_pool* pool, int layer, const ExParams& p, const CUtensorMa
     return fail(KVS_ERR_CUDA, "extend_attn: cannot raise the shared-memory limit");
   const unsigned grid = (unsigned)std::min<long long>(pool->num_sms, max_claims);
   const CUtensorMap& tk = D == 128 ? pool->tk1[layer] : pool->tk[layer];
-  const CUtensorMap& tv = D == 128 ? pool->tv1[layer] : pool->tv[layer];
+  const CUtensorMap& tv = pool->tv[layer];
   if (ex_launch(extend_attn_kernel<D>, dim3(grid), dim3(kExThreads), ex_smem<D>(), stream, p, tq, tk, tv) != cudaSuccess)
     return fail(KVS_ERR_CUDA, std::string("extend_attn: ") + cudaGetErrorString(cudaGetLastError()));
   count_launch();
-  // about 16 CTAs per SM over units, heads and blocks of eight rows
+  // about 16 CTAs per SM over units, heads and blocks of sixteen rows
   const unsigned units = (unsigned)std::min(p.w.max_units / 2, 4096);
-  const long long most = std::min<long long>(32, ((long long)p.n_tokens * p.g + 7) / 8);
+  const long long most = std::min<long long>(32 / kExMergeRows, ((long long)p.n_tokens * p.g + 8 * kExMergeRows - 1) / (8 * kExMergeRows));
   const unsigned z = (unsigned)std::clamp<long long>(16ll * pool->num_sms / ((long long)units * p.hkv), 1, most);
   if (ex_launch(extend_merge_kernel<D>, dim3(units, (unsigned)p.hkv, z), dim3(256), 0, stream, p) != cudaSuccess)
     return fail(KVS_ERR_CUDA, std::string("extend_attn merge: ") + cudaGetErrorString(cudaGetLastError()));
