@@ -1346,9 +1346,11 @@ kvs_status ex_check(const kvs_pool* pool, const char* what, int n_tokens, int n_
   if (n_q_heads < 1 || n_q_heads % d.num_kv_heads)
     return fail(KVS_ERR_INVALID_ARG, std::string(what) + ": n_q_heads must be a multiple of num_kv_heads");
   if (n_q_heads / d.num_kv_heads > 16) return fail(KVS_ERR_UNSUPPORTED, std::string(what) + ": more than 16 query heads per KV head");
-  // key tiles, part rows and units are counted in 32 bits
-  if ((long long)max_blocks * 16 > (1ll << 30) || (long long)n_tokens * n_q_heads > (1ll << 30))
-    return fail(KVS_ERR_CAPACITY, std::string(what) + ": too many tokens");
+  // key tiles, part rows and claims (units x KV heads) are counted in 32
+  // bits, KV heads are a grid dimension
+  const long long rows = (long long)n_tokens * n_q_heads, units = 4ll * n_seq * d.num_kv_heads;
+  if ((long long)max_blocks * 16 > (1ll << 30) || rows > (1ll << 30) || units > (1ll << 30) || d.num_kv_heads > 65535)
+    return fail(KVS_ERR_CAPACITY, std::string(what) + ": too many tokens, sequences or KV heads");
   return KVS_OK;
 }
 

@@ -365,6 +365,10 @@ def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str
     dt = t.dtype
     if dt is not _BF16 and dt is not _I16:
         raise ValueError(f"{what}: bf16 rows (torch.bfloat16, or their bits as int16) are wanted, got {dt}")
+    if not t.is_cuda:
+        raise ValueError(f"{what}: a CUDA tensor is wanted")
+    if t.is_contiguous() and t.numel() == n_tokens * n_heads * head_dim:
+        return t.data_ptr(), n_heads * head_dim
     shape = t.shape
     if len(shape) != 3 or shape[0] < n_tokens or shape[1] != n_heads or shape[2] != head_dim:
         raise ValueError(f"{what}: shape {tuple(shape)} is not [>= {n_tokens}][{n_heads}][{head_dim}]")
@@ -379,8 +383,8 @@ def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str
 def _ints(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype is not _I32 or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what}: a contiguous int32 tensor of at least {n} values is wanted")
+    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: a contiguous int32 CUDA tensor of at least {n} values is wanted")
     return t.data_ptr()
 
 

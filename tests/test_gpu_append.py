@@ -310,6 +310,36 @@ def test_append_refusals():
     call(tokens=0)
 
 
+def test_rows_of_other_shapes_are_refused():
+    ok = torch.zeros(4, 6, 64, dtype=torch.bfloat16, device=DEV)
+    assert K._rows(ok[:, 2:4], 4, 2, 64, "x") == (ok.data_ptr() + 2 * 64 * 2, 6 * 64)
+    assert K._rows(ok, 3, 6, 64, "x")[1] == 6 * 64
+    for bad in (ok[:3], ok[:, :, ::2], ok.transpose(0, 1), ok[0], ok[:, ::2], ok.cpu()):
+        with pytest.raises(ValueError):
+            K._rows(bad, 4, 6, 64, "x")
+    for bad in (torch.zeros(3, dtype=torch.int32, device=DEV), torch.zeros(8, dtype=torch.int32, device=DEV)[::2],
+                torch.zeros(4, dtype=torch.int32)):
+        with pytest.raises(ValueError):
+            K._ints(bad, 4, "tok_off")
+
+
+def test_append_to_a_far_block():
+    """Rows behind 2^31 bytes of a slab (and past 2^30 elements)."""
+    hkv, d, cap = 32, 128, 18000                   # 18,000 blocks of 131,072 bytes
+    k, v = (torch.zeros(cap, hkv, 16, d, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    pool = K.kvs_pool_create(1, hkv, d, 16, K.KVS_DTYPE_BF16, cap, 1, [k], [v])
+    kn, vn = randn(1, 20, hkv, d), randn(2, 20, hkv, d)
+    table, lens, off = H.i32([[cap - 1, cap - 2]]), H.i32([20]), H.i32([0, 20])
+    K.kvs_append(pool, 0, kn, vn, 20, off, table, 2, lens, 1)
+    assert torch.equal(k[cap - 1], kn[:16].transpose(0, 1)) and torch.equal(v[cap - 2, :, :4], vn[16:].transpose(0, 1))
+    assert not k[: cap - 2].any() and not v[: cap - 2].any() and not k[cap - 2, :, 4:].any()
+    q, out = randn(3, 20, hkv, d), torch.empty(20, hkv, d, dtype=torch.bfloat16, device=DEV)
+    ws = H.workspace(K.kvs_extend_workspace_size(pool, 20, 1, 2, hkv))
+    K.kvs_extend_attn(pool, 0, q, 20, off, hkv, table, 2, lens, 1, True, d ** -0.5, out, ws)
+    assert K.kvs_pool_check(pool) == 0
+    assert torch.equal(out[0], vn[0])              # the first row sees itself alone
+
+
 def test_append_in_a_graph_and_on_another_stream():
     c = Case([1, 1, 1], [5, 40, 16], 2, 128)
     k, v = randn(1, 3, 2, 128), randn(2, 3, 2, 128)

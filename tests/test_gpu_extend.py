@@ -200,6 +200,108 @@ def test_many_sequences():
     Batch(new, lens, 4, 1, 64, seed=2).check(True)
 
 
+@pytest.mark.parametrize("hkv, n, prefix", [(1, 700, 384), (2, 600, 256), (4, 300, 640)])
+def test_many_sequences_over_one_prefix(hkv, n, prefix):
+    """Families larger than the plan keeps in shared memory, and calls with so
+    many units that nothing is split."""
+    r = np.random.default_rng(n)
+    new = r.integers(0, 3, n)
+    new[:5] = 2
+    lens = prefix + r.integers(0, 30, n) + new
+    b = Batch(new, lens, 4 * hkv, hkv, 64, prefix=prefix, seed=2)
+    out = b.run(True)
+    rows = r.choice(np.nonzero(np.diff(b.off) > 0)[0], 60, replace=False)
+    check_sequences(b, out, rows, True)
+
+
+def check_sequences(b, out, seqs, causal):
+    k, v = f64(b.k), f64(b.v)
+    for a in seqs:
+        t0, t1, n = b.off[a], b.off[a + 1], int(b.lens[a])
+        ids = b.table[a, : -(-n // 16)]
+        kk, vv = np.nan_to_num(k[ids], posinf=0.0), np.nan_to_num(v[ids], posinf=0.0)
+        exp, mag, big = OE.extend_attention(f64(b.q[t0:t1]), kk, vv, np.arange(len(ids))[None], [0, t1 - t0], [n], 16,
+                                            b.scale, causal)
+        assert_attention(f64(out[t0:t1]), exp, mag, big, b.d)
+
+
+@pytest.mark.parametrize("hq, hkv, d, new, n", [(1, 1, 128, 1, 40000), (8, 8, 64, 2, 24000), (12, 1, 64, 3, 33333)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_one_long_context(hq, hkv, d, new, n, causal):
+    """Few rows over a long context: more parts than a warp joins at a time."""
+    b = Batch([new], [n], hq, hkv, d, seed=4)
+    check_sequences(b, b.run(causal), [0], causal)
+
+
+def test_a_call_too_large_for_parts():
+    """So many rows that nothing is split or shared; sampled rows."""
+    hq, hkv, d, n, prefix = 64, 4, 64, 4, 512
+    new = [2100, 2200, 2050, 2077]
+    b = Batch(new, [prefix + m + 100 for m in new], hq, hkv, d, prefix=prefix, seed=6)
+    assert b.T * hq > 1 << 19
+    out = b.run(True)
+    k, v = np.nan_to_num(f64(b.k), posinf=0.0), np.nan_to_num(f64(b.v), posinf=0.0)
+    q, o = f64(b.q), f64(out)
+    r = np.random.default_rng(1)
+    for t in r.integers(0, b.T, 24):
+        a = int(np.searchsorted(b.off, t, side="right") - 1)
+        lim = int(b.lens[a] - b.new[a] + (t - b.off[a]) + 1)
+        ids = b.table[a, : -(-lim // 16)]
+        for h in r.integers(0, hq, 3):
+            exp, mag, big = OE.extend_attention(q[t:t + 1, h:h + 1], k[ids][:, h // 16:h // 16 + 1], v[ids][:, h // 16:h // 16 + 1],
+                                                np.arange(len(ids))[None], [0, 1], [lim], 16, b.scale, True)
+            assert_attention(o[t:t + 1, h:h + 1], exp, mag, big, d)
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_batches(seed):
+    """Batches drawn over the whole range: groups, prefixes, empty sequences,
+    lengths that end anywhere, padded rows."""
+    r = np.random.default_rng(1000 + seed)
+    hkv = int(r.choice([1, 2, 3]))
+    hq = hkv * int(r.choice([1, 2, 3, 4, 5, 7, 8, 16]))
+    d = int(r.choice([64, 128]))
+    n = int(r.integers(1, 14))
+    fams = int(r.integers(1, 4))
+    groups = np.sort(r.integers(0, fams, n)).tolist()
+    prefix = [16 * int(x) for x in r.integers(0, 40, fams)]
+    new = r.integers(0, int(r.choice([2, 9, 90])), n)
+    own = r.integers(0, int(r.choice([3, 200, 900])), n)
+    lens = [max(0, prefix[g] * int(r.random() < 0.9) + int(o) + int(m) - int(r.integers(0, 3))) for g, o, m in zip(groups, own, new)]
+    b = Batch(new, lens, hq, hkv, d, prefix=prefix, groups=groups, seed=seed, pad=int(r.integers(0, 4)),
+              qscale=float(r.choice([0.5, 2.0, 6.0])))
+    if b.T:
+        b.check(bool(r.random() < 0.6))
+
+
+def test_two_graphs_share_a_workspace():
+    """Two captured calls of different batches and forms on one workspace,
+    replayed in turn."""
+    a = Batch([4, 9, 2, 30], [700, 650, 600, 900], 8, 2, 64, prefix=512)
+    c = Batch([1] * 7, [90, 1, 300, 40, 5, 77, 1200], 8, 2, 64, seed=9)
+    ws = max((a.ws(), c.ws()), key=lambda w: w.numel())
+    want = [a.run(True), c.run(False)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graphs, outs = [], []
+    keep = []
+    for b, causal in ((a, True), (c, False)):
+        off, tab, lens = b.dev()
+        out = torch.full_like(want[len(outs)], 7.0)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            K.kvs_extend_attn(b.pool, 0, b.q, b.T, off, b.hq, tab, b.mb, lens, b.n, causal, b.scale, out, ws)
+        graphs.append(g)
+        outs.append(out)
+        keep.append((off, tab, lens))
+    for i in (0, 1, 1, 0, 1):
+        outs[i].fill_(7.0)
+        graphs[i].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i], want[i])
+    assert K.kvs_pool_check(a.pool) == 0 and K.kvs_pool_check(c.pool) == 0
+
+
 def test_query_rows_of_one_projection():
     b = Batch([5, 30], [50, 400], 8, 2, 128)
     rows = randn(9, b.T, 12, 128)
