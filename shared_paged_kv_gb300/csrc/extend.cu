@@ -149,7 +149,9 @@ struct ExPlanParams {
   ExWorkspace w;
   const int32_t *tok_off, *seq_len, *table;
   uint32_t* status;
-  int n_tokens, n_seq, max_blocks, capacity, g, hkv, causal, sms, share;
+  int n_tokens, n_seq, max_blocks, capacity, g, hkv, causal, sms;
+  int share;      // 1: look for common parts, 0: one sequence, -1: neither shared parts nor splits
+  int lcp_here;   // the plan kernel finds the common parts itself
 };
 
 // {first row, rows (-1: bad offsets), keys, key tiles that every row of the
@@ -207,6 +209,7 @@ constexpr int kPlanThreads = 256;
 constexpr int kPlanSeqs = 512;     // up to this many sequences the plan's arrays stay in shared memory
 constexpr int kPlanUnits = 640;    // more units than calls that are split have (4 per SM)
 constexpr int kPlanCands = 16;     // piece lengths that are tried
+constexpr long long kPlanTable = 8192;   // table entries up to which the plan kernel compares neighbours itself
 
 // Exclusive scan over the CTA plus a running total, one barrier per call:
 // calls alternate between two rows of warp sums.
@@ -268,7 +271,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   int4* const run = small ? sm_run : p.w.run;          // {shared tiles, first sequence, sequences, rows}
   int2* const seg = small ? sm_seg : p.w.seg;          // {run, first unit} of a sequence
   int2* const runseg = small ? sm_runseg : p.w.runseg; // {first shared unit, shared units} of a run
-  const int* const lcp = small ? sm_lcp : p.w.lcp;
+  int* const lcp = small ? sm_lcp : p.w.lcp;           // key tiles in common with the next sequence
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int tu = 2 * (kExTile / p.g), tt = kExTile / p.g;
   int* hdr = p.w.hdr;
@@ -280,7 +283,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   pdl_enter();
   int bad = 0;
   for (int a = tid; a < p.n_seq; a += kPlanThreads) {
-    if (small && p.share > 0) sm_lcp[a] = a + 1 < p.n_seq ? p.w.lcp[a] : 0;
+    if (small && p.share > 0 && !p.lcp_here) sm_lcp[a] = a + 1 < p.n_seq ? p.w.lcp[a] : 0;
     const int4 s = ex_seq(p, a, true);
     bad |= s.y < 0;
     seq[a] = s;
@@ -294,6 +297,33 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
       hdr[kHItems] = hdr[kHUnits] = hdr[kHCounter] = 0;
     }
     return;
+  }
+  if (p.lcp_here) {   // short tables: a warp per pair of neighbours
+    for (int a = warp; a + 1 < p.n_seq; a += kPlanThreads / 32) {
+      const int n = min(seq[a].w, seq[a + 1].w) * kExBlocks;
+      const int32_t* x = p.table + (size_t)a * p.max_blocks;
+      const int32_t* y = x + p.max_blocks;
+      int first = n;
+      constexpr int U = 4;   // loads in flight per lane and row
+      for (int b0 = 0; b0 < first; b0 += 32 * U) {
+        int xv[U], yv[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int b = b0 + u * 32 + lane;
+          xv[u] = b < n ? __ldg(x + b) : 0;
+          yv[u] = b < n ? __ldg(y + b) : 0;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int b = b0 + u * 32 + lane;
+          if (b < n && (xv[u] != yv[u] || xv[u] < 0 || xv[u] >= p.capacity)) first = min(first, b);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) first = min(first, __shfl_xor_sync(0xffffffffu, first, o));
+      }
+      if (lane == 0) lcp[a] = first / kExBlocks;
+    }
+    __syncthreads();
   }
   // runs: a sequence starts a new one unless its common part with the one
   // before it is at least half of the neighbouring common parts (so that a
@@ -563,7 +593,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
       if (slot < p.w.max_items) p.w.items[slot] = it;
     }
   };
-  if (split) {
+  if (split && n_items <= 4 * n_units) {   // few pieces each: a thread per unit
+    for (int u = tid; u < n_units; u += kPlanThreads)
+      emit(u, tiles_of[u] & ~(1 << 30), src_of[u], skip_of(src_of[u]), 0, 1, true);
+  } else if (split) {
     for (int u0 = 0; u0 < n_units; u0 += kPlanThreads / 16) {   // whole warps take part in the exchanges
       const int u = u0 + (tid >> 4), at = min(u, n_units - 1);
       emit(u, tiles_of[at] & ~(1 << 30), src_of[at], skip_of(src_of[at]), tid & 15, 16, u < n_units);
@@ -1430,7 +1463,11 @@ extern "C" kvs_status kvs_extend_plan(kvs_pool* pool, const int32_t* tok_off_dev
   p.sms = pool->num_sms;
   const bool parts = (long long)n_tokens * n_q_heads <= kExPartRows;
   p.share = !parts ? -1 : n_seq > 1 ? 1 : 0;
-  if (p.share == 1) {
+  // Short tables are compared by the plan's one CTA (12 sequences of 94 blocks:
+  // 7.4 -> 6.2 us for the plan), long ones by a CTA per pair before it (64
+  // sequences of 900 blocks: 11.0 us, 22.2 in the one CTA).
+  p.lcp_here = p.share == 1 && (long long)n_seq * max_blocks <= kPlanTable;
+  if (p.share == 1 && !p.lcp_here) {
     if (launch_pdl(extend_lcp_kernel, dim3((unsigned)(n_seq - 1)), dim3(256), stream, p) != cudaSuccess)
       return fail(KVS_ERR_CUDA, std::string("extend_plan: ") + cudaGetErrorString(cudaGetLastError()));
     count_launch();
