@@ -964,8 +964,9 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
       if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
       __syncwarp();
       if (done) break;
-      const int nt = max(na, nb);
+      const int nt = max(na, nb), last_x = nb > 0 ? 1 : 0;
       if (nt == 0) continue;
+      Pos kj = at;
       if (!wait(&bars.full[at.s], at.par) || !wait(&bars.q_full, q_par)) { ok = false; break; }
       q_par ^= 1u;
 #pragma unroll
@@ -977,7 +978,6 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
         issue_s(x, at);
       }
       if (!ok) break;
-      commit(&bars.empty[at.s]);
       if (nt == 1) commit(&bars.q_empty);
       at.next();
       for (int j = 0; j < nt; ++j) {
@@ -996,6 +996,11 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
           if (!wait(&bars.p_half[x], par)) { ok = false; break; }
           tc_fence_after();
           issue_pv(x, v, 0, j > 0);
+          // weights of the last row tile: its S, the last to read this K, is
+          // complete.  Stages are handed back by plain arrivals where a wait
+          // has shown them free: a commit costs the MMA pipe more (1.5 % of a
+          // long chunk for two of six).
+          if (x == last_x && lane == 0) mbar_arrive(&bars.empty[kj.s]);
           if (!wait(&bars.p_full[x], par)) { ok = false; break; }
           tc_fence_after();
           issue_pv(x, v, 4, true);
@@ -1003,11 +1008,13 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
             if (!wait(&bars.full[k.s], k.par) || !wait(&bars.pv_done[x], par)) { ok = false; break; }   // S goes where P was
             tc_fence_after();
             issue_s(x, k);
+            if (x == last_x && lane == 0) mbar_arrive(&bars.empty[v.s]);
+          } else if (x == last_x) {
+            commit(&bars.empty[v.s]);
           }
         }
         if (!ok) break;
-        commit(&bars.empty[v.s]);
-        if (more) commit(&bars.empty[k.s]);
+        kj = k;
         if (j + 2 == nt) commit(&bars.q_empty);
       }
       if (!ok) break;
