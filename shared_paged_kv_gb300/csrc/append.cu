@@ -106,48 +106,60 @@ struct AppendParams {
 };
 
 // 4-bit codes of one 64-element group held by 8 consecutive lanes, 8 values
-// each: bit for bit those of kvs_quantize_q4, rint of the rounded quotient
-// (x - b) / s.  The product with 1 / s is within 2^-21 of the quotient's size
-// (at most 16), so its rint is the same unless it lies within 1e-4 of a half;
-// then (and where it is no number) the quotients are taken.  Sixteen divisions
-// a lane made the call compute-bound (7,700 tokens, 8 KV and 32 query heads:
-// 57 us).
-__device__ __forceinline__ uint32_t q4_codes(const float* x, __half2& sb) {
-  float mn = x[0], mx = x[0];
+// each as bf16 pairs: bit for bit those of kvs_quantize_q4, rint of the
+// rounded quotient (x - b) / s.
+//  * The extremes are found on the bf16 values (exact): minimum and negated
+//    maximum side by side in one register, so that one exchange serves both.
+//  * 15 times (x - b) * (1 / (15 s)), clamped on the way, is within 2^-18 of
+//    the clamped quotient, so its rint is the same unless it lies within 1e-4
+//    of a half; then the quotients are taken.  Rint by the addition of
+//    1.5 * 2^23, whose last place is 1.
+// With a division per value and scalar extremes the call was bound by its
+// instructions (7,700 tokens, 8 KV and 32 query heads: 57 us).
+__device__ __forceinline__ uint32_t min_bf16x2(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<const __nv_bfloat162*>(&a), *reinterpret_cast<const __nv_bfloat162*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t q4_codes(const uint32_t* w, __half2& sb) {
+  constexpr uint32_t kNeg = 0x80008000u;
+  const uint32_t lo = min_bf16x2(min_bf16x2(w[0], w[1]), min_bf16x2(w[2], w[3]));
+  const uint32_t hi = min_bf16x2(min_bf16x2(w[0] ^ kNeg, w[1] ^ kNeg), min_bf16x2(w[2] ^ kNeg, w[3] ^ kNeg));
+  uint32_t ext = min_bf16x2(__byte_perm(lo, hi, 0x5410), __byte_perm(lo, hi, 0x7632));   // {min, -max}
 #pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    mn = fminf(mn, x[e]);
-    mx = fmaxf(mx, x[e]);
-  }
-#pragma unroll
-  for (int o = 1; o < 8; o <<= 1) {
-    mn = fminf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
-    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-  }
+  for (int o = 1; o < 8; o <<= 1) ext = min_bf16x2(ext, __shfl_xor_sync(0xffffffffu, ext, o));
+  const float mn = bf16_lo(ext), mx = -bf16_hi(ext);
   const __half s16 = __float2half_rn(__fdiv_rn(__fsub_rn(mx, mn), 15.0f));
   const __half b16 = __float2half_rn(mn);
   const float s = __half2float(s16), b = __half2float(b16);
   sb = __halves2half2(s16, b16);
   if (s == 0.f) return 0u;
-  const float inv = __frcp_rn(s);
-  uint32_t w = 0;
+  const float inv = __frcp_rn(s) * (1.f / 15.f), magic = 12582912.f;
+  const float2 b2 = make_float2(-b, -b), m2 = make_float2(magic, magic), k2 = make_float2(15.f, 15.f);
+  const float2 n2 = make_float2(-magic, -magic);
+  float n[8];
   bool clear = true;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    // rint by the addition of 1.5 * 2^23, whose last place is 1; a quotient
-    // outside [0, 15] has the code of its bound either way
-    const float q = fminf(fmaxf(__fmul_rn(__fsub_rn(x[e], b), inv), 0.f), 15.f);
-    const float t = __fadd_rn(q, 12582912.f);
-    clear &= fabsf(__fsub_rn(q, __fsub_rn(t, 12582912.f))) < 0.4999f;
-    w |= (__float_as_uint(t) & 15u) << (4 * e);
+  for (int e = 0; e < 4; ++e) {
+    const float2 d = __fadd2_rn(make_float2(bf16_lo(w[e]), bf16_hi(w[e])), b2);
+    const float2 y = make_float2(__saturatef(d.x * inv), __saturatef(d.y * inv));
+    const float2 r = __fadd2_rn(__ffma2_rn(y, k2, m2), n2);
+    const float2 off = __ffma2_rn(y, k2, make_float2(-r.x, -r.y));
+    clear &= fabsf(off.x) < 0.4999f;
+    clear &= fabsf(off.y) < 0.4999f;
+    n[2 * e] = r.x;
+    n[2 * e + 1] = r.y;
   }
   if (!clear) {
-    w = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      w |= (static_cast<uint32_t>(fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(x[e], b), s)), 0.f), 15.f)) & 15u) << (4 * e);
+    for (int e = 0; e < 4; ++e) {
+      n[2 * e] = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(bf16_lo(w[e]), b), s)), 0.f), 15.f);
+      n[2 * e + 1] = fminf(fmaxf(rintf(__fdiv_rn(__fsub_rn(bf16_hi(w[e]), b), s)), 0.f), 15.f);
+    }
   }
-  return w;
+  // four codes as one whole number below 2^16 each, exact in float32
+  const float a = fmaf(4096.f, n[3], fmaf(256.f, n[2], fmaf(16.f, n[1], n[0]))) + magic;
+  const float c = fmaf(4096.f, n[7], fmaf(256.f, n[6], fmaf(16.f, n[5], n[4]))) + magic;
+  return __byte_perm(__float_as_uint(a), __float_as_uint(c), 0x5410);
 }
 
 enum { kApBf16 = 0, kApQ4 = 1, kApRows = 2 };   // pool type, or rows only (kvs_rope_apply)
@@ -246,16 +258,8 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) append_kernel(const __gri
         const uint32_t lw[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w};
         const uint32_t hw[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
         if (__any_sync(0xffffffffu, r < 2 * p.hkv)) {
-          float xl[8], xh[8];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            xl[2 * e] = bf16_lo(lw[e]);
-            xl[2 * e + 1] = bf16_hi(lw[e]);
-            xh[2 * e] = bf16_lo(hw[e]);
-            xh[2 * e + 1] = bf16_hi(hw[e]);
-          }
           __half2 sl, sh;
-          const uint32_t cl = q4_codes(xl, sl), ch = q4_codes(xh, sh);
+          const uint32_t cl = q4_codes(lw, sl), ch = q4_codes(hw, sh);
           if (r < 2 * p.hkv && w.phys >= 0) {
             const size_t row = ((size_t)w.phys * p.hkv + (is_v ? r - p.hkv : r)) * p.at.block_tokens + w.at;
             uint8_t* code = (is_v ? p.vslab : p.kslab) + row * (D / 2);
