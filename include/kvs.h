@@ -549,8 +549,12 @@ kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* tok_off_dev,
  * As for decoding, a plan per step serves every layer: kvs_extend_plan writes
  * it into ws, kvs_extend_attn_planned runs a layer with it (same arguments;
  * other shapes set KVS_DEVERR_PLAN and nothing is written), kvs_extend_attn is
- * the one after the other.  ws: kvs_extend_workspace_size bytes, of one stream
- * at a time. */
+ * the one after the other.  Calls of at most 32 sequences that need neither
+ * split key ranges nor shared parts (short tables and few rows; or chunks long
+ * enough to fill the device) are one launch without a plan, and
+ * kvs_extend_plan writes nothing for them: the host tells from n_tokens,
+ * n_seq, max_blocks and the heads.  The results agree to rounding.  ws:
+ * kvs_extend_workspace_size bytes, of one stream at a time. */
 kvs_status kvs_extend_workspace_size(const kvs_pool* pool, int32_t n_tokens, int32_t n_seq, int32_t max_blocks,
                                      int32_t n_q_heads, size_t* bytes);
 kvs_status kvs_extend_plan(kvs_pool* pool, const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,
@@ -582,6 +586,9 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  * kvs_pool_set_test_flags clears it.  Results agree between the two paths to
  * rounding. */
 #define KVS_TEST_TOKEN_MAJOR 0x2u
+/* KVS_TEST_EXTEND_PLANNED: while set, kvs_extend_attn and its two steps take
+ * the planned path also for calls that would be a single launch. */
+#define KVS_TEST_EXTEND_PLANNED 0x4u
 kvs_status kvs_pool_set_test_flags(kvs_pool* pool, uint32_t flags);
 
 /* Workspace bytes for an operation with the given call shape. */

@@ -55,7 +55,14 @@ constexpr int kExMagic = 0x45585431;
 constexpr long long kExPartRows = 1ll << 19;
 constexpr int kExMergeRows = 2;          // rows a warp of the merge joins at a time
 constexpr int kExItemsPerSm = 4;         // pieces aimed at per SM
+// Writing 256 rows of a part (133 KB) and reading them again, in key tiles of
+// a row tile pair at a 152nd of the L2's rate
+constexpr float kExPartCost = 5.f;
 constexpr int kExMinPiece = 2;           // key tiles of the shortest piece
+// Calls that run without a plan: up to this many blocks a sequence, and rounds
+// of units over the SMs (see ex_direct).
+constexpr int kExDirectBlocks = 96, kExDirectShort = 256;
+constexpr int kExDirectRounds = 4;
 
 template <int D>
 __host__ __device__ constexpr int ex_tile_bytes() { return kExTile * D * 2; }
@@ -66,7 +73,7 @@ __host__ __device__ constexpr int ex_smem() { return 1024 + ex_tile_bytes<D>() *
 constexpr uint32_t kExCols = 512;        // S/P of A and B at 0 and 128, O at 256 and 256 + D
 
 // Plan header (int indices)
-enum { kHMagic, kHSeq, kHBlocks, kHGroup, kHKv, kHCausal, kHTokens, kHItems, kHCounter, kHUnits, kHParts, kHSharedUnits, kHTotal = 16 };
+enum { kHMagic, kHSeq, kHBlocks, kHGroup, kHKv, kHCausal, kHTokens, kHItems, kHCounter, kHUnits, kHParts, kHTotal = 16 };
 
 // One item: a row-tile pair over a range of key tiles of one block table.
 struct __align__(16) ExItem {
@@ -262,6 +269,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   __shared__ float cost[kPlanCands];
   __shared__ int s_parts, s_most, s_sum;
   __shared__ int tiles_of[kPlanUnits];
+  __shared__ float part_of[kPlanUnits];   // what a part of the unit costs, in key tiles
   __shared__ int2 src_of[kPlanUnits];   // {sequence, or ~run, index in it}
   __shared__ int4 sm_seq[kPlanSeqs], sm_run[kPlanSeqs];
   __shared__ int2 sm_seg[kPlanSeqs], sm_runseg[kPlanSeqs];
@@ -440,6 +448,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
         most = max(most, tiles);
         sum += tiles;
         tiles_of[u] = tiles | (two_tiles(src) ? 1 << 30 : 0);
+        part_of[u] = kExPartCost * (float)(min(tu, (own ? seq[lo].y : run[lo].w) - src.y * tu) * p.g) / (2.f * kExTile);
         src_of[u] = src;
       }
     } else {
@@ -463,9 +472,10 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   int piece = most;
   // piece length: of 16 candidates the one with the least estimated time (the
   // mean load of an SM, or the rounds that the larger half of the pieces
-  // takes; a piece costs its tiles and about 1.5 more, with one row tile 0.6
-  // of that); no splits in calls that fill the device, or are too large for
-  // part buffers.  Sixteen lanes work on a candidate.
+  // takes; a piece costs its tiles, 0.8 of them with one row tile, 1.5 more,
+  // and what writing and joining its part takes); no splits in calls that
+  // fill the device, or are too large for part buffers.  Sixteen lanes work on
+  // a candidate.
   if (split) {
     const float heads = (float)p.hkv, sms = (float)p.sms;
     const int least = max(kExMinPiece, (int)ceilf((float)s_sum * heads / (kExItemsPerSm * sms)));
@@ -474,7 +484,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     auto piece_cost = [&](int u, float& np) {
       const float tiles = (float)(tiles_of[u] & ~(1 << 30));
       np = fmaxf(1.f, ceilf(tiles * inv - 1e-4f));
-      return (tiles_of[u] >> 30 ? 1.f : 0.6f) * (__fdividef(tiles, np) + 1.5f);
+      return (tiles_of[u] >> 30 ? 1.f : 0.8f) * __fdividef(tiles, np) + 1.5f + (np > 1.f ? part_of[u] : 0.f);
     };
     float load = 0.f, big = 0.f, n_big = 0.f, top = 0.f, np;
     for (int u = tid & 15; u < n_units; u += 16) top = fmaxf(top, piece_cost(u, np));
@@ -604,6 +614,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   } else {
     walk([&](int unit, int tiles, int2 src, int skip) { emit(unit, tiles, src, skip, 0, 1, true); });
   }
+  __syncthreads();
   if (tid == 0) {
     hdr[kHSeq] = p.n_seq;
     hdr[kHBlocks] = p.max_blocks;
@@ -613,6 +624,7 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
     hdr[kHTokens] = p.n_tokens;
     hdr[kHItems] = min(n_items, p.w.max_items);
     hdr[kHCounter] = 0;
+    hdr[kHParts] = s_parts;
     hdr[kHUnits] = min(own_units, p.w.max_units);
     hdr[kHMagic] = kExMagic;
   }
@@ -621,9 +633,11 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
 // -------------------------------------------------------------- attention ---
 struct ExParams {
   ExWorkspace w;
-  const int32_t* table;
+  const int32_t *table, *tok_off, *seq_len;
   uint16_t* out;
   uint32_t* status;
+  uint32_t* claims;   // DIRECT: the pool's claim counter and count of CTAs that are through, both 0 between calls;
+                      // nullptr where the grid holds every item
   int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows;
   float scale_log2;
 };
@@ -748,7 +762,10 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-template <int D>
+// DIRECT (small calls, at most 32 sequences): no plan; the TMA warp makes each
+// item from the offsets and lengths, a unit over its whole key range, and the
+// result is written without parts.
+template <int D, bool DIRECT>
 __global__ void __launch_bounds__(kExThreads, 1)
 extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ CUtensorMap tq,
                    const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
@@ -802,9 +819,6 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;");
   const int tt = kExTile / p.g;
-  const bool plan_ok = ex_plan_ok(p.w.hdr, p.n_seq, p.max_blocks, p.g, p.hkv, p.causal, p.n_tokens);
-  if (!plan_ok && threadIdx.x == 0) set_err(p.status, KVS_DEVERR_PLAN);
-  const int n_claims = plan_ok ? min(p.w.hdr[kHItems], p.w.max_items) * p.hkv : 0;
   auto stop = [&]() { return __any_sync(0xffffffffu, s_abort != 0); };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
     const bool ok = mbar_wait_bounded(bar, parity, p.status);
@@ -819,6 +833,35 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
     int armed = -1, q_armed = 0;
     int claim = blockIdx.x;
     bool ok = true;
+    int n_claims = 0;
+    int4 seq{};          // DIRECT: lane a holds sequence a ({first row, rows, keys}) and the units up to its last
+    int upto = 0;
+    const int tu = 2 * tt;
+    if constexpr (DIRECT) {
+      bool bad = false;
+      if (lane < p.n_seq) {
+        const int t0 = __ldg(p.tok_off + lane), t1 = __ldg(p.tok_off + lane + 1), n = __ldg(p.seq_len + lane);
+        bad = t0 < 0 || t1 < t0 || t1 > p.n_tokens;
+        const int most = p.max_blocks * 16;
+        if ((n < 0 || n > most) && blockIdx.x == 0) set_err(p.status, KVS_DEVERR_SEQ_LEN);
+        seq = make_int4(t0, t1 - t0, min(max(n, 0), most), 0);
+        upto = (seq.y + tu - 1) / tu;
+      }
+      if (__any_sync(0xffffffffu, bad)) {   // as in the plan: nothing is written
+        if (lane == 0 && blockIdx.x == 0) set_err(p.status, KVS_DEVERR_JOB);
+        upto = 0;
+      }
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int v = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += v;
+      }
+      n_claims = __shfl_sync(0xffffffffu, upto, 31) * p.hkv;
+    } else {
+      const bool plan_ok = ex_plan_ok(p.w.hdr, p.n_seq, p.max_blocks, p.g, p.hkv, p.causal, p.n_tokens);
+      if (!plan_ok && lane == 0) set_err(p.status, KVS_DEVERR_PLAN);
+      n_claims = plan_ok ? min(p.w.hdr[kHItems], p.w.max_items) * p.hkv : 0;
+    }
     auto copy = [&](const CUtensorMap* map, bool is_v, int id, int head) {
       // stage n: lanes k < 8 copy block k of the tile; a block without an id
       // lies behind the slab's last row and arrives as zeros
@@ -849,12 +892,31 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
       if (!end) {
         const int item = claim / p.hkv;
         head = claim - item * p.hkv;
-        const int4* src = reinterpret_cast<const int4*>(p.w.items + item);
-        int4* dst = reinterpret_cast<int4*>(&it);
-        dst[0] = __ldg(src);
-        dst[1] = __ldg(src + 1);
-        dst[2] = __ldg(src + 2);
-        if (lane == 0) next = (int)gridDim.x + atomicAdd(p.w.hdr + kHCounter, 1);
+        if constexpr (DIRECT) {
+          const int a = __ffs(__ballot_sync(0xffffffffu, upto > item)) - 1;   // the first sequence with a unit behind it
+          const int t0 = __shfl_sync(0xffffffffu, seq.x, a), rows = __shfl_sync(0xffffffffu, seq.y, a);
+          const int keys = __shfl_sync(0xffffffffu, seq.z, a), end = __shfl_sync(0xffffffffu, upto, a);
+          const int i = end - 1 - item;   // the last unit, which sees most, first
+          it.t0 = t0 + i * tu;
+          it.n_tok = min(tu, rows - i * tu);
+          it.seq = a;
+          it.kv1 = ex_own_tiles(make_int4(t0, rows, keys, 0), i, tu, p.causal, 0);
+          it.lim0 = p.causal ? keys - rows + i * tu + 1 : keys;
+          it.step = p.causal;
+          it.kv_end = keys;
+          it.part = -1;
+          if (p.claims == nullptr)
+            next = n_claims;   // one round: every CTA has one item at most
+          else if (lane == 0)
+            next = (int)gridDim.x + (int)atomicAdd(p.claims, 1u);
+        } else {
+          const int4* src = reinterpret_cast<const int4*>(p.w.items + item);
+          int4* dst = reinterpret_cast<int4*>(&it);
+          dst[0] = __ldg(src);
+          dst[1] = __ldg(src + 1);
+          dst[2] = __ldg(src + 2);
+          if (lane == 0) next = (int)gridDim.x + atomicAdd(p.w.hdr + kHCounter, 1);
+        }
       }
       if (lane == 0) {
         work[slot].it = it;
@@ -1210,6 +1272,8 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
     tc_fence_after();
     tmem_dealloc(tmem, kExCols);
   }
+  // the last CTA through (nobody claims any more) clears the claim counter
+  if (DIRECT && p.claims && threadIdx.x == 0 && atomicInc(p.claims + 1, gridDim.x - 1) == gridDim.x - 1) atomicExch(p.claims, 0u);
 }
 
 // ------------------------------------------------------------------ merge ---
@@ -1244,6 +1308,7 @@ __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant
     }
     return x;
   };
+  if (p.w.hdr[kHParts] == 0) return;   // every row has been written by the attention
   for (int i = blockIdx.x; i < n_units; i += gridDim.x) {
     const ExUnit u = p.w.units[i];
     if (u.part < 0 && u.sh_unit < 0) continue;   // written by the attention itself
@@ -1409,20 +1474,55 @@ cudaError_t ex_launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem
   return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 
+// Whether the whole attention goes in one launch (DIRECT), with nothing split
+// or shared; the rule goes by what the host knows.
+//  * Short tables and at most two rounds of units: a plan and a merge take
+//    longer than they save (4 sequences of 24 blocks, head_dim 64: 19.0 us planned,
+//    8.9 in one launch; 12 sequences of 94 blocks: 28.8 and 22.1; 8 items of
+//    16 key tiles would take 22 planned and 29 in one launch).
+//  * Chunks of at least a unit on the mean, which share nothing worth while,
+//    that fill the SMs without splits (8 x 256 rows after 1,800 tokens, 8 KV
+//    heads: 76 and 64 us; 2,048 rows after 2,048 tokens, 32 KV heads: 110 and
+//    98), unless the last round would be mostly empty and long (32 x 96 rows
+//    after 5,400 tokens, 2 KV heads: 146 and 160 us).  Beyond kExDirectRounds
+//    rounds the plan's order by length is worth more than its time.
+bool ex_direct(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks, int g) {
+  if (pool->test_flags & KVS_TEST_EXTEND_PLANNED) return false;
+  const long long tu = ex_tokens_per_unit(g), whole = n_tokens / tu, hkv = pool->desc.num_kv_heads, sms = pool->num_sms;
+  if (n_seq > 32) return false;
+  const bool small = max_blocks <= kExDirectBlocks && (whole + n_seq) * hkv <= 2 * sms;
+  const long long likely = (2 * whole + n_seq) * hkv / 2, rounds = (likely + sms - 1) / sms;   // half a unit left per sequence
+  const bool even = 4 * likely >= 3 * rounds * sms || max_blocks <= kExDirectShort;
+  const bool full = n_tokens >= n_seq * tu && whole * hkv >= sms && rounds <= kExDirectRounds && even;
+  return small || full;
+}
+
+template <int D>
+kvs_status ex_direct_run(kvs_pool* pool, int layer, const ExParams& p, const CUtensorMap& tq, long long max_claims, cudaStream_t stream) {
+  if (!smem_limit_once<extend_attn_kernel<D, true>>(ex_smem<D>(), pool->device))
+    return fail(KVS_ERR_CUDA, "extend_attn: cannot raise the shared-memory limit");
+  const unsigned grid = (unsigned)std::min<long long>(pool->num_sms, max_claims);
+  const CUtensorMap& tk = D == 128 ? pool->tk1[layer] : pool->tk[layer];
+  if (ex_launch(extend_attn_kernel<D, true>, dim3(grid), dim3(kExThreads), ex_smem<D>(), stream, p, tq, tk, pool->tv[layer]) != cudaSuccess)
+    return fail(KVS_ERR_CUDA, std::string("extend_attn: ") + cudaGetErrorString(cudaGetLastError()));
+  count_launch();
+  return check_launch("extend_attn");
+}
+
 template <int D>
 kvs_status ex_run(kvs_pool* pool, int layer, const ExParams& p, const CUtensorMap& tq, long long max_claims, cudaStream_t stream) {
-  if (!smem_limit_once<extend_attn_kernel<D>>(ex_smem<D>(), pool->device))
+  if (!smem_limit_once<extend_attn_kernel<D, false>>(ex_smem<D>(), pool->device))
     return fail(KVS_ERR_CUDA, "extend_attn: cannot raise the shared-memory limit");
   const unsigned grid = (unsigned)std::min<long long>(pool->num_sms, max_claims);
   const CUtensorMap& tk = D == 128 ? pool->tk1[layer] : pool->tk[layer];
   const CUtensorMap& tv = pool->tv[layer];
-  if (ex_launch(extend_attn_kernel<D>, dim3(grid), dim3(kExThreads), ex_smem<D>(), stream, p, tq, tk, tv) != cudaSuccess)
+  if (ex_launch(extend_attn_kernel<D, false>, dim3(grid), dim3(kExThreads), ex_smem<D>(), stream, p, tq, tk, tv) != cudaSuccess)
     return fail(KVS_ERR_CUDA, std::string("extend_attn: ") + cudaGetErrorString(cudaGetLastError()));
   count_launch();
-  // about 16 CTAs per SM over units, heads and blocks of sixteen rows
+  // about 8 CTAs per SM over units, heads and blocks of sixteen rows
   const unsigned units = (unsigned)std::min(p.w.max_units / 2, 4096);
   const long long most = std::min<long long>(32 / kExMergeRows, ((long long)p.n_tokens * p.g + 8 * kExMergeRows - 1) / (8 * kExMergeRows));
-  const unsigned z = (unsigned)std::clamp<long long>(16ll * pool->num_sms / ((long long)units * p.hkv), 1, most);
+  const unsigned z = (unsigned)std::clamp<long long>(8ll * pool->num_sms / ((long long)units * p.hkv), 1, most);
   if (ex_launch(extend_merge_kernel<D>, dim3(units, (unsigned)p.hkv, z), dim3(256), 0, stream, p) != cudaSuccess)
     return fail(KVS_ERR_CUDA, std::string("extend_attn merge: ") + cudaGetErrorString(cudaGetLastError()));
   count_launch();
@@ -1456,6 +1556,7 @@ extern "C" kvs_status kvs_extend_plan(kvs_pool* pool, const int32_t* tok_off_dev
   p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
   if (ws_bytes < p.w.bytes) return fail(KVS_ERR_CAPACITY, "extend_plan: workspace too small");
   if (kvs_status st = check_pool_device(pool, "extend_plan"); st != KVS_OK) return st;
+  if (ex_direct(pool, n_tokens, n_seq, max_blocks, g)) return KVS_OK;
   p.tok_off = tok_off_dev;
   p.seq_len = seq_len_dev;
   p.table = block_table_dev;
@@ -1508,6 +1609,8 @@ extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, con
   if (ws_bytes < p.w.bytes) return fail(KVS_ERR_CAPACITY, "extend_attn: workspace too small");
   if (kvs_status st = check_pool_device(pool, "extend_attn"); st != KVS_OK) return st;
   p.table = block_table_dev;
+  p.tok_off = tok_off_dev;
+  p.seq_len = seq_len_dev;
   p.out = static_cast<uint16_t*>(out_dev);
   p.status = pool->status;
   p.n_tokens = n_tokens;
@@ -1523,6 +1626,12 @@ extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, con
   CUtensorMap tq;
   if (!ex_query_map(&tq, q_dev, n_tokens, g, d.num_kv_heads, d.head_dim, q_stride))
     return fail(KVS_ERR_CUDA, "extend_attn: cuTensorMapEncodeTiled failed for q");
+  if (ex_direct(pool, n_tokens, n_seq, max_blocks, g)) {
+    const long long claims = (n_tokens / ex_tokens_per_unit(g) + n_seq) * (long long)d.num_kv_heads;
+    p.claims = claims > pool->num_sms ? pool->status + 2 : nullptr;
+    return d.head_dim == 128 ? ex_direct_run<128>(pool, layer, p, tq, claims, stream)
+                             : ex_direct_run<64>(pool, layer, p, tq, claims, stream);
+  }
   const long long max_claims = (long long)p.w.max_items * d.num_kv_heads;
   return d.head_dim == 128 ? ex_run<128>(pool, layer, p, tq, max_claims, stream)
                            : ex_run<64>(pool, layer, p, tq, max_claims, stream);

@@ -25,7 +25,9 @@ def f64(t):
 class Batch:
     """Sequences of given new rows and lengths; groups share their leading
     `prefix` tokens (whole blocks).  Blocks behind a sequence's last token and
-    rows of the last block behind it hold NaN."""
+    rows of the last block behind it hold NaN.  The pool takes the planned path
+    for every call; check() runs the library's own choice too (small calls: one
+    launch without a plan)."""
 
     def __init__(self, new, lens, hq, hkv, d, prefix=0, groups=None, seed=0, pad=0, qscale=1.0):
         self.new, self.lens = np.array(new), np.array(lens)
@@ -57,6 +59,7 @@ class Batch:
         self.hq, self.hkv, self.d = hq, hkv, d
         self.pool = K.kvs_pool_create(1, hkv, d, 16, K.KVS_DTYPE_BF16, cap, max(self.n, 1), [self.k], [self.v])
         self.scale = d ** -0.5
+        K.kvs_pool_set_test_flags(self.pool, K.KVS_TEST_EXTEND_PLANNED)
 
     def dev(self):
         return H.i32(self.off), H.i32(self.table), H.i32(self.lens)
@@ -75,7 +78,11 @@ class Batch:
         return out
 
     def check(self, causal, out=None):
-        out = self.run(causal) if out is None else out
+        if out is None:
+            K.kvs_pool_set_test_flags(self.pool, 0)
+            self.check(causal, self.run(causal))
+            K.kvs_pool_set_test_flags(self.pool, K.KVS_TEST_EXTEND_PLANNED)
+            out = self.run(causal)
         k, v = np.nan_to_num(f64(self.k), posinf=0.0), np.nan_to_num(f64(self.v), posinf=0.0)
         exp, mag, big = OE.extend_attention(f64(self.q), k, v, self.table, self.off, self.lens, 16, self.scale, causal)
         rows = ~np.isnan(exp[:, 0, 0])
@@ -314,6 +321,7 @@ def test_plan_serves_layers_graphs_and_streams():
     b = Batch([4, 9, 2, 30], [700, 650, 600, 900], hq, hkv, d, prefix=512)
     k2, v2 = randn(31, *b.k.shape), randn(32, *b.v.shape)
     pool = K.kvs_pool_create(2, hkv, d, 16, K.KVS_DTYPE_BF16, b.k.shape[0], b.n, [b.k, k2], [b.v, v2])
+    K.kvs_pool_set_test_flags(pool, K.KVS_TEST_EXTEND_PLANNED)
     off, tab, lens = b.dev()
     ws = b.ws()
     ref = b.run(True)
@@ -369,8 +377,10 @@ def test_plan_of_another_call_is_refused():
     b.check(True, out=out)
 
 
-def test_bad_tables_lengths_and_offsets_are_flagged():
+@pytest.mark.parametrize("flags", [0, K.KVS_TEST_EXTEND_PLANNED])
+def test_bad_tables_lengths_and_offsets_are_flagged(flags):
     b = Batch([4, 9], [70, 65], 8, 2, 64)
+    K.kvs_pool_set_test_flags(b.pool, flags)
     out = b.run(True)
     good = b.table.copy()
     # unmapped and out-of-range ids count as zero keys and values
@@ -402,6 +412,52 @@ def test_bad_tables_lengths_and_offsets_are_flagged():
         torch.cuda.synchronize()
         assert K.kvs_pool_check(b.pool) & K.KVS_DEVERR_JOB
         assert (got == 7).all()
+
+
+@pytest.mark.parametrize("n, new, mb", [(32, 1, 96), (31, 3, 90), (1, 64, 96), (32, 0, 3), (7, 40, 95)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_calls_of_one_launch(n, new, mb, causal):
+    """The largest calls that run without a plan, and a plan that such a call
+    does not need: the steps apart give the same bits."""
+    r = np.random.default_rng(n)
+    rows = np.full(n, new)
+    rows[0] = max(new, 1)
+    rows[n // 2:n // 2 + 1] += 1
+    lens = np.maximum(r.integers(0, 16 * mb + 1, n), 0)
+    lens[-1] = 16 * mb
+    b = Batch(rows, lens, 8, 2, 64, seed=n)
+    b.mb, b.table = mb, np.ascontiguousarray(b.table[:, :mb])
+    K.kvs_pool_set_test_flags(b.pool, 0)
+    before = K.kvs_launch_count()
+    out = b.run(causal)
+    assert K.kvs_launch_count() == before + 1
+    b.check(causal, out)
+    off, tab, lens = b.dev()
+    ws, again = b.ws(), torch.full_like(out, 7.0)
+    K.kvs_extend_plan(b.pool, b.T, off, 8, tab, b.mb, lens, b.n, causal, ws)
+    assert (ws == 255).all()
+    K.kvs_extend_attn_planned(b.pool, 0, b.q, b.T, off, 8, tab, b.mb, lens, b.n, causal, b.scale, again, ws)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("new, ctx, hq, hkv, d", [([1800, 900, 1300], [100, 0, 1111], 16, 4, 64), ([700, 64, 0, 1500], [0, 0, 50, 3], 8, 8, 128)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_long_chunks_of_one_launch(new, ctx, hq, hkv, d, causal):
+    """Chunks that fill the device without splits: claims beyond the first go
+    through the pool's counter, which is clear again for the next call."""
+    lens = [n + c for n, c in zip(new, ctx)]
+    b = Batch(new, lens, hq, hkv, d, seed=3, pad=2)
+    planned = b.run(causal)
+    K.kvs_pool_set_test_flags(b.pool, 0)
+    before = K.kvs_launch_count()
+    out = b.run(causal)
+    assert K.kvs_launch_count() == before + 1
+    for _ in range(2):
+        assert torch.equal(out, b.run(causal))
+    assert (out[-2:] == 7).all()
+    # two results within their roundings (P and output, 2^-8 each) of one value
+    assert (out.float() - planned.float()).abs().max() <= 2.0 ** -6 * float(b.v[torch.isfinite(b.v)].abs().max())
+    check_sequences(b, out, [len(new) - 3], causal)
 
 
 def test_refusals():
