@@ -27,7 +27,8 @@
 // which lie side by side in the packed batch, into common tiles over the
 // common part ("shared" items) and go on alone behind it.  Rows with more than
 // one part leave (m, l, O) in fp32, and a merge kernel joins them in a fixed
-// order.  CTAs claim items (longest first) from a counter in the plan.
+// order.  CTAs claim items (longest first) from a counter in the plan.  Calls with
+// nothing to split or share go without a plan, in one launch (ex_direct).
 #include <algorithm>
 #include <cmath>
 
@@ -267,7 +268,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   __shared__ int sums[2][kPlanThreads / 32];
   __shared__ int hist[256];
   __shared__ float cost[kPlanCands];
-  __shared__ int s_parts, s_most, s_sum;
+  __shared__ int s_parts, s_most;
+  __shared__ unsigned long long s_sum;
   __shared__ int tiles_of[kPlanUnits];
   __shared__ float part_of[kPlanUnits];   // what a part of the unit costs, in key tiles
   __shared__ int2 src_of[kPlanUnits];   // {sequence, or ~run, index in it}
@@ -285,7 +287,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   int* hdr = p.w.hdr;
   hist[tid] = 0;
   if (tid == 0) {
-    s_parts = s_sum = 0;
+    s_parts = 0;
+    s_sum = 0;
     s_most = 1;
   }
   pdl_enter();
@@ -424,7 +427,8 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   // whether a unit fills more than one row tile
   auto two_tiles = [&](int2 src) { return (src.x >= 0 ? seq[src.x].y : run[~src.x].w) - src.y * tu > tt; };
   {
-    int most = 1, sum = 0;
+    int most = 1;
+    unsigned long long sum = 0;
     if (split) {   // few units: a thread each, its sequence or run found by bisection
       for (int u = tid; u < n_units; u += kPlanThreads) {
         const bool own = u < own_units;
@@ -636,8 +640,6 @@ struct ExParams {
   const int32_t *table, *tok_off, *seq_len;
   uint16_t* out;
   uint32_t* status;
-  uint32_t* claims;   // DIRECT: the pool's claim counter and count of CTAs that are through, both 0 between calls;
-                      // nullptr where the grid holds every item
   int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows;
   float scale_log2;
 };
@@ -762,9 +764,9 @@ __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, i
       : "memory");
 }
 
-// DIRECT (small calls, at most 32 sequences): no plan; the TMA warp makes each
-// item from the offsets and lengths, a unit over its whole key range, and the
-// result is written without parts.
+// DIRECT (at most 32 sequences): no plan; the TMA warp makes each item from
+// the offsets and lengths, a unit over its whole key range, the CTAs take the
+// items in turn and write the result without parts.
 template <int D, bool DIRECT>
 __global__ void __launch_bounds__(kExThreads, 1)
 extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ CUtensorMap tq,
@@ -905,10 +907,9 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
           it.step = p.causal;
           it.kv_end = keys;
           it.part = -1;
-          if (p.claims == nullptr)
-            next = n_claims;   // one round: every CTA has one item at most
-          else if (lane == 0)
-            next = (int)gridDim.x + (int)atomicAdd(p.claims, 1u);
+          // rounds over the CTAs in alternating order, so that whoever had a
+          // long item takes a short one (a causal chunk's units get shorter)
+          next = claim + (ni & 1 ? 2 * (int)blockIdx.x + 1 : 2 * (int)(gridDim.x - blockIdx.x) - 1);
         } else {
           const int4* src = reinterpret_cast<const int4*>(p.w.items + item);
           int4* dst = reinterpret_cast<int4*>(&it);
@@ -1272,8 +1273,6 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
     tc_fence_after();
     tmem_dealloc(tmem, kExCols);
   }
-  // the last CTA through (nobody claims any more) clears the claim counter
-  if (DIRECT && p.claims && threadIdx.x == 0 && atomicInc(p.claims + 1, gridDim.x - 1) == gridDim.x - 1) atomicExch(p.claims, 0u);
 }
 
 // ------------------------------------------------------------------ merge ---
@@ -1628,7 +1627,6 @@ extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, con
     return fail(KVS_ERR_CUDA, "extend_attn: cuTensorMapEncodeTiled failed for q");
   if (ex_direct(pool, n_tokens, n_seq, max_blocks, g)) {
     const long long claims = (n_tokens / ex_tokens_per_unit(g) + n_seq) * (long long)d.num_kv_heads;
-    p.claims = claims > pool->num_sms ? pool->status + 2 : nullptr;
     return d.head_dim == 128 ? ex_direct_run<128>(pool, layer, p, tq, claims, stream)
                              : ex_direct_run<64>(pool, layer, p, tq, claims, stream);
   }

@@ -443,8 +443,8 @@ def test_calls_of_one_launch(n, new, mb, causal):
 @pytest.mark.parametrize("new, ctx, hq, hkv, d", [([1800, 900, 1300], [100, 0, 1111], 16, 4, 64), ([700, 64, 0, 1500], [0, 0, 50, 3], 8, 8, 128)])
 @pytest.mark.parametrize("causal", [True, False])
 def test_long_chunks_of_one_launch(new, ctx, hq, hkv, d, causal):
-    """Chunks that fill the device without splits: claims beyond the first go
-    through the pool's counter, which is clear again for the next call."""
+    """Chunks that fill the device without splits: several rounds of items over
+    the CTAs, the same result on every call."""
     lens = [n + c for n, c in zip(new, ctx)]
     b = Batch(new, lens, hq, hkv, d, seed=3, pad=2)
     planned = b.run(causal)
