@@ -29,6 +29,18 @@
 // one part leave (m, l, O) in fp32, and a merge kernel joins them in a fixed
 // order.  CTAs claim items (longest first) from a counter in the plan.  Calls with
 // nothing to split or share go without a plan, in one launch (ex_direct).
+//
+// What bounds it: long chunks the tensor cores and, on their way, shared memory.
+// The four products of a tile pair take 2,048 cycles of the tensor cores, and
+// the reads of their operands (S: both from shared memory) with the arriving
+// tiles fill shared memory for about as long, so neither can wait for the
+// other; a pair takes about 3,100 cycles.  8,192 rows after 8,192 tokens, 32
+// heads of 128: 1.13 to 1.16 ms, 1,430 to 1,460 TFLOP/s.  16 chunks over one
+// document of 8,192 states: 332 us, 1,300 TFLOP/s.  Few rows over long
+// contexts are bound by memory and the items' starts and ends (64 sequences of
+// 3 to 8 rows over 8,192 shared and 1,000 to 6,100 own tokens: 218 us, 4.6
+// TB/s), calls without a plan by one chain of key tiles (12 rows over 1,300
+// states: 22 us).
 #include <algorithm>
 #include <cmath>
 
@@ -262,8 +274,9 @@ __device__ __forceinline__ int ex_candidate(int most, int least, int i) {
 }
 
 // One CTA: runs of sequences, units, piece length, items sorted by cost.  A
-// chain of short dependent steps bounds it (6 to 9 us with 1,024 threads and
-// a piece per loop step, 3 to 5 us so).
+// chain of short dependent steps bounds it: 4.4 us for one sequence, 8 to 9 us
+// with the search for common parts of 32 or 64 long tables (1,024 threads and a
+// piece per loop step: 7 and 12 us).
 __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_constant__ ExPlanParams p) {
   __shared__ int sums[2][kPlanThreads / 32];
   __shared__ int hist[256];
@@ -1281,7 +1294,8 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
 // gridDim.z-th sixteen rows of it, a warp two rows at a time.  The parts lie
 // in L2 and the chain of loads bounds it: up to four parts of both rows are
 // loaded at once; with more, 32 lanes take the factors of 32 parts and four
-// parts are in flight.
+// parts are in flight.  2,800 rows of 16 heads with two to four parts: 18 us
+// alone (71 us with a row per warp, parts one by one).
 template <int D>
 __global__ void __launch_bounds__(256) extend_merge_kernel(const __grid_constant__ ExParams p) {
   pdl_enter();
@@ -1482,7 +1496,7 @@ cudaError_t ex_launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem
 //  * Chunks of at least a unit on the mean, which share nothing worth while,
 //    that fill the SMs without splits (8 x 256 rows after 1,800 tokens, 8 KV
 //    heads: 76 and 64 us; 2,048 rows after 2,048 tokens, 32 KV heads: 110 and
-//    98), unless the last round would be mostly empty and long (32 x 96 rows
+//    88), unless the last round would be mostly empty and long (32 x 96 rows
 //    after 5,400 tokens, 2 KV heads: 146 and 160 us).  Beyond kExDirectRounds
 //    rounds the plan's order by length is worth more than its time.
 bool ex_direct(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks, int g) {
