@@ -30,13 +30,12 @@
 // order.  CTAs claim items (longest first) from a counter in the plan.  Calls with
 // nothing to split or share go without a plan, in one launch (ex_direct).
 //
-// What bounds it: long chunks the tensor cores and, on their way, shared memory.
-// The four products of a tile pair take 2,048 cycles of the tensor cores, and
-// the reads of their operands (S: both from shared memory) with the arriving
-// tiles fill shared memory for about as long, so neither can wait for the
-// other; a pair takes about 3,100 cycles.  8,192 rows after 8,192 tokens, 32
-// heads of 128: 1.13 to 1.16 ms, 1,430 to 1,460 TFLOP/s.  16 chunks over one
-// document of 8,192 states: 332 us, 1,300 TFLOP/s.  Few rows over long
+// What bounds it: in long chunks the chain S, softmax, P V of a row tile.  The
+// four products of a tile pair take 2,048 cycles of the tensor cores, a tile's
+// softmax 1,560, and two chains share the SM: a pair takes about 3,100
+// cycles.  8,192 rows after 8,192 tokens, 32 heads of 128: 1.13 to 1.16 ms,
+// 1,430 to 1,460 TFLOP/s.  16 chunks over one document of 8,192 states: 332 us,
+// 1,300 TFLOP/s.  Few rows over long
 // contexts are bound by memory and the items' starts and ends (64 sequences of
 // 3 to 8 rows over 8,192 shared and 1,000 to 6,100 own tokens: 218 us, 4.6
 // TB/s), calls without a plan by one chain of key tiles (12 rows over 1,300

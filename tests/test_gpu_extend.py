@@ -460,6 +460,32 @@ def test_long_chunks_of_one_launch(new, ctx, hq, hkv, d, causal):
     check_sequences(b, out, [len(new) - 3], causal)
 
 
+@pytest.mark.parametrize("new, ctx, hq, hkv", [([2600], [77], 32, 32), ([900, 2000], [1000, 0], 40, 8), ([3500], [0], 24, 4)])
+@pytest.mark.parametrize("causal", [True, False])
+def test_long_chunks_against_sampled_rows(new, ctx, hq, hkv, causal):
+    """Long chunks of head_dim 128 in one launch: several rounds, row tiles
+    that end anywhere, key ends inside blocks, NaN behind them."""
+    lens = [n + c for n, c in zip(new, ctx)]
+    b = Batch(new, lens, hq, hkv, 128, seed=6, pad=3)
+    planned = b.run(causal)
+    K.kvs_pool_set_test_flags(b.pool, 0)
+    before = K.kvs_launch_count()
+    out = b.run(causal)
+    assert K.kvs_launch_count() == before + 1
+    assert torch.equal(out, b.run(causal))
+    assert (out[-3:] == 7).all()
+    # two results within their roundings (P and output, 2^-8 each) of one value
+    assert (out.float() - planned.float()).abs().max() <= 2.0 ** -6 * float(b.v[torch.isfinite(b.v)].abs().max())
+    k, v = np.nan_to_num(f64(b.k)), np.nan_to_num(f64(b.v), posinf=0.0)
+    for a in range(len(new)):
+        ids = b.table[a, : -(-int(b.lens[a]) // 16)]
+        for j in [0, new[a] - 1, *np.random.default_rng(a).integers(0, new[a], 12)]:
+            t, n = int(b.off[a]) + int(j), int(b.lens[a]) - new[a] + int(j) + 1 if causal else int(b.lens[a])
+            exp, mag, big = OE.extend_attention(f64(b.q[t:t + 1]), k[ids], v[ids], np.arange(len(ids))[None], [0, 1], [n], 16,
+                                                b.scale, False)
+            assert_attention(f64(out[t:t + 1]), exp, mag, big, b.d)
+
+
 def test_refusals():
     b = Batch([4, 9], [70, 65], 8, 2, 64)
     off, tab, lens = b.dev()
