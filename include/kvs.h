@@ -538,7 +538,9 @@ kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* tok_off_dev,
  * Requires n_q_heads % num_kv_heads == 0, a group of at most 16 query heads
  * per KV head and a BF16 pool.  Stored keys and values of tokens below
  * seq_len are finite; what the pool holds behind them (the rest of a block)
- * is never used.  Bad block ids (KVS_DEVERR_BLOCK_ID) count as zero keys and
+ * is never used.  Scores and sums are float32, the weights that multiply the
+ * values have 15 significant bits or more, the result is rounded once, to
+ * bf16.  Bad block ids (KVS_DEVERR_BLOCK_ID) count as zero keys and
  * values; seq_len outside [0, max_blocks * 16] (KVS_DEVERR_SEQ_LEN) is
  * clamped; with offsets outside [0, n_tokens] or decreasing ones
  * (KVS_DEVERR_JOB) nothing is written.

@@ -15,10 +15,16 @@
 //    swizzle) feeds four 128 x 128 x head_dim products.
 //  * S = Q K^T lands in tensor memory; two warpgroups (one per tile, one row
 //    per thread, so the softmax needs no shuffles) turn it into P = 2^(s - m)
-//    as bf16 in the same columns, and O += P V takes P from tensor memory.
+//    in the same columns, and O += P V takes P from tensor memory.
 //    While one tile's softmax runs, the tensor cores work for the other tile.
-//  * P is rounded to bf16 (relative error at most 2^-8 per weight; the output's own
-//    rounding is of that size); l sums the unrounded weights; O, m, l are fp32.
+//  * P is held as two bf16 parts, as decode attention holds it: the upper 16 bits
+//    of the float32 weight and the remainder, rounded (2^-15 of a weight is
+//    lost), so that O += P V is two products; the parts fill the columns that S
+//    took.  With one rounded part the result was 2.0e-3 to 2.3e-3 (relative L2)
+//    from 64 bits, beyond the 2e-3 that every attention here keeps; with two it
+//    is the 1.7e-3 of the bf16 output.  It costs a third of the rate of long
+//    chunks (8,192 rows after 8,192 tokens, 32 heads: 1,160 us with one part),
+//    a sixth in calls of few rows.  l sums the whole weights; O, m, l are fp32.
 //  * Warp 8 issues the MMAs, warp 9 the TMA copies and the work claims.
 //
 // The plan lists the work as items (row tile pair, block table, key range).
@@ -30,16 +36,15 @@
 // order.  CTAs claim items (longest first) from a counter in the plan.  Calls with
 // nothing to split or share go without a plan, in one launch (ex_direct).
 //
-// What bounds it: in long chunks the chain S, softmax, P V of a row tile.  The
-// four products of a tile pair take 2,048 cycles of the tensor cores, a tile's
-// softmax 1,560, and two chains share the SM: a pair takes about 3,100
-// cycles.  8,192 rows after 8,192 tokens, 32 heads of 128: 1.13 to 1.16 ms,
-// 1,430 to 1,460 TFLOP/s.  16 chunks over one document of 8,192 states: 332 us,
-// 1,300 TFLOP/s.  Few rows over long
-// contexts are bound by memory and the items' starts and ends (64 sequences of
-// 3 to 8 rows over 8,192 shared and 1,000 to 6,100 own tokens: 218 us, 4.6
-// TB/s), calls without a plan by one chain of key tiles (12 rows over 1,300
-// states: 22 us).
+// What bounds it: in long chunks the products, and the chain S, softmax, P V of a
+// row tile.  The six products of a tile pair take 3,072 cycles of the tensor
+// cores (2,048 of them P V's two parts), and two chains share the SM: a pair
+// takes about 4,600.  Replayed in a CUDA graph: 8,192 rows after 8,192 tokens,
+// 32 heads of 128: 1.56 ms, 1,055 TFLOP/s; 16 chunks over one document of 8,192
+// states: 440 us, 980 TFLOP/s.  Few rows over long contexts are bound by the
+// items' chains, starts and ends (64 sequences of 3 to 8 rows over 8,192 shared
+// and 1,000 to 6,100 own tokens: 260 us, 3.8 TB/s), calls without a plan by one
+// chain of key tiles (12 rows over 1,300 states: 25 us).
 #include <algorithm>
 #include <cmath>
 
@@ -54,10 +59,10 @@ namespace {
 
 // Two softmax warpgroups; MMA warp, TMA warp and two idle ones that complete
 // their warpgroup.  384 threads start with 168 registers each (64,512 in all);
-// the softmax threads, which hold a row's 128 scores, take 208 and the others
-// 88: 256 * 208 + 128 * 88 = 64,512.
+// the softmax threads, which hold a row's 128 scores, take 216 (with 208 they
+// spill) and the others 72: 256 * 216 + 128 * 72 = 64,512.
 constexpr int kExThreads = 384;
-constexpr int kExRegsSoftmax = 208, kExRegsOther = 88;
+constexpr int kExRegsSoftmax = 216, kExRegsOther = 72;
 constexpr int kExTile = 128;             // keys of a tile, rows of a row tile
 constexpr int kExBlocks = kExTile / 16;  // pool blocks of a key tile
 constexpr int kExMagic = 0x45585431;
@@ -686,37 +691,34 @@ __device__ __forceinline__ int ex_tiles(const ExItem& it, int x, int tt) {
   return max(0, min((lim + kExTile - 1) / kExTile, it.kv1) - it.kv0);
 }
 
-__device__ __forceinline__ void tmem_ld64_issue(uint32_t taddr, uint32_t* r) {
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t* r) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x64.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,"
-      "%32,%33,%34,%35,%36,%37,%38,%39,%40,%41,%42,%43,%44,%45,%46,%47,"
-      "%48,%49,%50,%51,%52,%53,%54,%55,%56,%57,%58,%59,%60,%61,%62,%63}, [%64];"
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]),
-        "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]),
-        "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31]),
-        "=r"(r[32]), "=r"(r[33]), "=r"(r[34]), "=r"(r[35]), "=r"(r[36]), "=r"(r[37]), "=r"(r[38]), "=r"(r[39]),
-        "=r"(r[40]), "=r"(r[41]), "=r"(r[42]), "=r"(r[43]), "=r"(r[44]), "=r"(r[45]), "=r"(r[46]), "=r"(r[47]),
-        "=r"(r[48]), "=r"(r[49]), "=r"(r[50]), "=r"(r[51]), "=r"(r[52]), "=r"(r[53]), "=r"(r[54]), "=r"(r[55]),
-        "=r"(r[56]), "=r"(r[57]), "=r"(r[58]), "=r"(r[59]), "=r"(r[60]), "=r"(r[61]), "=r"(r[62]), "=r"(r[63])
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+        "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]),
+        "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]),
+        "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr)
       : "memory");
 }
 
 // Completes the loads issued before; the registers pass through the statement
 // so that nothing computed from them can move in front of it.
-__device__ __forceinline__ void tmem_ld64_wait(uint32_t* r) {
+__device__ __forceinline__ void tmem_ld32x2_wait(uint32_t* a, uint32_t* b) {
   asm volatile(
       "tcgen05.wait::ld.sync.aligned;"
-      : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-        "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-        "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
-        "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31]),
-        "+r"(r[32]), "+r"(r[33]), "+r"(r[34]), "+r"(r[35]), "+r"(r[36]), "+r"(r[37]), "+r"(r[38]), "+r"(r[39]),
-        "+r"(r[40]), "+r"(r[41]), "+r"(r[42]), "+r"(r[43]), "+r"(r[44]), "+r"(r[45]), "+r"(r[46]), "+r"(r[47]),
-        "+r"(r[48]), "+r"(r[49]), "+r"(r[50]), "+r"(r[51]), "+r"(r[52]), "+r"(r[53]), "+r"(r[54]), "+r"(r[55]),
-        "+r"(r[56]), "+r"(r[57]), "+r"(r[58]), "+r"(r[59]), "+r"(r[60]), "+r"(r[61]), "+r"(r[62]), "+r"(r[63])
+      : "+r"(a[0]), "+r"(a[1]), "+r"(a[2]), "+r"(a[3]), "+r"(a[4]), "+r"(a[5]), "+r"(a[6]), "+r"(a[7]),
+        "+r"(a[8]), "+r"(a[9]), "+r"(a[10]), "+r"(a[11]), "+r"(a[12]), "+r"(a[13]), "+r"(a[14]),
+        "+r"(a[15]), "+r"(a[16]), "+r"(a[17]), "+r"(a[18]), "+r"(a[19]), "+r"(a[20]), "+r"(a[21]),
+        "+r"(a[22]), "+r"(a[23]), "+r"(a[24]), "+r"(a[25]), "+r"(a[26]), "+r"(a[27]), "+r"(a[28]),
+        "+r"(a[29]), "+r"(a[30]), "+r"(a[31]),
+        "+r"(b[0]), "+r"(b[1]), "+r"(b[2]), "+r"(b[3]), "+r"(b[4]), "+r"(b[5]), "+r"(b[6]), "+r"(b[7]),
+        "+r"(b[8]), "+r"(b[9]), "+r"(b[10]), "+r"(b[11]), "+r"(b[12]), "+r"(b[13]), "+r"(b[14]),
+        "+r"(b[15]), "+r"(b[16]), "+r"(b[17]), "+r"(b[18]), "+r"(b[19]), "+r"(b[20]), "+r"(b[21]),
+        "+r"(b[22]), "+r"(b[23]), "+r"(b[24]), "+r"(b[25]), "+r"(b[26]), "+r"(b[27]), "+r"(b[28]),
+        "+r"(b[29]), "+r"(b[30]), "+r"(b[31])
       :
       : "memory");
 }
@@ -1019,9 +1021,9 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
       if (elect_one()) {
         const uint32_t b = v_lo + v.s * (kTile / 16);
 #pragma unroll
-        for (int kk = 0; kk < 4; ++kk)
-          ex_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 8u * (k0 + kk), b + (k0 + kk) * (kBlock / 16), kHi, idO,
-                    acc || kk > 0);
+        for (int kk = 0; kk < 8; ++kk)   // per 32 keys 16 columns of first parts, then 16 of second ones
+          ex_mma_ts(tmem + 256u + (uint32_t)D * x, tmem + 128u * x + 16u * k0 + 32u * (kk >> 2) + 8u * (kk >> 1 & 1) + 16u * (kk & 1),
+                    b + (k0 + (kk >> 1)) * (kBlock / 16), kHi, idO, acc || kk > 0);
         if (k0) umma_commit(&bars.pv_done[x]);
       }
       __syncwarp();
@@ -1126,36 +1128,36 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
       // there, but 0 * NaN is not)
       const int tail = it.kv_end - (it.kv0 + nt_all - 1) * kExTile;
       const bool fix_tail = nt == nt_all && (x == 0 || nt_other < nt_all) && tail < kExTile && (tail & 15);
-      // m: reference point of l and O; next: where it moves with the next tile
-      float m = -INFINITY, next = -INFINITY, l = 0.f;
+      float m = -INFINITY, l = 0.f;   // reference point of l and O, sum of the weights
       const float2 sc2 = make_float2(sl2, sl2);
       float2 sum0, sum1;
-      // s[0..31] = 2^(s - ref) of the 64 scores, packed in place; returns
-      // their maximum
-      auto half = [&](uint32_t* s, float ref) {
-        const float2 rf2 = make_float2(-ref, -ref);
-        float ma = -INFINITY, mb = -INFINITY;
+      // p[0..15] and p[16..31] = the two bf16 parts of 2^(s - ref) of 32 scores
+      auto weigh = [&](const uint32_t* s, uint32_t* p, float ref) {
+        const float2 rf2 = make_float2(-ref, -ref), neg = make_float2(-1.f, -1.f);
+        auto split = [&](float2 w, uint32_t& h, uint32_t& rest) {   // the remainder is exact
+          const uint32_t x = __float_as_uint(w.x), y = __float_as_uint(w.y);
+          h = __byte_perm(x, y, 0x7632);
+          const float2 r = __ffma2_rn(make_float2(__uint_as_float(x & 0xffff0000u), __uint_as_float(y & 0xffff0000u)), neg, w);
+          rest = pack_bf16(r.x, r.y);
+        };
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
+        for (int i = 0; i < 32; i += 4) {
           float2 a = make_float2(__uint_as_float(s[i]), __uint_as_float(s[i + 1]));
           float2 b = make_float2(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3]));
-          ma = fmaxf(ma, fmaxf(a.x, a.y));
-          mb = fmaxf(mb, fmaxf(b.x, b.y));
           a = __ffma2_rn(a, sc2, rf2);
           b = __ffma2_rn(b, sc2, rf2);
           a = make_float2(fast_exp2(a.x), fast_exp2(a.y));
           b = make_float2(fast_exp2(b.x), fast_exp2(b.y));
           sum0 = __fadd2_rn(sum0, a);
           sum1 = __fadd2_rn(sum1, b);
-          s[i / 2] = pack_bf16(a.x, a.y);
-          s[i / 2 + 1] = pack_bf16(b.x, b.y);
+          split(a, p[i / 2], p[16 + i / 2]);
+          split(b, p[i / 2 + 1], p[17 + i / 2]);
         }
-        return fmaxf(ma, mb);
       };
       auto most = [&](const uint32_t* s) {
         float a = -INFINITY, b = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < 64; i += 4) {
+        for (int i = 0; i < 32; i += 4) {
           a = fmaxf(a, fmaxf(__uint_as_float(s[i]), __uint_as_float(s[i + 1])));
           b = fmaxf(b, fmaxf(__uint_as_float(s[i + 2]), __uint_as_float(s[i + 3])));
         }
@@ -1164,41 +1166,37 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
       for (int j = 0; j < nt; ++j) {
         if (!wait(&bars.s_full[x], ns & 1)) { ok = false; break; }
         tc_fence_after();
-        uint32_t s0[64], s1[64];
-        tmem_ld64_issue(tS, s0);
-        tmem_ld64_wait(s0);
-        tmem_ld64_issue(tS + 64, s1);
+        uint32_t sa[32], sb[32], sc[32], sd[32], pa[32];
+        tmem_ld32_issue(tS, sa);
+        tmem_ld32_issue(tS + 32, sb);
+        tmem_ld32x2_wait(sa, sb);
+        tmem_ld32_issue(tS + 64, sc);
+        tmem_ld32_issue(tS + 96, sd);
         const int rem = lim - (it.kv0 + j) * kExTile;   // visible keys of this tile
         const bool masked = __any_sync(0xffffffffu, rem < kExTile && live);
-        // The weights are taken against the reference of the tiles before
-        // (exact for any reference), so the first half's exponentials do not
-        // wait for this tile's maximum; only a tile that exceeds it by 2^32,
-        // the first one and masked ones move it before they start.
-        const bool fresh = __any_sync(0xffffffffu, next == -INFINITY) || masked;
-        sum0 = sum1 = make_float2(0.f, 0.f);
-        float ref = next;
-        float mx = -INFINITY;
-        if (!fresh) mx = half(s0, ref);
-        tmem_ld64_wait(s1);
-        if (masked) {
+        auto mask = [&](uint32_t* v, int first) {
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            if (i >= rem) s0[i] = 0xff800000u;
-            if (i + 64 >= rem) s1[i] = 0xff800000u;
-          }
+          for (int i = 0; i < 32; ++i)
+            if (i + first >= rem) v[i] = 0xff800000u;
+        };
+        if (masked) {
+          mask(sa, 0);
+          mask(sb, 32);
         }
-        if (fresh) mx = most(s0);
-        mx = fmaxf(mx, most(s1)) * sl2;
-        if (fresh || __any_sync(0xffffffffu, mx > ref + 32.f)) {
-          if (!fresh) {
-            tmem_ld64_issue(tS, s0);
-            tmem_ld64_wait(s0);
-          }
-          if (next == -INFINITY || mx > next + 8.f) next = fmaxf(next, mx);
-          ref = next == -INFINITY ? 0.f : next;   // nothing visible yet: 2^(-inf - 0) = 0
-          sum0 = sum1 = make_float2(0.f, 0.f);
-          half(s0, ref);
+        float mx = fmaxf(most(sa), most(sb));
+        tmem_ld32x2_wait(sc, sd);
+        if (masked) {
+          mask(sc, 64);
+          mask(sd, 96);
         }
+        mx = fmaxf(mx, fmaxf(most(sc), most(sd))) * sl2;
+        const float next = mx > m + 8.f ? mx : m;
+        const float ref = next == -INFINITY ? 0.f : next;   // nothing visible yet: 2^(-inf - 0) = 0
+        sum0 = sum1 = make_float2(0.f, 0.f);
+        weigh(sa, pa, ref);
+        tmem_st32(tS, pa);
+        weigh(sb, pa, ref);
+        tmem_st32(tS + 32, pa);
         // a row whose reference moved rescales its O once the P V before is done
         const bool move = m != -INFINITY && next > m;
         if (__any_sync(0xffffffffu, move)) {
@@ -1216,7 +1214,6 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
           l *= f;
         }
         m = next;
-        tmem_st32(tS, s0);
         if (j == nt - 1 && fix_tail) {
           const int mv = n + 2 * j + 1;
           if (!wait(&bars.full[mv % ST], (mv / ST) & 1)) { ok = false; break; }
@@ -1231,10 +1228,11 @@ extend_attn_kernel(const __grid_constant__ ExParams p, const __grid_constant__ C
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.p_half[x]);
-        half(s1, ref);
+        weigh(sc, pa, ref);
+        tmem_st32(tS + 64, pa);
+        weigh(sd, pa, ref);
+        tmem_st32(tS + 96, pa);
         l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
-        tmem_st32(tS + 32, s1);
-        if (mx > m + 8.f) next = mx;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
