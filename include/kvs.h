@@ -551,11 +551,12 @@ kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* tok_off_dev,
  * As for decoding, a plan per step serves every layer: kvs_extend_plan writes
  * it into ws, kvs_extend_attn_planned runs a layer with it (same arguments;
  * other shapes set KVS_DEVERR_PLAN and nothing is written), kvs_extend_attn is
- * the one after the other.  Calls of at most 32 sequences that need neither
- * split key ranges nor shared parts (short tables and few rows; or chunks long
- * enough to fill the device) are one launch without a plan, and
- * kvs_extend_plan writes nothing for them: the host tells from n_tokens,
- * n_seq, max_blocks and the heads.  The results agree to rounding.  ws:
+ * the one after the other.  Calls of at most 32 sequences that are worth
+ * neither split key ranges nor shared parts (short tables and few rows; or
+ * chunks long enough to fill the device, of one sequence or over tables of at
+ * most 256 blocks) are one launch without a plan, in which common parts are not
+ * shared, and kvs_extend_plan writes nothing for them: the host tells from
+ * n_tokens, n_seq, max_blocks and the heads.  The results agree to rounding.  ws:
  * kvs_extend_workspace_size bytes, of one stream at a time. */
 kvs_status kvs_extend_workspace_size(const kvs_pool* pool, int32_t n_tokens, int32_t n_seq, int32_t max_blocks,
                                      int32_t n_q_heads, size_t* bytes);

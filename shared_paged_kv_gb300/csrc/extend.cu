@@ -41,7 +41,7 @@
 // cores (2,048 of them P V's two parts), and two chains share the SM: a pair
 // takes about 4,600.  Replayed in a CUDA graph: 8,192 rows after 8,192 tokens,
 // 32 heads of 128: 1.56 ms, 1,055 TFLOP/s; 16 chunks over one document of 8,192
-// states: 440 us, 980 TFLOP/s.  Few rows over long contexts are bound by the
+// states: 447 us, 968 TFLOP/s.  Few rows over long contexts are bound by the
 // items' chains, starts and ends (64 sequences of 3 to 8 rows over 8,192 shared
 // and 1,000 to 6,100 own tokens: 260 us, 3.8 TB/s), calls without a plan by one
 // chain of key tiles (12 rows over 1,300 states: 25 us).
@@ -1485,24 +1485,32 @@ cudaError_t ex_launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem
 }
 
 // Whether the whole attention goes in one launch (DIRECT), with nothing split
-// or shared; the rule goes by what the host knows.
-//  * Short tables and at most two rounds of units: a plan and a merge take
-//    longer than they save (4 sequences of 24 blocks, head_dim 64: 19.0 us planned,
-//    8.9 in one launch; 12 sequences of 94 blocks: 28.8 and 22.1; 8 items of
-//    16 key tiles would take 22 planned and 29 in one launch).
-//  * Chunks of at least a unit on the mean, which share nothing worth while,
-//    that fill the SMs without splits (8 x 256 rows after 1,800 tokens, 8 KV
-//    heads: 76 and 64 us; 2,048 rows after 2,048 tokens, 32 KV heads: 110 and
-//    88), unless the last round would be mostly empty and long (32 x 96 rows
-//    after 5,400 tokens, 2 KV heads: 146 and 160 us).  Beyond kExDirectRounds
-//    rounds the plan's order by length is worth more than its time.
+// or shared; the rule goes by what the host knows.  Times below are of CUDA-graph
+// replays, planned and in one launch.
+//  * Short tables and at most two rounds of units: a plan and a merge mostly take
+//    longer than they save (16 x 4 rows after 1,000 tokens, 40 / 8 heads: 30 and
+//    19 us; 8 x 128 rows after 1,000, 32 / 8: 36 and 27; 2 x 64 rows after 300,
+//    8 / 2: 21 and 13).  The bound is crude: few rows near it would gain from
+//    splits (1 row after 1,500, 32 / 8: 20 and 25), and calls behind it that
+//    fill the device once would do without (16 x 4 after 2,000, 40 / 8: 49 and 33).
+//  * Chunks of at least a unit on the mean that fill the SMs without splits (8 x
+//    256 rows after 1,800 tokens, 32 / 8 heads: 93 and 81 us; 1 x 2,048 rows after
+//    2,048, 32 / 32: 128 and 112).  The host knows the longest table, not
+//    whose it is: with several sequences a single row may own it, so the tables
+//    must be short enough that this row's chain of key tiles costs no more than
+//    the plan (2,048 rows and 1 row after 4,000: 72 and 90 us; 1 row after 8,000:
+//    72 and 141, after 60,000: 116 and 800; 2 x 1,024 rows after 8,000, which
+//    are planned for that reason: 311 and 304).  One sequence's units are about
+//    equally long; its last round must not be mostly empty where they are long.
+//    Beyond kExDirectRounds rounds the plan's order by length is worth more than
+//    its time.
 bool ex_direct(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks, int g) {
   if (pool->test_flags & KVS_TEST_EXTEND_PLANNED) return false;
   const long long tu = ex_tokens_per_unit(g), whole = n_tokens / tu, hkv = pool->desc.num_kv_heads, sms = pool->num_sms;
   if (n_seq > 32) return false;
   const bool small = max_blocks <= kExDirectBlocks && (whole + n_seq) * hkv <= 2 * sms;
   const long long likely = (2 * whole + n_seq) * hkv / 2, rounds = (likely + sms - 1) / sms;   // half a unit left per sequence
-  const bool even = 4 * likely >= 3 * rounds * sms || max_blocks <= kExDirectShort;
+  const bool even = max_blocks <= kExDirectShort || (n_seq == 1 && 4 * likely >= 3 * rounds * sms);
   const bool full = n_tokens >= n_seq * tu && whole * hkv >= sms && rounds <= kExDirectRounds && even;
   return small || full;
 }
