@@ -556,8 +556,10 @@ kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* tok_off_dev,
  * chunks long enough to fill the device, of one sequence or over tables of at
  * most 256 blocks) are one launch without a plan, in which common parts are not
  * shared, and kvs_extend_plan writes nothing for them: the host tells from
- * n_tokens, n_seq, max_blocks and the heads.  The results agree to rounding.  ws:
- * kvs_extend_workspace_size bytes, of one stream at a time. */
+ * n_tokens, n_seq, max_blocks and the heads.  The results agree to rounding.
+ * ws: kvs_extend_workspace_size bytes, of one stream at a time; enough as well
+ * for every call with the same heads and no more tokens, sequences and blocks.
+ * Calls of one launch leave it alone (it may be NULL or smaller). */
 kvs_status kvs_extend_workspace_size(const kvs_pool* pool, int32_t n_tokens, int32_t n_seq, int32_t max_blocks,
                                      int32_t n_q_heads, size_t* bytes);
 kvs_status kvs_extend_plan(kvs_pool* pool, const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,

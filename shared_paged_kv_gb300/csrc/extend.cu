@@ -141,12 +141,16 @@ ExWorkspace ex_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blo
   // piece is at least the total over kExItemsPerSm * SMs / heads
   const long long extra = (long long)kExItemsPerSm * pool->num_sms / hkv + 1;
   w.max_items = (int)(w.max_units + extra);
-  const bool parts = (long long)n_tokens * g * hkv <= kExPartRows;
-  // rows of a unit x its pieces: every row of its own and of a shared range
-  // once, and 2 * 128 rows for each piece beyond the first
-  w.part_rows = parts ? 2ll * n_tokens * g + extra * 2 * kExTile : 0;
+  // Rows of a unit x its pieces: every row of its own and of a shared range
+  // once, and 2 * 128 rows for each piece beyond the first.  One sequence shares
+  // nothing, and its units are split only while they are few (the plan's rule).
+  // Calls above kExPartRows make no parts; they keep the room of those below, so
+  // that a workspace serves every call of no more tokens, sequences and blocks.
+  const long long with_parts = std::min<long long>(n_tokens, kExPartRows / ((long long)g * hkv));
+  const long long few = (long long)((4 * pool->num_sms - 1) / hkv) * tu;
+  w.part_rows = (n_seq > 1 ? 2 * with_parts : std::min(with_parts, few)) * g + extra * 2 * kExTile;
   const long long tiles = ((long long)max_blocks + kExBlocks - 1) / kExBlocks + 1;
-  w.part_rows = std::min(w.part_rows, (long long)n_tokens * g * (tiles + 1));   // at most a piece per key tile
+  w.part_rows = std::min(w.part_rows, with_parts * g * (tiles + 1));   // at most a piece per key tile
   char* p = static_cast<char*>(base);
   size_t o = 0;
   auto take = [&](size_t b) {
@@ -1469,6 +1473,13 @@ kvs_status ex_check(const kvs_pool* pool, const char* what, int n_tokens, int n_
   return KVS_OK;
 }
 
+kvs_status ex_check_ws(const ExWorkspace& w, const void* ws, size_t ws_bytes, const char* what) {
+  if (!ws) return fail(KVS_ERR_INVALID_ARG, std::string(what) + ": null workspace");
+  if (!aligned32(ws)) return fail(KVS_ERR_INVALID_ARG, std::string(what) + ": ws must be 32-byte aligned");
+  if (ws_bytes < w.bytes) return fail(KVS_ERR_CAPACITY, std::string(what) + ": workspace too small");
+  return KVS_OK;
+}
+
 template <typename... KArgs, typename... Args>
 cudaError_t ex_launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
   cudaLaunchConfig_t cfg = {};
@@ -1567,14 +1578,13 @@ extern "C" kvs_status kvs_extend_plan(kvs_pool* pool, const int32_t* tok_off_dev
   if (kvs_status st = ex_check(pool, "extend_plan", n_tokens, n_seq, max_blocks, n_q_heads); st != KVS_OK) return st;
   if (causal != 0 && causal != 1) return fail(KVS_ERR_INVALID_ARG, "extend_plan: causal is 0 or 1");
   if (n_tokens == 0 || n_seq == 0) return KVS_OK;
-  if (!tok_off_dev || !block_table_dev || !seq_len_dev || !ws) return fail(KVS_ERR_INVALID_ARG, "extend_plan: null pointer");
-  if (!aligned32(ws)) return fail(KVS_ERR_INVALID_ARG, "extend_plan: ws must be 32-byte aligned");
+  if (!tok_off_dev || !block_table_dev || !seq_len_dev) return fail(KVS_ERR_INVALID_ARG, "extend_plan: null pointer");
   const int hkv = pool->desc.num_kv_heads, g = n_q_heads / hkv;
-  ExPlanParams p{};
-  p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
-  if (ws_bytes < p.w.bytes) return fail(KVS_ERR_CAPACITY, "extend_plan: workspace too small");
   if (kvs_status st = check_pool_device(pool, "extend_plan"); st != KVS_OK) return st;
   if (ex_direct(pool, n_tokens, n_seq, max_blocks, g)) return KVS_OK;
+  ExPlanParams p{};
+  p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
+  if (kvs_status st = ex_check_ws(p.w, ws, ws_bytes, "extend_plan"); st != KVS_OK) return st;
   p.tok_off = tok_off_dev;
   p.seq_len = seq_len_dev;
   p.table = block_table_dev;
@@ -1617,14 +1627,17 @@ extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, con
   const long long row = (long long)n_q_heads * d.head_dim;
   if (q_stride < row || (q_stride & 7)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: q_stride must hold n_q_heads * head_dim elements and be a multiple of 8");
   if (n_tokens == 0 || n_seq == 0) return KVS_OK;
-  if (!q_dev || !tok_off_dev || !block_table_dev || !seq_len_dev || !out_dev || !ws)
+  if (!q_dev || !tok_off_dev || !block_table_dev || !seq_len_dev || !out_dev)
     return fail(KVS_ERR_INVALID_ARG, "extend_attn: null pointer");
-  if (!aligned16(q_dev) || !aligned32(out_dev) || !aligned32(ws))
-    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q must be 16-byte, out and ws 32-byte aligned");
+  if (!aligned16(q_dev) || !aligned32(out_dev))
+    return fail(KVS_ERR_INVALID_ARG, "extend_attn: q must be 16-byte, out 32-byte aligned");
   const int g = n_q_heads / d.num_kv_heads;
+  const bool direct = ex_direct(pool, n_tokens, n_seq, max_blocks, g);
   ExParams p{};
-  p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
-  if (ws_bytes < p.w.bytes) return fail(KVS_ERR_CAPACITY, "extend_attn: workspace too small");
+  if (!direct) {
+    p.w = ex_layout(pool, n_tokens, n_seq, max_blocks, g, ws);
+    if (kvs_status st = ex_check_ws(p.w, ws, ws_bytes, "extend_attn"); st != KVS_OK) return st;
+  }
   if (kvs_status st = check_pool_device(pool, "extend_attn"); st != KVS_OK) return st;
   p.table = block_table_dev;
   p.tok_off = tok_off_dev;
@@ -1644,7 +1657,7 @@ extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, con
   CUtensorMap tq;
   if (!ex_query_map(&tq, q_dev, n_tokens, g, d.num_kv_heads, d.head_dim, q_stride))
     return fail(KVS_ERR_CUDA, "extend_attn: cuTensorMapEncodeTiled failed for q");
-  if (ex_direct(pool, n_tokens, n_seq, max_blocks, g)) {
+  if (direct) {
     const long long claims = (n_tokens / ex_tokens_per_unit(g) + n_seq) * (long long)d.num_kv_heads;
     return d.head_dim == 128 ? ex_direct_run<128>(pool, layer, p, tq, claims, stream)
                              : ex_direct_run<64>(pool, layer, p, tq, claims, stream);

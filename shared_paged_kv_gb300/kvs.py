@@ -433,6 +433,11 @@ def kvs_gather(pool: Pool, layer, n_tokens, tok_off, block_table, max_blocks, se
                              _ints(seq_len, n_seq, "seq_len"), n_seq, kp, vp, _stream(stream)))
 
 
+def _ws(ws):
+    """(pointer, bytes) of a workspace, (NULL, 0) of none."""
+    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+
+
 def kvs_extend_workspace_size(pool: Pool, n_tokens: int, n_seq: int, max_blocks: int, n_q_heads: int) -> int:
     out = ctypes.c_size_t()
     _check(load().kvs_extend_workspace_size(pool.handle, n_tokens, n_seq, max_blocks, n_q_heads, ctypes.byref(out)))
@@ -444,8 +449,7 @@ def kvs_extend_plan(pool: Pool, n_tokens, tok_off, n_q_heads, block_table, max_b
     """The work plan of a batch of query chunks, for every layer of a step."""
     _check(load().kvs_extend_plan(pool.handle, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens, n_q_heads,
                                   _ints(block_table, n_seq * max_blocks, "block_table"), max_blocks,
-                                  _ints(seq_len, n_seq, "seq_len"), n_seq, int(causal), _ptr(ws),
-                                  ws.numel() * ws.element_size(), _stream(stream)))
+                                  _ints(seq_len, n_seq, "seq_len"), n_seq, int(causal), *_ws(ws), _stream(stream)))
 
 
 def _extend(fn, pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq, causal, scale, out,
@@ -457,7 +461,7 @@ def _extend(fn, pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_b
         raise ValueError("out: rows without gaps are wanted")
     _check(fn(pool.handle, layer, qp, qs, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens, n_q_heads,
               _ints(block_table, n_seq * max_blocks, "block_table"), max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq,
-              int(causal), scale, op, _ptr(ws), ws.numel() * ws.element_size(), _stream(stream)))
+              int(causal), scale, op, *_ws(ws), _stream(stream)))
 
 
 def kvs_extend_attn_planned(pool: Pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq,
