@@ -466,16 +466,15 @@ extern "C" kvs_status kvs_append(kvs_pool* pool, int32_t layer, const void* k_de
   if (layer < 0 || layer >= d.num_layers) return fail(KVS_ERR_INVALID_ARG, "append: layer out of range");
   if (n_tokens < 0 || n_seq < 0 || max_blocks < 1 || n_q_heads < 0) return fail(KVS_ERR_INVALID_ARG, "append: bad sizes");
   if (n_seq > d.max_seqs) return fail(KVS_ERR_CAPACITY, "append: n_seq exceeds the pool's max_seqs");
-  if (!q_dev != !q_out_dev || (q_dev != nullptr) != (n_q_heads > 0))
-    return fail(KVS_ERR_INVALID_ARG, "append: q, q_out and n_q_heads go together");
-  if (axes) {
+  if (axes)
     if (const char* e = axes_error(axes, d.head_dim); *e) return fail(KVS_ERR_INVALID_ARG, std::string("append: ") + e);
-    if (!pos_dev && axes->n_axes != 1) return fail(KVS_ERR_INVALID_ARG, "append: several axes need positions");
-  }
   const long long krow = (long long)d.num_kv_heads * d.head_dim, qrow = (long long)n_q_heads * d.head_dim;
   if (bad_stride(k_stride, krow) || bad_stride(v_stride, krow) || (q_dev && bad_stride(q_stride, qrow)))
     return fail(KVS_ERR_INVALID_ARG, "append: a stride must hold heads * head_dim elements and be a multiple of 8");
   if (n_tokens == 0 || n_seq == 0) return KVS_OK;
+  if (!q_dev != !q_out_dev || (q_dev != nullptr) != (n_q_heads > 0))
+    return fail(KVS_ERR_INVALID_ARG, "append: q, q_out and n_q_heads go together");
+  if (axes && !pos_dev && axes->n_axes != 1) return fail(KVS_ERR_INVALID_ARG, "append: several axes need positions");
   if (!k_dev || !v_dev || !tok_off_dev || !block_table_dev || !seq_len_dev)
     return fail(KVS_ERR_INVALID_ARG, "append: null pointer");
   if (!aligned16(k_dev) || !aligned16(v_dev) || !aligned16(q_dev) || !aligned16(q_out_dev))

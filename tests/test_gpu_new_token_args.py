@@ -1,0 +1,41 @@
+"""Arguments of the operators on new tokens: empty steps.
+"""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+from shared_paged_kv_gb300 import kvs as K
+import harness as H
+from test_gpu_append import Case, randn
+from test_gpu_extend import Batch
+
+DEV = H.DEV
+
+
+def test_an_empty_step_with_queries_does_nothing():
+    """No new token of any sequence: every call of the step is a no-op, also
+    with (empty) queries beside the rows."""
+    c = Case([0, 0], [5, 40], 2, 128)
+    before = [s.clone() for s in c.slabs]
+    k, q = randn(1, 0, 2, 128), randn(2, 0, 8, 128)
+    c.append(k, k, rope=K.RopeAxes(1e6, (64,)), q=q, n_q_heads=8, q_out=torch.empty_like(q))
+    none = torch.empty(3, 0, dtype=torch.int32, device=DEV)
+    c.append(k, k, rope=K.RopeAxes(1e6, (16, 24, 24)), pos=none, q=q, n_q_heads=8, q_out=torch.empty_like(q))
+    c.gather(k, k.clone())
+    K.kvs_rope_apply(q, torch.empty(1, 0, dtype=torch.int32, device=DEV), K.RopeAxes(1e6, (64,)), torch.empty_like(q), 0, 8, 128)
+    off, tab, mb, lens, n = c.args()
+    ws = H.workspace(K.kvs_extend_workspace_size(c.pool, 0, n, mb, 8))
+    K.kvs_extend_attn(c.pool, 0, q, 0, off, 8, tab, mb, lens, n, True, 1.0, torch.empty_like(q), ws)
+    assert K.kvs_pool_check(c.pool) == 0
+    assert torch.equal(before[0], c.slabs[0]) and torch.equal(before[1], c.slabs[1])
+
+
+def test_queries_and_their_result_go_together_in_a_step_with_rows():
+    c = Case([2], [5], 2, 128)
+    k, q = randn(1, 2, 2, 128), randn(2, 2, 8, 128)
+    for kw in (dict(q=q, n_q_heads=8), dict(q_out=q, n_q_heads=8), dict(n_q_heads=8),
+               dict(rope=K.RopeAxes(1e6, (16, 24, 24)))):
+        with pytest.raises((K.KvsError, ValueError)):
+            c.append(k, k, **kw)
