@@ -389,12 +389,20 @@ def _ints(t, n: int, what: str):
     return t.data_ptr()
 
 
+def _positions(pos, n_axes: int, n_tokens: int):
+    """Positions [n_axes][n_tokens].  One axis may go on behind n_tokens; with
+    several, that would put the second one elsewhere."""
+    if pos is not None and n_axes > 1 and pos.shape != (n_axes, n_tokens) and pos.shape != (n_axes * n_tokens,):
+        raise ValueError(f"pos: shape {tuple(pos.shape)} is not [{n_axes}][{n_tokens}]")
+    return _ints(pos, n_axes * n_tokens, "pos")
+
+
 def kvs_rope_apply(x, pos, rope: RopeAxes, out, n_tokens, n_heads, head_dim, inverse=False, stream=None):
     """out[t][h] = x[t][h] rotated by its positions pos int32 [axes][n_tokens]
     (taken back with inverse); x and out may be views into wider rows."""
     xp, xs = _rows(x, n_tokens, n_heads, head_dim, "x")
     op, os_ = _rows(out, n_tokens, n_heads, head_dim, "out")
-    _check(load().kvs_rope_apply(xp, xs, _ints(pos, rope.n_axes * n_tokens, "pos"), ctypes.byref(rope), int(inverse), op,
+    _check(load().kvs_rope_apply(xp, xs, _positions(pos, rope.n_axes, n_tokens), ctypes.byref(rope), int(inverse), op,
                                  os_, n_tokens, n_heads, head_dim, _stream(stream)))
 
 
@@ -414,7 +422,7 @@ def kvs_append(pool: Pool, layer, k_new, v_new, n_tokens, tok_off, block_table, 
             raise ValueError("q_out: rows without gaps are wanted")
     _check(load().kvs_append(
         pool.handle, layer, kp, ks, vp, vs, qp, qs, n_q_heads, op, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens,
-        _ints(pos, (rope.n_axes if rope is not None else 1) * n_tokens, "pos"),
+        _positions(pos, rope.n_axes if rope is not None else 1, n_tokens),
         ctypes.byref(rope) if rope is not None else None, _ints(block_table, n_seq * max_blocks, "block_table"),
         max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq, _stream(stream)))
 

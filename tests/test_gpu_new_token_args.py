@@ -1,5 +1,5 @@
-"""Arguments of the operators on new tokens: empty steps.
-"""
+"""Arguments of the operators on new tokens: empty steps, tensors laid out for
+another shape."""
 import numpy as np
 import pytest
 
@@ -39,3 +39,30 @@ def test_queries_and_their_result_go_together_in_a_step_with_rows():
                dict(rope=K.RopeAxes(1e6, (16, 24, 24)))):
         with pytest.raises((K.KvsError, ValueError)):
             c.append(k, k, **kw)
+
+
+def test_positions_of_another_length_are_refused():
+    """Positions are [axes][n_tokens]: of a longer padded batch the second axis
+    would be read at the wrong place."""
+    c = Case([4, 3], [0, 9], 2, 128)
+    k, v = randn(1, 7, 2, 128), randn(2, 7, 2, 128)
+    rope = K.RopeAxes(1e6, (16, 24, 24))
+    pos = H.i32(np.arange(3 * 9).reshape(3, 9))
+    x = randn(3, 7, 4, 128)
+    for bad in (pos, pos.flatten(), pos[:2], H.i32(np.arange(21).reshape(7, 3))):
+        with pytest.raises(ValueError):
+            c.append(k, v, rope=rope, pos=bad)
+        with pytest.raises(ValueError):
+            K.kvs_rope_apply(x, bad, rope, torch.empty_like(x), 7, 4, 128)
+    good = pos[:, :7].contiguous()
+    a, b = torch.empty_like(x), torch.empty_like(x)
+    K.kvs_rope_apply(x, good, rope, a, 7, 4, 128)
+    K.kvs_rope_apply(x, good.flatten(), rope, b, 7, 4, 128)
+    assert torch.equal(a, b)
+    c.append(k, v, rope=rope, pos=good)
+    # on one axis a longer tensor begins with the same positions
+    one = K.RopeAxes(1e6, (64,))
+    K.kvs_rope_apply(x, pos[0, :7].contiguous(), one, a, 7, 4, 128)
+    K.kvs_rope_apply(x, pos[:1], one, b, 7, 4, 128)
+    assert torch.equal(a, b)
+    assert K.kvs_pool_check(c.pool) == 0
