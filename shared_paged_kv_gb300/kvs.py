@@ -397,6 +397,14 @@ def _positions(pos, n_axes: int, n_tokens: int):
     return _ints(pos, n_axes * n_tokens, "pos")
 
 
+def _table(t, n_seq: int, max_blocks: int):
+    """Block table [>= n_seq][max_blocks], or its values in one dimension; the
+    row of a single sequence may go on."""
+    if t is not None and t.dim() != 1 and (t.shape[-1] < max_blocks or (n_seq > 1 and t.shape[-1] > max_blocks)):
+        raise ValueError(f"block_table: rows of {t.shape[-1]} blocks, max_blocks is {max_blocks}")
+    return _ints(t, n_seq * max_blocks, "block_table")
+
+
 def kvs_rope_apply(x, pos, rope: RopeAxes, out, n_tokens, n_heads, head_dim, inverse=False, stream=None):
     """out[t][h] = x[t][h] rotated by its positions pos int32 [axes][n_tokens]
     (taken back with inverse); x and out may be views into wider rows."""
@@ -423,7 +431,7 @@ def kvs_append(pool: Pool, layer, k_new, v_new, n_tokens, tok_off, block_table, 
     _check(load().kvs_append(
         pool.handle, layer, kp, ks, vp, vs, qp, qs, n_q_heads, op, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens,
         _positions(pos, rope.n_axes if rope is not None else 1, n_tokens),
-        ctypes.byref(rope) if rope is not None else None, _ints(block_table, n_seq * max_blocks, "block_table"),
+        ctypes.byref(rope) if rope is not None else None, _table(block_table, n_seq, max_blocks),
         max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq, _stream(stream)))
 
 
@@ -437,7 +445,7 @@ def kvs_gather(pool: Pool, layer, n_tokens, tok_off, block_table, max_blocks, se
     if ks != gap or vs != gap:
         raise ValueError("k_out, v_out: rows without gaps are wanted")
     _check(load().kvs_gather(pool.handle, layer, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens,
-                             _ints(block_table, n_seq * max_blocks, "block_table"), max_blocks,
+                             _table(block_table, n_seq, max_blocks), max_blocks,
                              _ints(seq_len, n_seq, "seq_len"), n_seq, kp, vp, _stream(stream)))
 
 
@@ -456,7 +464,7 @@ def kvs_extend_plan(pool: Pool, n_tokens, tok_off, n_q_heads, block_table, max_b
                     stream=None):
     """The work plan of a batch of query chunks, for every layer of a step."""
     _check(load().kvs_extend_plan(pool.handle, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens, n_q_heads,
-                                  _ints(block_table, n_seq * max_blocks, "block_table"), max_blocks,
+                                  _table(block_table, n_seq, max_blocks), max_blocks,
                                   _ints(seq_len, n_seq, "seq_len"), n_seq, int(causal), *_ws(ws), _stream(stream)))
 
 
@@ -468,7 +476,7 @@ def _extend(fn, pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_b
     if os_ != n_q_heads * d.head_dim:
         raise ValueError("out: rows without gaps are wanted")
     _check(fn(pool.handle, layer, qp, qs, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens, n_q_heads,
-              _ints(block_table, n_seq * max_blocks, "block_table"), max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq,
+              _table(block_table, n_seq, max_blocks), max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq,
               int(causal), scale, op, *_ws(ws), _stream(stream)))
 
 

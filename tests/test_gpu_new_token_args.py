@@ -66,3 +66,31 @@ def test_positions_of_another_length_are_refused():
     K.kvs_rope_apply(x, pos[:1], one, b, 7, 4, 128)
     assert torch.equal(a, b)
     assert K.kvs_pool_check(c.pool) == 0
+
+
+def test_tables_of_another_width_are_refused():
+    """A table is [n_seq][max_blocks]: with wider rows the second sequence's
+    blocks would be read from the first one's."""
+    c = Case([4, 3], [0, 9], 2, 128)
+    k, v, q = randn(1, 7, 2, 128), randn(2, 7, 2, 128), randn(3, 7, 8, 128)
+    off, tab, mb, lens, n = c.args()
+    assert mb > 1
+    ws = H.workspace(K.kvs_extend_workspace_size(c.pool, 7, n, mb, 8))
+    out = torch.empty_like(q)
+    for m in (mb - 1, mb + 1):
+        with pytest.raises(ValueError):
+            K.kvs_append(c.pool, 0, k, v, 7, off, tab, m, lens, n)
+        with pytest.raises(ValueError):
+            K.kvs_gather(c.pool, 0, 7, off, tab, m, lens, n, k, v)
+        with pytest.raises(ValueError):
+            K.kvs_extend_plan(c.pool, 7, off, 8, tab, m, lens, n, True, ws)
+        for f in (K.kvs_extend_attn, K.kvs_extend_attn_planned):
+            with pytest.raises(ValueError):
+                f(c.pool, 0, q, 7, off, 8, tab, m, lens, n, True, 1.0, out, ws)
+    with pytest.raises(ValueError):                          # one row does not go on in the next
+        K.kvs_append(c.pool, 0, k, v, 7, off, tab, 2 * mb, lens, 1)
+    K.kvs_gather(c.pool, 0, 4, off, tab, mb - 1, lens, 1, k[:4].clone(), v[:4].clone())   # a row may be longer than asked
+    wide = torch.cat([tab, torch.full_like(tab, -1)])       # more sequences than the call's: the first rows
+    K.kvs_append(c.pool, 0, k, v, 7, off, wide, mb, lens, n)
+    K.kvs_append(c.pool, 0, k, v, 7, off, tab.flatten(), mb, lens, n)
+    assert K.kvs_pool_check(c.pool) == 0
