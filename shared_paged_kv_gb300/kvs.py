@@ -450,8 +450,12 @@ def kvs_gather(pool: Pool, layer, n_tokens, tok_off, block_table, max_blocks, se
 
 
 def _ws(ws):
-    """(pointer, bytes) of a workspace, (NULL, 0) of none."""
-    return (None, 0) if ws is None else (_ptr(ws), ws.numel() * ws.element_size())
+    """(pointer, bytes) of a workspace of any type, (NULL, 0) of none."""
+    if ws is None:
+        return None, 0
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous CUDA tensor is wanted")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
 def kvs_extend_workspace_size(pool: Pool, n_tokens: int, n_seq: int, max_blocks: int, n_q_heads: int) -> int:

@@ -1,5 +1,5 @@
 """Arguments of the operators on new tokens: empty steps, tensors laid out for
-another shape."""
+another shape, workspaces that are not on the GPU."""
 import numpy as np
 import pytest
 
@@ -94,3 +94,19 @@ def test_tables_of_another_width_are_refused():
     K.kvs_append(c.pool, 0, k, v, 7, off, wide, mb, lens, n)
     K.kvs_append(c.pool, 0, k, v, 7, off, tab.flatten(), mb, lens, n)
     assert K.kvs_pool_check(c.pool) == 0
+
+
+def test_a_workspace_that_is_not_on_the_gpu_is_refused():
+    b = Batch([4, 9], [70, 65], 8, 2, 64)
+    off, tab, lens = b.dev()
+    n = b.ws().numel()
+    out = torch.empty_like(b.q)
+    for bad in (torch.empty(n, dtype=torch.uint8), torch.empty(n, 2, dtype=torch.uint8, device=DEV)[:, 0]):
+        with pytest.raises(ValueError):
+            K.kvs_extend_plan(b.pool, b.T, off, 8, tab, b.mb, lens, b.n, True, bad)
+        for f in (K.kvs_extend_attn, K.kvs_extend_attn_planned):
+            with pytest.raises(ValueError):
+                f(b.pool, 0, b.q, b.T, off, 8, tab, b.mb, lens, b.n, True, b.scale, out, bad)
+    wide = torch.empty(-(-n // 4), dtype=torch.int32, device=DEV)     # any type: its bytes count
+    K.kvs_extend_attn(b.pool, 0, b.q, b.T, off, 8, tab, b.mb, lens, b.n, True, b.scale, out, wide)
+    assert torch.equal(out, b.run(True))
