@@ -360,14 +360,19 @@ def kvs_quantize_q4(pool: Pool, layer, k_src, v_src, dst_blocks, n_blocks, strea
 _BF16, _I16, _I32 = torch.bfloat16, torch.int16, torch.int32
 
 
+def _here(t) -> bool:
+    """Whether t lies on the current device."""
+    return t.is_cuda and t.get_device() == (_cur_dev() if _cur_dev is not None else torch.cuda.current_device())
+
+
 def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str):
     """(pointer, elements between two tokens) of packed rows [n_tokens][heads]
     [head_dim] of 16-bit elements; the tokens may lie apart."""
     dt = t.dtype
     if dt is not _BF16 and dt is not _I16:
         raise ValueError(f"{what}: bf16 rows (torch.bfloat16, or their bits as int16) are wanted, got {dt}")
-    if not t.is_cuda:
-        raise ValueError(f"{what}: a CUDA tensor is wanted")
+    if not _here(t):
+        raise ValueError(f"{what}: a CUDA tensor of the current device is wanted")
     if t.is_contiguous() and t.numel() == n_tokens * n_heads * head_dim:
         return t.data_ptr(), n_heads * head_dim
     shape = t.shape
@@ -384,8 +389,8 @@ def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str
 def _ints(t, n: int, what: str):
     if t is None:
         return None
-    if t.dtype is not _I32 or not t.is_cuda or not t.is_contiguous() or t.numel() < n:
-        raise ValueError(f"{what}: a contiguous int32 CUDA tensor of at least {n} values is wanted")
+    if t.dtype is not _I32 or not _here(t) or not t.is_contiguous() or t.numel() < n:
+        raise ValueError(f"{what}: a contiguous int32 CUDA tensor of at least {n} values on the current device is wanted")
     return t.data_ptr()
 
 
@@ -453,8 +458,8 @@ def _ws(ws):
     """(pointer, bytes) of a workspace of any type, (NULL, 0) of none."""
     if ws is None:
         return None, 0
-    if not ws.is_cuda or not ws.is_contiguous():
-        raise ValueError("ws: a contiguous CUDA tensor is wanted")
+    if not _here(ws) or not ws.is_contiguous():
+        raise ValueError("ws: a contiguous CUDA tensor of the current device is wanted")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
 
