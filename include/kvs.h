@@ -534,7 +534,7 @@ kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* tok_off_dev,
  * q_dev         bf16 [n_tokens][n_q_heads][head_dim] with row stride q_stride,
  *               already position-encoded; out_dev bf16, without gaps, must
  *               not overlap q.  out and ws are 32-byte aligned.  scale is
- *               positive and finite.
+ *               positive, and scale * log2(e) finite in float32.
  * Requires n_q_heads % num_kv_heads == 0, a group of at most 16 query heads
  * per KV head and a BF16 pool.  Stored keys and values of tokens below
  * seq_len are finite; what the pool holds behind them (the rest of a block)

@@ -1473,6 +1473,9 @@ kvs_status ex_check(const kvs_pool* pool, const char* what, int n_tokens, int n_
   return KVS_OK;
 }
 
+constexpr float kExLog2e = 1.4426950408889634f;   // scores are taken to base 2
+bool ex_scale_ok(float scale) { return scale > 0.f && std::isfinite(scale * kExLog2e); }
+
 kvs_status ex_check_ws(const ExWorkspace& w, const void* ws, size_t ws_bytes, const char* what) {
   if (!ws) return fail(KVS_ERR_INVALID_ARG, std::string(what) + ": null workspace");
   if (!aligned32(ws)) return fail(KVS_ERR_INVALID_ARG, std::string(what) + ": ws must be 32-byte aligned");
@@ -1623,7 +1626,7 @@ extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, con
   const kvs_pool_desc& d = pool->desc;
   if (layer < 0 || layer >= d.num_layers) return fail(KVS_ERR_INVALID_ARG, "extend_attn: layer out of range");
   if (causal != 0 && causal != 1) return fail(KVS_ERR_INVALID_ARG, "extend_attn: causal is 0 or 1");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: scale must be positive and finite");
+  if (!ex_scale_ok(scale)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: scale must be positive, and scale * log2(e) finite");
   const long long row = (long long)n_q_heads * d.head_dim;
   if (q_stride < row || (q_stride & 7)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: q_stride must hold n_q_heads * head_dim elements and be a multiple of 8");
   if (n_tokens == 0 || n_seq == 0) return KVS_OK;
@@ -1653,7 +1656,7 @@ extern "C" kvs_status kvs_extend_attn_planned(kvs_pool* pool, int32_t layer, con
   p.hq = n_q_heads;
   p.causal = causal;
   p.slab_rows = d.capacity_blocks * d.num_kv_heads * d.block_tokens;
-  p.scale_log2 = scale * 1.4426950408889634f;
+  p.scale_log2 = scale * kExLog2e;
   CUtensorMap tq;
   if (!ex_query_map(&tq, q_dev, n_tokens, g, d.num_kv_heads, d.head_dim, q_stride))
     return fail(KVS_ERR_CUDA, "extend_attn: cuTensorMapEncodeTiled failed for q");
@@ -1675,7 +1678,7 @@ extern "C" kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void*
   // the layer's own arguments are checked before the plan is enqueued
   if (!pool) return fail(KVS_ERR_INVALID_ARG, "extend_attn: null pool");
   if (layer < 0 || layer >= pool->desc.num_layers) return fail(KVS_ERR_INVALID_ARG, "extend_attn: layer out of range");
-  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: scale must be positive and finite");
+  if (!ex_scale_ok(scale)) return fail(KVS_ERR_INVALID_ARG, "extend_attn: scale must be positive, and scale * log2(e) finite");
   if (n_tokens > 0 && n_seq > 0 && (!q_dev || !out_dev || !aligned16(q_dev) || !aligned32(out_dev)))
     return fail(KVS_ERR_INVALID_ARG, "extend_attn: q must be set and 16-byte, out set and 32-byte aligned");
   if (q_stride < (long long)n_q_heads * pool->desc.head_dim || (q_stride & 7))

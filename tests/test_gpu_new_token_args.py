@@ -1,5 +1,6 @@
 """Arguments of the operators on new tokens: empty steps, tensors laid out for
-another shape, workspaces that are not on the GPU."""
+another shape, workspaces that are not on the GPU, scales at the end of the
+range."""
 import numpy as np
 import pytest
 
@@ -110,3 +111,18 @@ def test_a_workspace_that_is_not_on_the_gpu_is_refused():
     wide = torch.empty(-(-n // 4), dtype=torch.int32, device=DEV)     # any type: its bytes count
     K.kvs_extend_attn(b.pool, 0, b.q, b.T, off, 8, tab, b.mb, lens, b.n, True, b.scale, out, wide)
     assert torch.equal(out, b.run(True))
+
+
+def test_scales_at_the_end_of_the_range():
+    """The exponent's base change must not leave the float32 range: a scale
+    that does is refused, the largest that does not gives finite results."""
+    b = Batch([3], [3], 8, 2, 64)
+    off, tab, lens = b.dev()
+    q, out = torch.zeros_like(b.q), torch.empty_like(b.q)
+    ws = b.ws()
+    for scale in (3e38, 2.4e38):
+        with pytest.raises(K.KvsError):
+            K.kvs_extend_attn(b.pool, 0, q, b.T, off, 8, tab, b.mb, lens, b.n, True, scale, out, ws)
+    K.kvs_extend_attn(b.pool, 0, q, b.T, off, 8, tab, b.mb, lens, b.n, True, 2.3e38, out, ws)
+    assert K.kvs_pool_check(b.pool) == 0
+    assert torch.isfinite(out.float()).all() and (out[0, 0] == b.v[b.table[0, 0], 0, 0]).all()
