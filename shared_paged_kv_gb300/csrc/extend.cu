@@ -138,7 +138,8 @@ ExWorkspace ex_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blo
   const long long own = n_tokens / tu + n_seq;
   w.max_units = (int)(2 * own);
   // sum of pieces <= (all key tiles of all units) / piece + units, and the
-  // piece is at least the total over kExItemsPerSm * SMs / heads
+  // piece is at least the total over kExItemsPerSm * SMs / heads (calls with
+  // many units: over 2 * SMs / heads, so that at most 2 * SMs / heads units are cut)
   const long long extra = (long long)kExItemsPerSm * pool->num_sms / hkv + 1;
   w.max_items = (int)(w.max_units + extra);
   // Rows of a unit x its pieces: every row of its own and of a shared range
@@ -498,9 +499,11 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
   // piece length: of 16 candidates the one with the least estimated time (the
   // mean load of an SM, or the rounds that the larger half of the pieces
   // takes; a piece costs its tiles, 0.8 of them with one row tile, 1.5 more,
-  // and what writing and joining its part takes); no splits in calls that
-  // fill the device, or are too large for part buffers.  Sixteen lanes work on
-  // a candidate.
+  // and what writing and joining its part takes).  Sixteen lanes work on a
+  // candidate.  Calls with at least four units per SM fill the device unsplit,
+  // and only units longer than an SM's mean load are cut, into halves of it
+  // (128 single rows, 127 of them after 1,000 tokens and one after 60,000, 32 / 8
+  // heads: 821 us uncut, 189 cut).  Calls too large for part buffers are not cut.
   if (split) {
     const float heads = (float)p.hkv, sms = (float)p.sms;
     const int least = max(kExMinPiece, (int)ceilf((float)s_sum * heads / (kExItemsPerSm * sms)));
@@ -543,6 +546,9 @@ __global__ void __launch_bounds__(kPlanThreads) extend_plan_kernel(const __grid_
       }
     }
     piece = ex_candidate(most, least, best);
+  } else if (p.share >= 0) {
+    const unsigned long long even = (s_sum * p.hkv + p.sms - 1) / p.sms;
+    if ((unsigned long long)most > even) piece = max(kExMinPiece, (int)((even + 1) / 2));
   }
   // items by cost (key tiles x row tiles), largest first: 256 classes; the
   // order inside a class changes no result.  The pieces of a unit are equal
