@@ -360,18 +360,19 @@ def kvs_quantize_q4(pool: Pool, layer, k_src, v_src, dst_blocks, n_blocks, strea
 _BF16, _I16, _I32 = torch.bfloat16, torch.int16, torch.int32
 
 
-def _here(t) -> bool:
-    """Whether t lies on the current device."""
-    return t.is_cuda and t.get_device() == (_cur_dev() if _cur_dev is not None else torch.cuda.current_device())
+def _device() -> int:
+    """The current device (a call asks once, and compares its tensors' with it)."""
+    return _cur_dev() if _cur_dev is not None else torch.cuda.current_device()
 
 
-def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str):
+def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str, dev=None):
     """(pointer, elements between two tokens) of packed rows [n_tokens][heads]
     [head_dim] of 16-bit elements; the tokens may lie apart."""
     dt = t.dtype
     if dt is not _BF16 and dt is not _I16:
         raise ValueError(f"{what}: bf16 rows (torch.bfloat16, or their bits as int16) are wanted, got {dt}")
-    if not _here(t):
+    at = t.get_device()     # -1 on the host
+    if at < 0 or at != (_device() if dev is None else dev):
         raise ValueError(f"{what}: a CUDA tensor of the current device is wanted")
     if t.is_contiguous() and t.numel() == n_tokens * n_heads * head_dim:
         return t.data_ptr(), n_heads * head_dim
@@ -386,36 +387,40 @@ def _rows(t: torch.Tensor, n_tokens: int, n_heads: int, head_dim: int, what: str
     return t.data_ptr(), st[0]
 
 
-def _ints(t, n: int, what: str):
+def _ints(t, n: int, what: str, dev=None):
     if t is None:
         return None
-    if t.dtype is not _I32 or not _here(t) or not t.is_contiguous() or t.numel() < n:
+    at = t.get_device()
+    if (t.dtype is not _I32 or at < 0 or at != (_device() if dev is None else dev) or not t.is_contiguous()
+            or t.numel() < n):
         raise ValueError(f"{what}: a contiguous int32 CUDA tensor of at least {n} values on the current device is wanted")
     return t.data_ptr()
 
 
-def _positions(pos, n_axes: int, n_tokens: int):
+def _positions(pos, n_axes: int, n_tokens: int, dev=None):
     """Positions [n_axes][n_tokens].  One axis may go on behind n_tokens; with
     several, that would put the second one elsewhere."""
-    if pos is not None and n_axes > 1 and pos.shape != (n_axes, n_tokens) and pos.shape != (n_axes * n_tokens,):
+    n = n_axes * n_tokens
+    if n_axes > 1 and pos is not None and (pos.numel() != n or (pos.dim() != 1 and pos.shape != (n_axes, n_tokens))):
         raise ValueError(f"pos: shape {tuple(pos.shape)} is not [{n_axes}][{n_tokens}]")
-    return _ints(pos, n_axes * n_tokens, "pos")
+    return _ints(pos, n, "pos", dev)
 
 
-def _table(t, n_seq: int, max_blocks: int):
+def _table(t, n_seq: int, max_blocks: int, dev=None):
     """Block table [>= n_seq][max_blocks], or its values in one dimension; the
     row of a single sequence may go on."""
-    if t is not None and t.dim() != 1 and (t.shape[-1] < max_blocks or (n_seq > 1 and t.shape[-1] > max_blocks)):
-        raise ValueError(f"block_table: rows of {t.shape[-1]} blocks, max_blocks is {max_blocks}")
-    return _ints(t, n_seq * max_blocks, "block_table")
+    if t is not None and (w := t.size(-1)) != max_blocks and t.dim() != 1 and (w < max_blocks or n_seq > 1):
+        raise ValueError(f"block_table: rows of {w} blocks, max_blocks is {max_blocks}")
+    return _ints(t, n_seq * max_blocks, "block_table", dev)
 
 
 def kvs_rope_apply(x, pos, rope: RopeAxes, out, n_tokens, n_heads, head_dim, inverse=False, stream=None):
     """out[t][h] = x[t][h] rotated by its positions pos int32 [axes][n_tokens]
     (taken back with inverse); x and out may be views into wider rows."""
-    xp, xs = _rows(x, n_tokens, n_heads, head_dim, "x")
-    op, os_ = _rows(out, n_tokens, n_heads, head_dim, "out")
-    _check(load().kvs_rope_apply(xp, xs, _positions(pos, rope.n_axes, n_tokens), ctypes.byref(rope), int(inverse), op,
+    dev = _device()
+    xp, xs = _rows(x, n_tokens, n_heads, head_dim, "x", dev)
+    op, os_ = _rows(out, n_tokens, n_heads, head_dim, "out", dev)
+    _check(load().kvs_rope_apply(xp, xs, _positions(pos, rope.n_axes, n_tokens, dev), ctypes.byref(rope), int(inverse), op,
                                  os_, n_tokens, n_heads, head_dim, _stream(stream)))
 
 
@@ -423,42 +428,43 @@ def kvs_append(pool: Pool, layer, k_new, v_new, n_tokens, tok_off, block_table, 
                rope: Optional[RopeAxes] = None, q=None, n_q_heads=0, q_out=None, stream=None):
     """Write packed new rows k_new / v_new through the block table, keys
     rotated; rotate q into q_out (without gaps) in the same pass."""
-    d = pool.desc
-    kp, ks = _rows(k_new, n_tokens, d.num_kv_heads, d.head_dim, "k_new")
-    vp, vs = _rows(v_new, n_tokens, d.num_kv_heads, d.head_dim, "v_new")
+    d, dev = pool.desc, _device()
+    kp, ks = _rows(k_new, n_tokens, d.num_kv_heads, d.head_dim, "k_new", dev)
+    vp, vs = _rows(v_new, n_tokens, d.num_kv_heads, d.head_dim, "v_new", dev)
     qp = qs = op = 0
     if q is not None:
-        qp, qs = _rows(q, n_tokens, n_q_heads, d.head_dim, "q")
+        qp, qs = _rows(q, n_tokens, n_q_heads, d.head_dim, "q", dev)
     if q_out is not None:
-        op, os_ = _rows(q_out, n_tokens, n_q_heads, d.head_dim, "q_out")
+        op, os_ = _rows(q_out, n_tokens, n_q_heads, d.head_dim, "q_out", dev)
         if os_ != n_q_heads * d.head_dim:
             raise ValueError("q_out: rows without gaps are wanted")
     _check(load().kvs_append(
-        pool.handle, layer, kp, ks, vp, vs, qp, qs, n_q_heads, op, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens,
-        _positions(pos, rope.n_axes if rope is not None else 1, n_tokens),
-        ctypes.byref(rope) if rope is not None else None, _table(block_table, n_seq, max_blocks),
-        max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq, _stream(stream)))
+        pool.handle, layer, kp, ks, vp, vs, qp, qs, n_q_heads, op, _ints(tok_off, n_seq + 1, "tok_off", dev), n_tokens,
+        _positions(pos, rope.n_axes if rope is not None else 1, n_tokens, dev),
+        ctypes.byref(rope) if rope is not None else None, _table(block_table, n_seq, max_blocks, dev),
+        max_blocks, _ints(seq_len, n_seq, "seq_len", dev), n_seq, _stream(stream)))
 
 
 def kvs_gather(pool: Pool, layer, n_tokens, tok_off, block_table, max_blocks, seq_len, n_seq, k_out, v_out, stream=None):
     """Read the rows that kvs_append with the same arguments would write, as
     bf16 [n_tokens][num_kv_heads][head_dim]."""
-    d = pool.desc
+    d, dev = pool.desc, _device()
     gap = d.num_kv_heads * d.head_dim
-    kp, ks = _rows(k_out, n_tokens, d.num_kv_heads, d.head_dim, "k_out")
-    vp, vs = _rows(v_out, n_tokens, d.num_kv_heads, d.head_dim, "v_out")
+    kp, ks = _rows(k_out, n_tokens, d.num_kv_heads, d.head_dim, "k_out", dev)
+    vp, vs = _rows(v_out, n_tokens, d.num_kv_heads, d.head_dim, "v_out", dev)
     if ks != gap or vs != gap:
         raise ValueError("k_out, v_out: rows without gaps are wanted")
-    _check(load().kvs_gather(pool.handle, layer, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens,
-                             _table(block_table, n_seq, max_blocks), max_blocks,
-                             _ints(seq_len, n_seq, "seq_len"), n_seq, kp, vp, _stream(stream)))
+    _check(load().kvs_gather(pool.handle, layer, _ints(tok_off, n_seq + 1, "tok_off", dev), n_tokens,
+                             _table(block_table, n_seq, max_blocks, dev), max_blocks,
+                             _ints(seq_len, n_seq, "seq_len", dev), n_seq, kp, vp, _stream(stream)))
 
 
-def _ws(ws):
+def _ws(ws, dev=None):
     """(pointer, bytes) of a workspace of any type, (NULL, 0) of none."""
     if ws is None:
         return None, 0
-    if not _here(ws) or not ws.is_contiguous():
+    at = ws.get_device()
+    if at < 0 or at != (_device() if dev is None else dev) or not ws.is_contiguous():
         raise ValueError("ws: a contiguous CUDA tensor of the current device is wanted")
     return ws.data_ptr(), ws.numel() * ws.element_size()
 
@@ -472,21 +478,22 @@ def kvs_extend_workspace_size(pool: Pool, n_tokens: int, n_seq: int, max_blocks:
 def kvs_extend_plan(pool: Pool, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq, causal, ws,
                     stream=None):
     """The work plan of a batch of query chunks, for every layer of a step."""
-    _check(load().kvs_extend_plan(pool.handle, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens, n_q_heads,
-                                  _table(block_table, n_seq, max_blocks), max_blocks,
-                                  _ints(seq_len, n_seq, "seq_len"), n_seq, int(causal), *_ws(ws), _stream(stream)))
+    dev = _device()
+    _check(load().kvs_extend_plan(pool.handle, _ints(tok_off, n_seq + 1, "tok_off", dev), n_tokens, n_q_heads,
+                                  _table(block_table, n_seq, max_blocks, dev), max_blocks,
+                                  _ints(seq_len, n_seq, "seq_len", dev), n_seq, int(causal), *_ws(ws, dev), _stream(stream)))
 
 
 def _extend(fn, pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq, causal, scale, out,
             ws, stream):
-    d = pool.desc
-    qp, qs = _rows(q, n_tokens, n_q_heads, d.head_dim, "q")
-    op, os_ = _rows(out, n_tokens, n_q_heads, d.head_dim, "out")
+    d, dev = pool.desc, _device()
+    qp, qs = _rows(q, n_tokens, n_q_heads, d.head_dim, "q", dev)
+    op, os_ = _rows(out, n_tokens, n_q_heads, d.head_dim, "out", dev)
     if os_ != n_q_heads * d.head_dim:
         raise ValueError("out: rows without gaps are wanted")
-    _check(fn(pool.handle, layer, qp, qs, _ints(tok_off, n_seq + 1, "tok_off"), n_tokens, n_q_heads,
-              _table(block_table, n_seq, max_blocks), max_blocks, _ints(seq_len, n_seq, "seq_len"), n_seq,
-              int(causal), scale, op, *_ws(ws), _stream(stream)))
+    _check(fn(pool.handle, layer, qp, qs, _ints(tok_off, n_seq + 1, "tok_off", dev), n_tokens, n_q_heads,
+              _table(block_table, n_seq, max_blocks, dev), max_blocks, _ints(seq_len, n_seq, "seq_len", dev), n_seq,
+              int(causal), scale, op, *_ws(ws, dev), _stream(stream)))
 
 
 def kvs_extend_attn_planned(pool: Pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq,

@@ -25,6 +25,9 @@ class On:
     def dim(self):
         return len(self.shape)
 
+    def size(self, i):
+        return self.shape[i]
+
     def numel(self):
         n = 1
         for x in self.shape:
