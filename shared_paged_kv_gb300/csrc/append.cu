@@ -4,11 +4,13 @@
 // All three move rows of head_dim values once from one place to another, so
 // HBM bounds them (large calls) or the chain of dependent loads that finds a
 // token's place: its sequence (a search of tok_off), the sequence's length,
-// the block table's entry (single-token calls).  Measured: 11,600 prompt
-// tokens, 32 KV and 32 query heads: 88 us, 6.4 TB/s; 16,384 rows of 40 heads on
-// three axes: 51 us, 6.6 TB/s; 32 single tokens: 3.5 us.  Into a 4-bit pool the
-// codes' arithmetic is the limit, 60 % of the issue slots (7,900 tokens, 8 KV
-// and 32 query heads: 38.5 us, 4.4 TB/s); read back from it, 11.7 us.
+// the block table's entry (single-token calls).  Measured in CUDA-graph replays:
+// 11,600 prompt tokens, 32 KV and 32 query heads: 88 us, 6.4 TB/s; 16,384 rows of
+// 40 heads on three axes: 51 us, 6.6 TB/s; 32 single tokens: 3.5 us (as a call
+// from Python 8 to 10, the host's time).  Into a 4-bit pool the codes'
+// arithmetic is the limit, 60 % of the issue slots (7,900 tokens, 8 KV and 32
+// query heads: 38.5 us, 4.4 TB/s; at five CTAs per SM, 48 registers, a thread of
+// this kernel spills 64 bytes); read back from it, 11.7 us.
 //
 // Split: a CTA takes 1 or 4 tokens.  Its first step finds each token's place
 // and computes cos / sin once for all heads of a token (head_dim / 2 angles,

@@ -12,7 +12,7 @@
 //    M = 128 rows of a tile.  A CTA holds two tiles, A and B, of consecutive
 //    tokens, and streams the keys in tiles of 128 through both: each K / V tile
 //    that TMA brings (block by block through the block table, 128-byte
-//    swizzle) feeds four 128 x 128 x head_dim products.
+//    swizzle) feeds six 128 x 128 x head_dim products.
 //  * S = Q K^T lands in tensor memory; two warpgroups (one per tile, one row
 //    per thread, so the softmax needs no shuffles) turn it into P = 2^(s - m)
 //    in the same columns, and O += P V takes P from tensor memory.
@@ -39,12 +39,14 @@
 // What bounds it: in long chunks the products, and the chain S, softmax, P V of a
 // row tile.  The six products of a tile pair take 3,072 cycles of the tensor
 // cores (2,048 of them P V's two parts), and two chains share the SM: a pair
-// takes about 4,600.  Replayed in a CUDA graph: 8,192 rows after 8,192 tokens,
-// 32 heads of 128: 1.56 ms, 1,055 TFLOP/s; 16 chunks over one document of 8,192
-// states: 447 us, 968 TFLOP/s.  Few rows over long contexts are bound by the
-// items' chains, starts and ends (64 sequences of 3 to 8 rows over 8,192 shared
-// and 1,000 to 6,100 own tokens: 260 us, 3.8 TB/s), calls without a plan by one
-// chain of key tiles (12 rows over 1,300 states: 25 us).
+// takes about 4,600, the tensor pipe is busy 76 % of the time on the busiest SM.
+// Times of CUDA-graph replays / of public calls one by one: 8,192 rows after
+// 8,192 tokens, 32 heads of 128: 1.55 to 1.59 / 1.61 ms, 1,040 to 1,065 / 1,026
+// TFLOP/s of the formula's operations; 16 chunks over one document of 8,192
+// states: 450 / 471 us.  Few rows over long contexts are bound by the items'
+// chains, starts and ends (64 sequences of 3 to 8 rows over 8,192 shared and
+// 1,000 to 6,100 own tokens: 260 / 264 us, 3.8 TB/s), calls without a plan by one
+// chain of key tiles (12 rows over 1,300 states: 25 / 26 us).
 #include <algorithm>
 #include <cmath>
 
@@ -144,7 +146,7 @@ ExWorkspace ex_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blo
   w.max_items = (int)(w.max_units + extra);
   // Rows of a unit x its pieces: every row of its own and of a shared range
   // once, and 2 * 128 rows for each piece beyond the first.  One sequence shares
-  // nothing, and its units are split only while they are few (the plan's rule).
+  // nothing; at most 4 * SMs / heads units of it are split (the plan's rules).
   // Calls above kExPartRows make no parts; they keep the room of those below, so
   // that a workspace serves every call of no more tokens, sequences and blocks.
   const long long with_parts = std::min<long long>(n_tokens, kExPartRows / ((long long)g * hkv));
