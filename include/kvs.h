@@ -576,6 +576,56 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
                            int32_t n_seq, int32_t causal, float scale, void* out_dev, void* ws, size_t ws_bytes,
                            cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------
+ * Making room: eviction by accumulated attention weight.  Where kvs_evict_score
+ * judges whole blocks by age and region, these calls judge single tokens by
+ * the attention that they have received:
+ * mass          float [n_seq][max_blocks * block_tokens]: mass[a][t] is the
+ *               weight that token t of sequence a has gathered, over query
+ *               rows and heads (and layers, where a caller adds them up); only
+ *               t < seq_len[a] is read.
+ * A step of an eviction: the masses are gathered while the model runs,
+ * kvs_keep_heavy lists the tokens to keep, kvs_compact closes the gaps.  Keys
+ * stay as they were rotated; a later kvs_append gives its rows' true positions
+ * in pos.
+ *
+ * kvs_keep_heavy: of every sequence it keeps the first n_first and the last
+ * n_recent tokens, and of those between, the ones of largest mass (ties: the
+ * lower token; -0 equals 0, NaN is below every number), until budget_dev[a]
+ * tokens are kept (or more, where the first and the last are more; all, where
+ * the sequence has fewer).  Their indices, ascending, go to idx_out_dev
+ * [idx_off[a] .. idx_off[a + 1]), idx_off_dev int64 [n_seq + 1]; idx_out holds
+ * their number, at most n_seq * max_blocks * block_tokens.  budget_dev int32
+ * [n_seq].  seq_len outside the table's row (KVS_DEVERR_SEQ_LEN) is clamped.
+ * The masses are not changed.  Any pool. */
+kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* seq_len_dev, int32_t n_seq,
+                          int32_t max_blocks, const int32_t* budget_dev, int32_t n_first, int32_t n_recent,
+                          int32_t* idx_out_dev, int64_t* idx_off_dev, cudaStream_t stream);
+
+/* Compaction: in every layer, row idx[i] of a sequence moves to place i, for
+ * the list idx_dev [idx_off[a] .. idx_off[a + 1]) of kvs_keep_heavy or of the
+ * caller (strictly ascending, below seq_len[a]), and seq_len[a] becomes the
+ * list's length.  mass_dev (or NULL) moves along, and is 0 from there to the
+ * old length.  Blocks in front of the first token that moves stay as they are.
+ * The others are written in place where the sequence alone references them
+ * (refcount 1 when the call begins); a block with other references stays for
+ * those, and the sequence takes the block on top of the free stack (sequence by
+ * sequence, in block order).  Blocks behind the last kept token are given up:
+ * their table entries become -1.  Counts and the free stack as for
+ * kvs_block_write and kvs_seq_release: the blocks that reached 0 are pushed in
+ * descending order of their ids, after all were taken.  Rows behind a
+ * sequence's kept tokens, in its last block, are left as they were.
+ * A sequence is left as it was where its list is not ascending or leaves it
+ * (KVS_DEVERR_JOB), its seq_len lies outside its table row (KVS_DEVERR_SEQ_LEN),
+ * a block id outside the pool (KVS_DEVERR_BLOCK_ID), or the free stack does not
+ * hold enough blocks (KVS_DEVERR_CAPACITY).  Each sequence is listed once.
+ * Mirror diffs are not moved: a sequence with diffs is not compacted.
+ * Any pool.  ws: kvs_workspace_size(KVS_OP_COMPACT, n_seq, max_blocks) bytes. */
+kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blocks, int32_t* seq_len_dev,
+                       int32_t n_seq, const int32_t* idx_dev, const int64_t* idx_off_dev, float* mass_dev,
+                       int32_t* refcount_dev, int32_t* free_ids_dev, int32_t* n_free_dev, void* ws, size_t ws_bytes,
+                       cudaStream_t stream);
+
 /* Test-only switches.  KVS_TEST_STALL_ONE_STAGE: the next kvs_decode_attn /
  * kvs_decode_attn_planned launch with a query group <= 8 leaves one ring
  * stage of one warp unarmed, so that warp's bounded wait runs out (about a
@@ -603,6 +653,7 @@ kvs_status kvs_pool_set_test_flags(kvs_pool* pool, uint32_t flags);
 #define KVS_OP_SELECT 3
 #define KVS_OP_MIRROR 4
 #define KVS_OP_BLOCKS 5   /* n_seq = n_items = max(n_writes, n_seq); max_blocks unused */
+#define KVS_OP_COMPACT 6
 kvs_status kvs_workspace_size(const kvs_pool* pool, int32_t op, int32_t n_seq,
                               int32_t max_blocks, int32_t n_q_heads, size_t* bytes);
 

@@ -136,6 +136,9 @@ kvs_status launch_wide_tile(const WideParams& p, const kvs_pool* pool, int layer
 // Mirror construction (mirror.cu).
 size_t mirror_workspace_bytes(int n_seq, int max_blocks);
 
+// Compaction behind an eviction (compact.cu).
+size_t compact_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks);
+
 // Block lifetime (blocks.cu).
 size_t blocks_workspace_bytes(int capacity, int n_items);
 

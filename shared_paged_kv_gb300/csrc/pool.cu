@@ -327,6 +327,9 @@ kvs_status kvs_workspace_size(const kvs_pool* p, int32_t op, int32_t n_seq, int3
     case KVS_OP_BLOCKS:
       b = blocks_workspace_bytes(p->desc.capacity_blocks, n_seq);
       break;
+    case KVS_OP_COMPACT:
+      b = compact_workspace_bytes(p, n_seq, max_blocks);
+      break;
     default:
       return fail(KVS_ERR_INVALID_ARG, "workspace_size: unknown op");
   }

@@ -43,6 +43,7 @@ KVS_DTYPE_BF16 = 0
 KVS_DTYPE_Q4G64 = 1
 KVS_DEDUP_TEST_WEAK_KEYS = 0x1
 KVS_OP_DEDUP, KVS_OP_DECODE_ATTN, KVS_OP_DECODE_ATTN_Q4, KVS_OP_SELECT, KVS_OP_MIRROR, KVS_OP_BLOCKS = 0, 1, 2, 3, 4, 5
+KVS_OP_COMPACT = 6
 
 EXPORTED = [
     "kvs_pool_create", "kvs_pool_destroy", "kvs_fingerprint_dedup", "kvs_rope_rerotate",
@@ -52,7 +53,7 @@ EXPORTED = [
     "kvs_pool_block_bytes", "kvs_pool_export", "kvs_pool_import", "kvs_pool_set_test_flags",
     "kvs_workspace_size", "kvs_pool_check", "kvs_pool_stats", "kvs_last_error_string",
     "kvs_launch_count", "kvs_rope_apply", "kvs_append", "kvs_gather", "kvs_extend_workspace_size",
-    "kvs_extend_plan", "kvs_extend_attn_planned", "kvs_extend_attn",
+    "kvs_extend_plan", "kvs_extend_attn_planned", "kvs_extend_attn", "kvs_keep_heavy", "kvs_compact",
 ]
 
 
@@ -128,6 +129,8 @@ def load(path: str = LIB_PATH):
         "kvs_extend_plan": [P, P, I32, I32, P, I32, P, I32, I32, P, SZ, P],
         "kvs_extend_attn_planned": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, P, SZ, P],
         "kvs_extend_attn": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, P, SZ, P],
+        "kvs_keep_heavy": [P, P, P, I32, I32, P, I32, I32, P, P, P],
+        "kvs_compact": [P, P, I32, P, I32, P, P, P, P, P, P, P, SZ, P],
         "kvs_pool_check": [P, P, ctypes.POINTER(U32)],
         "kvs_pool_stats": [P, P, P, P, ctypes.POINTER(Stats)],
     }
@@ -357,7 +360,7 @@ def kvs_quantize_q4(pool: Pool, layer, k_src, v_src, dst_blocks, n_blocks, strea
                                   n_blocks, _stream(stream)))
 
 
-_BF16, _I16, _I32 = torch.bfloat16, torch.int16, torch.int32
+_BF16, _I16, _I32, _F32 = torch.bfloat16, torch.int16, torch.int32, torch.float32
 
 
 def _device() -> int:
@@ -507,6 +510,56 @@ def kvs_extend_attn(pool: Pool, layer, q, n_tokens, tok_off, n_q_heads, block_ta
     """Attention of packed query chunks (bf16 out); see include/kvs.h."""
     _extend(load().kvs_extend_attn, pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq,
             causal, scale, out, ws, stream)
+
+
+def _floats(t, n: int, what: str, dev=None):
+    """Pointer of a contiguous float32 tensor of at least n values."""
+    if t is None:
+        return None
+    at = t.get_device()
+    if (t.dtype is not _F32 or at < 0 or at != (_device() if dev is None else dev) or not t.is_contiguous()
+            or t.numel() < n):
+        raise ValueError(f"{what}: a contiguous float32 CUDA tensor of at least {n} values on the current device is wanted")
+    return t.data_ptr()
+
+
+def _offsets(t, n: int, what: str, dev=None):
+    at = t.get_device()
+    if (t.dtype is not torch.int64 or at < 0 or at != (_device() if dev is None else dev) or not t.is_contiguous()
+            or t.numel() < n):
+        raise ValueError(f"{what}: a contiguous int64 CUDA tensor of at least {n} values on the current device is wanted")
+    return t.data_ptr()
+
+
+def _mass(t, pool: Pool, n_seq: int, max_blocks: int, what: str, dev=None):
+    """Masses [>= n_seq][max_blocks * block_tokens], or their values in one dimension."""
+    most = max_blocks * pool.desc.block_tokens
+    if t is not None and t.dim() != 1 and t.size(-1) != most:
+        raise ValueError(f"{what}: rows of {t.size(-1)} tokens, a table row holds {most}")
+    return _floats(t, n_seq * most, what, dev)
+
+
+def kvs_keep_heavy(pool: Pool, mass, seq_len, n_seq, max_blocks, budget, n_first, n_recent, idx, idx_off, stream=None):
+    """List the tokens worth keeping: the first, the last, and of the others
+    those of largest mass, budget[a] in all.  idx holds as many values."""
+    dev = _device()
+    _check(load().kvs_keep_heavy(pool.handle, _mass(mass, pool, n_seq, max_blocks, "mass", dev),
+                                 _ints(seq_len, n_seq, "seq_len", dev), n_seq, max_blocks,
+                                 _ints(budget, n_seq, "budget", dev), n_first, n_recent, _ints(idx, 0, "idx", dev),
+                                 _offsets(idx_off, n_seq + 1, "idx_off", dev), _stream(stream)))
+
+
+def kvs_compact(pool: Pool, block_table, max_blocks, seq_len, n_seq, idx, idx_off, refcount, free_ids, n_free, ws, mass=None,
+                stream=None):
+    """Move the listed tokens' rows of every layer to the front of their
+    sequences, with tables, lengths, counts, the free stack and the masses."""
+    dev, cap = _device(), pool.desc.capacity_blocks
+    _check(load().kvs_compact(pool.handle, _table(block_table, n_seq, max_blocks, dev), max_blocks,
+                              _ints(seq_len, n_seq, "seq_len", dev), n_seq, _ints(idx, 0, "idx", dev),
+                              _offsets(idx_off, n_seq + 1, "idx_off", dev),
+                              _mass(mass, pool, n_seq, max_blocks, "mass", dev), _ints(refcount, cap, "refcount", dev),
+                              _ints(free_ids, cap, "free_ids", dev), _ints(n_free, 1, "n_free", dev), *_ws(ws, dev),
+                              _stream(stream)))
 
 
 def kvs_pool_check(pool: Pool, stream=None) -> int:
