@@ -69,7 +69,7 @@ typedef enum {
 #define KVS_DEVERR_PLAN         0x80u /* kvs_decode_attn_planned saw no matching plan in ws */
 #define KVS_DEVERR_REFCOUNT     0x100u /* a release took a reference count below zero */
 
-typedef enum { KVS_DTYPE_BF16 = 0, KVS_DTYPE_Q4G64 = 1 } kvs_dtype;
+typedef enum { KVS_DTYPE_BF16 = 0, KVS_DTYPE_Q4G64 = 1, KVS_DTYPE_MX4 = 2 } kvs_dtype;
 
 /* Pool geometry.  One K slab and one V slab per layer.
  *   BF16:   slab[capacity_blocks][num_kv_heads][block_tokens][head_dim] bf16.
@@ -78,13 +78,22 @@ typedef enum { KVS_DTYPE_BF16 = 0, KVS_DTYPE_Q4G64 = 1 } kvs_dtype;
  *           [capacity_blocks][num_kv_heads][block_tokens][head_dim/64][2] fp16
  *           (index 0 = scale, 1 = bias; value = scale * code + bias) — [Q4]
  *           §2.1 (ratio 0.281 fixes group 64 with fp16 scale and bias).
+ *   MX4:    codes[capacity_blocks][num_kv_heads][block_tokens][head_dim/2]
+ *           uint8 (element 2i in the low nibble of byte i) plus scales
+ *           [capacity_blocks][num_kv_heads][block_tokens][head_dim/32] uint8, in
+ *           the place of the scale/bias slabs: the microscaled 4-bit floating
+ *           point of the OCP MX formats.  A code is sign, two exponent bits and
+ *           one mantissa bit (0, 0.5, 1, 1.5, 2, 3, 4, 6), a scale byte e the
+ *           factor 2^(e - 127) of its 32 elements: 4.25 bits an element, 0.266
+ *           of bf16.
  *   Mirror diffs: dk/dv slabs [diff_capacity_blocks][num_kv_heads]
  *           [diff_tokens][head_dim] bf16 holding K and V differences added to
  *           a master block — [TD] section 3; diff_tokens = block_tokens for
  *           BF16 pools and 16 (one sub-block of a 256-token block) for Q4G64
  *           pools.
  * Supported by this build: head_dim 64 or 128; BF16 block_tokens 16;
- * Q4G64 block_tokens 256 with head_dim 128. */
+ * Q4G64 block_tokens 256 with head_dim 128; MX4 block_tokens 64 with head_dim
+ * 128, without mirror diffs. */
 typedef struct {
   int32_t num_layers;
   int32_t num_kv_heads;
@@ -100,7 +109,7 @@ typedef struct kvs_pool kvs_pool;
 
 /* Create a pool over caller-owned per-layer slabs.  The pointer arrays are
  * host arrays of num_layers device pointers (16-byte aligned); k_sb/v_sb are
- * required for Q4G64 and must be NULL for BF16; dk/dv are required when
+ * required for Q4G64 and MX4 and must be NULL for BF16; dk/dv are required when
  * diff_capacity_blocks > 0.  Builds one TMA tensor map per slab.  The pool
  * never frees the slabs.  Errors: INVALID_ARG, UNSUPPORTED, CUDA. */
 kvs_status kvs_pool_create(const kvs_pool_desc* desc,
@@ -503,7 +512,11 @@ kvs_status kvs_rope_apply(const void* x_dev, int64_t x_stride, const int32_t* po
  * pos_dev       int32 [n_axes][n_tokens], or NULL with one axis: p itself.
  * q_dev, q_out_dev   both or neither; q_out is bf16 [n_tokens][n_q_heads]
  *               [head_dim] without gaps and may be q itself when q has none.
- * A Q4G64 pool stores what kvs_quantize_q4 makes of the same bf16 values.
+ * A Q4G64 pool stores what kvs_quantize_q4 makes of the same bf16 values.  An
+ * MX4 pool stores, for 32 elements, e = max(0, 127 + floor(log2 max|x|) - 2)
+ * (0 where all are zero) and the codes nearest to x 2^(127 - e), ties to even,
+ * magnitudes above 6 as 6 (an infinity or NaN as one above 2^127, so that its
+ * group stays finite).
  * The written blocks belong to their sequence alone (kvs_block_write first
  * where they are shared): two rows for one place of the pool race.  A token
  * whose place is negative or past the table's row sets KVS_DEVERR_SEQ_LEN, a
@@ -517,7 +530,8 @@ kvs_status kvs_append(kvs_pool* pool, int32_t layer, const void* k_dev, int64_t 
 /* Gather, the way back: k_out / v_out bf16 [n_tokens][num_kv_heads][head_dim]
  * receive the pool's values of the tokens that kvs_append with the same
  * tok_off and seq_len would write (the last n of the first seq_len[a]); Q4G64
- * pools give scale * code + bias, rounded to bf16.  This is the k_cached of
+ * pools give scale * code + bias, rounded to bf16, MX4 pools code * scale, which is
+ * exact.  This is the k_cached of
  * kvs_select_critical.  Rows whose token has no valid place (device errors as
  * for kvs_append) are left as they were. */
 kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* tok_off_dev, int32_t n_tokens,
@@ -584,6 +598,27 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  *               weight that token t of sequence a has gathered, over query
  *               rows and heads (and layers, where a caller adds them up); only
  *               t < seq_len[a] is read.
+ * kvs_decode_attn_mass: attention of one query row per sequence as
+ * kvs_decode_attn computes it (BF16 pools, no mirror diffs, no rotation), and
+ *   mass[a][t] = carry * mass_in[a][t] + sum_h w_ah(t),   t < seq_len[a],
+ * w_ah the weights that multiply the values in out[a][h]; the other entries of
+ * mass are left as they were.  mass_in_dev NULL counts as zeros; it may be mass_dev
+ * itself, and must not overlap it otherwise.  carry 1 adds the step, a smaller
+ * one lets older weights fade.
+ * kvs_decode_attn_mx4: the same over an MX4 pool (the codes are read directly);
+ * mass_dev may be NULL (then mass_in_dev too): attention alone.
+ * q_dev bf16 [n_seq][n_q_heads][head_dim], out_dev float as kvs_decode_attn.
+ * n_q_heads % num_kv_heads == 0, at most 16 query heads per KV head; scale is
+ * positive, and scale * log2(e) finite in float32; stored keys and values below
+ * seq_len are finite, and what the pool holds behind them is never used.  A block
+ * id outside the pool (KVS_DEVERR_BLOCK_ID) takes its tokens out of the
+ * sequence (weight 0); seq_len outside the table's row (KVS_DEVERR_SEQ_LEN) is
+ * clamped; an empty context yields zeros.  Scores, sums and masses are float32,
+ * a weight that multiplies values keeps 16 bits or more.  MX4 values below 2^-27
+ * of the largest scale that their 32 channels have in the sequence count as 0.
+ * The result is the same to the bit for the same call.
+ * ws: kvs_workspace_size(KVS_OP_DECODE_MASS, n_seq, max_blocks, n_q_heads).
+ *
  * A step of an eviction: the masses are gathered while the model runs,
  * kvs_keep_heavy lists the tokens to keep, kvs_compact closes the gaps.  Keys
  * stay as they were rotated; a later kvs_append gives its rows' true positions
@@ -598,6 +633,14 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  * their number, at most n_seq * max_blocks * block_tokens.  budget_dev int32
  * [n_seq].  seq_len outside the table's row (KVS_DEVERR_SEQ_LEN) is clamped.
  * The masses are not changed.  Any pool. */
+kvs_status kvs_decode_attn_mass(kvs_pool* pool, int32_t layer, const void* q_dev, int32_t n_q_heads,
+                                const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                                int32_t n_seq, float scale, float* out_dev, const float* mass_in_dev, float carry,
+                                float* mass_dev, void* ws, size_t ws_bytes, cudaStream_t stream);
+kvs_status kvs_decode_attn_mx4(kvs_pool* pool, int32_t layer, const void* q_dev, int32_t n_q_heads,
+                               const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                               int32_t n_seq, float scale, float* out_dev, const float* mass_in_dev, float carry,
+                               float* mass_dev, void* ws, size_t ws_bytes, cudaStream_t stream);
 kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* seq_len_dev, int32_t n_seq,
                           int32_t max_blocks, const int32_t* budget_dev, int32_t n_first, int32_t n_recent,
                           int32_t* idx_out_dev, int64_t* idx_off_dev, cudaStream_t stream);
@@ -654,6 +697,7 @@ kvs_status kvs_pool_set_test_flags(kvs_pool* pool, uint32_t flags);
 #define KVS_OP_MIRROR 4
 #define KVS_OP_BLOCKS 5   /* n_seq = n_items = max(n_writes, n_seq); max_blocks unused */
 #define KVS_OP_COMPACT 6
+#define KVS_OP_DECODE_MASS 7   /* kvs_decode_attn_mass, kvs_decode_attn_mx4 */
 kvs_status kvs_workspace_size(const kvs_pool* pool, int32_t op, int32_t n_seq,
                               int32_t max_blocks, int32_t n_q_heads, size_t* bytes);
 

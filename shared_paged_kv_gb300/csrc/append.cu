@@ -168,7 +168,28 @@ __device__ __forceinline__ uint32_t q4_codes(const uint32_t* w, __half2& sb) {
   return __byte_perm(__float_as_uint(a), __float_as_uint(c), 0x5410);
 }
 
-enum { kApBf16 = 0, kApQ4 = 1, kApRows = 2 };   // pool type, or rows only (kvs_rope_apply)
+// Microscaled codes of one 32-element group held by 4 consecutive lanes, 8
+// values each as bf16 pairs.  The largest magnitude is found on the bf16 bits;
+// its exponent field less 2 is the scale byte, so that the largest value lies in
+// [4, 8) of the scale, and the products with 2^(127 - e) are exact.
+__device__ __forceinline__ uint32_t mx4_codes(const uint32_t* w, uint32_t& scale) {
+  constexpr uint32_t kAbs = 0x7fff7fffu;
+  uint32_t top = __vmaxu2(__vmaxu2(w[0] & kAbs, w[1] & kAbs), __vmaxu2(w[2] & kAbs, w[3] & kAbs));
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const uint32_t e = max(top & 0xffffu, top >> 16) >> 7;
+  scale = e > 2u ? min(e, 254u) - 2u : 0u;   // infinities and NaN as the largest finite exponent
+  const float up = __uint_as_float((254u - scale) << 23);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]) * up;
+    x[2 * i + 1] = bf16_hi(w[i]) * up;
+  }
+  return mx_codes(x);
+}
+
+enum { kApBf16 = 0, kApQ4 = 1, kApRows = 2, kApMx = 3 };   // pool type, or rows only (kvs_rope_apply)
 
 template <int D, int MODE>
 __global__ void __launch_bounds__(kApThreads, kApCtas) append_kernel(const __grid_constant__ AppendParams p, int tokens_per_cta) {
@@ -275,7 +296,24 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) append_kernel(const __gri
           }
         }
       }
-      if (r >= rows || (MODE == kApQ4 && !is_q)) continue;
+      if (MODE == kApMx) {
+        // groups of 32: four lanes of the low half of a row, four of the high half
+        const uint32_t lw[4] = {lo[i].x, lo[i].y, lo[i].z, lo[i].w};
+        const uint32_t hw[4] = {hi[i].x, hi[i].y, hi[i].z, hi[i].w};
+        if (__any_sync(0xffffffffu, r < 2 * p.hkv)) {
+          uint32_t sl, sh;
+          const uint32_t cl = mx4_codes(lw, sl), ch = mx4_codes(hw, sh);
+          const uint32_t mine = sl | (sh << 16), other = __shfl_down_sync(0xffffffffu, mine, 4);
+          if (r < 2 * p.hkv && w.phys >= 0) {
+            const size_t row = ((size_t)w.phys * p.hkv + (is_v ? r - p.hkv : r)) * p.at.block_tokens + w.at;
+            uint8_t* code = (is_v ? p.vslab : p.kslab) + row * (D / 2);
+            *reinterpret_cast<uint32_t*>(code + v * 4) = cl;
+            *reinterpret_cast<uint32_t*>(code + D / 4 + v * 4) = ch;
+            if (v == 0) reinterpret_cast<uint32_t*>(is_v ? p.vsb : p.ksb)[row] = mine | (other << 8);
+          }
+        }
+      }
+      if (r >= rows || ((MODE == kApQ4 || MODE == kApMx) && !is_q)) continue;
       uint16_t* dst;
       if (is_q) {
         dst = p.q_out + t * p.qos + (size_t)(MODE == kApRows ? r : r - 2 * p.hkv) * D;
@@ -299,7 +337,7 @@ struct GatherParams {
 };
 
 // D / 16 lanes take a row, 16 elements (32 bytes of output) each.
-template <int D, bool Q4>
+template <int D, int MODE>
 __global__ void __launch_bounds__(kApThreads) gather_kernel(const __grid_constant__ GatherParams p, int tokens_per_cta) {
   constexpr int NV = D / 16, RPW = 32 / NV;
   __shared__ Place where[kApTokens];
@@ -324,7 +362,11 @@ __global__ void __launch_bounds__(kApThreads) gather_kernel(const __grid_constan
       if (r >= rows) continue;
       const bool is_v = r >= p.hkv;
       const size_t row = ((size_t)w.phys * p.hkv + (is_v ? r - p.hkv : r)) * p.at.block_tokens + w.at;
-      if constexpr (Q4) {
+      if constexpr (MODE == kApMx) {
+        code[i] = __ldg(reinterpret_cast<const uint2*>((is_v ? p.vslab : p.kslab) + row * (D / 2)) + v);
+        const uint32_t e = __ldg(reinterpret_cast<const uint8_t*>(is_v ? p.vsb : p.ksb) + row * (D / 32) + v / 2);
+        sb[i].x = __uint_as_float(e ? e << 23 : 0x00400000u);   // 2^(e - 127)
+      } else if constexpr (MODE == kApQ4) {
         code[i] = __ldg(reinterpret_cast<const uint2*>((is_v ? p.vslab : p.kslab) + row * (D / 2)) + v);
         sb[i] = __half22float2(__ldg(reinterpret_cast<const __half2*>(is_v ? p.vsb : p.ksb) + row * 2 + v / 4));
       } else {
@@ -338,7 +380,18 @@ __global__ void __launch_bounds__(kApThreads) gather_kernel(const __grid_constan
       const int r = rb + i * rstep;
       if (r >= rows) continue;
       const bool is_v = r >= p.hkv;
-      if constexpr (Q4) {   // code * scale is exact in float32, so this is one rounding of the sum
+      if constexpr (MODE == kApMx) {
+        uint32_t h[8], o[8];
+        mx_pairs(code[i].x, h);
+        mx_pairs(code[i].y, h + 4);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h[e]));
+          o[e] = pack_bf16(f.x * sb[i].x, f.y * sb[i].x);
+        }
+        x[i][0] = make_uint4(o[0], o[1], o[2], o[3]);
+        x[i][1] = make_uint4(o[4], o[5], o[6], o[7]);
+      } else if constexpr (MODE == kApQ4) {   // code * scale is exact in float32, so this is one rounding of the sum
         uint32_t o[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
@@ -498,8 +551,8 @@ extern "C" kvs_status kvs_append(kvs_pool* pool, int32_t layer, const void* k_de
   p.pos = pos_dev;
   p.kslab = static_cast<uint8_t*>(pool->k[layer]);
   p.vslab = static_cast<uint8_t*>(pool->v[layer]);
-  const bool q4 = d.dtype == KVS_DTYPE_Q4G64;
-  if (q4) {
+  const bool q4 = d.dtype == KVS_DTYPE_Q4G64, mx = d.dtype == KVS_DTYPE_MX4;
+  if (q4 || mx) {
     p.ksb = static_cast<__half*>(pool->ksb[layer]);
     p.vsb = static_cast<__half*>(pool->vsb[layer]);
   }
@@ -508,7 +561,9 @@ extern "C" kvs_status kvs_append(kvs_pool* pool, int32_t layer, const void* k_de
   if (axes) axes_turns(axes, d.head_dim, p);
   const int tpc = append_tokens_per_cta(n_tokens, pool->num_sms);
   const unsigned grid = (unsigned)((n_tokens + tpc - 1) / tpc);
-  if (q4)
+  if (mx)
+    append_kernel<128, kApMx><<<grid, kApThreads, 0, stream>>>(p, tpc);
+  else if (q4)
     append_kernel<128, kApQ4><<<grid, kApThreads, 0, stream>>>(p, tpc);
   else if (d.head_dim == 128)
     append_kernel<128, kApBf16><<<grid, kApThreads, 0, stream>>>(p, tpc);
@@ -536,8 +591,8 @@ extern "C" kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* t
                    d.capacity_blocks, d.block_tokens};
   p.kslab = static_cast<const uint8_t*>(pool->k[layer]);
   p.vslab = static_cast<const uint8_t*>(pool->v[layer]);
-  const bool q4 = d.dtype == KVS_DTYPE_Q4G64;
-  if (q4) {
+  const bool q4 = d.dtype == KVS_DTYPE_Q4G64, mx = d.dtype == KVS_DTYPE_MX4;
+  if (q4 || mx) {
     p.ksb = static_cast<const __half*>(pool->ksb[layer]);
     p.vsb = static_cast<const __half*>(pool->vsb[layer]);
   }
@@ -546,12 +601,14 @@ extern "C" kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* t
   p.hkv = d.num_kv_heads;
   const int tpc = append_tokens_per_cta(n_tokens, pool->num_sms);
   const unsigned grid = (unsigned)((n_tokens + tpc - 1) / tpc);
-  if (q4)
-    gather_kernel<128, true><<<grid, kApThreads, 0, stream>>>(p, tpc);
+  if (mx)
+    gather_kernel<128, kApMx><<<grid, kApThreads, 0, stream>>>(p, tpc);
+  else if (q4)
+    gather_kernel<128, kApQ4><<<grid, kApThreads, 0, stream>>>(p, tpc);
   else if (d.head_dim == 128)
-    gather_kernel<128, false><<<grid, kApThreads, 0, stream>>>(p, tpc);
+    gather_kernel<128, kApBf16><<<grid, kApThreads, 0, stream>>>(p, tpc);
   else
-    gather_kernel<64, false><<<grid, kApThreads, 0, stream>>>(p, tpc);
+    gather_kernel<64, kApBf16><<<grid, kApThreads, 0, stream>>>(p, tpc);
   count_launch();
   return check_launch("gather");
 }

@@ -1,0 +1,806 @@
+// Decode attention that also adds up each stored token's attention weight, over
+// bf16 pools and pools of microscaled 4-bit values.
+//
+//   w_h(t) = e^(scale q_h.K_t) / sum_t' e^(scale q_h.K_t'),  out_h = sum_t w_h(t) V_t,
+//   mass[t] = carry * mass_in[t] + sum_h w_h(t)
+//
+// in one pass over keys and values: the weights need the whole sum, so the first
+// kernel leaves its scores (4 bytes per token and head, against 512 / G bytes of
+// keys and values) and the second turns them into weights with the final
+// maximum and sum.
+//
+// Work: the blocks of all sequences, KV head by KV head, form one line that the
+// CTAs of one wave share evenly, whatever the lengths; a CTA's stretch may
+// cover the ends of several (sequence, KV head) pairs, and a pair several CTAs,
+// whose parts the last one to arrive joins in their order.  A warp takes every
+// W-th unit of its CTA's stretch and brings it with its own ring of TMA copies,
+// which run on across the pairs' borders.
+//
+// Tokens are the 16 rows of the products, query heads the 8 (or twice 8)
+// columns: S^T = K q^T, O^T += V^T P^T.  P^T is the transposed accumulator of S^T
+// (movmatrix) in two 16-bit parts, so that a weight keeps 16 bits or more.  The
+// reference of the exponentials moves only when a score exceeds it by more than
+// 2^4, so that a unit needs no exchange between lanes.
+//
+// bf16: a unit is a block of 16 tokens; operands by ldmatrix.
+// Microscaled: a unit is 32 tokens.  A byte holds two e2m1 values, which one
+// conversion turns into an fp16 pair.  Keys: the products of a group of 32
+// channels are scaled by the group's power of two in fp32, exactly.  Values: a
+// token's scale multiplies the fp16 pairs, relative to the largest one that this
+// warp has met in the group (E): 2^(e - E + 13), exact for e >= E - 27 and zero
+// below, which is 2^-24 of nothing that a sum in fp32 would keep; the
+// accumulators follow E when it grows.  Row r of a product is token
+// r ^ (r >> 1 & 1) of its 16, with which all shared loads (64-byte swizzle) are
+// free of bank conflicts.
+#include <algorithm>
+#include <cmath>
+
+#include "common.cuh"
+#include "internal.h"
+#include "merge.cuh"
+
+namespace kvs {
+
+namespace {
+
+enum { kFmtBf16x64, kFmtBf16x128, kFmtMx };
+
+constexpr int kDmMaxGroup = 16, kDmMaxStages = 6;
+
+template <int FMT, int NT>
+struct Dm {   // what a format and the number of 8-column tiles fix
+  static constexpr bool mx = FMT == kFmtMx;
+  static constexpr int D = FMT == kFmtBf16x64 ? 64 : 128;
+  static constexpr int UT = mx ? 32 : 16;                 // tokens of a unit
+  static constexpr int kBlockTokens = mx ? 64 : 16;
+  static constexpr int W = mx || NT == 2 ? 8 : 4;         // warps of a CTA
+  static constexpr int kCtas = NT == 1 ? 2 : 1;           // per SM
+  static constexpr int kCodes = mx ? UT * D / 2 : UT * D * 2;   // bytes of a unit's K or V
+  static constexpr int kScales = mx ? UT * 4 : 0;
+  static constexpr int kStage = 2 * kCodes + (mx ? 512 : 0);    // scales in the last 512 bytes
+  static constexpr int ST = mx || NT == 2 ? 2 : FMT == kFmtBf16x64 ? 6 : 3;
+  static constexpr int kHead = W == 4 ? 1024 : 2048;      // barriers and the warps' sums, in front of the ring
+  // two CTAs with three stages of 128 channels and eight heads fill the SM's shared memory to the byte
+  static constexpr int kSmem = kHead + W * (ST * kStage + NT * 8 * D * 4);
+  static constexpr float kBias = mx ? 11.f : 0.f;         // weights reach 2^(kBias + kLag)
+};
+constexpr float kLag = 4.f;
+
+template <int W>
+struct DmShared {
+  uint64_t full[W][kDmMaxStages];
+  float2 ml[W][kDmMaxGroup];
+  float m[kDmMaxGroup], l[kDmMaxGroup];
+  int warp_sums[32];
+  int a, b, last;
+};
+
+struct DmParams {
+  const uint16_t* q;            // bf16 [n_seq][hq][D]
+  const int32_t *table, *seq_len;
+  const uint8_t *ksc, *vsc;     // scale bytes of this layer
+  float* out;
+  float* part;                  // [CTAs + pairs][g][D]
+  float* part_ml;               // [CTAs + pairs][g][2]
+  float2* fin;                  // [pairs][g] {reference, 1 / sum}
+  float* scores;                // [pair][max tokens][g], or nullptr
+  int32_t* tickets;
+  uint32_t* status;
+  int n_seq, max_blocks, hkv, g, hq, capacity, most;   // most: tokens of a table row
+  float scale_log2;
+};
+
+__device__ __forceinline__ uint32_t movm_t(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ void split_f16(float x, float y, uint32_t& hi, uint32_t& lo) {
+  hi = pack_f16(x, y);
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi));
+  lo = pack_f16(x - f.x, y - f.y);
+}
+__device__ __forceinline__ int mx_token(int r) { return r ^ ((r >> 1) & 1); }   // of row r of 16
+
+struct DmSpan {   // a sequence's length and units
+  int len, units;
+};
+template <int UT>
+__device__ __forceinline__ DmSpan dm_span(const DmParams& p, int a) {
+  const int len = min(max(__ldg(p.seq_len + a), 0), p.most);
+  return DmSpan{len, (len + UT - 1) / UT};
+}
+
+// A place on the line of units.
+struct DmAt {
+  int h, a, b, units;   // KV head, sequence, unit in it, its units
+};
+template <int UT>
+__device__ __forceinline__ void dm_advance(const DmParams& p, DmAt& at, int by) {
+  at.b += by;
+  while (at.h < p.hkv && at.b >= at.units) {
+    at.b -= at.units;
+    if (++at.a == p.n_seq) {
+      at.a = 0;
+      ++at.h;
+    }
+    at.units = dm_span<UT>(p, at.a).units;
+  }
+}
+
+template <int FMT, int NT>
+__global__ void __launch_bounds__(Dm<FMT, NT>::W * 32, Dm<FMT, NT>::kCtas)
+decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv) {
+  using F = Dm<FMT, NT>;
+  constexpr int D = F::D, W = F::W, UT = F::UT, ST = F::ST, MT = UT / 16, T = W * 32;
+  static_assert(sizeof(DmShared<W>) <= F::kHead && ST <= kDmMaxStages, "the ring begins behind the head");
+  extern __shared__ __align__(1024) uint8_t smem_raw[];   // no static shared memory: it begins on 1,024 bytes
+  DmShared<W>& sh = *reinterpret_cast<DmShared<W>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+  uint8_t* ring = smem_raw + F::kHead + warp * ST * F::kStage;
+  float* s_acc = reinterpret_cast<float*>(smem_raw + F::kHead + W * ST * F::kStage);   // [W][g][D]
+  if (tid == 0) {
+    prefetch_tmap(&tk);
+    prefetch_tmap(&tv);
+  }
+  if (lane == 0) {
+    for (int s = 0; s < ST; ++s) mbar_init(&sh.full[warp][s], 1);
+    fence_barrier_init();
+  }
+  pdl_enter();
+
+  // ---- this CTA's stretch of the line
+  int per_head = 0;
+  for (int a0 = 0; a0 < p.n_seq; a0 += T) {
+    const int a = a0 + tid;
+    int total;
+    block_exclusive_scan(a < p.n_seq ? dm_span<UT>(p, a).units : 0, sh.warp_sums, total);
+    per_head += total;
+  }
+  for (int a = blockIdx.x; a < p.n_seq; a += gridDim.x) {
+    const int raw = p.seq_len[a];
+    if (tid == 0 && (raw < 0 || raw > p.most)) set_err(p.status, KVS_DEVERR_SEQ_LEN);
+    if (raw <= 0)
+      for (int i = tid; i < p.hq * D; i += T) p.out[(size_t)a * p.hq * D + i] = 0.f;
+  }
+  const long long units = (long long)per_head * p.hkv;
+  const long long per = max((long long)W, (units + gridDim.x - 1) / gridDim.x);
+  const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
+  if (u0 >= u1) return;
+  const int h0 = (int)(u0 / per_head), r0 = (int)(u0 - (long long)h0 * per_head);
+  int carry = 0;
+  for (int a0 = 0; a0 < p.n_seq; a0 += T) {
+    const int a = a0 + tid, n = a < p.n_seq ? dm_span<UT>(p, a).units : 0;
+    int total;
+    const int before = carry + block_exclusive_scan(n, sh.warp_sums, total);
+    if (before <= r0 && r0 < before + n) {
+      sh.a = a;
+      sh.b = r0 - before;
+    }
+    carry += total;
+  }
+  __syncthreads();
+  const int n_mine = (int)(u1 - u0);
+  DmAt seg{h0, sh.a, sh.b, dm_span<UT>(p, sh.a).units};
+
+  // ---- copies of this warp's units k = warp, warp + W, ...
+  DmAt ahead = seg;
+  dm_advance<UT>(p, ahead, warp);
+  int k_ahead = warp;
+  auto look_up = [&]() {   // physical block of the unit ahead
+    if (k_ahead >= n_mine) return -1;
+    return __ldg(p.table + (size_t)ahead.a * p.max_blocks + ahead.b * UT / F::kBlockTokens);
+  };
+  int id_ahead = look_up(), stage_ahead = 0;
+  auto issue = [&]() {     // whole warp; lane 0 copies
+    if (k_ahead >= n_mine) return;
+    const int s = stage_ahead;
+    if (++stage_ahead == ST) stage_ahead = 0;
+    if (lane == 0) {
+      uint64_t* bar = &sh.full[warp][s];
+      if (id_ahead < 0 || id_ahead >= p.capacity) {
+        mbar_arrive(bar);
+      } else {
+        mbar_arrive_expect_tx(bar, 2 * (F::kCodes + F::kScales));
+        uint8_t* st = ring + s * F::kStage;
+        const int row = (id_ahead * p.hkv + ahead.h) * F::kBlockTokens + ahead.b * UT % F::kBlockTokens;
+        if constexpr (F::mx) {
+          tma_load_2d(st, &tk, 0, row, bar);
+          tma_load_2d(st + F::kCodes, &tv, 0, row, bar);
+          bulk_load(st + 2 * F::kCodes, p.ksc + (size_t)row * 4, F::kScales, bar);
+          bulk_load(st + 2 * F::kCodes + F::kScales, p.vsc + (size_t)row * 4, F::kScales, bar);
+        } else {
+          tma_load_kv_tile<D>(st, &tk, row, bar);
+          tma_load_kv_tile<D>(st + F::kCodes, &tv, row, bar);
+        }
+      }
+    }
+    k_ahead += W;
+    if (k_ahead < n_mine) dm_advance<UT>(p, ahead, W);
+    id_ahead = look_up();
+  };
+  for (int i = 0; i < ST; ++i) issue();
+
+  int k = warp;                    // this warp's next unit, relative to u0
+  int stage = 0, uses = 0;
+  uint32_t phase = 0;
+  bool dead = false;
+  DmAt cur = seg;
+  dm_advance<UT>(p, cur, warp);
+  for (int done = 0; done < n_mine;) {
+    // ---- one (sequence, KV head): units [seg.b, seg.units) as far as the stretch goes
+    const int n_seg = min(seg.units - seg.b, n_mine - done);
+    const int len = dm_span<UT>(p, seg.a).len;
+    const uint16_t* qp = p.q + ((size_t)seg.a * p.hq + seg.h * p.g) * D;
+    // queries as the B operand: column g of n-tile nt, in the order of the
+    // channels in which K's fragments come
+    uint32_t qb[NT][D / 16][2];
+    float cs[NT][2];   // scale of the scores of columns 2c and 2c + 1
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int row = nt * 8 + g;
+      const bool ok = row < p.g;
+      cs[nt][0] = cs[nt][1] = p.scale_log2;
+      if constexpr (F::mx) {
+        uint4 w[4];
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          w[j] = ok ? __ldg(reinterpret_cast<const uint4*>(qp + (size_t)row * D + 32 * j + 8 * c)) : make_uint4(0u, 0u, 0u, 0u);
+          const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(fabsf(bf16_lo(x[e])), fabsf(bf16_hi(x[e]))));
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // a power of two brings the row's largest value to [2^10, 2^11): products
+        // with codes up to 6 stay far inside fp32, and values down to 2^-24 of
+        // the largest keep all their bits
+        const int be = (int)((__float_as_uint(top) >> 23) & 255u);
+        int e = be > 0 && be < 255 ? be - 127 - 10 : 0;
+        e = min(max(e, -100), 113);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t x[4] = {w[j].x, w[j].y, w[j].z, w[j].w};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) qb[nt][2 * j + i / 2][i & 1] = pack_f16(bf16_lo(x[i]) * down, bf16_hi(x[i]) * down);
+        }
+        cs[nt][0] *= __shfl_sync(0xffffffffu, up, 8 * c);
+        cs[nt][1] *= __shfl_sync(0xffffffffu, up, 8 * c + 4);
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            qb[nt][j][i] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qp + (size_t)row * D + 16 * j + 8 * i + 2 * c)) : 0u;
+      }
+    }
+    float ref[NT][2], l[NT][2], acc[NT][D / 16][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      ref[nt][0] = ref[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < D / 16; ++j) acc[nt][j][0] = acc[nt][j][1] = acc[nt][j][2] = acc[nt][j][3] = 0.f;
+    }
+    uint32_t top_e = 0;   // microscaled: the largest scale byte met of each group of channels
+    float* sc_out = p.scores ? p.scores + ((size_t)seg.a * p.hkv + seg.h) * p.most * p.g : nullptr;
+
+    while (k < done + n_seg) {
+      const int t_unit = cur.b * UT, nv = min(UT, len - t_unit);
+      const int phys = __ldg(p.table + (size_t)cur.a * p.max_blocks + t_unit / F::kBlockTokens);
+      const bool in_pool = phys >= 0 && phys < p.capacity;
+      if (!in_pool && lane == 0) set_err(p.status, KVS_DEVERR_BLOCK_ID);
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[warp][stage], phase, p.status))) dead = true;
+      uint8_t* kc = ring + stage * F::kStage;
+      uint8_t* vc = kc + F::kCodes;
+      if (in_pool && !dead) {
+        float s[MT][NT][4];
+        // ---- S^T, in units of log2
+        if constexpr (F::mx) {
+          const uint8_t* ksc = kc + 2 * F::kCodes;
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            const int t0 = mt * 16 + mx_token(g), t1 = t0 + 8;
+            const uint32_t e0 = *reinterpret_cast<const uint32_t*>(ksc + t0 * 4), e1 = *reinterpret_cast<const uint32_t*>(ksc + t1 * 4);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              uint32_t x0[4], x1[4];
+              mx_pairs(*reinterpret_cast<const uint32_t*>(kc + swz64(t0 * 64 + 16 * j + 4 * c)), x0);
+              mx_pairs(*reinterpret_cast<const uint32_t*>(kc + swz64(t1 * 64 + 16 * j + 4 * c)), x1);
+              // a byte's power of two: the byte becomes the exponent
+              const float f0 = __uint_as_float((j == 3 ? e0 >> 1 : e0 << (23 - 8 * j)) & 0x7f800000u);
+              const float f1 = __uint_as_float((j == 3 ? e1 >> 1 : e1 << (23 - 8 * j)) & 0x7f800000u);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                float y[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(y, x0[0], x1[0], x0[1], x1[1], qb[nt][2 * j][0], qb[nt][2 * j][1]);
+                mma_f16(y, x0[2], x1[2], x0[3], x1[3], qb[nt][2 * j + 1][0], qb[nt][2 * j + 1][1]);
+                float* z = s[mt][nt];
+                const float2 a = __ffma2_rn(make_float2(y[0], y[1]), make_float2(f0, f0), make_float2(z[0], z[1]));
+                const float2 b = __ffma2_rn(make_float2(y[2], y[3]), make_float2(f1, f1), make_float2(z[2], z[3]));
+                z[0] = a.x; z[1] = a.y; z[2] = b.x; z[3] = b.y;
+              }
+            }
+          }
+        } else {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) s[0][nt][0] = s[0][nt][1] = s[0][nt][2] = s[0][nt][3] = 0.f;
+          const uint32_t ka = smem_u32(kc);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t x[4];
+            ldsm_x4(ka + kv_tile_off<D>(lane & 15, j * 16 + (lane >> 4) * 8), x[0], x[1], x[2], x[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_bf16(s[0][nt], x, qb[nt][j][0], qb[nt][j][1]);
+          }
+        }
+        bool above = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          const int t0 = mt * 16 + (F::mx ? mx_token(g) : g), t1 = t0 + 8;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& y = s[mt][nt][e];
+              y = (e < 2 ? t0 : t1) < nv ? y * cs[nt][e & 1] : -INFINITY;
+              above |= y > ref[nt][e & 1] + kLag;
+            }
+            if (sc_out) {
+              const int col = nt * 8 + 2 * c;
+              float* o0 = sc_out + (size_t)(t_unit + t0) * p.g + col;
+              float* o1 = sc_out + (size_t)(t_unit + t1) * p.g + col;
+              if ((p.g & 1) == 0) {
+                if (col < p.g && t0 < nv) *reinterpret_cast<float2*>(o0) = make_float2(s[mt][nt][0], s[mt][nt][1]);
+                if (col < p.g && t1 < nv) *reinterpret_cast<float2*>(o1) = make_float2(s[mt][nt][2], s[mt][nt][3]);
+              } else {
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                  if (col + i < p.g && t0 < nv) o0[i] = s[mt][nt][i];
+                  if (col + i < p.g && t1 < nv) o1[i] = s[mt][nt][2 + i];
+                }
+              }
+            }
+          }
+        }
+        if (__any_sync(0xffffffffu, above)) {
+          // some column's reference moves to its maximum so far
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float f[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float mx = -INFINITY;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(s[mt][nt][i], s[mt][nt][2 + i]));
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+              const float next = mx > ref[nt][i] + kLag ? mx : ref[nt][i];
+              f[i] = next > ref[nt][i] ? fast_exp2(ref[nt][i] - next) : 1.f;
+              ref[nt][i] = next;
+              l[nt][i] *= f[i];
+            }
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              acc[nt][j][0] *= f[0]; acc[nt][j][1] *= f[1];
+              acc[nt][j][2] *= f[0]; acc[nt][j][3] *= f[1];
+            }
+          }
+        }
+        // ---- weights, transposed into the B operand
+        uint32_t ph[MT][NT][2], pl[MT][NT][2];
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = fast_exp2(s[mt][nt][e] - (ref[nt][e & 1] - F::kBias));
+            l[nt][0] += w[0] + w[2];
+            l[nt][1] += w[1] + w[3];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              uint32_t hi, lo;
+              if constexpr (F::mx) split_f16(w[2 * i], w[2 * i + 1], hi, lo);
+              else split_bf16(w[2 * i], w[2 * i + 1], hi, lo);
+              ph[mt][nt][i] = movm_t(hi);
+              pl[mt][nt][i] = movm_t(lo);
+            }
+          }
+        // ---- O^T += V^T P^T
+        if constexpr (F::mx) {
+          const uint8_t* vsc = kc + 2 * F::kCodes + F::kScales;
+          // E: the largest scale so far in each group of channels, over tokens of the sequence
+          const uint32_t mine = lane < nv ? *reinterpret_cast<const uint32_t*>(vsc + lane * 4) : 0u;
+          if (__any_sync(0xffffffffu, __vcmpgtu4(mine, top_e) != 0u)) {
+            uint32_t next = __vmaxu4(mine, top_e);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) next = __vmaxu4(next, __shfl_xor_sync(0xffffffffu, next, o));
+            const int up = (int)((next >> (8 * (g >> 1))) & 255u) - (int)((top_e >> (8 * (g >> 1))) & 255u);
+            const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
+            top_e = next;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][j][e] *= f;
+          }
+          const int rel = 28 - (int)((top_e >> (8 * (g >> 1))) & 255u);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            {
+              // tokens of the four rows 2c, 2c + 1, 2c + 8, 2c + 9; channels 16 g .. 16 g + 15
+              uint2 v[4];
+              uint32_t sc[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const int t = mt * 16 + mx_token(2 * c + (i & 1)) + 8 * (i >> 1);
+                v[i] = *reinterpret_cast<const uint2*>(vc + swz64(t * 64 + 16 * (g >> 1)) + 8 * (g & 1));
+                const int e = (int)vsc[t * 4 + (g >> 1)] + rel;
+                sc[i] = (uint32_t)min(max(e, 0), 28) << 10;
+              }
+              const uint32_t s01 = sc[0] | (sc[1] << 16), s89 = sc[2] | (sc[3] << 16);
+#pragma unroll
+              for (int word = 0; word < 2; ++word) {
+                const uint32_t w0 = word ? v[0].y : v[0].x, w1 = word ? v[1].y : v[1].x;
+                const uint32_t w8 = word ? v[2].y : v[2].x, w9 = word ? v[3].y : v[3].x;
+                constexpr uint32_t kLow = 0x0f0f0f0fu;
+                uint32_t a0[4], a1[4], a2[4], a3[4];   // even channels, odd ones; tokens 2c, 2c + 1 and 2c + 8, 2c + 9
+                mx_pairs((w0 & kLow) | ((w1 << 4) & ~kLow), a0);
+                mx_pairs(((w0 >> 4) & kLow) | (w1 & ~kLow), a1);
+                mx_pairs((w8 & kLow) | ((w9 << 4) & ~kLow), a2);
+                mx_pairs(((w8 >> 4) & kLow) | (w9 & ~kLow), a3);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  const uint32_t x0 = mul_f16x2(a0[j], s01), x1 = mul_f16x2(a1[j], s01);
+                  const uint32_t x2 = mul_f16x2(a2[j], s89), x3 = mul_f16x2(a3[j], s89);
+#pragma unroll
+                  for (int nt = 0; nt < NT; ++nt) {
+                    mma_f16(acc[nt][word * 4 + j], x0, x1, x2, x3, ph[mt][nt][0], ph[mt][nt][1]);
+                    mma_f16(acc[nt][word * 4 + j], x0, x1, x2, x3, pl[mt][nt][0], pl[mt][nt][1]);
+                  }
+                }
+              }
+            }
+          }
+        } else {
+          if (nv < UT) {
+            // rows behind the end hold anything, and 0 * NaN is not 0
+            for (int i = lane; i < (UT - nv) * (D / 8); i += 32)
+              *reinterpret_cast<uint4*>(vc + kv_tile_off<D>(nv + i / (D / 8), (i % (D / 8)) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+            __syncwarp();
+          }
+          const uint32_t va = smem_u32(vc);
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            uint32_t x[4];
+            ldsm_x4_t(va + kv_tile_off<D>((lane & 7) + (lane >> 4) * 8, j * 16 + ((lane >> 3) & 1) * 8), x[0], x[1], x[2], x[3]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              mma_bf16(acc[nt][j], x, ph[0][nt][0], ph[0][nt][1]);
+              mma_bf16(acc[nt][j], x, pl[0][nt][0], pl[0][nt][1]);
+            }
+          }
+          if (nv < UT) fence_proxy_async_smem();   // the zeros are written before a copy overwrites them
+        }
+      } else if (sc_out) {
+        for (int i = lane; i < nv * p.g; i += 32) sc_out[(size_t)t_unit * p.g + i] = -INFINITY;
+      }
+      __syncwarp();
+      if (++stage == ST) {
+        stage = 0;
+        phase ^= 1u;
+      }
+      ++uses;
+      if (!dead) issue();
+      k += W;
+      if (k < n_mine) dm_advance<UT>(p, cur, W);
+    }
+
+    // ---- the warps' states become one
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], o);
+        const int row = nt * 8 + 2 * c + i;
+        if (row >= p.g) continue;
+        if (g == 0) sh.ml[warp][row] = make_float2(ref[nt][i] - F::kBias, l[nt][i]);
+        const int e = (int)((top_e >> (8 * (g >> 1))) & 255u) - 140;   // 2^(E - 127 - 13)
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          float* o = s_acc + ((size_t)warp * p.g + row) * D;
+          if constexpr (F::mx) {
+            *reinterpret_cast<float2*>(o + 16 * g + 2 * j) = make_float2(ldexpf(acc[nt][j][i], e), ldexpf(acc[nt][j][2 + i], e));
+          } else {
+            o[16 * j + g] = acc[nt][j][i];
+            o[16 * j + g + 8] = acc[nt][j][2 + i];
+          }
+        }
+      }
+    __syncthreads();
+    const long long first = u0 + done - seg.b;    // the pair's first unit on the line
+    const int cta0 = (int)(first / per), n_parts = (int)((first + seg.units - 1) / per) - cta0 + 1;
+    const int order = seg.h * p.n_seq + seg.a, pair = seg.a * p.hkv + seg.h;
+    const size_t slot = (size_t)blockIdx.x + order;
+    for (int i = tid; i < p.g * (D / 4); i += T) {
+      const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
+      float M = -INFINITY, L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < W; ++w)
+        if (sh.ml[w][row].y > 0.f) M = fmaxf(M, sh.ml[w][row].x);
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float2 ml = sh.ml[w][row];
+        const float f = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
+        const float4 x = *reinterpret_cast<const float4*>(s_acc + ((size_t)w * p.g + row) * D + col);
+        L += f * ml.y;
+        o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+      }
+      if (n_parts == 1) {
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        *reinterpret_cast<float4*>(p.out + ((size_t)seg.a * p.hq + seg.h * p.g + row) * D + col) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        if (col == 0 && p.scores) p.fin[(size_t)pair * p.g + row] = make_float2(L > 0.f ? M : 0.f, inv);
+      } else {
+        __stcg(reinterpret_cast<float4*>(p.part + (slot * p.g + row) * D + col), o);
+        if (col == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + (slot * p.g + row) * 2), make_float2(M, L));
+      }
+    }
+    if (n_parts > 1 && arrive_last(p.tickets + pair, n_parts, &sh.last)) {
+      // the last CTA of the pair joins the parts in their order
+      const size_t s0 = (size_t)cta0 + order;
+      for (int row = warp; row < p.g; row += W) {
+        float M = -INFINITY, L = 0.f;
+        for (int s = lane; s < n_parts; s += 32) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((s0 + s) * p.g + row) * 2));
+          if (ml.y > 0.f) M = fmaxf(M, ml.x);
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+        for (int s = lane; s < n_parts; s += 32) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((s0 + s) * p.g + row) * 2));
+          L += ml.y > 0.f ? fast_exp2(ml.x - M) * ml.y : 0.f;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+        if (lane == 0) {
+          sh.m[row] = M;
+          sh.l[row] = L > 0.f ? 1.f / L : 0.f;
+          if (p.scores) p.fin[(size_t)pair * p.g + row] = make_float2(L > 0.f ? M : 0.f, sh.l[row]);
+        }
+      }
+      __syncthreads();
+      for (int i = tid; i < p.g * (D / 4); i += T) {
+        const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
+        const float M = sh.m[row], inv = sh.l[row];
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+        for (int s = 0; s < n_parts; ++s) {
+          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((s0 + s) * p.g + row) * 2));
+          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part + ((s0 + s) * p.g + row) * D + col));
+          const float f = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
+          o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
+        }
+        *reinterpret_cast<float4*>(p.out + ((size_t)seg.a * p.hq + seg.h * p.g + row) * D + col) =
+            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+      }
+    }
+    __syncthreads();   // the states are read: the next pair's may be written
+    done += n_seg;
+    if (done < n_mine) dm_advance<UT>(p, seg, n_seg);
+  }
+  if (dead)   // copies in flight land before the shared memory goes away
+    for (int i = 0; i < ST; ++i) {
+      const int use = uses + i;
+      if (warp + use * W < k_ahead) mbar_drain(&sh.full[warp][use % ST], (use / ST) & 1);
+    }
+}
+
+// ------------------------------------------------------------------- mass ---
+struct AddMassParams {
+  const float* scores;
+  const float2* fin;
+  const int32_t* seq_len;
+  const float* mass_in;
+  float* mass;
+  int n_seq, hkv, g, most;
+  float carry;
+};
+
+constexpr int kMassThreads = 256;
+
+// A thread takes a token; the heads in their order, so the sum is the same in
+// every call.  G4: the heads of a group four at a time.
+template <bool G4>
+__global__ void __launch_bounds__(kMassThreads) add_mass_kernel(const __grid_constant__ AddMassParams p) {
+  extern __shared__ float2 s_fin[];   // [hkv * g]
+  const int a = blockIdx.y;
+  pdl_enter();
+  const int len = min(max(__ldg(p.seq_len + a), 0), p.most);
+  const int t = blockIdx.x * kMassThreads + threadIdx.x;
+  if ((int)blockIdx.x * kMassThreads >= len) return;
+  for (int i = threadIdx.x; i < p.hkv * p.g; i += kMassThreads) s_fin[i] = p.fin[(size_t)a * p.hkv * p.g + i];
+  __syncthreads();
+  if (t >= len) return;
+  float sum = 0.f;
+  const size_t step = (size_t)p.most * p.g;
+  const float* s = p.scores + (size_t)a * p.hkv * step + (size_t)t * p.g;
+  if constexpr (G4) {
+#pragma unroll 4
+    for (int h = 0; h < p.hkv; ++h, s += step)
+      for (int i = 0; i < p.g; i += 4) {
+        const float4 x = __ldcs(reinterpret_cast<const float4*>(s + i));
+        const float2* f = s_fin + h * p.g + i;
+        sum += fast_exp2(x.x - f[0].x) * f[0].y;
+        sum += fast_exp2(x.y - f[1].x) * f[1].y;
+        sum += fast_exp2(x.z - f[2].x) * f[2].y;
+        sum += fast_exp2(x.w - f[3].x) * f[3].y;
+      }
+  } else {
+#pragma unroll 8
+    for (int h = 0; h < p.hkv; ++h, s += step)
+      for (int i = 0; i < p.g; ++i) {
+        const float2 f = s_fin[h * p.g + i];
+        sum += fast_exp2(__ldcs(s + i) - f.x) * f.y;
+      }
+  }
+  const size_t o = (size_t)a * p.most + t;
+  p.mass[o] = p.mass_in ? fmaf(p.carry, p.mass_in[o], sum) : sum;
+}
+
+struct DmLayout {
+  size_t part, ml, fin, scores, total;
+};
+DmLayout dm_layout(const kvs_pool* pool, int n_seq, int max_blocks, int g) {
+  const kvs_pool_desc& d = pool->desc;
+  DmLayout l{};
+  size_t o = 0;
+  auto take = [&](size_t b) {
+    const size_t at = o;
+    o += (b + 255) & ~size_t{255};
+    return at;
+  };
+  const size_t pairs = (size_t)n_seq * d.num_kv_heads, parts = (size_t)pool->num_sms * 2 + pairs;
+  l.part = take(parts * g * d.head_dim * 4);
+  l.ml = take(parts * g * 8);
+  l.fin = take(pairs * g * 8);
+  l.scores = take(pairs * g * (size_t)max_blocks * d.block_tokens * 4);
+  l.total = o;
+  return l;
+}
+
+template <int FMT, int NT>
+bool launch_dm(const DmParams& p, const kvs_pool* pool, int layer, cudaStream_t stream) {
+  constexpr int smem = Dm<FMT, NT>::kSmem;
+  if (!smem_limit_once<decode_mass_kernel<FMT, NT>>(smem, pool->device)) return false;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(pool->num_sms * Dm<FMT, NT>::kCtas));
+  cfg.blockDim = dim3(Dm<FMT, NT>::W * 32);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, decode_mass_kernel<FMT, NT>, p, pool->tk[layer], pool->tv[layer]) == cudaSuccess;
+}
+
+kvs_status decode_mass(kvs_pool* pool, int32_t layer, const void* q, int32_t n_q_heads, const int32_t* table, int32_t max_blocks,
+                       const int32_t* seq_len, int32_t n_seq, float scale, float* out, const float* mass_in, float carry,
+                       float* mass, void* ws, size_t ws_bytes, cudaStream_t stream, const std::string& what) {
+  const kvs_pool_desc& d = pool->desc;
+  if (layer < 0 || layer >= d.num_layers) return fail(KVS_ERR_INVALID_ARG, what + ": layer out of range");
+  if (n_seq < 0 || max_blocks < 1) return fail(KVS_ERR_INVALID_ARG, what + ": bad sizes");
+  if (n_seq > d.max_seqs) return fail(KVS_ERR_CAPACITY, what + ": n_seq exceeds the pool's max_seqs");
+  if (n_q_heads < 1 || n_q_heads % d.num_kv_heads) return fail(KVS_ERR_INVALID_ARG, what + ": n_q_heads must be a multiple of num_kv_heads");
+  const int g = n_q_heads / d.num_kv_heads;
+  if (g > kDmMaxGroup) return fail(KVS_ERR_UNSUPPORTED, what + ": more than 16 query heads per KV head");
+  if (n_q_heads > 6144) return fail(KVS_ERR_UNSUPPORTED, what + ": more than 6,144 query heads");
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.f) || !std::isfinite(scale_log2)) return fail(KVS_ERR_INVALID_ARG, what + ": scale must be positive and finite");
+  if (!std::isfinite(carry)) return fail(KVS_ERR_INVALID_ARG, what + ": carry must be finite");
+  if (!mass && mass_in) return fail(KVS_ERR_INVALID_ARG, what + ": mass_in without mass");
+  if (n_seq > 65535) return fail(KVS_ERR_UNSUPPORTED, what + ": more than 65,535 sequences");
+  const long long most = (long long)max_blocks * d.block_tokens;
+  if (most > 0x40000000ll || most * n_seq > 0x7fffffffll * 8) return fail(KVS_ERR_CAPACITY, what + ": too many tokens in the tables");
+  if (n_seq == 0) return KVS_OK;
+  if (!q || !table || !seq_len || !out || !ws) return fail(KVS_ERR_INVALID_ARG, what + ": null pointer");
+  if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return fail(KVS_ERR_INVALID_ARG, what + ": q, out and ws must be 16-byte aligned");
+  const DmLayout l = dm_layout(pool, n_seq, max_blocks, g);
+  if (ws_bytes < l.total) return fail(KVS_ERR_CAPACITY, what + ": workspace too small");
+  if (kvs_status st = check_pool_device(pool, what.c_str()); st != KVS_OK) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  DmParams p{};
+  p.q = static_cast<const uint16_t*>(q);
+  p.table = table;
+  p.seq_len = seq_len;
+  const bool mx = d.dtype == KVS_DTYPE_MX4;
+  if (mx) {
+    p.ksc = static_cast<const uint8_t*>(pool->ksb[layer]);
+    p.vsc = static_cast<const uint8_t*>(pool->vsb[layer]);
+  }
+  p.out = out;
+  p.part = reinterpret_cast<float*>(w + l.part);
+  p.part_ml = reinterpret_cast<float*>(w + l.ml);
+  p.fin = reinterpret_cast<float2*>(w + l.fin);
+  p.scores = mass ? reinterpret_cast<float*>(w + l.scores) : nullptr;
+  p.tickets = pool->tickets;
+  p.status = pool->status;
+  p.n_seq = n_seq;
+  p.max_blocks = max_blocks;
+  p.hkv = d.num_kv_heads;
+  p.g = g;
+  p.hq = n_q_heads;
+  p.capacity = d.capacity_blocks;
+  p.most = (int)most;
+  p.scale_log2 = scale_log2;
+  bool ok;
+  if (mx)
+    ok = g <= 8 ? launch_dm<kFmtMx, 1>(p, pool, layer, stream) : launch_dm<kFmtMx, 2>(p, pool, layer, stream);
+  else if (d.head_dim == 128)
+    ok = g <= 8 ? launch_dm<kFmtBf16x128, 1>(p, pool, layer, stream) : launch_dm<kFmtBf16x128, 2>(p, pool, layer, stream);
+  else
+    ok = g <= 8 ? launch_dm<kFmtBf16x64, 1>(p, pool, layer, stream) : launch_dm<kFmtBf16x64, 2>(p, pool, layer, stream);
+  if (ok) count_launch();
+  if (ok && mass) {
+    AddMassParams m{p.scores, p.fin, seq_len, mass_in, mass, n_seq, p.hkv, g, p.most, carry};
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)((most + kMassThreads - 1) / kMassThreads), (unsigned)n_seq);
+    cfg.blockDim = dim3(kMassThreads);
+    cfg.dynamicSmemBytes = (size_t)n_q_heads * sizeof(float2);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    ok = cudaLaunchKernelEx(&cfg, g % 4 ? add_mass_kernel<false> : add_mass_kernel<true>, m) == cudaSuccess;
+    if (ok) count_launch();
+  }
+  return check_launch(what.c_str());
+}
+
+}  // namespace
+
+size_t decode_mass_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks, int g) {
+  return dm_layout(pool, n_seq, max_blocks, g).total;
+}
+
+}  // namespace kvs
+
+using namespace kvs;
+
+extern "C" kvs_status kvs_decode_attn_mass(kvs_pool* pool, int32_t layer, const void* q_dev, int32_t n_q_heads,
+                                           const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                                           int32_t n_seq, float scale, float* out_dev, const float* mass_in_dev, float carry,
+                                           float* mass_dev, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!pool) return fail(KVS_ERR_INVALID_ARG, "decode_attn_mass: null pool");
+  if (pool->desc.dtype != KVS_DTYPE_BF16) return fail(KVS_ERR_INVALID_ARG, "decode_attn_mass: pool is not BF16");
+  if (!mass_dev && n_seq != 0) return fail(KVS_ERR_INVALID_ARG, "decode_attn_mass: null mass");
+  return decode_mass(pool, layer, q_dev, n_q_heads, block_table_dev, max_blocks, seq_len_dev, n_seq, scale, out_dev, mass_in_dev,
+                     carry, mass_dev, ws, ws_bytes, stream, "decode_attn_mass");
+}
+
+extern "C" kvs_status kvs_decode_attn_mx4(kvs_pool* pool, int32_t layer, const void* q_dev, int32_t n_q_heads,
+                                          const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                                          int32_t n_seq, float scale, float* out_dev, const float* mass_in_dev, float carry,
+                                          float* mass_dev, void* ws, size_t ws_bytes, cudaStream_t stream) {
+  if (!pool) return fail(KVS_ERR_INVALID_ARG, "decode_attn_mx4: null pool");
+  if (pool->desc.dtype != KVS_DTYPE_MX4) return fail(KVS_ERR_INVALID_ARG, "decode_attn_mx4: pool is not MX4");
+  return decode_mass(pool, layer, q_dev, n_q_heads, block_table_dev, max_blocks, seq_len_dev, n_seq, scale, out_dev, mass_in_dev,
+                     carry, mass_dev, ws, ws_bytes, stream, "decode_attn_mx4");
+}

@@ -136,6 +136,9 @@ kvs_status launch_wide_tile(const WideParams& p, const kvs_pool* pool, int layer
 // Mirror construction (mirror.cu).
 size_t mirror_workspace_bytes(int n_seq, int max_blocks);
 
+// Decode attention with the tokens' weights (decode_mass.cu).
+size_t decode_mass_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks, int g);
+
 // Compaction behind an eviction (compact.cu).
 size_t compact_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks);
 

@@ -108,8 +108,8 @@ static bool encode_bf16_slab(CUtensorMap* m, void* base, long long rows, int hea
   return r == CUDA_SUCCESS;
 }
 
-// Q4 code slab [rows][64 bytes] (head_dim 128) as uint8 {64, rows}; box
-// {64, block_tokens}; 64-byte swizzle.
+// Code slab of 4-bit values [rows][64 bytes] (head_dim 128) as uint8 {64, rows};
+// box {64, block_tokens} (MX4: half a block); 64-byte swizzle.
 static bool encode_q4_slab(CUtensorMap* m, void* base, long long rows, int row_bytes, int box_rows) {
   auto enc = get_encoder();
   if (!enc) return false;
@@ -143,16 +143,20 @@ kvs_status kvs_pool_create(const kvs_pool_desc* d, void* const* k_layers, void* 
     return fail(KVS_ERR_INVALID_ARG, "pool_create: sizes must be positive");
   if (d->head_dim != 64 && d->head_dim != 128)
     return fail(KVS_ERR_UNSUPPORTED, "pool_create: head_dim must be 64 or 128");
-  const bool q4 = d->dtype == KVS_DTYPE_Q4G64;
-  if (d->dtype != KVS_DTYPE_BF16 && !q4) return fail(KVS_ERR_INVALID_ARG, "pool_create: unknown dtype");
-  if (!q4 && d->block_tokens != 16)
+  const bool q4 = d->dtype == KVS_DTYPE_Q4G64, mx = d->dtype == KVS_DTYPE_MX4, scaled = q4 || mx;
+  if (d->dtype != KVS_DTYPE_BF16 && !scaled) return fail(KVS_ERR_INVALID_ARG, "pool_create: unknown dtype");
+  if (!scaled && d->block_tokens != 16)
     return fail(KVS_ERR_UNSUPPORTED, "pool_create: bf16 pools use 16-token blocks");
   if (q4 && (d->block_tokens != 256 || d->head_dim != 128))
     return fail(KVS_ERR_UNSUPPORTED, "pool_create: Q4G64 pools use 256-token blocks and head_dim 128");
+  if (mx && (d->block_tokens != 64 || d->head_dim != 128))
+    return fail(KVS_ERR_UNSUPPORTED, "pool_create: MX4 pools use 64-token blocks and head_dim 128");
+  if (mx && d->diff_capacity_blocks > 0) return fail(KVS_ERR_UNSUPPORTED, "pool_create: MX4 pools hold no mirror diffs");
   if (q4 && (!k_sb_layers || !v_sb_layers))
     return fail(KVS_ERR_INVALID_ARG, "pool_create: Q4G64 needs scale/bias slabs");
-  if (!q4 && (k_sb_layers || v_sb_layers))
-    return fail(KVS_ERR_INVALID_ARG, "pool_create: scale/bias slabs are for Q4G64 pools only");
+  if (mx && (!k_sb_layers || !v_sb_layers)) return fail(KVS_ERR_INVALID_ARG, "pool_create: MX4 needs scale slabs");
+  if (!scaled && (k_sb_layers || v_sb_layers))
+    return fail(KVS_ERR_INVALID_ARG, "pool_create: scale/bias slabs are for Q4G64 and MX4 pools only");
   if (d->diff_capacity_blocks > 0 && (!dk_layers || !dv_layers))
     return fail(KVS_ERR_INVALID_ARG, "pool_create: diff slabs missing");
   const long long rows = static_cast<long long>(d->capacity_blocks) * d->num_kv_heads * d->block_tokens;
@@ -171,7 +175,7 @@ kvs_status kvs_pool_create(const kvs_pool_desc* d, void* const* k_layers, void* 
   const int L = d->num_layers;
   for (int l = 0; l < L; ++l) {
     const bool bad = !k_layers[l] || !v_layers[l] || !aligned16(k_layers[l]) || !aligned16(v_layers[l]) ||
-                     (q4 && (!k_sb_layers[l] || !v_sb_layers[l] || !aligned16(k_sb_layers[l]) ||
+                     (scaled && (!k_sb_layers[l] || !v_sb_layers[l] || !aligned16(k_sb_layers[l]) ||
                              !aligned16(v_sb_layers[l]))) ||
                      (d->diff_capacity_blocks > 0 &&
                       (!dk_layers[l] || !dv_layers[l] || !aligned16(dk_layers[l]) || !aligned16(dv_layers[l])));
@@ -181,7 +185,7 @@ kvs_status kvs_pool_create(const kvs_pool_desc* d, void* const* k_layers, void* 
     }
     p->k.push_back(k_layers[l]);
     p->v.push_back(v_layers[l]);
-    if (q4) {
+    if (scaled) {
       p->ksb.push_back(k_sb_layers[l]);
       p->vsb.push_back(v_sb_layers[l]);
     }
@@ -198,9 +202,10 @@ kvs_status kvs_pool_create(const kvs_pool_desc* d, void* const* k_layers, void* 
   }
   for (int l = 0; l < L; ++l) {
     bool ok;
-    if (q4) {
-      ok = encode_q4_slab(&p->tk[l], p->k[l], rows, d->head_dim / 2, d->block_tokens) &&
-           encode_q4_slab(&p->tv[l], p->v[l], rows, d->head_dim / 2, d->block_tokens);
+    if (scaled) {
+      const int box = mx ? d->block_tokens / 2 : d->block_tokens;
+      ok = encode_q4_slab(&p->tk[l], p->k[l], rows, d->head_dim / 2, box) &&
+           encode_q4_slab(&p->tv[l], p->v[l], rows, d->head_dim / 2, box);
     } else {
       ok = encode_bf16_slab(&p->tk[l], p->k[l], rows, d->head_dim, d->block_tokens) &&
            encode_bf16_slab(&p->tv[l], p->v[l], rows, d->head_dim, d->block_tokens);
@@ -226,11 +231,12 @@ kvs_status kvs_pool_create(const kvs_pool_desc* d, void* const* k_layers, void* 
   std::vector<long long> sbytes;
   const long long per_block_rows = static_cast<long long>(d->num_kv_heads) * d->block_tokens;
   for (int l = 0; l < L; ++l) {
-    const long long row = q4 ? d->head_dim / 2 : d->head_dim * 2;
+    const long long row = scaled ? d->head_dim / 2 : d->head_dim * 2;
     slabs.push_back(p->k[l]); sbytes.push_back(per_block_rows * row);
     slabs.push_back(p->v[l]); sbytes.push_back(per_block_rows * row);
-    if (q4) {
-      const long long sb = (d->head_dim / 64) * 4;   // fp16 scale + bias per 64-element group
+    if (scaled) {
+      // fp16 scale + bias per 64-element group, or a scale byte per 32
+      const long long sb = q4 ? (d->head_dim / 64) * 4 : d->head_dim / 32;
       slabs.push_back(p->ksb[l]); sbytes.push_back(per_block_rows * sb);
       slabs.push_back(p->vsb[l]); sbytes.push_back(per_block_rows * sb);
     }
@@ -327,6 +333,11 @@ kvs_status kvs_workspace_size(const kvs_pool* p, int32_t op, int32_t n_seq, int3
     case KVS_OP_BLOCKS:
       b = blocks_workspace_bytes(p->desc.capacity_blocks, n_seq);
       break;
+    case KVS_OP_DECODE_MASS: {
+      if (n_q_heads < 1 || n_q_heads % p->desc.num_kv_heads) return fail(KVS_ERR_INVALID_ARG, "workspace_size: n_q_heads");
+      b = decode_mass_workspace_bytes(p, n_seq, max_blocks, n_q_heads / p->desc.num_kv_heads);
+      break;
+    }
     case KVS_OP_COMPACT:
       b = compact_workspace_bytes(p, n_seq, max_blocks);
       break;
@@ -371,9 +382,7 @@ kvs_status kvs_pool_stats(const kvs_pool* p, const int32_t* refcount_dev, const 
     st.total_refs += r;
     if (r > 1) st.shared_blocks++;
   }
-  const int64_t per_block = p->desc.dtype == KVS_DTYPE_BF16
-                                ? 2ll * p->desc.num_kv_heads * p->desc.block_tokens * p->desc.head_dim * 2
-                                : 2ll * p->desc.num_kv_heads * p->desc.block_tokens * (p->desc.head_dim / 2 + p->desc.head_dim / 16);
+  const int64_t per_block = p->blk_record / p->desc.num_layers;
   st.pool_bytes = st.unique_blocks * per_block * p->desc.num_layers;
   st.dense_bytes = st.total_refs * per_block * p->desc.num_layers;
   *out = st;

@@ -41,9 +41,10 @@ KVS_TEST_EXTEND_PLANNED = 0x4
 
 KVS_DTYPE_BF16 = 0
 KVS_DTYPE_Q4G64 = 1
+KVS_DTYPE_MX4 = 2
 KVS_DEDUP_TEST_WEAK_KEYS = 0x1
 KVS_OP_DEDUP, KVS_OP_DECODE_ATTN, KVS_OP_DECODE_ATTN_Q4, KVS_OP_SELECT, KVS_OP_MIRROR, KVS_OP_BLOCKS = 0, 1, 2, 3, 4, 5
-KVS_OP_COMPACT = 6
+KVS_OP_COMPACT, KVS_OP_DECODE_MASS = 6, 7
 
 EXPORTED = [
     "kvs_pool_create", "kvs_pool_destroy", "kvs_fingerprint_dedup", "kvs_rope_rerotate",
@@ -54,6 +55,7 @@ EXPORTED = [
     "kvs_workspace_size", "kvs_pool_check", "kvs_pool_stats", "kvs_last_error_string",
     "kvs_launch_count", "kvs_rope_apply", "kvs_append", "kvs_gather", "kvs_extend_workspace_size",
     "kvs_extend_plan", "kvs_extend_attn_planned", "kvs_extend_attn", "kvs_keep_heavy", "kvs_compact",
+    "kvs_decode_attn_mass", "kvs_decode_attn_mx4",
 ]
 
 
@@ -129,6 +131,8 @@ def load(path: str = LIB_PATH):
         "kvs_extend_plan": [P, P, I32, I32, P, I32, P, I32, I32, P, SZ, P],
         "kvs_extend_attn_planned": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, P, SZ, P],
         "kvs_extend_attn": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, P, SZ, P],
+        "kvs_decode_attn_mass": [P, I32, P, I32, P, I32, P, I32, F32, P, P, F32, P, P, SZ, P],
+        "kvs_decode_attn_mx4": [P, I32, P, I32, P, I32, P, I32, F32, P, P, F32, P, P, SZ, P],
         "kvs_keep_heavy": [P, P, P, I32, I32, P, I32, I32, P, P, P],
         "kvs_compact": [P, P, I32, P, I32, P, P, P, P, P, P, P, SZ, P],
         "kvs_pool_check": [P, P, ctypes.POINTER(U32)],
@@ -537,6 +541,35 @@ def _mass(t, pool: Pool, n_seq: int, max_blocks: int, what: str, dev=None):
     if t is not None and t.dim() != 1 and t.size(-1) != most:
         raise ValueError(f"{what}: rows of {t.size(-1)} tokens, a table row holds {most}")
     return _floats(t, n_seq * most, what, dev)
+
+
+def _decode_mass(fn, pool, layer, q, n_q_heads, block_table, max_blocks, seq_len, n_seq, scale, out, mass_in, carry, mass, ws,
+                 stream):
+    d, dev = pool.desc, _device()
+    gap = n_q_heads * d.head_dim
+    qp, qs = _rows(q, n_seq, n_q_heads, d.head_dim, "q", dev)
+    if qs != gap:
+        raise ValueError("q: rows without gaps are wanted")
+    _check(fn(pool.handle, layer, qp, n_q_heads, _table(block_table, n_seq, max_blocks, dev), max_blocks,
+              _ints(seq_len, n_seq, "seq_len", dev), n_seq, scale, _floats(out, n_seq * gap, "out", dev),
+              _mass(mass_in, pool, n_seq, max_blocks, "mass_in", dev), carry,
+              _mass(mass, pool, n_seq, max_blocks, "mass", dev), *_ws(ws, dev), _stream(stream)))
+
+
+def kvs_decode_attn_mass(pool: Pool, layer, q, n_q_heads, block_table, max_blocks, seq_len, n_seq, scale, out, mass_in, carry,
+                         mass, ws, stream=None):
+    """Decode attention that also adds every token's weight, over the heads:
+    mass = carry * mass_in + weights (float32 [n_seq][max_blocks * block_tokens])."""
+    _decode_mass(load().kvs_decode_attn_mass, pool, layer, q, n_q_heads, block_table, max_blocks, seq_len, n_seq, scale, out,
+                 mass_in, carry, mass, ws, stream)
+
+
+def kvs_decode_attn_mx4(pool: Pool, layer, q, n_q_heads, block_table, max_blocks, seq_len, n_seq, scale, out, ws, mass_in=None,
+                        carry=1.0, mass=None, stream=None):
+    """Decode attention over a pool of microscaled 4-bit values; with mass, the
+    weights are added up as by kvs_decode_attn_mass."""
+    _decode_mass(load().kvs_decode_attn_mx4, pool, layer, q, n_q_heads, block_table, max_blocks, seq_len, n_seq, scale, out,
+                 mass_in, carry, mass, ws, stream)
 
 
 def kvs_keep_heavy(pool: Pool, mass, seq_len, n_seq, max_blocks, budget, n_first, n_recent, idx, idx_off, stream=None):
