@@ -619,6 +619,14 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  * The result is the same to the bit for the same call.
  * ws: kvs_workspace_size(KVS_OP_DECODE_MASS, n_seq, max_blocks, n_q_heads).
  *
+ * kvs_extend_mass: the same sum over the rows of query chunks,
+ *   mass[a][t] = carry * mass_in[a][t] + sum over rows j and heads of w(t),
+ * with rows, limits (causal), q, its stride and the bad cases as for
+ * kvs_extend_attn (weights of rows that see nothing are 0, bad block ids count as
+ * zero keys; with bad offsets nothing is written).  A window of observation is
+ * given as the last rows of every sequence.  Values are not read; BF16 pools.
+ * ws: kvs_extend_mass_workspace_size bytes, for calls with these arguments.
+ *
  * A step of an eviction: the masses are gathered while the model runs,
  * kvs_keep_heavy lists the tokens to keep, kvs_compact closes the gaps.  Keys
  * stay as they were rotated; a later kvs_append gives its rows' true positions
@@ -641,6 +649,13 @@ kvs_status kvs_decode_attn_mx4(kvs_pool* pool, int32_t layer, const void* q_dev,
                                const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
                                int32_t n_seq, float scale, float* out_dev, const float* mass_in_dev, float carry,
                                float* mass_dev, void* ws, size_t ws_bytes, cudaStream_t stream);
+kvs_status kvs_extend_mass_workspace_size(const kvs_pool* pool, int32_t n_tokens, int32_t n_seq, int32_t max_blocks,
+                                          int32_t n_q_heads, size_t* bytes);
+kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void* q_dev, int64_t q_stride,
+                           const int32_t* tok_off_dev, int32_t n_tokens, int32_t n_q_heads,
+                           const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
+                           int32_t n_seq, int32_t causal, float scale, const float* mass_in_dev, float carry,
+                           float* mass_dev, void* ws, size_t ws_bytes, cudaStream_t stream);
 kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* seq_len_dev, int32_t n_seq,
                           int32_t max_blocks, const int32_t* budget_dev, int32_t n_first, int32_t n_recent,
                           int32_t* idx_out_dev, int64_t* idx_off_dev, cudaStream_t stream);

@@ -1,0 +1,740 @@
+// The attention weights of query chunks, added up by stored token:
+//
+//   mass[t] = carry * mass_in[t] + sum over rows r and heads h of e^(x_rht) / sum_t' e^(x_rht'),
+//   x_rht = scale <q_rh, K_t>, t' and t below the row's limit
+//
+// Values are not read.  A weight needs its row's whole sum, and the scores of a
+// prompt do not fit anywhere (8,192 rows of 32 heads: 4 GB), so the products are
+// taken twice on the fifth-generation tensor cores, each time with the sum along
+// a thread's own accumulator row, so that nothing is exchanged between threads:
+//  pass 1  S = Q K^T: a thread has a row of 128 scores of a query row, and keeps
+//          that row's maximum and sum;
+//  pass 2  S^T = K Q^T: a thread has a key and adds up 2^(s - lse) over the
+//          columns, 128 (token, head) rows at a time, whose lse = log2 of the sum
+//          lies in shared memory.
+// Both are one kernel: two tiles of 128 rows (X) stay in shared memory, tiles of
+// the other operand (Y) stream through a TMA ring past both; S goes to tensor
+// memory, two buffers a tile; two warpgroups turn it into sums.  Scores and sums
+// are float32.
+//
+// Items (a pair of X tiles, a range of Y tiles) are claimed in order, the longest
+// first.  Calls with few of them cut the Y ranges: pass 1 leaves (m, l) of each
+// cut, which pass 2 joins where it needs them; pass 2 leaves a sum for each cut
+// and KV head, which the last kernel adds in a fixed order.  A plan kernel counts
+// the units of every sequence.
+#include <algorithm>
+#include <cmath>
+
+#include "tcgen05.cuh"
+#include "internal.h"
+
+namespace kvs {
+
+namespace {
+
+// Two softmax warpgroups; MMA warp, TMA warp, a warp for pass 2's columns and an
+// idle one.  Registers are split as 256 * 216 + 128 * 72 of the 64,512 that 384
+// threads start with.
+constexpr int kEmThreads = 384;
+constexpr int kEmRegsSoftmax = 216, kEmRegsOther = 72;
+constexpr int kEmTile = 128;
+constexpr int kEmMaxCuts = 16;
+constexpr uint32_t kEmCols = 512;
+constexpr float kEmLag = 8.f;    // the reference of a row's sum moves when a score exceeds it by more
+
+template <int D>
+__host__ __device__ constexpr int em_tile_bytes() { return kEmTile * D * 2; }
+template <int D>
+__host__ __device__ constexpr int em_stages() { return D == 128 ? 4 : 8; }
+template <int D>
+__host__ __device__ constexpr int em_smem() { return 1024 + em_tile_bytes<D>() * (2 + em_stages<D>()); }
+
+enum { kMClaim1, kMClaim2, kMBad, kMTotal = 16 };
+
+struct EmParams {
+  const int32_t *table, *tok_off, *seq_len;
+  uint32_t* status;
+  int* hdr;
+  int4* seq;          // [n_seq] {first row, rows, keys}
+  int *off1, *off2;   // [n_seq + 1] units before each sequence: pairs of row tiles, pairs of key tiles
+  float2* parts;      // pass 1: [cut][n_tokens][hq] {reference, sum}
+  float* sums;        // pass 2: [cut][hkv][n_seq][most]
+  int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2;
+  float scale_log2;
+};
+
+__global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ EmParams p) {
+  __shared__ int warp_sums[32];
+  const int tid = threadIdx.x, tu = 2 * (kEmTile / p.g);
+  pdl_enter();
+  int n1 = 0, n2 = 0, bad = 0;
+  for (int a0 = 0; a0 < p.n_seq; a0 += 1024) {
+    const int a = a0 + tid;
+    int u1 = 0, u2 = 0;
+    if (a < p.n_seq) {
+      const int t0 = __ldg(p.tok_off + a), t1 = __ldg(p.tok_off + a + 1), raw = __ldg(p.seq_len + a);
+      bad |= t0 < 0 || t1 < t0 || t1 > p.n_tokens;
+      if (raw < 0 || raw > p.most) set_err(p.status, KVS_DEVERR_SEQ_LEN);
+      const int keys = min(max(raw, 0), p.most), rows = t1 - t0;
+      p.seq[a] = make_int4(t0, rows, keys, 0);
+      u1 = rows > 0 ? (rows - 1) / tu + 1 : 0;
+      u2 = rows > 0 ? (keys + 2 * kEmTile - 1) / (2 * kEmTile) : 0;
+    }
+    int total;
+    const int b1 = block_exclusive_scan(u1, warp_sums, total);
+    if (a < p.n_seq) p.off1[a] = n1 + b1;
+    n1 += total;
+    const int b2 = block_exclusive_scan(u2, warp_sums, total);
+    if (a < p.n_seq) p.off2[a] = n2 + b2;
+    n2 += total;
+  }
+  bad = __syncthreads_or(bad);
+  if (tid == 0) {
+    if (bad) set_err(p.status, KVS_DEVERR_JOB);
+    p.off1[p.n_seq] = bad ? 0 : n1;
+    p.off2[p.n_seq] = bad ? 0 : n2;
+    p.hdr[kMClaim1] = p.hdr[kMClaim2] = 0;
+    p.hdr[kMBad] = bad;
+  }
+}
+
+struct __align__(16) EmItem {
+  int seq, head, cut, done;
+  int t0, rows, keys, x0;       // of the sequence; x0: first token (pass 1) or key (pass 2) of the X tiles
+  int y0, y1, pad[2];           // Y tiles of the item
+  int xs[2], xe[2];             // of them, those that X tile 0 / 1 takes
+};
+
+struct EmBars {
+  uint64_t full[8], empty[8];
+  uint64_t x_full, x_empty;
+  uint64_t s_full[2][2], s_empty[2][2];
+  uint64_t it_full[2], it_empty[2];
+  uint64_t fin;
+};
+
+struct EmCols {   // pass 2: of the 128 columns of a Y tile
+  float lse[kEmTile];
+  int lim[kEmTile];
+  int least;      // smallest limit
+  int pad[3];
+};
+
+// Whole warp: the number of i in [1, n] with off[i] <= v (off ascends).
+__device__ __forceinline__ int em_find(const int* off, int n, int v, int lane) {
+  int lo = 0;
+  while (n > 32) {
+    const int step = (n + 31) / 32, i = (lane + 1) * step;
+    const bool le = i <= n && __ldg(off + lo + i) <= v;
+    const int c = __popc(__ballot_sync(0xffffffffu, le));
+    lo += c * step;
+    n = min(step - 1, n - c * step);
+  }
+  const bool le = lane < n && __ldg(off + lo + lane + 1) <= v;
+  return lo + __popc(__ballot_sync(0xffffffffu, le));
+}
+
+template <int D, int PASS>
+__global__ void __launch_bounds__(kEmThreads, 1)
+em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk) {
+  constexpr int HF = D / 64;
+  constexpr int ST = em_stages<D>();
+  constexpr int kTile = em_tile_bytes<D>();
+  constexpr int kHalf = kEmTile * 128;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ EmBars bars;
+  __shared__ EmItem work[2];
+  __shared__ __align__(16) EmCols cols[PASS == 2 ? ST : 1];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&bars.full[i], PASS == 2 ? 2 : 1);     // the copies; pass 2: the column warp
+      mbar_init(&bars.empty[i], PASS == 2 ? 9 : 1);    // the products; pass 2: the softmax warps have read the columns
+    }
+    mbar_init(&bars.x_full, 1);
+    mbar_init(&bars.x_empty, 1);
+    for (int x = 0; x < 2; ++x) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars.s_full[x][b], 1);
+        mbar_init(&bars.s_empty[x][b], 4);
+      }
+      mbar_init(&bars.it_full[x], 1);
+      mbar_init(&bars.it_empty[x], PASS == 2 ? 10 : 9);
+    }
+    mbar_init(&bars.fin, 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, kEmCols);
+    tmem_relinquish();
+  }
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  auto sX = [&](int x) { return base + kTile * x; };
+  auto ring = [&](int i) { return base + kTile * (2 + i); };
+  // rows of a query tile behind its last whole token are never copied to
+  for (int i = threadIdx.x; i < (2 + ST) * kTile / 16; i += kEmThreads) reinterpret_cast<uint4*>(base)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tt = kEmTile / p.g;
+  auto stop = [&]() { return __any_sync(0xffffffffu, s_abort != 0); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_wait_bounded(bar, parity, p.status);
+    return __all_sync(0xffffffffu, ok);
+  };
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kEmRegsOther));
+    if (warp == 9) {
+      // --------------------------------------------- claims and TMA copies
+      const int* off = PASS == 1 ? p.off1 : p.off2;
+      const int cuts = PASS == 1 ? p.cuts1 : p.cuts2;
+      const long long claims = (long long)__ldg(off + p.n_seq) * p.hkv * cuts;
+      int* counter = p.hdr + (PASS == 1 ? kMClaim1 : kMClaim2);
+      int n = 0, nx = 0, ni = 0, armed = -1;
+      bool ok = true;
+      auto claim_next = [&]() {
+        int c = 0;
+        if (lane == 0) c = atomicAdd(counter, 1);
+        return (long long)(unsigned)__shfl_sync(0xffffffffu, c, 0);
+      };
+      // blocks of key tile j of the sequence: an id for lanes below 8, -1 where there is none
+      auto key_blocks = [&](int a, int j, int keys) {
+        const int b = j * 8 + lane;
+        int id = -1;
+        if (lane < 8 && b < (keys + 15) / 16) {
+          id = __ldg(p.table + (size_t)a * p.max_blocks + b);
+          if (id < 0 || id >= p.capacity) {
+            set_err(p.status, KVS_DEVERR_BLOCK_ID);
+            id = -1;
+          }
+        }
+        return id;
+      };
+      auto copy_keys = [&](uint8_t* dst, int id, int head, uint64_t* bar) {   // lanes below 8; a block without an id arrives as zeros
+        if (lane < 8) {
+          const int row = id >= 0 ? (id * p.hkv + head) * 16 : p.slab_rows;
+#pragma unroll
+          for (int hf = 0; hf < HF; ++hf) tma_load_3d(dst + hf * kHalf + lane * 2048, &tk, 0, row, hf, bar);
+        }
+        __syncwarp();
+      };
+      auto copy_rows = [&](uint8_t* dst, int tok, int head, uint64_t* bar) {  // one lane
+        for (int hf = 0; hf < HF; ++hf) tma_load_5d(dst + hf * kHalf, &tq, 0, 0, tok, head, hf, bar);
+      };
+      const uint32_t row_bytes = (uint32_t)(HF * tt * p.g * 128);
+      long long claim = claim_next();
+      while (true) {
+        if (stop()) { ok = false; break; }
+        const int slot = ni & 1;
+        if (ni >= 2 && !wait(&bars.it_empty[slot], ((ni - 2) >> 1) & 1)) { ok = false; break; }
+        EmItem it{};
+        it.done = claim >= claims;
+        int nt_x[2] = {0, 0};
+        if (!it.done) {
+          const long long u = claim / cuts;
+          it.cut = (int)(claim - u * cuts);
+          const int unit = (int)(u / p.hkv);
+          it.head = (int)(u - (long long)unit * p.hkv);
+          it.seq = em_find(off, p.n_seq, unit, lane);
+          const int4 s = __ldg(p.seq + it.seq);
+          const int first = __ldg(off + it.seq), count = __ldg(off + it.seq + 1) - first;
+          it.t0 = s.x;
+          it.rows = s.y;
+          it.keys = s.z;
+          const int before = s.z - s.y;   // row j sees keys up to before + j (causal)
+          if constexpr (PASS == 1) {
+            it.x0 = (count - 1 - (unit - first)) * 2 * tt;   // the last rows, which see most, first
+            for (int x = 0; x < 2; ++x) {
+              const int j0 = it.x0 + x * tt, j1 = min(it.rows, j0 + tt);
+              const int lim = p.causal ? min(max(before + j1, 0), s.z) : s.z;
+              nt_x[x] = j0 < it.rows ? (lim + kEmTile - 1) / kEmTile : 0;
+            }
+            const int nt = max(nt_x[0], nt_x[1]);
+            it.y0 = (int)((long long)nt * it.cut / cuts);
+            it.y1 = (int)((long long)nt * (it.cut + 1) / cuts);
+            for (int x = 0; x < 2; ++x) {
+              it.xs[x] = it.y0;
+              it.xe[x] = min(it.y1, nt_x[x]);
+            }
+          } else {
+            it.x0 = (unit - first) * 2 * kEmTile;
+            const int tiles = (it.rows + tt - 1) / tt;
+            for (int x = 0; x < 2; ++x) {
+              const int key = it.x0 + x * kEmTile;
+              nt_x[x] = key < it.keys ? min(tiles, p.causal ? max(0, key - before) / tt : 0) : tiles;   // first tile that sees the key
+            }
+            const int n_y = tiles - nt_x[0];
+            it.y0 = nt_x[0] + (int)((long long)n_y * it.cut / cuts);
+            it.y1 = nt_x[0] + (int)((long long)n_y * (it.cut + 1) / cuts);
+            for (int x = 0; x < 2; ++x) {
+              it.xs[x] = max(it.y0, nt_x[x]);
+              it.xe[x] = it.y1;
+            }
+          }
+        }
+        if (lane == 0) {
+          work[slot] = it;
+          mbar_arrive(&bars.it_full[slot]);
+        }
+        __syncwarp();
+        ++ni;
+        if (it.done) break;
+        claim = claim_next();
+        if (it.y0 >= it.y1) continue;
+        // X tiles, once the products of the item before have read theirs
+        if (nx >= 1 && !wait(&bars.x_empty, (nx - 1) & 1)) { ok = false; break; }
+        const bool two = PASS == 1 ? it.x0 + tt < it.rows : it.x0 + kEmTile < it.keys;
+        if (lane == 0) mbar_arrive_expect_tx(&bars.x_full, (two ? 2u : 1u) * (PASS == 1 ? row_bytes : (uint32_t)kTile));
+        __syncwarp();
+        for (int x = 0; x < (two ? 2 : 1); ++x) {
+          if constexpr (PASS == 1) {
+            if (lane == 0) copy_rows(sX(x), it.t0 + it.x0 + x * tt, it.head, &bars.x_full);
+            __syncwarp();
+          } else {
+            copy_keys(sX(x), key_blocks(it.seq, it.x0 / kEmTile + x, it.keys), it.head, &bars.x_full);
+          }
+        }
+        ++nx;
+        int id = PASS == 1 ? key_blocks(it.seq, it.y0, it.keys) : 0;
+        for (int j = it.y0; j < it.y1; ++j) {
+          const int id_next = PASS == 1 && j + 1 < it.y1 ? key_blocks(it.seq, j + 1, it.keys) : -1;
+          const int s = n % ST;
+          if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(&bars.full[s], PASS == 1 ? (uint32_t)kTile : row_bytes);
+          __syncwarp();
+          if constexpr (PASS == 1) {
+            copy_keys(ring(s), id, it.head, &bars.full[s]);
+          } else {
+            if (lane == 0) copy_rows(ring(s), it.t0 + j * tt, it.head, &bars.full[s]);
+            __syncwarp();
+          }
+          armed = n++;
+          id = id_next;
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        s_abort = 1;
+        // copies in flight land before the shared memory goes away
+        for (int m = max(0, armed - ST + 1); m <= armed; ++m) mbar_drain(&bars.full[m % ST], (m / ST) & 1);
+        if (nx) mbar_drain(&bars.x_full, (nx - 1) & 1);
+      }
+    } else if (warp == 8) {
+      // --------------------------------------------------------- MMA issue
+      constexpr uint32_t idS = umma_idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kHi = ex_desc_hi(1024);
+      const uint32_t x_lo = ex_desc_lo(smem_u32(base), 16), y_lo = ex_desc_lo(smem_u32(ring(0)), 16);
+      int n = 0, nx = 0, ns[2] = {0, 0};
+      bool ok = true;
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+      };
+      for (int ni = 0;; ++ni) {
+        const int slot = ni & 1;
+        if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+        const EmItem it = work[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+        if (it.done) break;
+        if (it.y0 >= it.y1) continue;
+        if (!wait(&bars.x_full, nx & 1)) { ok = false; break; }
+        ++nx;
+        for (int j = it.y0; j < it.y1; ++j) {
+          const int s = n % ST;
+          if (!wait(&bars.full[s], (n / ST) & 1)) { ok = false; break; }
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            if (j < it.xs[x] || j >= it.xe[x]) continue;
+            const int b = ns[x] & 1;
+            if (ns[x] >= 2 && !wait(&bars.s_empty[x][b], ((ns[x] - 2) >> 1) & 1)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t xa = x_lo + x * (kTile / 16), ya = y_lo + s * (kTile / 16);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) / 16;
+                ex_mma_ss(tmem + 256u * x + 128u * b, xa + o, ya + o, kHi, idS, kk > 0);
+              }
+              umma_commit(&bars.s_full[x][b]);
+            }
+            __syncwarp();
+            ++ns[x];
+          }
+          if (!ok) break;
+          commit(&bars.empty[s]);
+          ++n;
+        }
+        if (!ok) break;
+        commit(&bars.x_empty);
+      }
+      if (!ok) s_abort = 1;
+      // every product issued has completed before the tensor memory is released
+      commit(&bars.fin);
+      mbar_wait_bounded(&bars.fin, 0, p.status);
+    } else if (PASS == 2 && warp == 10) {
+      // ------------------------------------- columns: limits and log2 of the sums
+      int n = 0;
+      bool ok = true;
+      for (int ni = 0;; ++ni) {
+        const int slot = ni & 1;
+        if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+        const EmItem it = work[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+        if (it.done) break;
+        const size_t cut_rows = (size_t)p.n_tokens * p.hq;
+        for (int j = it.y0; j < it.y1; ++j) {
+          float lse[4];
+          int lim[4], least = 0x7fffffff;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = i * 32 + lane, tok = j * tt + c / p.g;
+            const bool live = c < tt * p.g && tok < it.rows;
+            float m = -INFINITY, l = 0.f;
+            if (live) {
+              const float2* part = p.parts + (size_t)(it.t0 + tok) * p.hq + it.head * p.g + c % p.g;
+              for (int k = 0; k < p.cuts1; ++k) {
+                const float2 v = part[k * cut_rows];
+                const float top = fmaxf(m, v.x);
+                if (v.y > 0.f) {
+                  l = (l > 0.f ? l * fast_exp2(m - top) : 0.f) + v.y * fast_exp2(v.x - top);
+                  m = top;
+                }
+              }
+            }
+            lse[i] = l > 0.f ? m + log2f(l) : INFINITY;
+            lim[i] = live && l > 0.f ? (p.causal ? max(it.keys - it.rows + tok + 1, 0) : it.keys) : 0;
+            least = min(least, lim[i]);
+          }
+          least = __reduce_min_sync(0xffffffffu, least);
+          const int s = n % ST;
+          if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) { ok = false; break; }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            cols[s].lse[i * 32 + lane] = lse[i];
+            cols[s].lim[i * 32 + lane] = lim[i];
+          }
+          if (lane == 0) cols[s].least = least;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.full[s]);
+          ++n;
+        }
+        if (!ok) break;
+      }
+      if (!ok) s_abort = 1;
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEmRegsSoftmax));
+    // ------------------------------------------------------------ sums
+    const int x = warp >> 2, r = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * x;
+    const int rt = r / p.g, rg = r - rt * p.g;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    int n = 0, ns = 0;
+    bool ok = true;
+    for (int ni = 0;; ++ni) {
+      const int slot = ni & 1;
+      if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+      const EmItem it = work[slot];
+      const int xs = work[slot].xs[x], xe = work[slot].xe[x];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+      if (it.done) break;
+      const int tok = it.x0 + x * tt + rt;               // pass 1: this row's token
+      const int key = it.x0 + x * kEmTile + r;           // pass 2: this row's key
+      const bool live = PASS == 1 ? rt < tt && tok < it.rows : key < it.keys;
+      const int lim = p.causal ? min(it.keys - it.rows + tok + 1, it.keys) : it.keys;   // pass 1: keys that the row sees
+      float m = -INFINITY, l = 0.f;
+      for (int j = it.y0; j < it.y1; ++j) {
+        const int s = n % ST;
+        // also where this X tile passes the Y tile by: a stage is handed back once a turn
+        if (PASS == 2 && !wait(&bars.full[s], (n / ST) & 1)) { ok = false; break; }
+        if (j >= xs && j < xe) {
+          const int b = ns & 1;
+          if (!wait(&bars.s_full[x][b], (ns >> 1) & 1)) { ok = false; break; }
+          tc_fence_after();
+          uint32_t sa[32], sb[32], sc[32], sd[32];
+          const uint32_t t = tS + 128u * b;
+          tmem_ld32_issue(t, sa);
+          tmem_ld32_issue(t + 32, sb);
+          tmem_ld32x2_wait(sa, sb);
+          tmem_ld32_issue(t + 64, sc);
+          tmem_ld32_issue(t + 96, sd);
+          auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars.s_empty[x][b]);
+          };
+          if constexpr (PASS == 1) {
+            const int rem = lim - j * kEmTile;   // visible keys of this tile
+            const bool masked = __any_sync(0xffffffffu, rem < kEmTile && live);
+            auto mask = [&](uint32_t* v, int first) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i + first >= rem) v[i] = 0xff800000u;
+            };
+            auto most = [&](const uint32_t* v) {
+              float a = -INFINITY, c = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                a = fmaxf(a, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
+                c = fmaxf(c, fmaxf(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])));
+              }
+              return fmaxf(a, c);
+            };
+            if (masked) {
+              mask(sa, 0);
+              mask(sb, 32);
+            }
+            float mx = fmaxf(most(sa), most(sb));
+            tmem_ld32x2_wait(sc, sd);
+            release();
+            if (masked) {
+              mask(sc, 64);
+              mask(sd, 96);
+            }
+            mx = fmaxf(mx, fmaxf(most(sc), most(sd))) * p.scale_log2;
+            const float next = mx > m + kEmLag ? mx : m;
+            const float ref = next == -INFINITY ? 0.f : next;
+            if (next > m) l *= fast_exp2(m - next);   // 0 before the first
+            m = next;
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+            const float2 rf2 = make_float2(-ref, -ref);
+            auto add = [&](const uint32_t* v) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float2 a = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, rf2);
+                float2 c = __ffma2_rn(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2, rf2);
+                sum0 = __fadd2_rn(sum0, make_float2(fast_exp2(a.x), fast_exp2(a.y)));
+                sum1 = __fadd2_rn(sum1, make_float2(fast_exp2(c.x), fast_exp2(c.y)));
+              }
+            };
+            add(sa);
+            add(sb);
+            add(sc);
+            add(sd);
+            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          } else {
+            const EmCols& cl = cols[s];
+            const bool masked = __any_sync(0xffffffffu, live && key >= cl.least);
+            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+            auto add = [&](uint32_t* v, int first) {
+              if (masked) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                  const int4 lm = *reinterpret_cast<const int4*>(cl.lim + first + i);
+                  if (key >= lm.x) v[i] = 0xff800000u;
+                  if (key >= lm.y) v[i + 1] = 0xff800000u;
+                  if (key >= lm.z) v[i + 2] = 0xff800000u;
+                  if (key >= lm.w) v[i + 3] = 0xff800000u;
+                }
+              }
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                const float4 e = *reinterpret_cast<const float4*>(cl.lse + first + i);
+                float2 a = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, make_float2(-e.x, -e.y));
+                float2 c = __ffma2_rn(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2, make_float2(-e.z, -e.w));
+                sum0 = __fadd2_rn(sum0, make_float2(fast_exp2(a.x), fast_exp2(a.y)));
+                sum1 = __fadd2_rn(sum1, make_float2(fast_exp2(c.x), fast_exp2(c.y)));
+              }
+            };
+            add(sa, 0);
+            add(sb, 32);
+            tmem_ld32x2_wait(sc, sd);
+            release();
+            add(sc, 64);
+            add(sd, 96);
+            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+          }
+          ++ns;
+        }
+        if (PASS == 2) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.empty[s]);
+        }
+        ++n;
+      }
+      if (!ok) break;
+      if (!live) continue;
+      if constexpr (PASS == 1)
+        p.parts[((size_t)it.cut * p.n_tokens + it.t0 + tok) * p.hq + it.head * p.g + rg] = make_float2(m, l);
+      else
+        p.sums[(((size_t)it.cut * p.hkv + it.head) * p.n_seq + it.seq) * p.most + key] = l;
+    }
+    if (!ok) s_abort = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kEmCols);
+  }
+}
+
+// Adds the cuts' and heads' sums in their order.
+__global__ void __launch_bounds__(256) em_add_kernel(const __grid_constant__ EmParams p, const float* mass_in, float carry, float* mass) {
+  pdl_enter();
+  if (p.hdr[kMBad]) return;
+  const int a = blockIdx.y, t = blockIdx.x * 256 + threadIdx.x;
+  const int4 s = p.seq[a];
+  if (t >= s.z) return;
+  float sum = 0.f;
+  if (s.y > 0) {
+    const float* v = p.sums + (size_t)a * p.most + t;
+    const size_t step = (size_t)p.n_seq * p.most;
+    const int n = p.cuts2 * p.hkv;
+#pragma unroll 8
+    for (int i = 0; i < n; ++i) sum += v[i * step];
+  }
+  const size_t o = (size_t)a * p.most + t;
+  mass[o] = mass_in ? fmaf(carry, mass_in[o], sum) : sum;
+}
+
+struct EmLayout {
+  size_t hdr, seq, off1, off2, parts, sums, total;
+  int cuts1, cuts2;
+};
+EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks, int hq) {
+  const kvs_pool_desc& d = pool->desc;
+  const int hkv = d.num_kv_heads, g = hq / hkv, tt = kEmTile / g;
+  EmLayout l{};
+  // cuts: as many as bring two items to every SM where the units are too few
+  const long long sms2 = 2ll * pool->num_sms, key_tiles = ((long long)max_blocks * 16 + kEmTile - 1) / kEmTile;
+  const long long u1 = ((long long)n_tokens / (2 * tt) + n_seq) * hkv, u2 = (long long)n_seq * ((key_tiles + 1) / 2) * hkv;
+  const long long row_tiles = ((long long)n_tokens + tt - 1) / tt;
+  auto cuts = [&](long long units, long long tiles) {
+    return (int)std::clamp<long long>((sms2 + units - 1) / std::max(1ll, units), 1, std::clamp<long long>(tiles / 2, 1, kEmMaxCuts));
+  };
+  l.cuts1 = cuts(u1, key_tiles);
+  l.cuts2 = cuts(u2, row_tiles);
+  size_t o = 0;
+  auto take = [&](size_t b) {
+    const size_t at = o;
+    o += (b + 255) & ~size_t{255};
+    return at;
+  };
+  l.hdr = take(kMTotal * 4);
+  l.seq = take((size_t)n_seq * 16);
+  l.off1 = take((size_t)(n_seq + 1) * 4);
+  l.off2 = take((size_t)(n_seq + 1) * 4);
+  l.parts = take((size_t)l.cuts1 * n_tokens * hq * 8);
+  l.sums = take((size_t)l.cuts2 * hkv * n_seq * max_blocks * 16 * 4);
+  l.total = o;
+  return l;
+}
+
+template <typename... KArgs, typename... Args>
+cudaError_t em_launch(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t st, Args... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <int D>
+kvs_status em_run(const kvs_pool* pool, int layer, const EmParams& p, const CUtensorMap& tq, const float* mass_in, float carry,
+                  float* mass, cudaStream_t stream) {
+  if (!smem_limit_once<em_pass_kernel<D, 1>>(em_smem<D>(), pool->device) ||
+      !smem_limit_once<em_pass_kernel<D, 2>>(em_smem<D>(), pool->device))
+    return fail(KVS_ERR_CUDA, "extend_mass: cannot raise the shared-memory limit");
+  const CUtensorMap& tk = D == 128 ? pool->tk1[layer] : pool->tk[layer];
+  const dim3 grid((unsigned)pool->num_sms);
+  bool ok = true;
+  if (p.n_tokens > 0)
+    ok = em_launch(em_pass_kernel<D, 1>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess &&
+         em_launch(em_pass_kernel<D, 2>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess;
+  if (ok && p.n_tokens > 0) count_launch(2);
+  if (ok && em_launch(em_add_kernel, dim3((unsigned)((p.most + 255) / 256), (unsigned)p.n_seq), dim3(256), 0, stream, p, mass_in, carry,
+                      mass) == cudaSuccess)
+    count_launch();
+  return check_launch("extend_mass");
+}
+
+}  // namespace
+
+}  // namespace kvs
+
+using namespace kvs;
+
+extern "C" kvs_status kvs_extend_mass_workspace_size(const kvs_pool* pool, int32_t n_tokens, int32_t n_seq, int32_t max_blocks,
+                                                     int32_t n_q_heads, size_t* bytes) {
+  if (!bytes) return fail(KVS_ERR_INVALID_ARG, "extend_mass_workspace_size: null pointer");
+  if (kvs_status st = ex_check(pool, "extend_mass_workspace_size", n_tokens, n_seq, max_blocks, n_q_heads); st != KVS_OK) return st;
+  *bytes = em_layout(pool, n_tokens, n_seq, max_blocks, n_q_heads).total;
+  return KVS_OK;
+}
+
+extern "C" kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void* q_dev, int64_t q_stride, const int32_t* tok_off_dev,
+                                      int32_t n_tokens, int32_t n_q_heads, const int32_t* block_table_dev, int32_t max_blocks,
+                                      const int32_t* seq_len_dev, int32_t n_seq, int32_t causal, float scale,
+                                      const float* mass_in_dev, float carry, float* mass_dev, void* ws, size_t ws_bytes,
+                                      cudaStream_t stream) {
+  if (kvs_status st = ex_check(pool, "extend_mass", n_tokens, n_seq, max_blocks, n_q_heads); st != KVS_OK) return st;
+  const kvs_pool_desc& d = pool->desc;
+  if (layer < 0 || layer >= d.num_layers) return fail(KVS_ERR_INVALID_ARG, "extend_mass: layer out of range");
+  if (causal != 0 && causal != 1) return fail(KVS_ERR_INVALID_ARG, "extend_mass: causal is 0 or 1");
+  const float scale_log2 = scale * 1.4426950408889634f;
+  if (!(scale > 0.f) || !std::isfinite(scale_log2))
+    return fail(KVS_ERR_INVALID_ARG, "extend_mass: scale must be positive, and scale * log2(e) finite");
+  if (!std::isfinite(carry)) return fail(KVS_ERR_INVALID_ARG, "extend_mass: carry must be finite");
+  const long long row = (long long)n_q_heads * d.head_dim;
+  if (q_stride < row || (q_stride & 7)) return fail(KVS_ERR_INVALID_ARG, "extend_mass: q_stride must hold n_q_heads * head_dim elements and be a multiple of 8");
+  if (n_seq > 65535) return fail(KVS_ERR_UNSUPPORTED, "extend_mass: more than 65,535 sequences");
+  if (n_seq == 0) return KVS_OK;
+  if ((n_tokens > 0 && !q_dev) || !tok_off_dev || !block_table_dev || !seq_len_dev || !mass_dev || !ws)
+    return fail(KVS_ERR_INVALID_ARG, "extend_mass: null pointer");
+  if (!aligned16(q_dev) || !aligned16(ws)) return fail(KVS_ERR_INVALID_ARG, "extend_mass: q and ws must be 16-byte aligned");
+  const EmLayout l = em_layout(pool, n_tokens, n_seq, max_blocks, n_q_heads);
+  if (ws_bytes < l.total) return fail(KVS_ERR_CAPACITY, "extend_mass: workspace too small");
+  if (kvs_status st = check_pool_device(pool, "extend_mass"); st != KVS_OK) return st;
+  uint8_t* w = static_cast<uint8_t*>(ws);
+  EmParams p{};
+  p.table = block_table_dev;
+  p.tok_off = tok_off_dev;
+  p.seq_len = seq_len_dev;
+  p.status = pool->status;
+  p.hdr = reinterpret_cast<int*>(w + l.hdr);
+  p.seq = reinterpret_cast<int4*>(w + l.seq);
+  p.off1 = reinterpret_cast<int*>(w + l.off1);
+  p.off2 = reinterpret_cast<int*>(w + l.off2);
+  p.parts = reinterpret_cast<float2*>(w + l.parts);
+  p.sums = reinterpret_cast<float*>(w + l.sums);
+  p.n_tokens = n_tokens;
+  p.n_seq = n_seq;
+  p.max_blocks = max_blocks;
+  p.capacity = d.capacity_blocks;
+  p.hkv = d.num_kv_heads;
+  p.g = n_q_heads / d.num_kv_heads;
+  p.hq = n_q_heads;
+  p.causal = causal;
+  p.slab_rows = d.capacity_blocks * d.num_kv_heads * d.block_tokens;
+  p.most = max_blocks * 16;
+  p.cuts1 = l.cuts1;
+  p.cuts2 = l.cuts2;
+  p.scale_log2 = scale_log2;
+  CUtensorMap tq{};
+  if (n_tokens > 0 && !ex_query_map(&tq, q_dev, n_tokens, p.g, p.hkv, d.head_dim, q_stride))
+    return fail(KVS_ERR_CUDA, "extend_mass: cuTensorMapEncodeTiled failed for q");
+  if (launch_pdl(em_plan_kernel, dim3(1), dim3(1024), stream, p) != cudaSuccess) return check_launch("extend_mass");
+  count_launch();
+  return d.head_dim == 128 ? em_run<128>(pool, layer, p, tq, mass_in_dev, carry, mass_dev, stream)
+                           : em_run<64>(pool, layer, p, tq, mass_in_dev, carry, mass_dev, stream);
+}

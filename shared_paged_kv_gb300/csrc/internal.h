@@ -133,6 +133,11 @@ int runs_wide_ctas(const kvs_pool* pool);
 kvs_status launch_wide_tile(const WideParams& p, const kvs_pool* pool, int layer, int max_claims,
                             cudaStream_t stream);
 
+// Of the operators on query chunks (extend.cu): the argument checks that they
+// share, and the tensor map that brings row tiles of packed queries.
+kvs_status ex_check(const kvs_pool* pool, const char* what, int n_tokens, int n_seq, int max_blocks, int n_q_heads);
+bool ex_query_map(CUtensorMap* m, const void* q, int n_tokens, int g, int hkv, int d, long long stride);
+
 // Mirror construction (mirror.cu).
 size_t mirror_workspace_bytes(int n_seq, int max_blocks);
 

@@ -56,6 +56,7 @@ EXPORTED = [
     "kvs_launch_count", "kvs_rope_apply", "kvs_append", "kvs_gather", "kvs_extend_workspace_size",
     "kvs_extend_plan", "kvs_extend_attn_planned", "kvs_extend_attn", "kvs_keep_heavy", "kvs_compact",
     "kvs_decode_attn_mass", "kvs_decode_attn_mx4",
+    "kvs_extend_mass_workspace_size", "kvs_extend_mass",
 ]
 
 
@@ -133,6 +134,8 @@ def load(path: str = LIB_PATH):
         "kvs_extend_attn": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, P, SZ, P],
         "kvs_decode_attn_mass": [P, I32, P, I32, P, I32, P, I32, F32, P, P, F32, P, P, SZ, P],
         "kvs_decode_attn_mx4": [P, I32, P, I32, P, I32, P, I32, F32, P, P, F32, P, P, SZ, P],
+        "kvs_extend_mass_workspace_size": [P, I32, I32, I32, I32, ctypes.POINTER(SZ)],
+        "kvs_extend_mass": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, F32, P, P, SZ, P],
         "kvs_keep_heavy": [P, P, P, I32, I32, P, I32, I32, P, P, P],
         "kvs_compact": [P, P, I32, P, I32, P, P, P, P, P, P, P, SZ, P],
         "kvs_pool_check": [P, P, ctypes.POINTER(U32)],
@@ -570,6 +573,25 @@ def kvs_decode_attn_mx4(pool: Pool, layer, q, n_q_heads, block_table, max_blocks
     weights are added up as by kvs_decode_attn_mass."""
     _decode_mass(load().kvs_decode_attn_mx4, pool, layer, q, n_q_heads, block_table, max_blocks, seq_len, n_seq, scale, out,
                  mass_in, carry, mass, ws, stream)
+
+
+def kvs_extend_mass_workspace_size(pool: Pool, n_tokens: int, n_seq: int, max_blocks: int, n_q_heads: int) -> int:
+    out = ctypes.c_size_t()
+    _check(load().kvs_extend_mass_workspace_size(pool.handle, n_tokens, n_seq, max_blocks, n_q_heads, ctypes.byref(out)))
+    return out.value
+
+
+def kvs_extend_mass(pool: Pool, layer, q, n_tokens, tok_off, n_q_heads, block_table, max_blocks, seq_len, n_seq, causal, scale,
+                    mass_in, carry, mass, ws, stream=None):
+    """Add every token's weight over the rows and heads of packed query chunks:
+    mass = carry * mass_in + weights (float32 [n_seq][max_blocks * block_tokens])."""
+    d, dev = pool.desc, _device()
+    qp, qs = _rows(q, n_tokens, n_q_heads, d.head_dim, "q", dev)
+    _check(load().kvs_extend_mass(
+        pool.handle, layer, qp, qs, _ints(tok_off, n_seq + 1, "tok_off", dev), n_tokens, n_q_heads,
+        _table(block_table, n_seq, max_blocks, dev), max_blocks, _ints(seq_len, n_seq, "seq_len", dev), n_seq, int(causal), scale,
+        _mass(mass_in, pool, n_seq, max_blocks, "mass_in", dev), carry, _mass(mass, pool, n_seq, max_blocks, "mass", dev),
+        *_ws(ws, dev), _stream(stream)))
 
 
 def kvs_keep_heavy(pool: Pool, mass, seq_len, n_seq, max_blocks, budget, n_first, n_recent, idx, idx_off, stream=None):
