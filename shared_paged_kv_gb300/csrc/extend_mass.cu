@@ -32,11 +32,12 @@ namespace kvs {
 
 namespace {
 
-// Two softmax warpgroups; MMA warp, TMA warp, a warp for pass 2's columns and an
-// idle one.  Registers are split as 256 * 216 + 128 * 72 of the 64,512 that 384
-// threads start with.
-constexpr int kEmThreads = 384;
-constexpr int kEmRegsSoftmax = 216, kEmRegsOther = 72;
+// Four warpgroups of sums, two for each X tile: one takes columns 0 to 63 of a
+// product, one the others, so that a scheduler has four warps to choose from
+// (two of them: 1.0 us for a pair of products, with four TBD).  Behind them a warp
+// that issues the products, one for the copies, one for pass 2's columns.
+constexpr int kEmSumWarps = 16, kEmThreads = (kEmSumWarps + 4) * 32;
+constexpr int kEmMma = kEmSumWarps, kEmTma = kEmSumWarps + 1, kEmCol = kEmSumWarps + 2;
 constexpr int kEmTile = 128;
 constexpr int kEmMaxCuts = 16;
 constexpr uint32_t kEmCols = 512;
@@ -57,8 +58,9 @@ struct EmParams {
   int* hdr;
   int4* seq;          // [n_seq] {first row, rows, keys}
   int *off1, *off2;   // [n_seq + 1] units before each sequence: pairs of row tiles, pairs of key tiles
-  float2* parts;      // pass 1: [cut][n_tokens][hq] {reference, sum}
-  float* sums;        // pass 2: [cut][hkv][n_seq][most]
+  float2* parts;      // pass 1: [cut][column half][n_tokens][hq] {reference, sum}
+  float* nlse;        // [hkv][n_tokens][g] -log2 of the rows' sums
+  float* sums;        // pass 2: [cut][column half][hkv][n_seq][most]
   int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2;
   float scale_log2;
 };
@@ -114,7 +116,7 @@ struct EmBars {
 };
 
 struct EmCols {   // pass 2: of the 128 columns of a Y tile
-  float lse[kEmTile];
+  float nlse[kEmTile];
   int lim[kEmTile];
   int least;      // smallest limit
   int pad[3];
@@ -153,17 +155,17 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     prefetch_tmap(&tk);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.full[i], PASS == 2 ? 2 : 1);     // the copies; pass 2: the column warp
-      mbar_init(&bars.empty[i], PASS == 2 ? 9 : 1);    // the products; pass 2: the softmax warps have read the columns
+      mbar_init(&bars.empty[i], PASS == 2 ? 1 + kEmSumWarps : 1);   // the products; pass 2: the columns are read
     }
     mbar_init(&bars.x_full, 1);
     mbar_init(&bars.x_empty, 1);
     for (int x = 0; x < 2; ++x) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars.s_full[x][b], 1);
-        mbar_init(&bars.s_empty[x][b], 4);
+        mbar_init(&bars.s_empty[x][b], kEmSumWarps / 2);
       }
       mbar_init(&bars.it_full[x], 1);
-      mbar_init(&bars.it_empty[x], PASS == 2 ? 10 : 9);
+      mbar_init(&bars.it_empty[x], kEmSumWarps + (PASS == 2 ? 2 : 1));
     }
     mbar_init(&bars.fin, 1);
     s_abort = 0;
@@ -192,9 +194,8 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     return __all_sync(0xffffffffu, ok);
   };
 
-  if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kEmRegsOther));
-    if (warp == 9) {
+  if (warp >= kEmSumWarps) {
+    if (warp == kEmTma) {
       // --------------------------------------------- claims and TMA copies
       const int* off = PASS == 1 ? p.off1 : p.off2;
       const int cuts = PASS == 1 ? p.cuts1 : p.cuts2;
@@ -329,7 +330,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         for (int m = max(0, armed - ST + 1); m <= armed; ++m) mbar_drain(&bars.full[m % ST], (m / ST) & 1);
         if (nx) mbar_drain(&bars.x_full, (nx - 1) & 1);
       }
-    } else if (warp == 8) {
+    } else if (warp == kEmMma) {
       // --------------------------------------------------------- MMA issue
       constexpr uint32_t idS = umma_idesc_bf16(128, 128, false, false);
       constexpr uint32_t kHi = ex_desc_hi(1024);
@@ -382,8 +383,8 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       // every product issued has completed before the tensor memory is released
       commit(&bars.fin);
       mbar_wait_bounded(&bars.fin, 0, p.status);
-    } else if (PASS == 2 && warp == 10) {
-      // ------------------------------------- columns: limits and log2 of the sums
+    } else if (PASS == 2 && warp == kEmCol) {
+      // ------------------------------------- columns: limits and sums of the rows
       int n = 0;
       bool ok = true;
       for (int ni = 0;; ++ni) {
@@ -393,36 +394,35 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
         if (it.done) break;
-        const size_t cut_rows = (size_t)p.n_tokens * p.hq;
+        // column c of tile j is row (j tt g + c) of the sequence and KV head
+        const float* rows = p.nlse + ((size_t)it.head * p.n_tokens + it.t0) * p.g;
+        const int n_rows = it.rows * p.g, per = tt * p.g;
+        float next[4];
+        auto load = [&](int j) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int c = i * 32 + lane, row = j * per + c;
+            next[i] = c < per && row < n_rows ? rows[row] : -INFINITY;
+          }
+        };
+        if (it.y0 < it.y1) load(it.y0);
         for (int j = it.y0; j < it.y1; ++j) {
-          float lse[4];
+          float v[4];
           int lim[4], least = 0x7fffffff;
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
+            v[i] = next[i];
             const int c = i * 32 + lane, tok = j * tt + c / p.g;
-            const bool live = c < tt * p.g && tok < it.rows;
-            float m = -INFINITY, l = 0.f;
-            if (live) {
-              const float2* part = p.parts + (size_t)(it.t0 + tok) * p.hq + it.head * p.g + c % p.g;
-              for (int k = 0; k < p.cuts1; ++k) {
-                const float2 v = part[k * cut_rows];
-                const float top = fmaxf(m, v.x);
-                if (v.y > 0.f) {
-                  l = (l > 0.f ? l * fast_exp2(m - top) : 0.f) + v.y * fast_exp2(v.x - top);
-                  m = top;
-                }
-              }
-            }
-            lse[i] = l > 0.f ? m + log2f(l) : INFINITY;
-            lim[i] = live && l > 0.f ? (p.causal ? max(it.keys - it.rows + tok + 1, 0) : it.keys) : 0;
+            lim[i] = v[i] == -INFINITY ? 0 : p.causal ? max(it.keys - it.rows + tok + 1, 0) : it.keys;
             least = min(least, lim[i]);
           }
+          if (j + 1 < it.y1) load(j + 1);
           least = __reduce_min_sync(0xffffffffu, least);
           const int s = n % ST;
           if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) { ok = false; break; }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            cols[s].lse[i * 32 + lane] = lse[i];
+            cols[s].nlse[i * 32 + lane] = v[i];
             cols[s].lim[i * 32 + lane] = lim[i];
           }
           if (lane == 0) cols[s].least = least;
@@ -435,10 +435,9 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       if (!ok) s_abort = 1;
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kEmRegsSoftmax));
     // ------------------------------------------------------------ sums
-    const int x = warp >> 2, r = (warp & 3) * 32 + lane;
-    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * x;
+    const int x = (warp >> 2) & 1, half = warp >> 3, r = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * x + 64u * half;
     const int rt = r / p.g, rg = r - rt * p.g;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
     int n = 0, ns = 0;
@@ -464,100 +463,73 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
           const int b = ns & 1;
           if (!wait(&bars.s_full[x][b], (ns >> 1) & 1)) { ok = false; break; }
           tc_fence_after();
-          uint32_t sa[32], sb[32], sc[32], sd[32];
-          const uint32_t t = tS + 128u * b;
-          tmem_ld32_issue(t, sa);
-          tmem_ld32_issue(t + 32, sb);
+          uint32_t sa[32], sb[32];
+          tmem_ld32_issue(tS + 128u * b, sa);
+          tmem_ld32_issue(tS + 128u * b + 32, sb);
           tmem_ld32x2_wait(sa, sb);
-          tmem_ld32_issue(t + 64, sc);
-          tmem_ld32_issue(t + 96, sd);
-          auto release = [&]() {
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars.s_empty[x][b]);
-          };
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&bars.s_empty[x][b]);
+          ++ns;
+          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
           if constexpr (PASS == 1) {
-            const int rem = lim - j * kEmTile;   // visible keys of this tile
-            const bool masked = __any_sync(0xffffffffu, rem < kEmTile && live);
-            auto mask = [&](uint32_t* v, int first) {
+            const int rem = lim - j * kEmTile - 64 * half;   // visible ones of these keys
+            if (__any_sync(0xffffffffu, rem < 64 && live)) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (i + first >= rem) v[i] = 0xff800000u;
-            };
-            auto most = [&](const uint32_t* v) {
-              float a = -INFINITY, c = -INFINITY;
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                a = fmaxf(a, fmaxf(__uint_as_float(v[i]), __uint_as_float(v[i + 1])));
-                c = fmaxf(c, fmaxf(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])));
+              for (int i = 0; i < 32; ++i) {
+                if (i >= rem) sa[i] = 0xff800000u;
+                if (i + 32 >= rem) sb[i] = 0xff800000u;
               }
-              return fmaxf(a, c);
-            };
-            if (masked) {
-              mask(sa, 0);
-              mask(sb, 32);
             }
-            float mx = fmaxf(most(sa), most(sb));
-            tmem_ld32x2_wait(sc, sd);
-            release();
-            if (masked) {
-              mask(sc, 64);
-              mask(sd, 96);
+            float t0 = -INFINITY, t1 = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              t0 = fmaxf(t0, fmaxf(__uint_as_float(sa[i]), __uint_as_float(sa[i + 1])));
+              t1 = fmaxf(t1, fmaxf(__uint_as_float(sb[i]), __uint_as_float(sb[i + 1])));
             }
-            mx = fmaxf(mx, fmaxf(most(sc), most(sd))) * p.scale_log2;
+            const float mx = fmaxf(t0, t1) * p.scale_log2;
             const float next = mx > m + kEmLag ? mx : m;
             const float ref = next == -INFINITY ? 0.f : next;
             if (next > m) l *= fast_exp2(m - next);   // 0 before the first
             m = next;
-            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
             const float2 rf2 = make_float2(-ref, -ref);
-            auto add = [&](const uint32_t* v) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float2 a = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, rf2);
-                float2 c = __ffma2_rn(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2, rf2);
-                sum0 = __fadd2_rn(sum0, make_float2(fast_exp2(a.x), fast_exp2(a.y)));
-                sum1 = __fadd2_rn(sum1, make_float2(fast_exp2(c.x), fast_exp2(c.y)));
-              }
-            };
-            add(sa);
-            add(sb);
-            add(sc);
-            add(sd);
-            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+            for (int i = 0; i < 32; i += 2) {
+              const float2 a = __ffma2_rn(make_float2(__uint_as_float(sa[i]), __uint_as_float(sa[i + 1])), sc2, rf2);
+              const float2 c = __ffma2_rn(make_float2(__uint_as_float(sb[i]), __uint_as_float(sb[i + 1])), sc2, rf2);
+              sum0 = __fadd2_rn(sum0, make_float2(fast_exp2(a.x), fast_exp2(a.y)));
+              sum1 = __fadd2_rn(sum1, make_float2(fast_exp2(c.x), fast_exp2(c.y)));
+            }
           } else {
             const EmCols& cl = cols[s];
-            const bool masked = __any_sync(0xffffffffu, live && key >= cl.least);
-            float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
-            auto add = [&](uint32_t* v, int first) {
-              if (masked) {
-#pragma unroll
-                for (int i = 0; i < 32; i += 4) {
-                  const int4 lm = *reinterpret_cast<const int4*>(cl.lim + first + i);
-                  if (key >= lm.x) v[i] = 0xff800000u;
-                  if (key >= lm.y) v[i + 1] = 0xff800000u;
-                  if (key >= lm.z) v[i + 2] = 0xff800000u;
-                  if (key >= lm.w) v[i + 3] = 0xff800000u;
-                }
-              }
+            if (__any_sync(0xffffffffu, live && key >= cl.least)) {
 #pragma unroll
               for (int i = 0; i < 32; i += 4) {
-                const float4 e = *reinterpret_cast<const float4*>(cl.lse + first + i);
-                float2 a = __ffma2_rn(make_float2(__uint_as_float(v[i]), __uint_as_float(v[i + 1])), sc2, make_float2(-e.x, -e.y));
-                float2 c = __ffma2_rn(make_float2(__uint_as_float(v[i + 2]), __uint_as_float(v[i + 3])), sc2, make_float2(-e.z, -e.w));
+                const int4 u = *reinterpret_cast<const int4*>(cl.lim + 64 * half + i), v = *reinterpret_cast<const int4*>(cl.lim + 64 * half + 32 + i);
+                if (key >= u.x) sa[i] = 0xff800000u;
+                if (key >= u.y) sa[i + 1] = 0xff800000u;
+                if (key >= u.z) sa[i + 2] = 0xff800000u;
+                if (key >= u.w) sa[i + 3] = 0xff800000u;
+                if (key >= v.x) sb[i] = 0xff800000u;
+                if (key >= v.y) sb[i + 1] = 0xff800000u;
+                if (key >= v.z) sb[i + 2] = 0xff800000u;
+                if (key >= v.w) sb[i + 3] = 0xff800000u;
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                const uint32_t* w = (k ? sb : sa) + i;
+                const float4 e = *reinterpret_cast<const float4*>(cl.nlse + 64 * half + 32 * k + i);
+                const float2 a = __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), sc2, make_float2(e.x, e.y));
+                const float2 c = __ffma2_rn(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), sc2, make_float2(e.z, e.w));
                 sum0 = __fadd2_rn(sum0, make_float2(fast_exp2(a.x), fast_exp2(a.y)));
                 sum1 = __fadd2_rn(sum1, make_float2(fast_exp2(c.x), fast_exp2(c.y)));
               }
-            };
-            add(sa, 0);
-            add(sb, 32);
-            tmem_ld32x2_wait(sc, sd);
-            release();
-            add(sc, 64);
-            add(sd, 96);
-            l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
+            }
           }
-          ++ns;
+          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
         }
         if (PASS == 2) {
           __syncwarp();
@@ -567,10 +539,11 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       }
       if (!ok) break;
       if (!live) continue;
+      const size_t cut = 2 * it.cut + half;
       if constexpr (PASS == 1)
-        p.parts[((size_t)it.cut * p.n_tokens + it.t0 + tok) * p.hq + it.head * p.g + rg] = make_float2(m, l);
+        p.parts[(cut * p.n_tokens + it.t0 + tok) * p.hq + it.head * p.g + rg] = make_float2(m, l);
       else
-        p.sums[(((size_t)it.cut * p.hkv + it.head) * p.n_seq + it.seq) * p.most + key] = l;
+        p.sums[((cut * p.hkv + it.head) * p.n_seq + it.seq) * p.most + key] = l;
     }
     if (!ok) s_abort = 1;
   }
@@ -580,6 +553,23 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     tc_fence_after();
     tmem_dealloc(tmem, kEmCols);
   }
+}
+
+// Joins the parts of every row: -log2 of its whole sum, -inf where it has none.
+__global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ EmParams p) {
+  pdl_enter();
+  if (p.hdr[kMBad]) return;
+  const size_t rows = (size_t)p.n_tokens * p.hq;
+  const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
+  const int t = (int)(i / p.hq), h = (int)(i - (size_t)t * p.hq);
+  if (i >= rows || t < p.tok_off[0] || t >= p.tok_off[p.n_seq]) return;   // rows of no sequence have no parts
+  float m = -INFINITY, l = 0.f;
+  for (int k = 0; k < 2 * p.cuts1; ++k) m = fmaxf(m, p.parts[k * rows + i].x);
+  for (int k = 0; k < 2 * p.cuts1; ++k) {
+    const float2 v = p.parts[k * rows + i];
+    if (v.y > 0.f) l += v.y * fast_exp2(v.x - m);
+  }
+  p.nlse[((size_t)(h / p.g) * p.n_tokens + t) * p.g + h % p.g] = l > 0.f ? -(m + log2f(l)) : -INFINITY;
 }
 
 // Adds the cuts' and heads' sums in their order.
@@ -593,7 +583,7 @@ __global__ void __launch_bounds__(256) em_add_kernel(const __grid_constant__ EmP
   if (s.y > 0) {
     const float* v = p.sums + (size_t)a * p.most + t;
     const size_t step = (size_t)p.n_seq * p.most;
-    const int n = p.cuts2 * p.hkv;
+    const int n = 2 * p.cuts2 * p.hkv;
 #pragma unroll 8
     for (int i = 0; i < n; ++i) sum += v[i * step];
   }
@@ -602,7 +592,7 @@ __global__ void __launch_bounds__(256) em_add_kernel(const __grid_constant__ EmP
 }
 
 struct EmLayout {
-  size_t hdr, seq, off1, off2, parts, sums, total;
+  size_t hdr, seq, off1, off2, parts, nlse, sums, total;
   int cuts1, cuts2;
 };
 EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks, int hq) {
@@ -628,8 +618,9 @@ EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks
   l.seq = take((size_t)n_seq * 16);
   l.off1 = take((size_t)(n_seq + 1) * 4);
   l.off2 = take((size_t)(n_seq + 1) * 4);
-  l.parts = take((size_t)l.cuts1 * n_tokens * hq * 8);
-  l.sums = take((size_t)l.cuts2 * hkv * n_seq * max_blocks * 16 * 4);
+  l.parts = take((size_t)2 * l.cuts1 * n_tokens * hq * 8);
+  l.nlse = take((size_t)n_tokens * hq * 4);
+  l.sums = take((size_t)2 * l.cuts2 * hkv * n_seq * max_blocks * 16 * 4);
   l.total = o;
   return l;
 }
@@ -660,8 +651,9 @@ kvs_status em_run(const kvs_pool* pool, int layer, const EmParams& p, const CUte
   bool ok = true;
   if (p.n_tokens > 0)
     ok = em_launch(em_pass_kernel<D, 1>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess &&
+         em_launch(em_join_kernel, dim3((unsigned)(((long long)p.n_tokens * p.hq + 255) / 256)), dim3(256), 0, stream, p) == cudaSuccess &&
          em_launch(em_pass_kernel<D, 2>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess;
-  if (ok && p.n_tokens > 0) count_launch(2);
+  if (ok && p.n_tokens > 0) count_launch(3);
   if (ok && em_launch(em_add_kernel, dim3((unsigned)((p.most + 255) / 256), (unsigned)p.n_seq), dim3(256), 0, stream, p, mass_in, carry,
                       mass) == cudaSuccess)
     count_launch();
@@ -716,6 +708,7 @@ extern "C" kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void*
   p.off1 = reinterpret_cast<int*>(w + l.off1);
   p.off2 = reinterpret_cast<int*>(w + l.off2);
   p.parts = reinterpret_cast<float2*>(w + l.parts);
+  p.nlse = reinterpret_cast<float*>(w + l.nlse);
   p.sums = reinterpret_cast<float*>(w + l.sums);
   p.n_tokens = n_tokens;
   p.n_seq = n_seq;
