@@ -61,7 +61,8 @@ struct Dm {   // what a format and the number of 8-column tiles fix
   static constexpr int ST = mx || NT == 2 ? 2 : FMT == kFmtBf16x64 ? 6 : 3;
   static constexpr int kHead = W == 4 ? 1024 : 2048;      // barriers and the warps' sums, in front of the ring
   // two CTAs with three stages of 128 channels and eight heads fill the SM's shared memory to the byte
-  static constexpr int kSmem = kHead + W * (ST * kStage + NT * 8 * D * 4);
+  static constexpr int kPrep = mx ? UT * 16 + 4 * UT * 2 : 0;   // a warp's prepared scales
+  static constexpr int kSmem = kHead + W * (ST * kStage + NT * 8 * D * 4 + kPrep);
   static constexpr float kBias = mx ? 11.f : 0.f;         // weights reach 2^(kBias + kLag)
 };
 constexpr float kLag = 4.f;
@@ -144,6 +145,7 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
   uint8_t* ring = smem_raw + F::kHead + warp * ST * F::kStage;
   float* s_acc = reinterpret_cast<float*>(smem_raw + F::kHead + W * ST * F::kStage);   // [W][g][D]
+  uint8_t* prep = smem_raw + F::kSmem - W * F::kPrep + warp * F::kPrep;   // microscaled: a unit's scales, prepared
   if (tid == 0) {
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
@@ -191,19 +193,23 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
   // ---- copies of this warp's units k = warp, warp + W, ...
   DmAt ahead = seg;
   dm_advance<UT>(p, ahead, warp);
-  int k_ahead = warp;
+  int k_ahead = warp, stage_ahead = 0;
+  uint32_t there = 0;      // bit s: the block of the unit in stage s lies in the pool
   auto look_up = [&]() {   // physical block of the unit ahead
     if (k_ahead >= n_mine) return -1;
     return __ldg(p.table + (size_t)ahead.a * p.max_blocks + ahead.b * UT / F::kBlockTokens);
   };
-  int id_ahead = look_up(), stage_ahead = 0;
+  int id_ahead = look_up();
   auto issue = [&]() {     // whole warp; lane 0 copies
     if (k_ahead >= n_mine) return;
     const int s = stage_ahead;
     if (++stage_ahead == ST) stage_ahead = 0;
+    const bool ok = id_ahead >= 0 && id_ahead < p.capacity;
+    there = (there & ~(1u << s)) | ((ok ? 1u : 0u) << s);
     if (lane == 0) {
       uint64_t* bar = &sh.full[warp][s];
-      if (id_ahead < 0 || id_ahead >= p.capacity) {
+      if (!ok) {
+        set_err(p.status, KVS_DEVERR_BLOCK_ID);
         mbar_arrive(bar);
       } else {
         mbar_arrive_expect_tx(bar, 2 * (F::kCodes + F::kScales));
@@ -221,7 +227,8 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
       }
     }
     k_ahead += W;
-    if (k_ahead < n_mine) dm_advance<UT>(p, ahead, W);
+    ahead.b += W;
+    if (ahead.b >= ahead.units && k_ahead < n_mine) dm_advance<UT>(p, ahead, 0);
     id_ahead = look_up();
   };
   for (int i = 0; i < ST; ++i) issue();
@@ -230,8 +237,6 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
   int stage = 0, uses = 0;
   uint32_t phase = 0;
   bool dead = false;
-  DmAt cur = seg;
-  dm_advance<UT>(p, cur, warp);
   for (int done = 0; done < n_mine;) {
     // ---- one (sequence, KV head): units [seg.b, seg.units) as far as the stretch goes
     const int n_seg = min(seg.units - seg.b, n_mine - done);
@@ -281,53 +286,94 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
             qb[nt][j][i] = ok ? __ldg(reinterpret_cast<const uint32_t*>(qp + (size_t)row * D + 16 * j + 8 * i + 2 * c)) : 0u;
       }
     }
-    float ref[NT][2], l[NT][2], acc[NT][D / 16][4];
+    // ref: reference of the exponentials; thr: scores above it move ref (both in
+    // the units in which the products come, cs times which is log2)
+    float ref[NT][2], thr[NT][2], l[NT][2], acc[NT][D / 16][4];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      ref[nt][0] = ref[nt][1] = -INFINITY;
+      ref[nt][0] = ref[nt][1] = thr[nt][0] = thr[nt][1] = -INFINITY;
       l[nt][0] = l[nt][1] = 0.f;
 #pragma unroll
       for (int j = 0; j < D / 16; ++j) acc[nt][j][0] = acc[nt][j][1] = acc[nt][j][2] = acc[nt][j][3] = 0.f;
     }
-    uint32_t top_e = 0;   // microscaled: the largest scale byte met of each group of channels
-    float* sc_out = p.scores ? p.scores + ((size_t)seg.a * p.hkv + seg.h) * p.most * p.g : nullptr;
+    uint32_t top_e = 0, top01 = 0, top23 = 0;   // microscaled: the largest scale byte met of each group of channels; two to a word
+    const int row0 = F::mx ? mx_token(g) : g;   // token of this lane's first row
+    float* sc_out = p.scores ? p.scores + (((size_t)seg.a * p.hkv + seg.h) * p.most + row0) * p.g + 2 * c : nullptr;
 
-    while (k < done + n_seg) {
-      const int t_unit = cur.b * UT, nv = min(UT, len - t_unit);
-      const int phys = __ldg(p.table + (size_t)cur.a * p.max_blocks + t_unit / F::kBlockTokens);
-      const bool in_pool = phys >= 0 && phys < p.capacity;
-      if (!in_pool && lane == 0) set_err(p.status, KVS_DEVERR_BLOCK_ID);
+    for (; k < done + n_seg; k += W) {
+      const int t_unit = (seg.b + k - done) * UT, nv = len - t_unit;   // nv: tokens of the sequence from here on
       if (!dead && !__all_sync(0xffffffffu, mbar_wait_bounded(&sh.full[warp][stage], phase, p.status))) dead = true;
-      uint8_t* kc = ring + stage * F::kStage;
-      uint8_t* vc = kc + F::kCodes;
-      if (in_pool && !dead) {
+      const uint8_t* kc = ring + stage * F::kStage;
+      const uint8_t* vc = kc + F::kCodes;
+      if (((there >> stage) & 1u) && !dead) {
         float s[MT][NT][4];
-        // ---- S^T, in units of log2
+        // ---- S^T
         if constexpr (F::mx) {
-          const uint8_t* ksc = kc + 2 * F::kCodes;
+          // every lane turns the scales of one token into what the products take:
+          // keys' powers of two (the byte becomes the exponent), row by row; values'
+          // relative to the largest so far, 2^(e - E + 13) as fp16, group by group
+          const uint32_t ke = *reinterpret_cast<const uint32_t*>(kc + 2 * F::kCodes + lane * 4);
+          const uint32_t ve = *reinterpret_cast<const uint32_t*>(kc + 2 * F::kCodes + F::kScales + lane * 4);
+          const int at = (lane & 16) | mx_token(lane & 15);   // the row of token `lane` (the map is its own inverse)
+          *reinterpret_cast<float4*>(prep + at * 16) =
+              make_float4(__uint_as_float((ke << 23) & 0x7f800000u), __uint_as_float((ke << 15) & 0x7f800000u),
+                          __uint_as_float((ke << 7) & 0x7f800000u), __uint_as_float((ke >> 1) & 0x7f800000u));
+          const uint32_t mine = lane < nv ? ve : 0u;
+          const uint32_t v01 = __byte_perm(mine, 0u, 0x4140), v23 = __byte_perm(mine, 0u, 0x4342);
+          const uint32_t m01 = __vmaxu2(v01, top01), m23 = __vmaxu2(v23, top23);
+          if (__any_sync(0xffffffffu, m01 != top01 || m23 != top23)) {
+            uint32_t n01 = m01, n23 = m23;
+#pragma unroll
+            for (int o = 16; o; o >>= 1) {
+              n01 = __vmaxu2(n01, __shfl_xor_sync(0xffffffffu, n01, o));
+              n23 = __vmaxu2(n23, __shfl_xor_sync(0xffffffffu, n23, o));
+            }
+            const uint32_t next = __byte_perm(n01, n23, 0x6420);
+            const int up = (int)((next >> (8 * (g >> 1))) & 255u) - (int)((top_e >> (8 * (g >> 1))) & 255u);
+            const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
+            top_e = next;
+            top01 = n01;
+            top23 = n23;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][j][e] *= f;
+          }
+          // 28 less the distance to the largest, none beyond 28: exponent bits of fp16
+          const uint32_t x01 = (0x001c001cu - __vminu2(top01 - v01, 0x001c001cu)) << 10;
+          const uint32_t x23 = (0x001c001cu - __vminu2(top23 - v23, 0x001c001cu)) << 10;
+          uint16_t* vf = reinterpret_cast<uint16_t*>(prep + 512) + at;
+          vf[0] = (uint16_t)x01;
+          vf[32] = (uint16_t)(x01 >> 16);
+          vf[64] = (uint16_t)x23;
+          vf[96] = (uint16_t)(x23 >> 16);
+          __syncwarp();
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            const int t0 = mt * 16 + mx_token(g), t1 = t0 + 8;
-            const uint32_t e0 = *reinterpret_cast<const uint32_t*>(ksc + t0 * 4), e1 = *reinterpret_cast<const uint32_t*>(ksc + t1 * 4);
+            const int t0 = mt * 16 + row0;
+            const float4 e0 = *reinterpret_cast<const float4*>(prep + (mt * 16 + g) * 16);
+            const float4 e1 = *reinterpret_cast<const float4*>(prep + (mt * 16 + g + 8) * 16);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) s[mt][nt][0] = s[mt][nt][1] = s[mt][nt][2] = s[mt][nt][3] = 0.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               uint32_t x0[4], x1[4];
-              mx_pairs(*reinterpret_cast<const uint32_t*>(kc + swz64(t0 * 64 + 16 * j + 4 * c)), x0);
-              mx_pairs(*reinterpret_cast<const uint32_t*>(kc + swz64(t1 * 64 + 16 * j + 4 * c)), x1);
-              // a byte's power of two: the byte becomes the exponent
-              const float f0 = __uint_as_float((j == 3 ? e0 >> 1 : e0 << (23 - 8 * j)) & 0x7f800000u);
-              const float f1 = __uint_as_float((j == 3 ? e1 >> 1 : e1 << (23 - 8 * j)) & 0x7f800000u);
+              const uint8_t* kr = kc + swz64(t0 * 64 + 16 * j + 4 * c);   // rows 8 apart have the same swizzle
+              mx_pairs(*reinterpret_cast<const uint32_t*>(kr), x0);
+              mx_pairs(*reinterpret_cast<const uint32_t*>(kr + 512), x1);
+              const float f0 = j == 0 ? e0.x : j == 1 ? e0.y : j == 2 ? e0.z : e0.w;
+              const float f1 = j == 0 ? e1.x : j == 1 ? e1.y : j == 2 ? e1.z : e1.w;
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt) {
                 float y[4] = {0.f, 0.f, 0.f, 0.f};
                 mma_f16(y, x0[0], x1[0], x0[1], x1[1], qb[nt][2 * j][0], qb[nt][2 * j][1]);
                 mma_f16(y, x0[2], x1[2], x0[3], x1[3], qb[nt][2 * j + 1][0], qb[nt][2 * j + 1][1]);
-                float* z = s[mt][nt];
-                const float2 a = __ffma2_rn(make_float2(y[0], y[1]), make_float2(f0, f0), make_float2(z[0], z[1]));
-                const float2 b = __ffma2_rn(make_float2(y[2], y[3]), make_float2(f1, f1), make_float2(z[2], z[3]));
-                z[0] = a.x; z[1] = a.y; z[2] = b.x; z[3] = b.y;
+                s[mt][nt][0] = fmaf(y[0], f0, s[mt][nt][0]);
+                s[mt][nt][1] = fmaf(y[1], f0, s[mt][nt][1]);
+                s[mt][nt][2] = fmaf(y[2], f1, s[mt][nt][2]);
+                s[mt][nt][3] = fmaf(y[3], f1, s[mt][nt][3]);
               }
             }
           }
@@ -343,35 +389,48 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
             for (int nt = 0; nt < NT; ++nt) mma_bf16(s[0][nt], x, qb[nt][j][0], qb[nt][j][1]);
           }
         }
-        bool above = false;
+        if (nv < UT) {   // the sequence ends here
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
-          const int t0 = mt * 16 + (F::mx ? mx_token(g) : g), t1 = t0 + 8;
+          for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float& y = s[mt][nt][e];
-              y = (e < 2 ? t0 : t1) < nv ? y * cs[nt][e & 1] : -INFINITY;
-              above |= y > ref[nt][e & 1] + kLag;
-            }
-            if (sc_out) {
-              const int col = nt * 8 + 2 * c;
-              float* o0 = sc_out + (size_t)(t_unit + t0) * p.g + col;
-              float* o1 = sc_out + (size_t)(t_unit + t1) * p.g + col;
-              if ((p.g & 1) == 0) {
-                if (col < p.g && t0 < nv) *reinterpret_cast<float2*>(o0) = make_float2(s[mt][nt][0], s[mt][nt][1]);
-                if (col < p.g && t1 < nv) *reinterpret_cast<float2*>(o1) = make_float2(s[mt][nt][2], s[mt][nt][3]);
-              } else {
+              for (int e = 0; e < 4; ++e)
+                if (mt * 16 + row0 + 8 * (e >> 1) >= nv) s[mt][nt][e] = -INFINITY;
+        }
+        if (sc_out) {
+          float* o = sc_out + (size_t)t_unit * p.g;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                  if (col + i < p.g && t0 < nv) o0[i] = s[mt][nt][i];
-                  if (col + i < p.g && t1 < nv) o1[i] = s[mt][nt][2 + i];
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int hr = 0; hr < 2; ++hr) {
+              const int t = mt * 16 + 8 * hr;
+              if (t + row0 >= nv) continue;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt) {
+                const int col = nt * 8 + 2 * c;
+                const float y0 = s[mt][nt][2 * hr] * cs[nt][0], y1 = s[mt][nt][2 * hr + 1] * cs[nt][1];
+                float* q = o + t * p.g + nt * 8;
+                if ((p.g & 1) == 0) {
+                  if (col < p.g) *reinterpret_cast<float2*>(q) = make_float2(y0, y1);
+                } else {
+                  if (col < p.g) q[0] = y0;
+                  if (col + 1 < p.g) q[1] = y1;
                 }
               }
             }
-          }
         }
+        bool above = false;
+        float top[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            top[nt][i] = fmaxf(s[0][nt][i], s[0][nt][2 + i]);
+#pragma unroll
+            for (int mt = 1; mt < MT; ++mt) top[nt][i] = fmaxf(top[nt][i], fmaxf(s[mt][nt][i], s[mt][nt][2 + i]));
+            above |= top[nt][i] > thr[nt][i];
+          }
         if (__any_sync(0xffffffffu, above)) {
           // some column's reference moves to its maximum so far
 #pragma unroll
@@ -379,14 +438,14 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
             float f[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              float mx = -INFINITY;
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt) mx = fmaxf(mx, fmaxf(s[mt][nt][i], s[mt][nt][2 + i]));
+              float mx = top[nt][i];
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-              const float next = mx > ref[nt][i] + kLag ? mx : ref[nt][i];
-              f[i] = next > ref[nt][i] ? fast_exp2(ref[nt][i] - next) : 1.f;
+              const bool move = mx > thr[nt][i];
+              const float next = move ? mx * cs[nt][i] : ref[nt][i];
+              f[i] = move ? fast_exp2(ref[nt][i] - next) : 1.f;
               ref[nt][i] = next;
+              if (move) thr[nt][i] = mx + kLag / cs[nt][i];
               l[nt][i] *= f[i];
             }
 #pragma unroll
@@ -404,7 +463,7 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
           for (int nt = 0; nt < NT; ++nt) {
             float w[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] = fast_exp2(s[mt][nt][e] - (ref[nt][e & 1] - F::kBias));
+            for (int e = 0; e < 4; ++e) w[e] = fast_exp2(fmaf(s[mt][nt][e], cs[nt][e & 1], F::kBias - ref[nt][e & 1]));
             l[nt][0] += w[0] + w[2];
             l[nt][1] += w[1] + w[3];
 #pragma unroll
@@ -416,60 +475,50 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
               pl[mt][nt][i] = movm_t(lo);
             }
           }
-        // ---- O^T += V^T P^T
-        if constexpr (F::mx) {
-          const uint8_t* vsc = kc + 2 * F::kCodes + F::kScales;
-          // E: the largest scale so far in each group of channels, over tokens of the sequence
-          const uint32_t mine = lane < nv ? *reinterpret_cast<const uint32_t*>(vsc + lane * 4) : 0u;
-          if (__any_sync(0xffffffffu, __vcmpgtu4(mine, top_e) != 0u)) {
-            uint32_t next = __vmaxu4(mine, top_e);
-#pragma unroll
-            for (int o = 16; o; o >>= 1) next = __vmaxu4(next, __shfl_xor_sync(0xffffffffu, next, o));
-            const int up = (int)((next >> (8 * (g >> 1))) & 255u) - (int)((top_e >> (8 * (g >> 1))) & 255u);
-            const float f = up > 126 ? 0.f : __uint_as_float((uint32_t)(127 - up) << 23);
-            top_e = next;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[nt][j][e] *= f;
+        // ---- O^T += V^T P^T.  Each unit's products are added in plain fp32: the
+        // tensor cores cut their sums, which over a long context is a bias (16,384
+        // tokens: 5.5e-6 of the result, added here 1.5e-6).
+        auto values = [&](int nt, int j, const uint32_t* x, int mt) {
+          float y[4] = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (F::mx) {
+            mma_f16(y, x[0], x[1], x[2], x[3], ph[mt][nt][0], ph[mt][nt][1]);
+            mma_f16(y, x[0], x[1], x[2], x[3], pl[mt][nt][0], pl[mt][nt][1]);
+          } else {
+            mma_bf16(y, x, ph[mt][nt][0], ph[mt][nt][1]);
+            mma_bf16(y, x, pl[mt][nt][0], pl[mt][nt][1]);
           }
-          const int rel = 28 - (int)((top_e >> (8 * (g >> 1))) & 255u);
+          float* a = acc[nt][j];
+          const float2 u = __fadd2_rn(make_float2(a[0], a[1]), make_float2(y[0], y[1]));
+          const float2 v = __fadd2_rn(make_float2(a[2], a[3]), make_float2(y[2], y[3]));
+          a[0] = u.x; a[1] = u.y; a[2] = v.x; a[3] = v.y;
+        };
+        if constexpr (F::mx) {
+          const uint8_t* vf = prep + 512 + (g >> 1) * 64 + 4 * c;
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt) {
-            {
-              // tokens of the four rows 2c, 2c + 1, 2c + 8, 2c + 9; channels 16 g .. 16 g + 15
-              uint2 v[4];
-              uint32_t sc[4];
+            // tokens of the four rows 2c, 2c + 1, 2c + 8, 2c + 9; channels 16 g .. 16 g + 15
+            uint2 v[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int t = mt * 16 + mx_token(2 * c + (i & 1)) + 8 * (i >> 1);
-                v[i] = *reinterpret_cast<const uint2*>(vc + swz64(t * 64 + 16 * (g >> 1)) + 8 * (g & 1));
-                const int e = (int)vsc[t * 4 + (g >> 1)] + rel;
-                sc[i] = (uint32_t)min(max(e, 0), 28) << 10;
-              }
-              const uint32_t s01 = sc[0] | (sc[1] << 16), s89 = sc[2] | (sc[3] << 16);
+            for (int i = 0; i < 4; ++i) {
+              const int t = mt * 16 + mx_token(2 * c + (i & 1));
+              v[i] = *reinterpret_cast<const uint2*>(vc + swz64(t * 64 + 16 * (g >> 1)) + 8 * (g & 1) + 512 * (i >> 1));
+            }
+            const uint32_t s01 = *reinterpret_cast<const uint32_t*>(vf + mt * 32), s89 = *reinterpret_cast<const uint32_t*>(vf + mt * 32 + 16);
 #pragma unroll
-              for (int word = 0; word < 2; ++word) {
-                const uint32_t w0 = word ? v[0].y : v[0].x, w1 = word ? v[1].y : v[1].x;
-                const uint32_t w8 = word ? v[2].y : v[2].x, w9 = word ? v[3].y : v[3].x;
-                constexpr uint32_t kLow = 0x0f0f0f0fu;
-                uint32_t a0[4], a1[4], a2[4], a3[4];   // even channels, odd ones; tokens 2c, 2c + 1 and 2c + 8, 2c + 9
-                mx_pairs((w0 & kLow) | ((w1 << 4) & ~kLow), a0);
-                mx_pairs(((w0 >> 4) & kLow) | (w1 & ~kLow), a1);
-                mx_pairs((w8 & kLow) | ((w9 << 4) & ~kLow), a2);
-                mx_pairs(((w8 >> 4) & kLow) | (w9 & ~kLow), a3);
+            for (int word = 0; word < 2; ++word) {
+              const uint32_t w0 = word ? v[0].y : v[0].x, w1 = word ? v[1].y : v[1].x;
+              const uint32_t w8 = word ? v[2].y : v[2].x, w9 = word ? v[3].y : v[3].x;
+              constexpr uint32_t kLow = 0x0f0f0f0fu;
+              uint32_t a0[4], a1[4], a2[4], a3[4];   // even channels, odd ones; tokens 2c, 2c + 1 and 2c + 8, 2c + 9
+              mx_pairs((w0 & kLow) | ((w1 << 4) & ~kLow), a0);
+              mx_pairs(((w0 >> 4) & kLow) | (w1 & ~kLow), a1);
+              mx_pairs((w8 & kLow) | ((w9 << 4) & ~kLow), a2);
+              mx_pairs(((w8 >> 4) & kLow) | (w9 & ~kLow), a3);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  const uint32_t x0 = mul_f16x2(a0[j], s01), x1 = mul_f16x2(a1[j], s01);
-                  const uint32_t x2 = mul_f16x2(a2[j], s89), x3 = mul_f16x2(a3[j], s89);
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t x[4] = {mul_f16x2(a0[j], s01), mul_f16x2(a1[j], s01), mul_f16x2(a2[j], s89), mul_f16x2(a3[j], s89)};
 #pragma unroll
-                  for (int nt = 0; nt < NT; ++nt) {
-                    mma_f16(acc[nt][word * 4 + j], x0, x1, x2, x3, ph[mt][nt][0], ph[mt][nt][1]);
-                    mma_f16(acc[nt][word * 4 + j], x0, x1, x2, x3, pl[mt][nt][0], pl[mt][nt][1]);
-                  }
-                }
+                for (int nt = 0; nt < NT; ++nt) values(nt, word * 4 + j, x, mt);
               }
             }
           }
@@ -477,7 +526,7 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
           if (nv < UT) {
             // rows behind the end hold anything, and 0 * NaN is not 0
             for (int i = lane; i < (UT - nv) * (D / 8); i += 32)
-              *reinterpret_cast<uint4*>(vc + kv_tile_off<D>(nv + i / (D / 8), (i % (D / 8)) * 8)) = make_uint4(0u, 0u, 0u, 0u);
+              *reinterpret_cast<uint4*>(const_cast<uint8_t*>(vc) + kv_tile_off<D>(nv + i / (D / 8), (i % (D / 8)) * 8)) = make_uint4(0u, 0u, 0u, 0u);
             __syncwarp();
           }
           const uint32_t va = smem_u32(vc);
@@ -486,15 +535,13 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
             uint32_t x[4];
             ldsm_x4_t(va + kv_tile_off<D>((lane & 7) + (lane >> 4) * 8, j * 16 + ((lane >> 3) & 1) * 8), x[0], x[1], x[2], x[3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              mma_bf16(acc[nt][j], x, ph[0][nt][0], ph[0][nt][1]);
-              mma_bf16(acc[nt][j], x, pl[0][nt][0], pl[0][nt][1]);
-            }
+            for (int nt = 0; nt < NT; ++nt) values(nt, j, x, 0);
           }
           if (nv < UT) fence_proxy_async_smem();   // the zeros are written before a copy overwrites them
         }
-      } else if (sc_out) {
-        for (int i = lane; i < nv * p.g; i += 32) sc_out[(size_t)t_unit * p.g + i] = -INFINITY;
+      } else if (p.scores) {
+        float* o = p.scores + (((size_t)seg.a * p.hkv + seg.h) * p.most + t_unit) * p.g;
+        for (int i = lane; i < min(nv, UT) * p.g; i += 32) o[i] = -INFINITY;
       }
       __syncwarp();
       if (++stage == ST) {
@@ -503,8 +550,6 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
       }
       ++uses;
       if (!dead) issue();
-      k += W;
-      if (k < n_mine) dm_advance<UT>(p, cur, W);
     }
 
     // ---- the warps' states become one
@@ -620,42 +665,61 @@ struct AddMassParams {
   float carry;
 };
 
-constexpr int kMassThreads = 256;
+constexpr int kMassThreads = 128;
 
 // A thread takes a token; the heads in their order, so the sum is the same in
-// every call.  G4: the heads of a group four at a time.
-template <bool G4>
+// every call.  G: query heads of a KV head (0: any), as many scores side by side.
+// The scores were just written and lie in L2 for the most part; sixteen loads are
+// in flight a thread.
+template <int G>
 __global__ void __launch_bounds__(kMassThreads) add_mass_kernel(const __grid_constant__ AddMassParams p) {
   extern __shared__ float2 s_fin[];   // [hkv * g]
-  const int a = blockIdx.y;
+  const int a = blockIdx.y, g = G ? G : p.g;
   pdl_enter();
   const int len = min(max(__ldg(p.seq_len + a), 0), p.most);
   const int t = blockIdx.x * kMassThreads + threadIdx.x;
   if ((int)blockIdx.x * kMassThreads >= len) return;
-  for (int i = threadIdx.x; i < p.hkv * p.g; i += kMassThreads) s_fin[i] = p.fin[(size_t)a * p.hkv * p.g + i];
+  for (int i = threadIdx.x; i < p.hkv * g; i += kMassThreads) s_fin[i] = p.fin[(size_t)a * p.hkv * g + i];
   __syncthreads();
   if (t >= len) return;
   float sum = 0.f;
-  const size_t step = (size_t)p.most * p.g;
-  const float* s = p.scores + (size_t)a * p.hkv * step + (size_t)t * p.g;
-  if constexpr (G4) {
-#pragma unroll 4
+  const size_t step = (size_t)p.most * g;
+  const float* s = p.scores + (size_t)a * p.hkv * step + (size_t)t * g;
+  auto add = [&](float x, int i) {
+    const float2 f = s_fin[i];
+    sum += fast_exp2(x - f.x) * f.y;
+  };
+  if constexpr (G == 0) {
     for (int h = 0; h < p.hkv; ++h, s += step)
-      for (int i = 0; i < p.g; i += 4) {
-        const float4 x = __ldcs(reinterpret_cast<const float4*>(s + i));
-        const float2* f = s_fin + h * p.g + i;
-        sum += fast_exp2(x.x - f[0].x) * f[0].y;
-        sum += fast_exp2(x.y - f[1].x) * f[1].y;
-        sum += fast_exp2(x.z - f[2].x) * f[2].y;
-        sum += fast_exp2(x.w - f[3].x) * f[3].y;
-      }
+      for (int i = 0; i < g; ++i) add(__ldcs(s + i), h * g + i);
   } else {
-#pragma unroll 8
-    for (int h = 0; h < p.hkv; ++h, s += step)
-      for (int i = 0; i < p.g; ++i) {
-        const float2 f = s_fin[h * p.g + i];
-        sum += fast_exp2(__ldcs(s + i) - f.x) * f.y;
-      }
+    constexpr int V = G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1, U = G >= 16 ? 1 : 16 / G;   // values a load, KV heads at a time
+    int h = 0;
+    for (; h + U <= p.hkv; h += U, s += U * step) {
+      float x[U][G];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < G; i += V) {
+          const float* q = s + u * step + i;
+          if constexpr (V == 4) {
+            const float4 y = __ldcs(reinterpret_cast<const float4*>(q));
+            x[u][i] = y.x; x[u][i + 1] = y.y; x[u][i + 2] = y.z; x[u][i + 3] = y.w;
+          } else if constexpr (V == 2) {
+            const float2 y = __ldcs(reinterpret_cast<const float2*>(q));
+            x[u][i] = y.x; x[u][i + 1] = y.y;
+          } else {
+            x[u][i] = __ldcs(q);
+          }
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int i = 0; i < G; ++i) add(x[u][i], (h + u) * G + i);
+    }
+    for (; h < p.hkv; ++h, s += step)
+#pragma unroll
+      for (int i = 0; i < G; ++i) add(__ldcs(s + i), h * G + i);
   }
   const size_t o = (size_t)a * p.most + t;
   p.mass[o] = p.mass_in ? fmaf(p.carry, p.mass_in[o], sum) : sum;
@@ -768,7 +832,9 @@ kvs_status decode_mass(kvs_pool* pool, int32_t layer, const void* q, int32_t n_q
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    ok = cudaLaunchKernelEx(&cfg, g % 4 ? add_mass_kernel<false> : add_mass_kernel<true>, m) == cudaSuccess;
+    auto kern = g == 1 ? add_mass_kernel<1> : g == 2 ? add_mass_kernel<2> : g == 4 ? add_mass_kernel<4> : g == 8 ? add_mass_kernel<8>
+                : g == 5 ? add_mass_kernel<5> : g == 16 ? add_mass_kernel<16> : add_mass_kernel<0>;
+    ok = cudaLaunchKernelEx(&cfg, kern, m) == cudaSuccess;
     if (ok) count_launch();
   }
   return check_launch(what.c_str());

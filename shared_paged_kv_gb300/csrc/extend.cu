@@ -703,14 +703,6 @@ __device__ __forceinline__ int ex_tiles(const ExItem& it, int x, int tt) {
   return max(0, min((lim + kExTile - 1) / kExTile, it.kv1) - it.kv0);
 }
 
-__device__ __forceinline__ void ex_mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t hi, uint32_t idesc, uint32_t acc) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tmov.b64 db, {%2, %3};\n\t"
-      "setp.ne.b32 p, %5, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}" ::"r"(d),
-      "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"(acc)
-      : "memory");
-}
-
 // A 32-byte store: a thread's columns of a row fill whole sectors.
 __device__ __forceinline__ void st_global_v8(void* p, const uint32_t* v) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),

@@ -33,15 +33,14 @@ namespace kvs {
 namespace {
 
 // Four warpgroups of sums, two for each X tile: one takes columns 0 to 63 of a
-// product, one the others, so that a scheduler has four warps to choose from
-// (two of them: 1.0 us for a pair of products, with four TBD).  Behind them a warp
-// that issues the products, one for the copies, one for pass 2's columns.
+// product, one the others, so that a scheduler has four warps to choose from.
+// Behind them a warp for each X tile that issues its products, one for the copies,
+// one for pass 2's columns.
 constexpr int kEmSumWarps = 16, kEmThreads = (kEmSumWarps + 4) * 32;
-constexpr int kEmMma = kEmSumWarps, kEmTma = kEmSumWarps + 1, kEmCol = kEmSumWarps + 2;
+constexpr int kEmMma = kEmSumWarps, kEmTma = kEmSumWarps + 2, kEmCol = kEmSumWarps + 3;
 constexpr int kEmTile = 128;
 constexpr int kEmMaxCuts = 16;
-constexpr uint32_t kEmCols = 512;
-constexpr float kEmLag = 8.f;    // the reference of a row's sum moves when a score exceeds it by more
+constexpr uint32_t kEmCols = 512, kEmX = 384;   // scores in three buffers of 128 columns, behind them the X tiles
 
 template <int D>
 __host__ __device__ constexpr int em_tile_bytes() { return kEmTile * D * 2; }
@@ -109,10 +108,10 @@ struct __align__(16) EmItem {
 
 struct EmBars {
   uint64_t full[8], empty[8];
-  uint64_t x_full, x_empty;
-  uint64_t s_full[2][2], s_empty[2][2];
+  uint64_t x_full, x_empty, x_there;     // X tiles in shared memory, read from there, in tensor memory
+  uint64_t s_full[2][2], s_empty[2][2];  // scores of X tile 0 in buffers 0 and 1, of X tile 1 in buffer 2
   uint64_t it_full[2], it_empty[2];
-  uint64_t fin;
+  uint64_t fin[2];
 };
 
 struct EmCols {   // pass 2: of the 128 columns of a Y tile
@@ -155,19 +154,21 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     prefetch_tmap(&tk);
     for (int i = 0; i < ST; ++i) {
       mbar_init(&bars.full[i], PASS == 2 ? 2 : 1);     // the copies; pass 2: the column warp
-      mbar_init(&bars.empty[i], PASS == 2 ? 1 + kEmSumWarps : 1);   // the products; pass 2: the columns are read
+      mbar_init(&bars.empty[i], PASS == 2 ? 2 + kEmSumWarps : 2);   // both X tiles' products; pass 2: the columns are read
     }
     mbar_init(&bars.x_full, 1);
-    mbar_init(&bars.x_empty, 1);
+    mbar_init(&bars.x_empty, kEmSumWarps);
+    mbar_init(&bars.x_there, kEmSumWarps);
     for (int x = 0; x < 2; ++x) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&bars.s_full[x][b], 1);
         mbar_init(&bars.s_empty[x][b], kEmSumWarps / 2);
       }
       mbar_init(&bars.it_full[x], 1);
-      mbar_init(&bars.it_empty[x], kEmSumWarps + (PASS == 2 ? 2 : 1));
+      mbar_init(&bars.it_empty[x], kEmSumWarps + (PASS == 2 ? 3 : 2));
     }
-    mbar_init(&bars.fin, 1);
+    mbar_init(&bars.fin[0], 1);
+    mbar_init(&bars.fin[1], 1);
     s_abort = 0;
     fence_barrier_init();
   }
@@ -208,11 +209,11 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         if (lane == 0) c = atomicAdd(counter, 1);
         return (long long)(unsigned)__shfl_sync(0xffffffffu, c, 0);
       };
-      // blocks of key tile j of the sequence: an id for lanes below 8, -1 where there is none
+      // blocks of key tiles j .. j + 3 of the sequence, eight lanes a tile; -1 where there is none
       auto key_blocks = [&](int a, int j, int keys) {
         const int b = j * 8 + lane;
         int id = -1;
-        if (lane < 8 && b < (keys + 15) / 16) {
+        if (b < (keys + 15) / 16) {
           id = __ldg(p.table + (size_t)a * p.max_blocks + b);
           if (id < 0 || id >= p.capacity) {
             set_err(p.status, KVS_DEVERR_BLOCK_ID);
@@ -292,7 +293,9 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         if (it.done) break;
         claim = claim_next();
         if (it.y0 >= it.y1) continue;
-        // X tiles, once the products of the item before have read theirs
+        int ids = PASS == 1 ? key_blocks(it.seq, it.y0, it.keys) : key_blocks(it.seq, it.x0 / kEmTile, it.keys);
+        int ids_next = PASS == 1 ? key_blocks(it.seq, it.y0 + 4, it.keys) : 0;
+        // X tiles, once those of the item before are in tensor memory
         if (nx >= 1 && !wait(&bars.x_empty, (nx - 1) & 1)) { ok = false; break; }
         const bool two = PASS == 1 ? it.x0 + tt < it.rows : it.x0 + kEmTile < it.keys;
         if (lane == 0) mbar_arrive_expect_tx(&bars.x_full, (two ? 2u : 1u) * (PASS == 1 ? row_bytes : (uint32_t)kTile));
@@ -302,25 +305,27 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
             if (lane == 0) copy_rows(sX(x), it.t0 + it.x0 + x * tt, it.head, &bars.x_full);
             __syncwarp();
           } else {
-            copy_keys(sX(x), key_blocks(it.seq, it.x0 / kEmTile + x, it.keys), it.head, &bars.x_full);
+            copy_keys(sX(x), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * x), it.head, &bars.x_full);
           }
         }
         ++nx;
-        int id = PASS == 1 ? key_blocks(it.seq, it.y0, it.keys) : 0;
         for (int j = it.y0; j < it.y1; ++j) {
-          const int id_next = PASS == 1 && j + 1 < it.y1 ? key_blocks(it.seq, j + 1, it.keys) : -1;
+          const int turn = (j - it.y0) & 3;
+          if (PASS == 1 && turn == 0 && j > it.y0) {
+            ids = ids_next;
+            ids_next = key_blocks(it.seq, j + 4, it.keys);
+          }
           const int s = n % ST;
           if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) { ok = false; break; }
           if (lane == 0) mbar_arrive_expect_tx(&bars.full[s], PASS == 1 ? (uint32_t)kTile : row_bytes);
           __syncwarp();
           if constexpr (PASS == 1) {
-            copy_keys(ring(s), id, it.head, &bars.full[s]);
+            copy_keys(ring(s), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * turn), it.head, &bars.full[s]);
           } else {
             if (lane == 0) copy_rows(ring(s), it.t0 + j * tt, it.head, &bars.full[s]);
             __syncwarp();
           }
           armed = n++;
-          id = id_next;
         }
         if (!ok) break;
       }
@@ -330,12 +335,14 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         for (int m = max(0, armed - ST + 1); m <= armed; ++m) mbar_drain(&bars.full[m % ST], (m / ST) & 1);
         if (nx) mbar_drain(&bars.x_full, (nx - 1) & 1);
       }
-    } else if (warp == kEmMma) {
-      // --------------------------------------------------------- MMA issue
+    } else if (warp < kEmTma) {
+      // ------------------------------------------- products of one X tile
+      const int x = warp - kEmMma;
       constexpr uint32_t idS = umma_idesc_bf16(128, 128, false, false);
       constexpr uint32_t kHi = ex_desc_hi(1024);
-      const uint32_t x_lo = ex_desc_lo(smem_u32(base), 16), y_lo = ex_desc_lo(smem_u32(ring(0)), 16);
-      int n = 0, nx = 0, ns[2] = {0, 0};
+      const uint32_t y_lo = ex_desc_lo(smem_u32(ring(0)), 16), tX = tmem + kEmX + (uint32_t)(D / 2) * x;
+      int nx = 0, b = 0, s = 0;
+      uint32_t full_par = 0, free_par = 1;   // a fresh buffer counts as handed back
       bool ok = true;
       auto commit = [&](uint64_t* bar) {
         if (elect_one()) umma_commit(bar);
@@ -344,45 +351,43 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       for (int ni = 0;; ++ni) {
         const int slot = ni & 1;
         if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
-        const EmItem it = work[slot];
+        const int y0 = work[slot].y0, y1 = work[slot].y1, xs = work[slot].xs[x], xe = work[slot].xe[x], done = work[slot].done;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
-        if (it.done) break;
-        if (it.y0 >= it.y1) continue;
-        if (!wait(&bars.x_full, nx & 1)) { ok = false; break; }
+        if (done) break;
+        if (y0 >= y1) continue;
+        if (!wait(&bars.x_there, nx & 1)) { ok = false; break; }
         ++nx;
-        for (int j = it.y0; j < it.y1; ++j) {
-          const int s = n % ST;
-          if (!wait(&bars.full[s], (n / ST) & 1)) { ok = false; break; }
-#pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            if (j < it.xs[x] || j >= it.xe[x]) continue;
-            const int b = ns[x] & 1;
-            if (ns[x] >= 2 && !wait(&bars.s_empty[x][b], ((ns[x] - 2) >> 1) & 1)) { ok = false; break; }
+        for (int j = y0; j < y1; ++j) {
+          if (!wait(&bars.full[s], full_par)) { ok = false; break; }
+          if (j >= xs && j < xe) {
+            if (!wait(&bars.s_empty[x][b], free_par)) { ok = false; break; }
             tc_fence_after();
             if (elect_one()) {
-              const uint32_t xa = x_lo + x * (kTile / 16), ya = y_lo + s * (kTile / 16);
+              const uint32_t ya = y_lo + s * (kTile / 16), d = tmem + 128u * (2 * x + b);
 #pragma unroll
-              for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) / 16;
-                ex_mma_ss(tmem + 256u * x + 128u * b, xa + o, ya + o, kHi, idS, kk > 0);
-              }
+              for (int kk = 0; kk < D / 16; ++kk)
+                ex_mma_ts(d, tX + 8u * kk, ya + ((kk >> 2) * kHalf + (kk & 3) * 32) / 16, kHi, idS, kk > 0);
               umma_commit(&bars.s_full[x][b]);
+              umma_commit(&bars.empty[s]);
             }
             __syncwarp();
-            ++ns[x];
+            if (x == 1 || b == 1) free_par ^= 1u;
+            if (x == 0) b ^= 1;
+          } else {
+            commit(&bars.empty[s]);
           }
-          if (!ok) break;
-          commit(&bars.empty[s]);
-          ++n;
+          if (++s == ST) {
+            s = 0;
+            full_par ^= 1u;
+          }
         }
         if (!ok) break;
-        commit(&bars.x_empty);
       }
       if (!ok) s_abort = 1;
       // every product issued has completed before the tensor memory is released
-      commit(&bars.fin);
-      mbar_wait_bounded(&bars.fin, 0, p.status);
+      commit(&bars.fin[x]);
+      mbar_wait_bounded(&bars.fin[x], 0, p.status);
     } else if (PASS == 2 && warp == kEmCol) {
       // ------------------------------------- columns: limits and sums of the rows
       int n = 0;
@@ -437,10 +442,11 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
   } else {
     // ------------------------------------------------------------ sums
     const int x = (warp >> 2) & 1, half = warp >> 3, r = (warp & 3) * 32 + lane;
-    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * x + 64u * half;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16, tS = tmem + lanes + 256u * x + 64u * half;
     const int rt = r / p.g, rg = r - rt * p.g;
     const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
-    int n = 0, ns = 0;
+    int n = 0, nx = 0, b = 0;   // Y tiles, items with any, score buffer
+    uint32_t s_par = 0;
     bool ok = true;
     for (int ni = 0;; ++ni) {
       const int slot = ni & 1;
@@ -454,82 +460,109 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       const int key = it.x0 + x * kEmTile + r;           // pass 2: this row's key
       const bool live = PASS == 1 ? rt < tt && tok < it.rows : key < it.keys;
       const int lim = p.causal ? min(it.keys - it.rows + tok + 1, it.keys) : it.keys;   // pass 1: keys that the row sees
-      float m = -INFINITY, l = 0.f;
+      float m = 0.f, l = 0.f;
+      if (it.y0 < it.y1) {
+        // X goes to tensor memory (a product that takes it from there reads half
+        // as much of shared memory, which bounds it otherwise): every thread half
+        // of its row.  The products of the item before are complete: this
+        // thread has seen its X tile's last ones.
+        if (!wait(&bars.x_full, nx & 1)) { ok = false; break; }
+        ++nx;
+        uint32_t w[D / 4];
+        const uint8_t* row = sX(x) + (D == 128 ? half * kHalf : 0);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint4 v = *reinterpret_cast<const uint4*>(row + swz128((uint32_t)r * 128 + 16 * (i + (D == 128 ? 0 : 4 * half))));
+          w[4 * i] = v.x;
+          w[4 * i + 1] = v.y;
+          w[4 * i + 2] = v.z;
+          w[4 * i + 3] = v.w;
+        }
+        const uint32_t tX = tmem + lanes + kEmX + (uint32_t)(D / 2) * x + (uint32_t)(D / 4) * half;
+        if constexpr (D == 128) tmem_st32(tX, w);
+        else tmem_st16(tX, w);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&bars.x_empty);
+          mbar_arrive(&bars.x_there);
+        }
+      }
+      // Pass 1: keys below `whole` are visible to every live row of the warp.
+      // Pass 2: this warp's last key.
+      const int whole = PASS == 1 ? __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff) : 0;
+      const int last_key = it.x0 + x * kEmTile + (warp & 3) * 32 + 31;
+      uint32_t v[64];
+      auto sum_up = [&](auto by) {   // by(i): what is added to columns i and i + 1
+        float2 sum[4] = {};
+#pragma unroll
+        for (int i = 0; i < 64; i += 16) {
+          float2 a[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            a[k] = __ffma2_rn(make_float2(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1])), sc2, by(i + 2 * k));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) a[k] = make_float2(fast_exp2(a[k].x), fast_exp2(a[k].y));
+#pragma unroll
+          for (int k = 0; k < 8; ++k) sum[k & 3] = __fadd2_rn(sum[k & 3], a[k]);
+        }
+        const float2 t = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+        return t.x + t.y;
+      };
       for (int j = it.y0; j < it.y1; ++j) {
         const int s = n % ST;
         // also where this X tile passes the Y tile by: a stage is handed back once a turn
         if (PASS == 2 && !wait(&bars.full[s], (n / ST) & 1)) { ok = false; break; }
         if (j >= xs && j < xe) {
-          const int b = ns & 1;
-          if (!wait(&bars.s_full[x][b], (ns >> 1) & 1)) { ok = false; break; }
+          if (!wait(&bars.s_full[x][b], s_par)) { ok = false; break; }
           tc_fence_after();
-          uint32_t sa[32], sb[32];
-          tmem_ld32_issue(tS + 128u * b, sa);
-          tmem_ld32_issue(tS + 128u * b + 32, sb);
-          tmem_ld32x2_wait(sa, sb);
+          tmem_ld32_issue(tS + 128u * b, v);
+          tmem_ld32_issue(tS + 128u * b + 32, v + 32);
+          tmem_ld32x2_wait(v, v + 32);
           tc_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&bars.s_empty[x][b]);
-          ++ns;
-          float2 sum0 = make_float2(0.f, 0.f), sum1 = sum0;
+          if (x == 1 || b == 1) s_par ^= 1u;
+          if (x == 0) b ^= 1;
           if constexpr (PASS == 1) {
-            const int rem = lim - j * kEmTile - 64 * half;   // visible ones of these keys
-            if (__any_sync(0xffffffffu, rem < 64 && live)) {
+            const int key0 = j * kEmTile + 64 * half;
+            if (key0 + 64 > whole) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                if (i >= rem) sa[i] = 0xff800000u;
-                if (i + 32 >= rem) sb[i] = 0xff800000u;
+              for (int i = 0; i < 64; ++i)
+                if (key0 + i >= lim) v[i] = 0xff800000u;
+            }
+            // The reference is the maximum of the first columns (a row that sees
+            // later ones sees all of these) and moves only where a sum gets out of
+            // hand: any reference within 2^60 of the maximum serves float32 as well.
+            const bool fresh = j == xs;
+            float sum = fresh ? INFINITY : sum_up([&](int) { return make_float2(-m, -m); });
+            if (__any_sync(0xffffffffu, !(sum < 0x1p60f))) {
+              float top = __uint_as_float(v[0]);
+#pragma unroll
+              for (int i = 1; i < 64; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+              top *= p.scale_log2;
+              if (!(sum < 0x1p60f)) {
+                if (!fresh) l *= fast_exp2(m - top);
+                m = top == -INFINITY ? 0.f : top;
               }
+              sum = sum_up([&](int) { return make_float2(-m, -m); });
             }
-            float t0 = -INFINITY, t1 = -INFINITY;
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              t0 = fmaxf(t0, fmaxf(__uint_as_float(sa[i]), __uint_as_float(sa[i + 1])));
-              t1 = fmaxf(t1, fmaxf(__uint_as_float(sb[i]), __uint_as_float(sb[i + 1])));
-            }
-            const float mx = fmaxf(t0, t1) * p.scale_log2;
-            const float next = mx > m + kEmLag ? mx : m;
-            const float ref = next == -INFINITY ? 0.f : next;
-            if (next > m) l *= fast_exp2(m - next);   // 0 before the first
-            m = next;
-            const float2 rf2 = make_float2(-ref, -ref);
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 a = __ffma2_rn(make_float2(__uint_as_float(sa[i]), __uint_as_float(sa[i + 1])), sc2, rf2);
-              const float2 c = __ffma2_rn(make_float2(__uint_as_float(sb[i]), __uint_as_float(sb[i + 1])), sc2, rf2);
-              sum0 = __fadd2_rn(sum0, make_float2(fast_exp2(a.x), fast_exp2(a.y)));
-              sum1 = __fadd2_rn(sum1, make_float2(fast_exp2(c.x), fast_exp2(c.y)));
-            }
+            l += sum;
           } else {
             const EmCols& cl = cols[s];
-            if (__any_sync(0xffffffffu, live && key >= cl.least)) {
+            if (last_key >= cl.least) {
 #pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                const int4 u = *reinterpret_cast<const int4*>(cl.lim + 64 * half + i), v = *reinterpret_cast<const int4*>(cl.lim + 64 * half + 32 + i);
-                if (key >= u.x) sa[i] = 0xff800000u;
-                if (key >= u.y) sa[i + 1] = 0xff800000u;
-                if (key >= u.z) sa[i + 2] = 0xff800000u;
-                if (key >= u.w) sa[i + 3] = 0xff800000u;
-                if (key >= v.x) sb[i] = 0xff800000u;
-                if (key >= v.y) sb[i + 1] = 0xff800000u;
-                if (key >= v.z) sb[i + 2] = 0xff800000u;
-                if (key >= v.w) sb[i + 3] = 0xff800000u;
+              for (int i = 0; i < 64; i += 4) {
+                const int4 u = *reinterpret_cast<const int4*>(cl.lim + 64 * half + i);
+                if (key >= u.x) v[i] = 0xff800000u;
+                if (key >= u.y) v[i + 1] = 0xff800000u;
+                if (key >= u.z) v[i + 2] = 0xff800000u;
+                if (key >= u.w) v[i + 3] = 0xff800000u;
               }
             }
-#pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-#pragma unroll
-              for (int k = 0; k < 2; ++k) {
-                const uint32_t* w = (k ? sb : sa) + i;
-                const float4 e = *reinterpret_cast<const float4*>(cl.nlse + 64 * half + 32 * k + i);
-                const float2 a = __ffma2_rn(make_float2(__uint_as_float(w[0]), __uint_as_float(w[1])), sc2, make_float2(e.x, e.y));
-                const float2 c = __ffma2_rn(make_float2(__uint_as_float(w[2]), __uint_as_float(w[3])), sc2, make_float2(e.z, e.w));
-                sum0 = __fadd2_rn(sum0, make_float2(fast_exp2(a.x), fast_exp2(a.y)));
-                sum1 = __fadd2_rn(sum1, make_float2(fast_exp2(c.x), fast_exp2(c.y)));
-              }
-            }
+            l += sum_up([&](int i) { return *reinterpret_cast<const float2*>(cl.nlse + 64 * half + i); });
           }
-          l += (sum0.x + sum0.y) + (sum1.x + sum1.y);
         }
         if (PASS == 2) {
           __syncwarp();
@@ -564,7 +597,10 @@ __global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ Em
   const int t = (int)(i / p.hq), h = (int)(i - (size_t)t * p.hq);
   if (i >= rows || t < p.tok_off[0] || t >= p.tok_off[p.n_seq]) return;   // rows of no sequence have no parts
   float m = -INFINITY, l = 0.f;
-  for (int k = 0; k < 2 * p.cuts1; ++k) m = fmaxf(m, p.parts[k * rows + i].x);
+  for (int k = 0; k < 2 * p.cuts1; ++k) {
+    const float2 v = p.parts[k * rows + i];
+    if (v.y > 0.f) m = fmaxf(m, v.x);
+  }
   for (int k = 0; k < 2 * p.cuts1; ++k) {
     const float2 v = p.parts[k * rows + i];
     if (v.y > 0.f) l += v.y * fast_exp2(v.x - m);

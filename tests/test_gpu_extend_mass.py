@@ -82,6 +82,23 @@ def test_long_chunks(causal):
     check(s, call(s, causal), causal)
 
 
+def test_key_tiles_that_rows_pass_by():
+    """A causal chunk of many row tiles in one piece: the second 128 keys of a pair are seen eight row tiles later."""
+    s = chunk([3000], [3000], 64, 8, 64)
+    check(s, call(s, True), True)
+
+
+def test_scores_out_of_the_reference():
+    """The first keys of a row say nothing about the later ones: scores that jump by hundreds, up and down."""
+    s = chunk([900, 640], [200, 3], 4, 2, 64)
+    for b in range(s["k"][0].shape[0]):
+        s["k"][0][b] *= 30 if b % 3 == 0 else 0.1 if b % 3 == 1 else 1
+    s["values"][0] = np.nan_to_num(f64(s["k"][0]))
+    check(s, call(s, True), True)
+    s["q"] = s["q"] * -1
+    check(s, call(s, False), False)
+
+
 def test_many_sequences():
     r = np.random.default_rng(0)
     lens = r.integers(0, 60, 400)
