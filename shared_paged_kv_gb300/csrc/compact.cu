@@ -6,23 +6,26 @@
 // A cluster of CTAs takes a sequence; the threshold is found by a radix select
 // over the order-preserving bits of the masses, three digits of 11, 11 and 10
 // bits, each CTA with the histogram of its own slice, added up through
-// distributed shared memory.  Sixteen masses a thread stay in registers, so a
-// sequence is read once (up to 131,072 tokens on eight CTAs).
+// distributed shared memory.  A thread's masses stay in registers, so a sequence is
+// read once (up to 131,072 tokens on eight CTAs).
 //
 // kvs_compact: row i of a sequence's kept tokens moves from place idx[i] to
 // place i, in every layer's slabs.  Places only fall (idx[i] >= i), blocks in
 // front of the first change stay, and a block that others reference is replaced
-// by a free one.  Four launches:
+// by a free one.  Three launches:
 //  cp_check  a CTA per sequence: the list's order, the first change, which
 //            blocks have to be replaced;
 //  cp_apply  a CTA per sequence: tables, counts, lengths, masses;
-//  cp_move   the rows.  An item is 16 KB of one slab and head; its rows are all
-//            in registers before any is written.  A row may be written in place
-//            where another item still has to read: items publish that they have
-//            read, and an item that writes in place waits for the (at most few)
-//            items of lower places whose sources lie in its range.  Items are
-//            claimed in order, so the awaited ones are running or done;
-//  cp_push   one CTA: blocks that nobody references any more go back.
+//  cp_move   the rows.  An item is the next 16 KB of places of a sequence, looked
+//            up once, in some chains (a layer's K or V of one head) one after the
+//            other; a chain's rows are all in registers before any is written,
+//            and the next chain's are under way meanwhile.  A row may be written
+//            in place where another item still has to read: items publish
+//            that they have read, and an item that writes in place waits for
+//            the (at most few) items of lower places whose sources lie in its
+//            range.  Items are claimed in order, so the awaited ones are running
+//            or done.  The last CTA puts the blocks that nobody references any
+//            more onto the free stack.
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -37,9 +40,10 @@ namespace {
 
 // ------------------------------------------------------------ keep heavy ---
 constexpr int kKhThreads = 1024;
-constexpr int kKhKeys = 16;                     // masses a thread holds
-constexpr int kKhTile = kKhThreads * kKhKeys;
 constexpr int kKhBins = 2048;
+// Masses gather in few of the first digit's bins: four histograms, a lane in one
+// of them, eight banks apart.
+constexpr int kKhCopies = 4, kKhStride = kKhBins + 8;
 
 struct KeepParams {
   const float* mass;
@@ -73,16 +77,23 @@ __device__ __forceinline__ unsigned mass_key(float x) {
   return x != x ? 0u : (b >> 31 ? ~b : b | 0x80000000u);
 }
 
+// RANKS CTAs take a sequence, a thread holds KEYS masses at a time.
+template <int RANKS, int KEYS>
 __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_constant__ KeepParams p) {
-  __shared__ unsigned hist[kKhBins];
+  __shared__ unsigned hist4[kKhCopies * kKhStride], hist[kKhBins];
   __shared__ int wsum[32];
   __shared__ long long wlong[32];
   __shared__ unsigned s_prefix;
   __shared__ int s_left;
   __shared__ int2 s_count;                        // {above the threshold, equal to it} in this CTA's slice
-  __shared__ int s_pair[kKhKeys * 32];            // per (round, warp) of a tile: taken tokens before it
+  __shared__ int s_pair[KEYS * 32];            // per (round, warp) of a tile: taken tokens before it
   cg::cluster_group cluster = cg::this_cluster();
-  const int rank = (int)cluster.block_rank(), ranks = (int)cluster.num_blocks();
+  constexpr int ranks = RANKS, kKhKeys = KEYS, kKhTile = kKhThreads * KEYS;
+  const int rank = RANKS > 1 ? (int)cluster.block_rank() : 0;
+  auto sync_all = [&]() {
+    if constexpr (RANKS > 1) cluster.sync();
+    else __syncthreads();
+  };
   const int a = blockIdx.x / ranks, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   pdl_enter();
   const KeepRange r = keep_range(p, a);
@@ -129,22 +140,32 @@ __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_con
   int left = r.take;
   for (int digit = 0; digit < 3; ++digit) {
     const int shift = digit == 0 ? 21 : digit == 1 ? 10 : 0, bins = digit == 2 ? 1024 : 2048;
-    for (int i = tid; i < bins; i += kKhThreads) hist[i] = 0;
+    for (int i = tid; i < kKhCopies * kKhStride; i += kKhThreads) hist4[i] = 0;
     __syncthreads();
+    unsigned* mine4 = hist4 + (tid % kKhCopies) * kKhStride;
     for (int t0 = s0; t0 < s1; t0 += kKhTile) {
       if (t0 != s0 || (digit && s1 - s0 > kKhTile)) load(t0);
 #pragma unroll
       for (int i = 0; i < kKhKeys; ++i)
-        if (t0 + i * kKhThreads + tid < s1 && (key[i] & mask) == prefix) atomicAdd(&hist[(key[i] >> shift) & (bins - 1)], 1u);
+        if (t0 + i * kKhThreads + tid < s1 && (key[i] & mask) == prefix) atomicAdd(&mine4[(key[i] >> shift) & (bins - 1)], 1u);
     }
-    cluster.sync();
+    __syncthreads();
+    for (int i = tid; i < bins; i += kKhThreads) {
+      unsigned n = 0;
+#pragma unroll
+      for (int c = 0; c < kKhCopies; ++c) n += hist4[c * kKhStride + i];
+      hist[i] = n;
+    }
+    sync_all();
     // the bin that holds the left-th largest: thread t takes the t-th largest
     // two bins (digit 2: one) of all CTAs' histograms
     const int per = bins / kKhThreads;
     unsigned c[2] = {0u, 0u};
+#pragma unroll
     for (int q = 0; q < ranks; ++q) {
-      const unsigned* h = cluster.map_shared_rank(hist, q);
-      for (int j = 0; j < per; ++j) c[j] += h[bins - 1 - tid * per - j];
+      const unsigned* h = RANKS > 1 ? cluster.map_shared_rank(hist, q) : hist;
+      c[0] += h[bins - 1 - tid * per];
+      if (per > 1) c[1] += h[bins - 2 - tid * per];
     }
     int total;
     const int mine = (int)(c[0] + c[1]);
@@ -154,7 +175,7 @@ __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_con
       s_prefix = prefix | ((unsigned)(bins - 1 - tid * per - second) << shift);
       s_left = left - before - (second ? (int)c[0] : 0);
     }
-    cluster.sync();   // every CTA has read the histograms; s_prefix is there
+    sync_all();   // every CTA has read the histograms; s_prefix is there
     prefix = s_prefix;
     left = s_left;
     mask |= (unsigned)(bins - 1) << shift;
@@ -170,16 +191,22 @@ __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_con
       eq += in && key[i] == prefix;
     }
   }
-  int gt_all, eq_all;
-  block_exclusive_scan(gt, wsum, gt_all);
-  block_exclusive_scan(eq, wsum, eq_all);
-  if (tid == 0) s_count = make_int2(gt_all, eq_all);
-  cluster.sync();
   int base = 0, eq_seen = 0;   // of the slices before this one
-  for (int q = 0; q < rank; ++q) {
-    const int2 v = *cluster.map_shared_rank(&s_count, q);
-    base += v.x;
-    eq_seen += v.y;
+  if constexpr (RANKS > 1) {
+    gt = __reduce_add_sync(0xffffffffu, gt);
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    if (tid == 0) s_count = make_int2(0, 0);
+    __syncthreads();
+    if (lane == 0) {
+      if (gt) atomicAdd(&s_count.x, gt);
+      if (eq) atomicAdd(&s_count.y, eq);
+    }
+    cluster.sync();
+    for (int q = 0; q < rank; ++q) {
+      const int2 v = *cluster.map_shared_rank(&s_count, q);
+      base += v.x;
+      eq_seen += v.y;
+    }
   }
   base += min(eq_seen, left);
   for (int t0 = s0; t0 < s1; t0 += kKhTile) {
@@ -192,12 +219,11 @@ __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_con
       if (lane == 0) s_pair[i * 32 + warp] = __popc(g) | (__popc(e) << 16);
     }
     __syncthreads();
-    // a tile holds up to 16,384 of either: the two sums are scanned apart
-    const int v = tid < kKhKeys * 32 ? s_pair[tid] : 0;
-    int g_all, e_all;
-    const int g_before = block_exclusive_scan(v & 0xffff, wsum, g_all);
-    const int e_before = block_exclusive_scan(v >> 16, wsum, e_all);
-    if (tid < kKhKeys * 32) s_pair[tid] = g_before | (e_before << 16);
+    // a tile holds up to 16,384 of either, so both sums fit half a word
+    int all;
+    const int before = block_exclusive_scan(tid < kKhKeys * 32 ? s_pair[tid] : 0, wsum, all);
+    const int g_all = all & 0xffff, e_all = all >> 16;
+    if (tid < kKhKeys * 32) s_pair[tid] = before;
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kKhKeys; ++i) {
@@ -216,13 +242,14 @@ __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_con
     eq_seen += e_all;
     __syncthreads();
   }
-  cluster.sync();   // s_count of this CTA has been read
+  if constexpr (RANKS > 1) cluster.sync();   // s_count of this CTA has been read
 }
 
 // ---------------------------------------------------------------- compact ---
 constexpr int kCpThreads = 128;
 constexpr int kCpVecs = 8;                                  // 16-byte pieces a thread holds
-constexpr int kCpCtas = 4;                                  // per SM
+constexpr int kCpCtas = 5;                                  // per SM
+constexpr int kCpItemsPerSm = 16, kCpMaxGroup = 16;
 constexpr int kCpItem = kCpThreads * kCpVecs * 16;          // bytes of an item
 constexpr int kCpMaxRows = 256;
 constexpr int kCpSeqThreads = 1024;
@@ -231,7 +258,14 @@ struct __align__(16) CpSeq {
   int len, kept, start, need;   // start: first place that is written; need: blocks to take (-1: the sequence is left alone)
 };
 
-enum { kCpTicket, kCpSegs, kCpTaken, kCpHdr = 16 };
+// A segment: the next `rows` places of a sequence, as the moving kernel reads it.
+struct __align__(16) CpSeg {
+  int seq, i0, n, start;   // places i0 .. i0 + n; start: the sequence's first (-1 - start: all its written blocks are new)
+  long long idx0;          // where its list begins
+  int first, pad;          // the sequence's first segment
+};
+
+enum { kCpTicket, kCpSegs, kCpTaken, kCpDone, kCpGroup, kCpHdr = 16 };
 
 struct CompactParams {
   int32_t *table, *seq_len;
@@ -242,18 +276,20 @@ struct CompactParams {
   uint32_t* status;
   int* hdr;
   CpSeq* seq;
-  int* segoff;             // [n_seq + 1] items' first segment of each sequence
+  CpSeg* segs;
+  float* mass_was;         // [n_seq][max_blocks * B] masses before the call
   int32_t *old_tab, *new_tab;   // [n_seq][max_blocks]
   unsigned* freed;         // bitmap [capacity]
   uint8_t* flags;          // [segment][chain] 1: read
   void** slabs;
-  long long max_flags;
-  int n_seq, max_blocks, B, hkv, capacity, n_slabs, per_layer, row_bytes, sb_bytes, rows;   // rows: tokens of an item
+  long long max_segs;
+  int n_seq, max_blocks, B, hkv, capacity, chains, per_layer, row_bytes, sb_bytes, rows;   // chain: a layer's K or V of one head
+  int sms;
 };
 
 struct CpLayout {
-  size_t hdr, seq, segoff, old_tab, new_tab, freed, flags, total;
-  long long max_flags;
+  size_t hdr, seq, segs, mass, old_tab, new_tab, freed, flags, total;
+  long long max_segs;
 };
 
 int cp_rows(const kvs_pool_desc& d) {
@@ -272,7 +308,7 @@ CpLayout cp_layout(const kvs_pool* pool, int n_seq, int max_blocks) {
   };
   l.hdr = take(kCpHdr * 4);
   l.seq = take((size_t)n_seq * sizeof(CpSeq));
-  l.segoff = take((size_t)(n_seq + 1) * 4);
+  l.mass = take((size_t)n_seq * max_blocks * d.block_tokens * 4);
   l.old_tab = take((size_t)n_seq * max_blocks * 4);
   l.new_tab = take((size_t)n_seq * max_blocks * 4);
   l.freed = take(((size_t)d.capacity_blocks + 31) / 32 * 4 + 16);
@@ -280,19 +316,35 @@ CpLayout cp_layout(const kvs_pool* pool, int n_seq, int max_blocks) {
   const long long rows = cp_rows(d);
   const long long by_pool = (long long)d.capacity_blocks * d.block_tokens / rows + n_seq;
   const long long by_table = (long long)n_seq * (((long long)max_blocks * d.block_tokens + rows - 1) / rows);
-  l.max_flags = std::min(by_pool, by_table) * pool->n_blk_slabs * d.num_kv_heads;
-  l.flags = take((size_t)l.max_flags);
+  l.max_segs = std::min(by_pool, by_table);
+  l.segs = take((size_t)l.max_segs * sizeof(CpSeg));
+  l.flags = take((size_t)l.max_segs * 2 * d.num_layers * d.num_kv_heads);
   l.total = o;
   return l;
 }
 
-// A CTA per sequence.
+// gridDim.y CTAs take the masses of a sequence, each its share of [0, n).
+__device__ __forceinline__ int2 cp_share(int n) {
+  const int per = ((n + (int)gridDim.y - 1) / (int)gridDim.y + 3) & ~3;
+  return make_int2(min(n, (int)blockIdx.y * per), min(n, ((int)blockIdx.y + 1) * per));
+}
+
+// A CTA per sequence, and some more to copy long rows of masses.
 __global__ void __launch_bounds__(kCpSeqThreads) cp_check(const __grid_constant__ CompactParams p) {
   __shared__ int s_same, s_bad;
   const int a = blockIdx.x, tid = threadIdx.x;
   pdl_enter();
-  for (long long w = (long long)a * kCpSeqThreads + tid; w < (p.capacity + 31) / 32; w += (long long)p.n_seq * kCpSeqThreads)
+  for (long long w = (long long)(blockIdx.y * p.n_seq + a) * kCpSeqThreads + tid; w < (p.capacity + 31) / 32;
+       w += (long long)p.n_seq * gridDim.y * kCpSeqThreads)
     p.freed[w] = 0;
+  if (p.mass) {
+    const int2 mine = cp_share(min(max(p.seq_len[a], 0), p.max_blocks * p.B));
+    const float* from = p.mass + (size_t)a * p.max_blocks * p.B;
+    float* to = p.mass_was + (size_t)a * p.max_blocks * p.B;
+#pragma unroll 8
+    for (int i = mine.x + tid; i < mine.y; i += kCpSeqThreads) to[i] = from[i];
+  }
+  if (blockIdx.y > 0) return;
   const long long o0 = p.idx_off[a], o1 = p.idx_off[a + 1];
   const int len = p.seq_len[a];
   const bool ok = len >= 0 && len <= p.max_blocks * p.B && o0 >= 0 && o1 >= o0 && o1 - o0 <= len;
@@ -374,7 +426,8 @@ __device__ __forceinline__ int cp_segments(const CompactParams& p, const CpSeq& 
   return s.need < 0 ? 0 : (s.kept - s.start + p.rows - 1) / p.rows;
 }
 
-// A CTA per sequence: every CTA adds up what the sequences before it take.
+// A CTA per sequence (and some more for long rows of masses): every CTA adds up
+// what the sequences before it take.
 __global__ void __launch_bounds__(kCpSeqThreads) cp_apply(const __grid_constant__ CompactParams p) {
   __shared__ int warp_sums[32];
   __shared__ int s_base, s_seg, s_drop, s_taken;
@@ -382,7 +435,6 @@ __global__ void __launch_bounds__(kCpSeqThreads) cp_apply(const __grid_constant_
   pdl_enter();
   const CpSeq s = p.seq[a];
   const int avail = min(max(*p.n_free, 0), p.capacity);
-  const int chains = p.n_slabs * p.hkv;
   {
     long long need = 0;
     int before = 0, segs = 0, bad = 0;
@@ -425,22 +477,42 @@ __global__ void __launch_bounds__(kCpSeqThreads) cp_apply(const __grid_constant_
   __syncthreads();
   const int base = s_base, seg0 = s_seg;
   const int segs = s_drop ? 0 : cp_segments(p, s);
-  const bool fits = (long long)(seg0 + segs) * chains <= p.max_flags;   // counts that belong to no real pool
-  if (tid == 0) {
+  const bool fits = seg0 + segs <= p.max_segs;   // otherwise the counts belong to no real pool
+  if (tid == 0 && blockIdx.y == 0) {
     if (!fits) set_err(p.status, KVS_DEVERR_REFCOUNT);
-    p.segoff[a] = seg0;
     if (a == p.n_seq - 1) {
-      p.segoff[p.n_seq] = seg0 + segs;
-      p.hdr[kCpSegs] = (int)min((long long)(seg0 + segs), p.max_flags / chains);
+      const int total = (int)min((long long)(seg0 + segs), p.max_segs);
+      p.hdr[kCpSegs] = total;
       p.hdr[kCpTaken] = s_taken;
-      p.hdr[kCpTicket] = 0;
+      p.hdr[kCpTicket] = p.hdr[kCpDone] = 0;
+      // chains that an item takes one after the other: its places are looked up
+      // once; as many as leave sixteen items to an SM
+      const long long items = (long long)total * p.chains;
+      p.hdr[kCpGroup] = (int)min(max(items / (kCpItemsPerSm * (long long)p.sms), 1ll), (long long)kCpMaxGroup);
     }
   }
   if (s_drop) return;
-  if (fits)
-    for (long long i = (long long)seg0 * chains + tid; i < (long long)(seg0 + segs) * chains; i += kCpSeqThreads) p.flags[i] = 0;
-  const int nb_old = (s.len + p.B - 1) / p.B;
   const size_t row = (size_t)a * p.max_blocks;
+  if (p.mass) {   // list and lengths are those that cp_check read
+    const int32_t* idx = p.idx + p.idx_off[a];
+    const float* from = p.mass_was + row * p.B;
+    float* to = p.mass + row * p.B;
+    const int2 mine = cp_share(s.len);
+#pragma unroll 8
+    for (int i = mine.x + tid; i < mine.y; i += kCpSeqThreads) to[i] = i < s.kept ? from[idx[i]] : 0.f;
+  }
+  if (blockIdx.y > 0) return;
+  if (fits) {
+    const long long idx0 = p.idx_off[a];
+    const int all_new = s.need == (s.kept + p.B - 1) / p.B - s.start / p.B;
+    for (int i = tid; i < segs; i += kCpSeqThreads) {
+      const int i0 = s.start + i * p.rows;
+      p.segs[seg0 + i] = CpSeg{a, i0, min(p.rows, s.kept - i0), all_new ? -1 - s.start : s.start, idx0, seg0, 0};
+    }
+    if (!all_new)
+      for (long long i = (long long)seg0 * p.chains + tid; i < (long long)(seg0 + segs) * p.chains; i += kCpSeqThreads) p.flags[i] = 0;
+  }
+  const int nb_old = (s.len + p.B - 1) / p.B;
   int carry = base;
   for (int b0 = 0; b0 < nb_old; b0 += kCpSeqThreads) {
     const int b = b0 + tid;
@@ -469,28 +541,6 @@ __global__ void __launch_bounds__(kCpSeqThreads) cp_apply(const __grid_constant_
     }
   }
   if (tid == 0) p.seq_len[a] = s.kept;
-  if (!p.mass) return;
-  // masses: whole tiles are read before they are written (sources lie at or behind their places)
-  float* m = p.mass + row * p.B;
-  const int32_t* idx = p.idx + p.idx_off[a];
-  constexpr int U = 8;
-  for (int i0 = 0; i0 < s.kept; i0 += U * kCpSeqThreads) {
-    int src[U];
-    float v[U];
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * kCpSeqThreads + tid;
-      src[u] = i < s.kept ? idx[i] : -1;
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) v[u] = src[u] >= 0 ? m[src[u]] : 0.f;
-    __syncthreads();
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-      if (src[u] >= 0) m[i0 + u * kCpSeqThreads + tid] = v[u];
-  }
-  __syncthreads();
-  for (int i = s.kept + tid; i < s.len; i += kCpSeqThreads) m[i] = 0.f;
 }
 
 __device__ __forceinline__ int lower_bound(const int32_t* x, int n, int v) {   // first i with x[i] >= v
@@ -507,142 +557,41 @@ __device__ __forceinline__ int lower_bound(const int32_t* x, int n, int v) {   /
   return lo;
 }
 
-template <int VECS>   // VECS: 16-byte pieces of a row, 0: 4-byte words
-__device__ __forceinline__ void cp_rows_move(const CompactParams& p, uint8_t* slab, int row_bytes, int n, const int* src, const int* dst,
-                                             bool in_place, volatile uint8_t* flag, int wait0, int wait1, long long wait_at,
-                                             int chains) {
+// 16-byte pieces of an item's rows: thread v of the k-th hundred and twenty-eight
+// has piece v % VECS of row v / VECS.
+template <int VECS>
+struct CpRows {
   uint4 x[kCpVecs];
-  if constexpr (VECS > 0) {
+  __device__ __forceinline__ void load(const uint8_t* slab, int n, const int* src, int at) {
 #pragma unroll
     for (int k = 0; k < kCpVecs; ++k) {
       const int v = k * kCpThreads + threadIdx.x, r = v / VECS;
-      if (r < n && src[r] >= 0) x[k] = __ldcs(reinterpret_cast<const uint4*>(slab + (size_t)src[r] * row_bytes) + v % VECS);
-    }
-  } else {
-    uint32_t* w = reinterpret_cast<uint32_t*>(x);
-    const int words = row_bytes / 4;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int v = k * kCpThreads + threadIdx.x, r = v / words;
-      if (r < n && src[r] >= 0) w[k] = *(reinterpret_cast<const uint32_t*>(slab + (size_t)src[r] * row_bytes) + v % words);
+      if (r < n) x[k] = __ldcs(reinterpret_cast<const uint4*>(slab + (size_t)(src[r] + at) * (VECS * 16)) + v % VECS);
     }
   }
-  // every row of the item is read: said once the loads of all threads are done
-  if (in_place) {
-    __threadfence();
-    __syncthreads();
-    if (threadIdx.x == 0) *flag = 1;
-  }
-  if (wait1 > wait0) {
-    for (int s = wait0 + (int)threadIdx.x; s < wait1; s += kCpThreads) {
-      volatile uint8_t* f = p.flags + wait_at + (long long)s * chains;
-      const long long t0 = clock64();
-      while (!*f) {
-        if (clock64() - t0 > (1ll << 31)) {
-          set_err(p.status, KVS_DEVERR_WAIT_TIMEOUT);
-          break;
-        }
-      }
-    }
-    __threadfence();
-    __syncthreads();
-  }
-  if constexpr (VECS > 0) {
+  __device__ __forceinline__ void store(uint8_t* slab, int n, const int* dst, int at) const {
 #pragma unroll
     for (int k = 0; k < kCpVecs; ++k) {
       const int v = k * kCpThreads + threadIdx.x, r = v / VECS;
-      if (r < n && dst[r] >= 0) *(reinterpret_cast<uint4*>(slab + (size_t)dst[r] * row_bytes) + v % VECS) = x[k];
-    }
-  } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(x);
-    const int words = row_bytes / 4;
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int v = k * kCpThreads + threadIdx.x, r = v / words;
-      if (r < n && dst[r] >= 0) *(reinterpret_cast<uint32_t*>(slab + (size_t)dst[r] * row_bytes) + v % words) = w[k];
+      if (r < n && dst[r] >= 0) *(reinterpret_cast<uint4*>(slab + (size_t)(dst[r] + at) * (VECS * 16)) + v % VECS) = x[k];
     }
   }
-}
+};
 
-__global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_constant__ CompactParams p) {
-  __shared__ int s_item, s_wait[2];
-  __shared__ int s_src[kCpMaxRows], s_dst[kCpMaxRows];
-  pdl_enter();
-  const int chains = p.n_slabs * p.hkv, tid = threadIdx.x;
-  const long long items = (long long)p.hdr[kCpSegs] * chains;
-  while (true) {
-    if (tid == 0) {
-      s_item = atomicAdd(p.hdr + kCpTicket, 1);
-      s_wait[0] = s_wait[1] = 0;
-    }
-    __syncthreads();
-    const long long item = (unsigned)s_item;
-    if (item >= items) return;
-    const int sg = (int)(item / chains), chain = (int)(item - (long long)sg * chains);
-    // the sequence: the last one whose first segment is at most sg
-    int lo = 0, n = p.n_seq;
-    while (n > 1) {
-      const int h = n >> 1;
-      if (p.segoff[lo + h] <= sg) {
-        lo += h;
-        n -= h;
-      } else {
-        n = h;
-      }
-    }
-    const int a = lo, seg = sg - p.segoff[a];
-    const CpSeq s = p.seq[a];
-    const int32_t* idx = p.idx + p.idx_off[a];
-    const size_t row = (size_t)a * p.max_blocks;
-    const int i0 = s.start + seg * p.rows, m = min(p.rows, s.kept - i0);
-    const int slab = chain / p.hkv, head = chain - slab * p.hkv;
-    // nothing of a sequence is written in place where all its written blocks are new
-    const bool in_place = s.need < (s.kept + p.B - 1) / p.B - s.start / p.B;
-    for (int r = tid; r < m; r += kCpThreads) {
-      const int from = __ldg(idx + i0 + r), to = i0 + r;
-      const int sb = p.old_tab[row + from / p.B], db = p.new_tab[row + to / p.B];
-      s_src[r] = (sb * p.hkv + head) * p.B + from % p.B;
-      s_dst[r] = db >= 0 ? (db * p.hkv + head) * p.B + to % p.B : -1;
-    }
-    // rows of lower places whose sources this item overwrites
-    __syncthreads();
-    if (in_place && seg > 0) {
-      if (tid < 2) s_wait[tid] = lower_bound(idx + s.start, i0 - s.start, tid ? i0 + m : i0);
-      __syncthreads();
-    }
-    const int w0 = s_wait[0], w1 = s_wait[1];
-    const int wait0 = w0 / p.rows, wait1 = w1 > w0 ? (w1 - 1) / p.rows + 1 : wait0;
-    const long long wait_at = (long long)p.segoff[a] * chains + chain;
-    uint8_t* base = static_cast<uint8_t*>(p.slabs[slab]);
-    volatile uint8_t* flag = p.flags + item;
-    if (slab % p.per_layer >= 2)
-      cp_rows_move<0>(p, base, p.sb_bytes, m, s_src, s_dst, in_place, flag, wait0, wait1, wait_at, chains);
-    else if (p.row_bytes == 256)
-      cp_rows_move<16>(p, base, p.row_bytes, m, s_src, s_dst, in_place, flag, wait0, wait1, wait_at, chains);
-    else if (p.row_bytes == 128)
-      cp_rows_move<8>(p, base, p.row_bytes, m, s_src, s_dst, in_place, flag, wait0, wait1, wait_at, chains);
-    else
-      cp_rows_move<4>(p, base, p.row_bytes, m, s_src, s_dst, in_place, flag, wait0, wait1, wait_at, chains);
-    __syncthreads();
-  }
-}
-
-// One CTA: the blocks whose count reached zero go onto the stack, the smallest
-// id on top.
-__global__ void __launch_bounds__(kCpSeqThreads) cp_push(const __grid_constant__ CompactParams p) {
-  __shared__ int warp_sums[32];
-  pdl_enter();
+// The free stack of the call's end (by one CTA): the blocks whose count reached
+// zero go onto it, the smallest id on top.
+__device__ __forceinline__ void cp_push(const CompactParams& p, int* warp_sums) {
   const int words = (p.capacity + 31) / 32, tid = threadIdx.x;
-  const int per = (words + kCpSeqThreads - 1) / kCpSeqThreads;
+  const int per = (words + kCpThreads - 1) / kCpThreads;
   const int left = min(max(*p.n_free, 0), p.capacity) - p.hdr[kCpTaken];
   const int w1 = words - tid * per, w0 = max(0, w1 - per);   // this thread's words, from the highest down
   int n = 0, total;
-#pragma unroll 4
-  for (int w = w1 - 1; w >= w0; --w) n += __popc(p.freed[w]);
+#pragma unroll 8
+  for (int w = w1 - 1; w >= w0; --w) n += __popc(__ldcg(p.freed + w));
   int at = left + block_exclusive_scan(n, warp_sums, total);
   if (n)
     for (int w = w1 - 1; w >= w0; --w)
-      for (unsigned bits = p.freed[w]; bits; ) {
+      for (unsigned bits = __ldcg(p.freed + w); bits; ) {
         const int b = 31 - __clz(bits);
         bits &= ~(1u << b);
         if (at < p.capacity) p.free_ids[at] = w * 32 + b;
@@ -651,6 +600,109 @@ __global__ void __launch_bounds__(kCpSeqThreads) cp_push(const __grid_constant__
       }
   __syncthreads();
   if (tid == 0) *p.n_free = min(left + total, p.capacity);
+}
+
+template <int VECS>
+__global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_constant__ CompactParams p) {
+  __shared__ int s_item, s_wait[2], s_last;
+  __shared__ int warp_sums[32];
+  __shared__ int s_src[kCpMaxRows], s_dst[kCpMaxRows];
+  const int tid = threadIdx.x;
+  pdl_enter();
+  const int group = p.hdr[kCpGroup], n_groups = (p.chains + group - 1) / group;
+  const long long items = (long long)p.hdr[kCpSegs] * n_groups;
+  long long item = 0;
+  int ticket = 0;
+  if (tid == 0) ticket = atomicAdd(p.hdr + kCpTicket, 1);
+  while (true) {
+    if (tid == 0) s_item = ticket;
+    __syncthreads();
+    item = (unsigned)s_item;
+    if (item >= items) break;
+    if (tid == 0) ticket = atomicAdd(p.hdr + kCpTicket, 1);   // the next one, known when this one is done
+    const int sg = (int)(item / n_groups), c0 = (int)(item - (long long)sg * n_groups) * group;
+    const CpSeg s = p.segs[sg];
+    const int32_t* idx = p.idx + s.idx0;
+    const size_t row = (size_t)s.seq * p.max_blocks;
+    const bool in_place = s.start >= 0;
+    for (int r = tid; r < s.n; r += kCpThreads) {
+      const int from = __ldg(idx + s.i0 + r), to = s.i0 + r;
+      const int sb = p.old_tab[row + from / p.B], db = p.new_tab[row + to / p.B];
+      s_src[r] = sb * p.hkv * p.B + from % p.B;
+      s_dst[r] = db >= 0 ? db * p.hkv * p.B + to % p.B : -p.hkv * p.B;
+    }
+    // rows of lower places whose sources this item overwrites
+    int wait0 = 0, wait1 = 0;
+    if (in_place && s.i0 > s.start) {
+      if (tid < 2) s_wait[tid] = lower_bound(idx + s.start, s.i0 - s.start, tid ? s.i0 + s.n : s.i0);
+      __syncthreads();
+      wait0 = s_wait[0] / p.rows;
+      wait1 = s_wait[1] > s_wait[0] ? (s_wait[1] - 1) / p.rows + 1 : wait0;
+    }
+    __syncthreads();
+    const int c1 = min(p.chains, c0 + group);
+    auto slab_of = [&](int c, int more) {
+      const int kv = c / p.hkv;
+      return static_cast<uint8_t*>(p.slabs[(kv >> 1) * p.per_layer + (kv & 1) + more]);
+    };
+    // chain c, whose rows are under way into x; those of the next one go into y
+    auto step = [&](CpRows<VECS>& x, CpRows<VECS>& y, int c) {
+      const int at = c % p.hkv * p.B;
+      // a 4-bit row's scales go along, as words
+      uint32_t w[4];
+      const int words = p.sb_bytes / 4;   // 0, 1 or 2
+      if (VECS == 4) {
+        const uint8_t* slab = slab_of(c, 2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int v = k * kCpThreads + tid, r = v / words;
+          if (r < s.n) w[k] = *(reinterpret_cast<const uint32_t*>(slab + (size_t)(s_src[r] + at) * p.sb_bytes) + v % words);
+        }
+      }
+      if (in_place) {
+        // every row of this chain is read: said once the loads of all threads are done
+        __threadfence();
+        __syncthreads();
+        if (tid == 0) *const_cast<volatile uint8_t*>(p.flags + (size_t)sg * p.chains + c) = 1;
+        for (int q = wait0 + tid; q < wait1; q += kCpThreads) {
+          const volatile uint8_t* f = p.flags + (size_t)(s.first + q) * p.chains + c;
+          const long long t0 = clock64();
+          while (!*f) {
+            if (clock64() - t0 > (1ll << 31)) {
+              set_err(p.status, KVS_DEVERR_WAIT_TIMEOUT);
+              break;
+            }
+          }
+        }
+        __threadfence();
+        __syncthreads();
+      }
+      // the next chain's rows are on their way while this one's are written
+      if (c + 1 < c1) y.load(slab_of(c + 1, 0), s.n, s_src, (c + 1) % p.hkv * p.B);
+      x.store(slab_of(c, 0), s.n, s_dst, at);
+      if (VECS == 4) {
+        uint8_t* slab = slab_of(c, 2);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const int v = k * kCpThreads + tid, r = v / words;
+          if (r < s.n && s_dst[r] >= 0) *(reinterpret_cast<uint32_t*>(slab + (size_t)(s_dst[r] + at) * p.sb_bytes) + v % words) = w[k];
+        }
+      }
+    };
+    CpRows<VECS> x, y;
+    x.load(slab_of(c0, 0), s.n, s_src, c0 % p.hkv * p.B);
+    for (int c = c0; c < c1; c += 2) {
+      step(x, y, c);
+      if (c + 1 < c1) step(y, x, c + 1);
+    }
+    __syncthreads();
+  }
+  // the last CTA to find nothing left brings the free stack up to date: blocks
+  // that are given up are read by now
+  __threadfence();
+  if (tid == 0) s_last = atomicAdd(p.hdr + kCpDone, 1) == (int)gridDim.x - 1;
+  __syncthreads();
+  if (s_last) cp_push(p, warp_sums);
 }
 
 }  // namespace
@@ -680,6 +732,10 @@ extern "C" kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, cons
   // a CTA for every 4,096 tokens of the table row, eight at most
   int ranks = 1;
   while (ranks < 8 && most > 4096ll * ranks) ranks *= 2;
+  auto kern = ranks == 1   ? keep_heavy_kernel<1, 4>
+              : ranks == 2 ? keep_heavy_kernel<2, 4>
+              : ranks == 4 ? keep_heavy_kernel<4, 4>
+                           : keep_heavy_kernel<8, 16>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_seq * ranks);
   cfg.blockDim = dim3(kKhThreads);
@@ -692,7 +748,7 @@ extern "C" kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, cons
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 2;
-  if (cudaLaunchKernelEx(&cfg, keep_heavy_kernel, p) != cudaSuccess) return check_launch("keep_heavy");
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) return check_launch("keep_heavy");
   count_launch();
   return check_launch("keep_heavy");
 }
@@ -727,30 +783,33 @@ extern "C" kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int3
   p.status = pool->status;
   p.hdr = reinterpret_cast<int*>(w + l.hdr);
   p.seq = reinterpret_cast<CpSeq*>(w + l.seq);
-  p.segoff = reinterpret_cast<int*>(w + l.segoff);
+  p.segs = reinterpret_cast<CpSeg*>(w + l.segs);
+  p.mass_was = reinterpret_cast<float*>(w + l.mass);
   p.old_tab = reinterpret_cast<int32_t*>(w + l.old_tab);
   p.new_tab = reinterpret_cast<int32_t*>(w + l.new_tab);
   p.freed = reinterpret_cast<unsigned*>(w + l.freed);
   p.flags = w + l.flags;
   p.slabs = pool->blk_slabs;
-  p.max_flags = l.max_flags;
+  p.max_segs = l.max_segs;
   p.n_seq = n_seq;
   p.max_blocks = max_blocks;
   p.B = d.block_tokens;
   p.hkv = d.num_kv_heads;
   p.capacity = d.capacity_blocks;
-  p.n_slabs = pool->n_blk_slabs;
-  p.per_layer = p.n_slabs / d.num_layers;
+  p.chains = 2 * d.num_layers * d.num_kv_heads;
+  p.per_layer = pool->n_blk_slabs / d.num_layers;
   p.row_bytes = d.dtype == KVS_DTYPE_BF16 ? d.head_dim * 2 : d.head_dim / 2;
-  p.sb_bytes = d.dtype == KVS_DTYPE_Q4G64 ? d.head_dim / 16 : d.head_dim / 32;
+  p.sb_bytes = d.dtype == KVS_DTYPE_BF16 ? 0 : d.dtype == KVS_DTYPE_Q4G64 ? d.head_dim / 16 : d.head_dim / 32;
   p.rows = cp_rows(d);
-  const long long chains = (long long)p.n_slabs * p.hkv;
-  if (chains > 0x7fffffffll / 2) return fail(KVS_ERR_UNSUPPORTED, "compact: too many layers and heads");
-  const unsigned grid = (unsigned)std::max(1ll, std::min(p.max_flags, (long long)pool->num_sms * 8));
-  const bool ok = launch_pdl(cp_check, dim3(n_seq), dim3(kCpSeqThreads), stream, p) == cudaSuccess &&
-                  launch_pdl(cp_apply, dim3(n_seq), dim3(kCpSeqThreads), stream, p) == cudaSuccess &&
-                  launch_pdl(cp_move, dim3(grid), dim3(kCpThreads), stream, p) == cudaSuccess &&
-                  launch_pdl(cp_push, dim3(1), dim3(kCpSeqThreads), stream, p) == cudaSuccess;
-  if (ok) count_launch(4);
+  p.sms = pool->num_sms;
+  // more CTAs for the masses of a sequence whose table holds more than 8,192
+  const long long most = (long long)max_blocks * d.block_tokens;
+  const dim3 per_seq((unsigned)n_seq, (unsigned)(mass_dev ? std::clamp<long long>(most / 8192, 1, 16) : 1));
+  const unsigned grid = (unsigned)std::max(1ll, std::min(p.max_segs * p.chains, (long long)pool->num_sms * kCpCtas));
+  auto move = p.row_bytes == 256 ? cp_move<16> : p.row_bytes == 128 ? cp_move<8> : cp_move<4>;
+  const bool ok = launch_pdl(cp_check, per_seq, dim3(kCpSeqThreads), stream, p) == cudaSuccess &&
+                  launch_pdl(cp_apply, per_seq, dim3(kCpSeqThreads), stream, p) == cudaSuccess &&
+                  launch_pdl(move, dim3(grid), dim3(kCpThreads), stream, p) == cudaSuccess;
+  if (ok) count_launch(3);
   return check_launch("compact");
 }
