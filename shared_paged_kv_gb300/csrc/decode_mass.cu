@@ -298,6 +298,7 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     }
     uint32_t top_e = 0, top01 = 0, top23 = 0;   // microscaled: the largest scale byte met of each group of channels; two to a word
     const int row0 = F::mx ? mx_token(g) : g;   // token of this lane's first row
+    const bool even = (p.g & 1) == 0;
     float* sc_out = p.scores ? p.scores + (((size_t)seg.a * p.hkv + seg.h) * p.most + row0) * p.g + 2 * c : nullptr;
 
     for (; k < done + n_seg; k += W) {
@@ -399,26 +400,26 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
                 if (mt * 16 + row0 + 8 * (e >> 1) >= nv) s[mt][nt][e] = -INFINITY;
         }
         if (sc_out) {
+          // rows 8 apart are 8 g apart; lanes whose columns are no heads store nothing
           float* o = sc_out + (size_t)t_unit * p.g;
+          const int left = nv - row0;
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt)
+          for (int nt = 0; nt < NT; ++nt) {
+            const int cols = p.g - nt * 8 - 2 * c;   // heads from this lane's first column on
+            if (cols <= 0) continue;
+            float* q = o + nt * 8;
 #pragma unroll
-            for (int hr = 0; hr < 2; ++hr) {
-              const int t = mt * 16 + 8 * hr;
-              if (t + row0 >= nv) continue;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt) {
-                const int col = nt * 8 + 2 * c;
-                const float y0 = s[mt][nt][2 * hr] * cs[nt][0], y1 = s[mt][nt][2 * hr + 1] * cs[nt][1];
-                float* q = o + t * p.g + nt * 8;
-                if ((p.g & 1) == 0) {
-                  if (col < p.g) *reinterpret_cast<float2*>(q) = make_float2(y0, y1);
-                } else {
-                  if (col < p.g) q[0] = y0;
-                  if (col + 1 < p.g) q[1] = y1;
-                }
+            for (int hr = 0; hr < 2 * MT; ++hr, q += 8 * p.g) {
+              if (8 * hr >= left) break;
+              const float y0 = s[hr / 2][nt][2 * (hr & 1)] * cs[nt][0], y1 = s[hr / 2][nt][2 * (hr & 1) + 1] * cs[nt][1];
+              if (even) {
+                *reinterpret_cast<float2*>(q) = make_float2(y0, y1);
+              } else {
+                q[0] = y0;
+                if (cols > 1) q[1] = y1;
               }
             }
+          }
         }
         bool above = false;
         float top[NT][2];
@@ -553,6 +554,9 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     }
 
     // ---- the warps' states become one
+    // microscaled: times 2^(E - 127 - 13), as two factors that float32 holds
+    const int e_up = (int)((top_e >> (8 * (g >> 1))) & 255u) - 140;
+    const float up1 = __uint_as_float((uint32_t)(127 + e_up / 2) << 23), up2 = __uint_as_float((uint32_t)(127 + e_up - e_up / 2) << 23);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -562,12 +566,11 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
         const int row = nt * 8 + 2 * c + i;
         if (row >= p.g) continue;
         if (g == 0) sh.ml[warp][row] = make_float2(ref[nt][i] - F::kBias, l[nt][i]);
-        const int e = (int)((top_e >> (8 * (g >> 1))) & 255u) - 140;   // 2^(E - 127 - 13)
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           float* o = s_acc + ((size_t)warp * p.g + row) * D;
           if constexpr (F::mx) {
-            *reinterpret_cast<float2*>(o + 16 * g + 2 * j) = make_float2(ldexpf(acc[nt][j][i], e), ldexpf(acc[nt][j][2 + i], e));
+            *reinterpret_cast<float2*>(o + 16 * g + 2 * j) = make_float2(acc[nt][j][i] * up1 * up2, acc[nt][j][2 + i] * up1 * up2);
           } else {
             o[16 * j + g] = acc[nt][j][i];
             o[16 * j + g + 8] = acc[nt][j][2 + i];
