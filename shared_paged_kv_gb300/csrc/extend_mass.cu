@@ -35,9 +35,10 @@ namespace {
 // Four warpgroups of sums, two for each X tile: one takes columns 0 to 63 of a
 // product, one the others, so that a scheduler has four warps to choose from.
 // Behind them a warp for each X tile that issues its products, one for the copies,
-// one for pass 2's columns.
+// and one that has the columns of pass 2 and in pass 1 half of the copies: a key
+// tile is sixteen, which a warp issues in about 1,300 cycles.
 constexpr int kEmSumWarps = 16, kEmThreads = (kEmSumWarps + 4) * 32;
-constexpr int kEmMma = kEmSumWarps, kEmTma = kEmSumWarps + 2, kEmCol = kEmSumWarps + 3;
+constexpr int kEmMma = kEmSumWarps, kEmTma = kEmSumWarps + 2;   // and one more
 constexpr int kEmTile = 128;
 constexpr int kEmMaxCuts = 16;
 constexpr uint32_t kEmCols = 512, kEmX = 384;   // scores in three buffers of 128 columns, behind them the X tiles
@@ -49,7 +50,7 @@ __host__ __device__ constexpr int em_stages() { return D == 128 ? 4 : 8; }
 template <int D>
 __host__ __device__ constexpr int em_smem() { return 1024 + em_tile_bytes<D>() * (2 + em_stages<D>()); }
 
-enum { kMClaim1, kMClaim2, kMBad, kMTotal = 16 };
+enum { kMClaim1, kMClaim2, kMBad, kMCuts1, kMCuts2, kMTotal = 16 };
 
 struct EmParams {
   const int32_t *table, *tok_off, *seq_len;
@@ -60,15 +61,44 @@ struct EmParams {
   float2* parts;      // pass 1: [cut][column half][n_tokens][hq] {reference, sum}
   float* nlse;        // [hkv][n_tokens][g] -log2 of the rows' sums
   float* sums;        // pass 2: [cut][column half][hkv][n_seq][most]
-  int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2;
+  int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2, sms;   // cuts: the most there is room for
   float scale_log2;
 };
 
+// Cuts of every unit's Y tiles (1 to `most`, a lane each).  Items of about one
+// length go in rounds over the SMs, others fill them evenly but for the last one's
+// half; an item costs its tiles and about two more.
+__device__ __forceinline__ int em_cuts(float units, float tiles, float longest, int most, float sms, int lane) {
+  const float c = (float)(lane + 1), mean = tiles / fmaxf(units, 1.f), rounds = ceilf(units * c / sms);
+  const bool even = mean > 0.9f * longest;
+  float cost = (even ? rounds * mean / c : fmaxf(longest / c, tiles / sms + 0.5f * longest / c)) + 2.f * rounds;
+  if (lane >= most || (lane > 0 && longest < c)) cost = INFINITY;
+  int best = lane;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) {
+    const float cost2 = __shfl_xor_sync(0xffffffffu, cost, o);
+    const int best2 = __shfl_xor_sync(0xffffffffu, best, o);
+    if (cost2 < cost || (cost2 == cost && best2 < best)) {
+      cost = cost2;
+      best = best2;
+    }
+  }
+  return best + 1;
+}
+
 __global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ EmParams p) {
   __shared__ int warp_sums[32];
-  const int tid = threadIdx.x, tu = 2 * (kEmTile / p.g);
+  __shared__ unsigned long long s_tiles[2];   // twice the Y tiles of all units
+  __shared__ int s_longest[2];
+  const int tid = threadIdx.x, tt = kEmTile / p.g, tu = 2 * tt;
+  if (tid < 2) {
+    s_tiles[tid] = 0;
+    s_longest[tid] = 0;
+  }
   pdl_enter();
   int n1 = 0, n2 = 0, bad = 0;
+  unsigned long long tiles1 = 0, tiles2 = 0;
+  int longest1 = 0, longest2 = 0;
   for (int a0 = 0; a0 < p.n_seq; a0 += 1024) {
     const int a = a0 + tid;
     int u1 = 0, u2 = 0;
@@ -80,6 +110,13 @@ __global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ E
       p.seq[a] = make_int4(t0, rows, keys, 0);
       u1 = rows > 0 ? (rows - 1) / tu + 1 : 0;
       u2 = rows > 0 ? (keys + 2 * kEmTile - 1) / (2 * kEmTile) : 0;
+      if (rows > 0) {   // causal: the new tokens' share of either range is half full on the mean
+        const int t1 = (keys + kEmTile - 1) / kEmTile, t2 = (rows - 1) / tt + 1;
+        tiles1 += (unsigned long long)u1 * (2 * t1 - (p.causal ? min(t1, rows / kEmTile) : 0));
+        tiles2 += (unsigned long long)t2 * (2 * u2 - (p.causal ? min(u2, rows / (2 * kEmTile)) : 0));
+        longest1 = max(longest1, t1);
+        longest2 = max(longest2, t2);
+      }
     }
     int total;
     const int b1 = block_exclusive_scan(u1, warp_sums, total);
@@ -89,8 +126,20 @@ __global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ E
     if (a < p.n_seq) p.off2[a] = n2 + b2;
     n2 += total;
   }
+  if (longest1) {
+    atomicAdd(&s_tiles[0], tiles1);
+    atomicAdd(&s_tiles[1], tiles2);
+    atomicMax(&s_longest[0], longest1);
+    atomicMax(&s_longest[1], longest2);
+  }
   bad = __syncthreads_or(bad);
+  if (tid >= 32) return;
+  const float h = (float)p.hkv, sms = (float)p.sms;
+  const int cuts1 = em_cuts((float)n1 * h, 0.5f * (float)s_tiles[0] * h, (float)s_longest[0], p.cuts1, sms, tid);
+  const int cuts2 = em_cuts((float)n2 * h, 0.5f * (float)s_tiles[1] * h, (float)s_longest[1], p.cuts2, sms, tid);
   if (tid == 0) {
+    p.hdr[kMCuts1] = cuts1;
+    p.hdr[kMCuts2] = cuts2;
     if (bad) set_err(p.status, KVS_DEVERR_JOB);
     p.off1[p.n_seq] = bad ? 0 : n1;
     p.off2[p.n_seq] = bad ? 0 : n2;
@@ -165,7 +214,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         mbar_init(&bars.s_empty[x][b], kEmSumWarps / 2);
       }
       mbar_init(&bars.it_full[x], 1);
-      mbar_init(&bars.it_empty[x], kEmSumWarps + (PASS == 2 ? 3 : 2));
+      mbar_init(&bars.it_empty[x], kEmSumWarps + 3);
     }
     mbar_init(&bars.fin[0], 1);
     mbar_init(&bars.fin[1], 1);
@@ -195,11 +244,34 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     return __all_sync(0xffffffffu, ok);
   };
 
+  // blocks of key tiles j .. j + 3 of the sequence, eight lanes a tile; -1 where there is none
+  auto key_blocks = [&](int a, int j, int keys) {
+    const int b = j * 8 + lane;
+    int id = -1;
+    if (b < (keys + 15) / 16) {
+      id = __ldg(p.table + (size_t)a * p.max_blocks + b);
+      if (id < 0 || id >= p.capacity) {
+        set_err(p.status, KVS_DEVERR_BLOCK_ID);
+        id = -1;
+      }
+    }
+    return id;
+  };
+  // lanes [from, to): block `lane` of a key tile; one without an id arrives as zeros
+  auto copy_keys = [&](uint8_t* dst, int id, int head, uint64_t* bar, int from, int to) {
+    if (lane >= from && lane < to) {
+      const int row = id >= 0 ? (id * p.hkv + head) * 16 : p.slab_rows;
+#pragma unroll
+      for (int hf = 0; hf < HF; ++hf) tma_load_3d(dst + hf * kHalf + lane * 2048, &tk, 0, row, hf, bar);
+    }
+    __syncwarp();
+  };
+
   if (warp >= kEmSumWarps) {
     if (warp == kEmTma) {
       // --------------------------------------------- claims and TMA copies
       const int* off = PASS == 1 ? p.off1 : p.off2;
-      const int cuts = PASS == 1 ? p.cuts1 : p.cuts2;
+      const int cuts = __ldg(p.hdr + (PASS == 1 ? kMCuts1 : kMCuts2));
       const long long claims = (long long)__ldg(off + p.n_seq) * p.hkv * cuts;
       int* counter = p.hdr + (PASS == 1 ? kMClaim1 : kMClaim2);
       int n = 0, nx = 0, ni = 0, armed = -1;
@@ -208,27 +280,6 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         int c = 0;
         if (lane == 0) c = atomicAdd(counter, 1);
         return (long long)(unsigned)__shfl_sync(0xffffffffu, c, 0);
-      };
-      // blocks of key tiles j .. j + 3 of the sequence, eight lanes a tile; -1 where there is none
-      auto key_blocks = [&](int a, int j, int keys) {
-        const int b = j * 8 + lane;
-        int id = -1;
-        if (b < (keys + 15) / 16) {
-          id = __ldg(p.table + (size_t)a * p.max_blocks + b);
-          if (id < 0 || id >= p.capacity) {
-            set_err(p.status, KVS_DEVERR_BLOCK_ID);
-            id = -1;
-          }
-        }
-        return id;
-      };
-      auto copy_keys = [&](uint8_t* dst, int id, int head, uint64_t* bar) {   // lanes below 8; a block without an id arrives as zeros
-        if (lane < 8) {
-          const int row = id >= 0 ? (id * p.hkv + head) * 16 : p.slab_rows;
-#pragma unroll
-          for (int hf = 0; hf < HF; ++hf) tma_load_3d(dst + hf * kHalf + lane * 2048, &tk, 0, row, hf, bar);
-        }
-        __syncwarp();
       };
       auto copy_rows = [&](uint8_t* dst, int tok, int head, uint64_t* bar) {  // one lane
         for (int hf = 0; hf < HF; ++hf) tma_load_5d(dst + hf * kHalf, &tq, 0, 0, tok, head, hf, bar);
@@ -305,7 +356,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
             if (lane == 0) copy_rows(sX(x), it.t0 + it.x0 + x * tt, it.head, &bars.x_full);
             __syncwarp();
           } else {
-            copy_keys(sX(x), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * x), it.head, &bars.x_full);
+            copy_keys(sX(x), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * x), it.head, &bars.x_full, 0, 8);
           }
         }
         ++nx;
@@ -320,7 +371,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
           if (lane == 0) mbar_arrive_expect_tx(&bars.full[s], PASS == 1 ? (uint32_t)kTile : row_bytes);
           __syncwarp();
           if constexpr (PASS == 1) {
-            copy_keys(ring(s), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * turn), it.head, &bars.full[s]);
+            copy_keys(ring(s), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * turn), it.head, &bars.full[s], 0, 4);
           } else {
             if (lane == 0) copy_rows(ring(s), it.t0 + j * tt, it.head, &bars.full[s]);
             __syncwarp();
@@ -388,7 +439,41 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       // every product issued has completed before the tensor memory is released
       commit(&bars.fin[x]);
       mbar_wait_bounded(&bars.fin[x], 0, p.status);
-    } else if (PASS == 2 && warp == kEmCol) {
+    } else if (PASS == 1) {
+      // ---------------------------------- the other half of every key tile
+      int n = 0;
+      bool ok = true;
+      for (int ni = 0;; ++ni) {
+        const int slot = ni & 1;
+        if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+        const int seq = work[slot].seq, head = work[slot].head, keys = work[slot].keys, y0 = work[slot].y0, y1 = work[slot].y1;
+        const int done = work[slot].done;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+        if (done) break;
+        if (y0 >= y1) continue;
+        int ids = key_blocks(seq, y0, keys), ids_next = key_blocks(seq, y0 + 4, keys);
+        for (int j = y0; j < y1; ++j) {
+          const int turn = (j - y0) & 3, s = n % ST;
+          if (turn == 0 && j > y0) {
+            ids = ids_next;
+            ids_next = key_blocks(seq, j + 4, keys);
+          }
+          if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) { ok = false; break; }
+          // counted by the barrier that the other warp arms, before or after this
+          copy_keys(ring(s), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * turn), head, &bars.full[s], 4, 8);
+          ++n;
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        s_abort = 1;
+        // copies in flight land before the shared memory goes away
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 24)) {
+        }
+      }
+    } else {
       // ------------------------------------- columns: limits and sums of the rows
       int n = 0;
       bool ok = true;
@@ -491,6 +576,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       }
       // Pass 1: keys below `whole` are visible to every live row of the warp.
       // Pass 2: this warp's last key.
+      const bool any_live = __any_sync(0xffffffffu, live);
       const int whole = PASS == 1 ? __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff) : 0;
       const int last_key = it.x0 + x * kEmTile + (warp & 3) * 32 + 31;
       uint32_t v[64];
@@ -525,7 +611,9 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
           if (lane == 0) mbar_arrive(&bars.s_empty[x][b]);
           if (x == 1 || b == 1) s_par ^= 1u;
           if (x == 0) b ^= 1;
-          if constexpr (PASS == 1) {
+          if (!any_live) {
+            // no row of this warp belongs to the sequence
+          } else if constexpr (PASS == 1) {
             const int key0 = j * kEmTile + 64 * half;
             if (key0 + 64 > whole) {
 #pragma unroll
@@ -596,12 +684,15 @@ __global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ Em
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   const int t = (int)(i / p.hq), h = (int)(i - (size_t)t * p.hq);
   if (i >= rows || t < p.tok_off[0] || t >= p.tok_off[p.n_seq]) return;   // rows of no sequence have no parts
+  const int n = 2 * p.hdr[kMCuts1];
   float m = -INFINITY, l = 0.f;
-  for (int k = 0; k < 2 * p.cuts1; ++k) {
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
     const float2 v = p.parts[k * rows + i];
     if (v.y > 0.f) m = fmaxf(m, v.x);
   }
-  for (int k = 0; k < 2 * p.cuts1; ++k) {
+#pragma unroll 8
+  for (int k = 0; k < n; ++k) {
     const float2 v = p.parts[k * rows + i];
     if (v.y > 0.f) l += v.y * fast_exp2(v.x - m);
   }
@@ -619,7 +710,7 @@ __global__ void __launch_bounds__(256) em_add_kernel(const __grid_constant__ EmP
   if (s.y > 0) {
     const float* v = p.sums + (size_t)a * p.most + t;
     const size_t step = (size_t)p.n_seq * p.most;
-    const int n = 2 * p.cuts2 * p.hkv;
+    const int n = 2 * p.hdr[kMCuts2] * p.hkv;
 #pragma unroll 8
     for (int i = 0; i < n; ++i) sum += v[i * step];
   }
@@ -635,12 +726,13 @@ EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks
   const kvs_pool_desc& d = pool->desc;
   const int hkv = d.num_kv_heads, g = hq / hkv, tt = kEmTile / g;
   EmLayout l{};
-  // cuts: as many as bring two items to every SM where the units are too few
-  const long long sms2 = 2ll * pool->num_sms, key_tiles = ((long long)max_blocks * 16 + kEmTile - 1) / kEmTile;
-  const long long u1 = ((long long)n_tokens / (2 * tt) + n_seq) * hkv, u2 = (long long)n_seq * ((key_tiles + 1) / 2) * hkv;
+  // room for cuts: as many as bring four items to every SM where the units are
+  // few; the plan, which knows the lengths, takes no more
+  const long long sms4 = 4ll * pool->num_sms, key_tiles = ((long long)max_blocks * 16 + kEmTile - 1) / kEmTile;
+  const long long u1 = ((long long)n_tokens / (2 * tt) + 1) * hkv, u2 = ((key_tiles + 1) / 2) * hkv;   // of one sequence
   const long long row_tiles = ((long long)n_tokens + tt - 1) / tt;
   auto cuts = [&](long long units, long long tiles) {
-    return (int)std::clamp<long long>((sms2 + units - 1) / std::max(1ll, units), 1, std::clamp<long long>(tiles / 2, 1, kEmMaxCuts));
+    return (int)std::clamp<long long>((sms4 + units - 1) / std::max(1ll, units), 1, std::clamp<long long>(tiles, 1, kEmMaxCuts));
   };
   l.cuts1 = cuts(u1, key_tiles);
   l.cuts2 = cuts(u2, row_tiles);
@@ -758,6 +850,7 @@ extern "C" kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void*
   p.most = max_blocks * 16;
   p.cuts1 = l.cuts1;
   p.cuts2 = l.cuts2;
+  p.sms = pool->num_sms;
   p.scale_log2 = scale_log2;
   CUtensorMap tq{};
   if (n_tokens > 0 && !ex_query_map(&tq, q_dev, n_tokens, p.g, p.hkv, d.head_dim, q_stride))
