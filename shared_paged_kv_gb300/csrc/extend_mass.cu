@@ -60,8 +60,8 @@ struct EmParams {
   int *off1, *off2;   // [n_seq + 1] units before each sequence: pairs of row tiles, pairs of key tiles
   float2* parts;      // pass 1: [cut][column half][n_tokens][hq] {reference, sum}
   float* nlse;        // [hkv][n_tokens][g] -log2 of the rows' sums
-  float* sums;        // pass 2: [cut][column half][hkv][n_seq][most]
-  int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2, sms;   // cuts: the most there is room for
+  float* sums;        // pass 2: [cut][column half][hkv][n_seq][most], few rows: [row tile][column half][hkv][most]
+  int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2, sms, few;   // cuts: the most there is room for; few: em_keys_kernel is pass 2
   float scale_log2;
 };
 
@@ -109,13 +109,13 @@ __global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ E
       const int keys = min(max(raw, 0), p.most), rows = t1 - t0;
       p.seq[a] = make_int4(t0, rows, keys, 0);
       u1 = rows > 0 ? (rows - 1) / tu + 1 : 0;
-      u2 = rows > 0 ? (keys + 2 * kEmTile - 1) / (2 * kEmTile) : 0;
+      u2 = rows <= 0 ? 0 : p.few ? (rows - 1) / tt + 1 : (keys + 2 * kEmTile - 1) / (2 * kEmTile);
       if (rows > 0) {   // causal: the new tokens' share of either range is half full on the mean
         const int t1 = (keys + kEmTile - 1) / kEmTile, t2 = (rows - 1) / tt + 1;
         tiles1 += (unsigned long long)u1 * (2 * t1 - (p.causal ? min(t1, rows / kEmTile) : 0));
-        tiles2 += (unsigned long long)t2 * (2 * u2 - (p.causal ? min(u2, rows / (2 * kEmTile)) : 0));
+        tiles2 += p.few ? (unsigned long long)u2 * (2 * t1) : (unsigned long long)t2 * (2 * u2 - (p.causal ? min(u2, rows / (2 * kEmTile)) : 0));
         longest1 = max(longest1, t1);
-        longest2 = max(longest2, t2);
+        longest2 = max(longest2, p.few ? t1 : t2);
       }
     }
     int total;
@@ -184,6 +184,47 @@ __device__ __forceinline__ int em_find(const int* off, int n, int v, int lane) {
   return lo + __popc(__ballot_sync(0xffffffffu, le));
 }
 
+// Blocks of key tiles j .. j + 3 of sequence a, eight lanes a tile; -1 where there is none.
+__device__ __forceinline__ int em_blocks(const EmParams& p, int a, int j, int keys, int lane) {
+  const int b = j * 8 + lane;
+  int id = -1;
+  if (b < (keys + 15) / 16) {
+    id = __ldg(p.table + (size_t)a * p.max_blocks + b);
+    if (id < 0 || id >= p.capacity) {
+      set_err(p.status, KVS_DEVERR_BLOCK_ID);
+      id = -1;
+    }
+  }
+  return id;
+}
+
+// Lanes [from, to): block `lane` of a key tile; one without an id arrives as zeros.
+template <int HF>
+__device__ __forceinline__ void em_copy_keys(const EmParams& p, const CUtensorMap& tk, uint8_t* dst, int id, int head, uint64_t* bar,
+                                             int lane, int from, int to) {
+  if (lane >= from && lane < to) {
+    const int row = id >= 0 ? (id * p.hkv + head) * 16 : p.slab_rows;
+#pragma unroll
+    for (int hf = 0; hf < HF; ++hf) tma_load_3d(dst + hf * kEmTile * 128 + lane * 2048, &tk, 0, row, hf, bar);
+  }
+  __syncwarp();
+}
+
+// sum over 64 columns of 2^(scale v + by); by(i): what is added to columns i and i + 1.
+template <typename F>
+__device__ __forceinline__ float em_sum_up(const uint32_t* v, float2 scale, F by) {
+  float2 sum[4] = {};
+#pragma unroll
+  for (int i = 0; i < 64; i += 8)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 a = __ffma2_rn(make_float2(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1])), scale, by(i + 2 * k));
+      sum[k] = __fadd2_rn(sum[k], make_float2(fast_exp2(a.x), fast_exp2(a.y)));
+    }
+  const float2 t = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
+  return t.x + t.y;
+}
+
 template <int D, int PASS>
 __global__ void __launch_bounds__(kEmThreads, 1)
 em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk) {
@@ -244,27 +285,9 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     return __all_sync(0xffffffffu, ok);
   };
 
-  // blocks of key tiles j .. j + 3 of the sequence, eight lanes a tile; -1 where there is none
-  auto key_blocks = [&](int a, int j, int keys) {
-    const int b = j * 8 + lane;
-    int id = -1;
-    if (b < (keys + 15) / 16) {
-      id = __ldg(p.table + (size_t)a * p.max_blocks + b);
-      if (id < 0 || id >= p.capacity) {
-        set_err(p.status, KVS_DEVERR_BLOCK_ID);
-        id = -1;
-      }
-    }
-    return id;
-  };
-  // lanes [from, to): block `lane` of a key tile; one without an id arrives as zeros
+  auto key_blocks = [&](int a, int j, int keys) { return em_blocks(p, a, j, keys, lane); };
   auto copy_keys = [&](uint8_t* dst, int id, int head, uint64_t* bar, int from, int to) {
-    if (lane >= from && lane < to) {
-      const int row = id >= 0 ? (id * p.hkv + head) * 16 : p.slab_rows;
-#pragma unroll
-      for (int hf = 0; hf < HF; ++hf) tma_load_3d(dst + hf * kHalf + lane * 2048, &tk, 0, row, hf, bar);
-    }
-    __syncwarp();
+    em_copy_keys<HF>(p, tk, dst, id, head, bar, lane, from, to);
   };
 
   if (warp >= kEmSumWarps) {
@@ -580,22 +603,6 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       const int whole = PASS == 1 ? __reduce_min_sync(0xffffffffu, live ? lim : 0x7fffffff) : 0;
       const int last_key = it.x0 + x * kEmTile + (warp & 3) * 32 + 31;
       uint32_t v[64];
-      auto sum_up = [&](auto by) {   // by(i): what is added to columns i and i + 1
-        float2 sum[4] = {};
-#pragma unroll
-        for (int i = 0; i < 64; i += 16) {
-          float2 a[8];
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            a[k] = __ffma2_rn(make_float2(__uint_as_float(v[i + 2 * k]), __uint_as_float(v[i + 2 * k + 1])), sc2, by(i + 2 * k));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) a[k] = make_float2(fast_exp2(a[k].x), fast_exp2(a[k].y));
-#pragma unroll
-          for (int k = 0; k < 8; ++k) sum[k & 3] = __fadd2_rn(sum[k & 3], a[k]);
-        }
-        const float2 t = __fadd2_rn(__fadd2_rn(sum[0], sum[1]), __fadd2_rn(sum[2], sum[3]));
-        return t.x + t.y;
-      };
       for (int j = it.y0; j < it.y1; ++j) {
         const int s = n % ST;
         // also where this X tile passes the Y tile by: a stage is handed back once a turn
@@ -624,7 +631,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
             // later ones sees all of these) and moves only where a sum gets out of
             // hand: any reference within 2^60 of the maximum serves float32 as well.
             const bool fresh = j == xs;
-            float sum = fresh ? INFINITY : sum_up([&](int) { return make_float2(-m, -m); });
+            float sum = fresh ? INFINITY : em_sum_up(v, sc2, [&](int) { return make_float2(-m, -m); });
             if (__any_sync(0xffffffffu, !(sum < 0x1p60f))) {
               float top = __uint_as_float(v[0]);
 #pragma unroll
@@ -634,7 +641,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
                 if (!fresh) l *= fast_exp2(m - top);
                 m = top == -INFINITY ? 0.f : top;
               }
-              sum = sum_up([&](int) { return make_float2(-m, -m); });
+              sum = em_sum_up(v, sc2, [&](int) { return make_float2(-m, -m); });
             }
             l += sum;
           } else {
@@ -649,7 +656,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
                 if (key >= u.w) v[i + 3] = 0xff800000u;
               }
             }
-            l += sum_up([&](int i) { return *reinterpret_cast<const float2*>(cl.nlse + 64 * half + i); });
+            l += em_sum_up(v, sc2, [&](int i) { return *reinterpret_cast<const float2*>(cl.nlse + 64 * half + i); });
           }
         }
         if (PASS == 2) {
@@ -665,6 +672,339 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         p.parts[(cut * p.n_tokens + it.t0 + tok) * p.hq + it.head * p.g + rg] = make_float2(m, l);
       else
         p.sums[((cut * p.hkv + it.head) * p.n_seq + it.seq) * p.most + key] = l;
+    }
+    if (!ok) s_abort = 1;
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kEmCols);
+  }
+}
+
+// ------------------------------------------------- few rows: keys stream past
+// Pass 2 for calls whose rows are few tiles: a pair of key tiles would wait for
+// its copies, its items and its tensor memory to see one tile of rows.  Here a row
+// tile stays in shared memory and the keys stream past it, as in pass 1: S^T =
+// K Q^T of one key tile after the other, alternating between two groups of warps,
+// whose threads write the sum of a key's 64 columns for each half.  A key's sums
+// of all row tiles, halves and KV heads are added by the last kernel.
+struct EkBars {
+  uint64_t full[8], empty[8];
+  uint64_t x_full[2], x_empty[2], c_full[2], c_empty[2];
+  uint64_t s_full[2][2], s_empty[2][2];
+  uint64_t it_full[2], it_empty[2];
+  uint64_t fin[2];
+};
+
+struct EkItem {
+  int seq, head, tile, done;    // tile: row tile of the sequence
+  int t0, rows, keys, unit;     // unit: row tile of the call
+  int y0, y1, pad[2];           // key tiles
+};
+
+// Key tiles that row tile i of a sequence sees.
+__device__ __forceinline__ int ek_tiles(const EmParams& p, int rows, int keys, int i, int tt) {
+  const int lim = p.causal ? min(max(keys - rows + min(rows, (i + 1) * tt), 0), keys) : keys;
+  return (lim + kEmTile - 1) / kEmTile;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kEmThreads, 1)
+em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk) {
+  constexpr int HF = D / 64, ST = em_stages<D>(), kTile = em_tile_bytes<D>(), kHalf = kEmTile * 128;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ EkBars bars;
+  __shared__ EkItem work[2];
+  __shared__ __align__(16) EmCols cols[2];
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 2);      // both product warps
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars.x_full[i], 1);
+      mbar_init(&bars.x_empty[i], 2);
+      mbar_init(&bars.c_full[i], 1);
+      mbar_init(&bars.c_empty[i], kEmSumWarps);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars.s_full[i][b], 1);
+        mbar_init(&bars.s_empty[i][b], kEmSumWarps / 2);
+      }
+      mbar_init(&bars.it_full[i], 1);
+      mbar_init(&bars.it_empty[i], kEmSumWarps + 3);
+      mbar_init(&bars.fin[i], 1);
+    }
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, kEmCols);
+    tmem_relinquish();
+  }
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  auto ring = [&](int i) { return base + kTile * (2 + i); };
+  // rows of a query tile behind its last whole token are never copied to
+  for (int i = threadIdx.x; i < 2 * kTile / 16; i += kEmThreads) reinterpret_cast<uint4*>(base)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = s_tmem;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int tt = kEmTile / p.g;
+  auto stop = [&]() { return __any_sync(0xffffffffu, s_abort != 0); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_wait_bounded(bar, parity, p.status);
+    return __all_sync(0xffffffffu, ok);
+  };
+  auto key_blocks = [&](int a, int j, int keys) { return em_blocks(p, a, j, keys, lane); };
+  auto copy_keys = [&](uint8_t* dst, int id, int head, uint64_t* bar, int from, int to) {
+    em_copy_keys<HF>(p, tk, dst, id, head, bar, lane, from, to);
+  };
+
+  if (warp >= kEmSumWarps) {
+    bool ok = true;
+    if (warp == kEmTma) {
+      // ----------------------------------- claims, rows, half of every key tile
+      const int cuts = __ldg(p.hdr + kMCuts2);
+      const long long claims = (long long)__ldg(p.off2 + p.n_seq) * p.hkv * cuts;
+      auto claim_next = [&]() {
+        int c = 0;
+        if (lane == 0) c = atomicAdd(p.hdr + kMClaim2, 1);
+        return (long long)(unsigned)__shfl_sync(0xffffffffu, c, 0);
+      };
+      int n = 0, nx = 0, armed = -1;
+      long long claim = claim_next();
+      for (int ni = 0;; ++ni) {
+        if (stop()) { ok = false; break; }
+        const int slot = ni & 1;
+        if (ni >= 2 && !wait(&bars.it_empty[slot], ((ni - 2) >> 1) & 1)) { ok = false; break; }
+        EkItem it{};
+        it.done = claim >= claims;
+        if (!it.done) {
+          const long long u = claim / cuts;
+          const int cut = (int)(claim - u * cuts), unit = (int)(u / p.hkv);
+          it.head = (int)(u - (long long)unit * p.hkv);
+          it.seq = em_find(p.off2, p.n_seq, unit, lane);
+          const int4 s = __ldg(p.seq + it.seq);
+          it.unit = unit;
+          it.tile = unit - __ldg(p.off2 + it.seq);
+          it.t0 = s.x;
+          it.rows = s.y;
+          it.keys = s.z;
+          const int nt = ek_tiles(p, it.rows, it.keys, it.tile, tt);
+          it.y0 = (int)((long long)nt * cut / cuts);
+          it.y1 = (int)((long long)nt * (cut + 1) / cuts);
+        }
+        if (lane == 0) {
+          work[slot] = it;
+          mbar_arrive(&bars.it_full[slot]);
+        }
+        __syncwarp();
+        if (it.done) break;
+        claim = claim_next();
+        if (it.y0 >= it.y1) continue;
+        int ids = key_blocks(it.seq, it.y0, it.keys), ids_next = key_blocks(it.seq, it.y0 + 4, it.keys);
+        const int xs = nx & 1;
+        if (nx >= 2 && !wait(&bars.x_empty[xs], ((nx - 2) >> 1) & 1)) { ok = false; break; }
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&bars.x_full[xs], (uint32_t)(HF * tt * p.g * 128));
+          for (int hf = 0; hf < HF; ++hf)
+            tma_load_5d(base + xs * kTile + hf * kHalf, &tq, 0, 0, it.t0 + it.tile * tt, it.head, hf, &bars.x_full[xs]);
+        }
+        __syncwarp();
+        ++nx;
+        for (int j = it.y0; j < it.y1; ++j) {
+          const int turn = (j - it.y0) & 3, s = n % ST;
+          if (turn == 0 && j > it.y0) {
+            ids = ids_next;
+            ids_next = key_blocks(it.seq, j + 4, it.keys);
+          }
+          if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) { ok = false; break; }
+          if (lane == 0) mbar_arrive_expect_tx(&bars.full[s], kTile);
+          __syncwarp();
+          copy_keys(ring(s), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * turn), it.head, &bars.full[s], 0, 4);
+          armed = n++;
+        }
+        if (!ok) break;
+      }
+      if (!ok) {
+        for (int m = max(0, armed - ST + 1); m <= armed; ++m) mbar_drain(&bars.full[m % ST], (m / ST) & 1);
+        for (int m = max(0, nx - 2); m < nx; ++m) mbar_drain(&bars.x_full[m & 1], (m >> 1) & 1);
+      }
+    } else if (warp < kEmTma) {
+      // ------------------------------- products of every other key tile
+      const int x = warp - kEmMma;
+      constexpr uint32_t idS = umma_idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kHi = ex_desc_hi(1024);
+      const uint32_t x_lo = ex_desc_lo(smem_u32(base), 16), y_lo = ex_desc_lo(smem_u32(ring(0)), 16);
+      int nx = 0, b = 0, s = 0;
+      uint32_t full_par = 0, free_par = 1;
+      for (int ni = 0;; ++ni) {
+        const int slot = ni & 1;
+        if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+        const int y0 = work[slot].y0, y1 = work[slot].y1, done = work[slot].done;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+        if (done) break;
+        if (y0 >= y1) continue;
+        const int xs = nx & 1;
+        if (!wait(&bars.x_full[xs], (nx >> 1) & 1)) { ok = false; break; }
+        ++nx;
+        for (int j = y0; j < y1; ++j) {
+          if (!wait(&bars.full[s], full_par)) { ok = false; break; }
+          if (((j - y0) & 1) == x) {
+            if (!wait(&bars.s_empty[x][b], free_par)) { ok = false; break; }
+            tc_fence_after();
+            if (elect_one()) {
+              const uint32_t ya = y_lo + s * (kTile / 16), xa = x_lo + xs * (kTile / 16), d = tmem + 128u * (2 * x + b);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) / 16;
+                ex_mma_ss(d, ya + o, xa + o, kHi, idS, kk > 0);
+              }
+              umma_commit(&bars.s_full[x][b]);
+              umma_commit(&bars.empty[s]);
+            }
+            __syncwarp();
+            if (b) free_par ^= 1u;
+            b ^= 1;
+          } else {
+            if (lane == 0) mbar_arrive(&bars.empty[s]);
+            __syncwarp();
+          }
+          if (++s == ST) {
+            s = 0;
+            full_par ^= 1u;
+          }
+        }
+        if (!ok) break;
+        if (elect_one()) umma_commit(&bars.x_empty[xs]);
+        __syncwarp();
+      }
+      // every product issued has completed before the tensor memory is released
+      if (elect_one()) umma_commit(&bars.fin[x]);
+      __syncwarp();
+      mbar_wait_bounded(&bars.fin[x], 0, p.status);
+    } else {
+      // ------------------------- the rows' columns, the other half of the keys
+      int n = 0, nx = 0;
+      for (int ni = 0;; ++ni) {
+        const int slot = ni & 1;
+        if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+        const EkItem it = work[slot];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+        if (it.done) break;
+        if (it.y0 >= it.y1) continue;
+        int ids = key_blocks(it.seq, it.y0, it.keys), ids_next = key_blocks(it.seq, it.y0 + 4, it.keys);
+        const int per = tt * p.g, xs = nx & 1;
+        const float* rows = p.nlse + ((size_t)it.head * p.n_tokens + it.t0) * p.g;
+        float v[4];
+        int lim[4], least = 0x7fffffff;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = i * 32 + lane, row = it.tile * per + c;
+          v[i] = c < per && row < it.rows * p.g ? rows[row] : -INFINITY;
+          lim[i] = v[i] == -INFINITY ? 0 : p.causal ? max(it.keys - it.rows + row / p.g + 1, 0) : it.keys;
+          least = min(least, lim[i]);
+        }
+        least = __reduce_min_sync(0xffffffffu, least);
+        if (nx >= 2 && !wait(&bars.c_empty[xs], ((nx - 2) >> 1) & 1)) { ok = false; break; }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          cols[xs].nlse[i * 32 + lane] = v[i];
+          cols[xs].lim[i * 32 + lane] = lim[i];
+        }
+        if (lane == 0) cols[xs].least = least;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.c_full[xs]);
+        ++nx;
+        for (int j = it.y0; j < it.y1; ++j) {
+          const int turn = (j - it.y0) & 3, s = n % ST;
+          if (turn == 0 && j > it.y0) {
+            ids = ids_next;
+            ids_next = key_blocks(it.seq, j + 4, it.keys);
+          }
+          if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) { ok = false; break; }
+          // counted by the barrier that the other warp arms, before or after this
+          copy_keys(ring(s), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * turn), it.head, &bars.full[s], 4, 8);
+          ++n;
+        }
+        if (!ok) break;
+      }
+      if (!ok) {   // copies in flight land before the shared memory goes away
+        const long long t0 = clock64();
+        while (clock64() - t0 < (1ll << 24)) {
+        }
+      }
+    }
+    if (!ok) s_abort = 1;
+  } else {
+    // ------------------------------------------------------------ sums
+    const int x = (warp >> 2) & 1, half = warp >> 3, r = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * x + 64u * half;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    int nx = 0, b = 0;
+    uint32_t s_par = 0;
+    bool ok = true;
+    for (int ni = 0;; ++ni) {
+      const int slot = ni & 1;
+      if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
+      const EkItem it = work[slot];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
+      if (it.done) break;
+      if (it.y0 >= it.y1) continue;
+      const int xs = nx & 1;
+      if (!wait(&bars.c_full[xs], (nx >> 1) & 1)) { ok = false; break; }
+      ++nx;
+      const EmCols& cl = cols[xs];
+      // columns behind the tile's last row hold nothing: whole halves are passed by
+      const bool any = 64 * half < min(tt, it.rows - it.tile * tt) * p.g;
+      float* out = p.sums + ((size_t)(2 * it.unit + half) * p.hkv + it.head) * p.most;
+      for (int j = it.y0 + x; j < it.y1; j += 2) {
+        if (!wait(&bars.s_full[x][b], s_par)) { ok = false; break; }
+        tc_fence_after();
+        uint32_t v[64];
+        if (any) {
+          tmem_ld32_issue(tS + 128u * b, v);
+          tmem_ld32_issue(tS + 128u * b + 32, v + 32);
+          tmem_ld32x2_wait(v, v + 32);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars.s_empty[x][b]);
+        if (b) s_par ^= 1u;
+        b ^= 1;
+        const int key = j * kEmTile + r;
+        float l = 0.f;
+        if (any) {
+          if (j * kEmTile + (warp & 3) * 32 + 31 >= cl.least) {
+#pragma unroll
+            for (int i = 0; i < 64; i += 4) {
+              const int4 u = *reinterpret_cast<const int4*>(cl.lim + 64 * half + i);
+              if (key >= u.x) v[i] = 0xff800000u;
+              if (key >= u.y) v[i + 1] = 0xff800000u;
+              if (key >= u.z) v[i + 2] = 0xff800000u;
+              if (key >= u.w) v[i + 3] = 0xff800000u;
+            }
+          }
+          l = em_sum_up(v, sc2, [&](int i) { return *reinterpret_cast<const float2*>(cl.nlse + 64 * half + i); });
+        }
+        if (key < it.keys) out[key] = l;
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.c_empty[xs]);
     }
     if (!ok) s_abort = 1;
   }
@@ -707,20 +1047,30 @@ __global__ void __launch_bounds__(256) em_add_kernel(const __grid_constant__ EmP
   const int4 s = p.seq[a];
   if (t >= s.z) return;
   float sum = 0.f;
-  if (s.y > 0) {
-    const float* v = p.sums + (size_t)a * p.most + t;
-    const size_t step = (size_t)p.n_seq * p.most;
+  const float* v = p.sums + (size_t)a * p.most + t;
+  const size_t step = (size_t)p.n_seq * p.most;
+  const size_t o = (size_t)a * p.most + t;
+  if (s.y > 0 && p.few) {
+    // of every row tile that sees the key, and of its halves that hold rows
+    const int tt = kEmTile / p.g;
+    v = p.sums + (size_t)p.off2[a] * 2 * p.hkv * p.most + t;
+    for (int i = 0; i * tt < s.y; ++i) {
+      if (t / kEmTile >= ek_tiles(p, s.y, s.z, i, tt)) continue;
+      const int halves = min(tt, s.y - i * tt) * p.g > 64 ? 2 : 1;
+#pragma unroll 8
+      for (int k = 0; k < halves * p.hkv; ++k) sum += v[(size_t)(2 * i * p.hkv + k) * p.most];
+    }
+  } else if (s.y > 0) {
     const int n = 2 * p.hdr[kMCuts2] * p.hkv;
 #pragma unroll 8
     for (int i = 0; i < n; ++i) sum += v[i * step];
   }
-  const size_t o = (size_t)a * p.most + t;
   mass[o] = mass_in ? fmaf(carry, mass_in[o], sum) : sum;
 }
 
 struct EmLayout {
   size_t hdr, seq, off1, off2, parts, nlse, sums, total;
-  int cuts1, cuts2;
+  int cuts1, cuts2, few;
 };
 EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks, int hq) {
   const kvs_pool_desc& d = pool->desc;
@@ -735,7 +1085,13 @@ EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks
     return (int)std::clamp<long long>((sms4 + units - 1) / std::max(1ll, units), 1, std::clamp<long long>(tiles, 1, kEmMaxCuts));
   };
   l.cuts1 = cuts(u1, key_tiles);
-  l.cuts2 = cuts(u2, row_tiles);
+  // On the mean at most one row tile a sequence: the keys stream past them
+  // (em_keys_kernel; 8 x 32 rows after 6,000 tokens, 32 / 8 heads: 60 us, else 75;
+  // 64 x 4 after 8,000, 40 / 8: 375 and 573).  With more, each would read the keys
+  // again (1 x 128 rows after 6,000, 32 / 8: 48 and 42; 1 x 512 after 4,096, 16 / 2:
+  // 77 and 42).
+  l.few = row_tiles <= n_seq;
+  l.cuts2 = l.few ? cuts(hkv, key_tiles) : cuts(u2, row_tiles);
   size_t o = 0;
   auto take = [&](size_t b) {
     const size_t at = o;
@@ -748,7 +1104,7 @@ EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks
   l.off2 = take((size_t)(n_seq + 1) * 4);
   l.parts = take((size_t)2 * l.cuts1 * n_tokens * hq * 8);
   l.nlse = take((size_t)n_tokens * hq * 4);
-  l.sums = take((size_t)2 * l.cuts2 * hkv * n_seq * max_blocks * 16 * 4);
+  l.sums = take((size_t)2 * (l.few ? (size_t)(row_tiles + n_seq) : (size_t)l.cuts2 * n_seq) * hkv * max_blocks * 16 * 4);
   l.total = o;
   return l;
 }
@@ -772,7 +1128,8 @@ template <int D>
 kvs_status em_run(const kvs_pool* pool, int layer, const EmParams& p, const CUtensorMap& tq, const float* mass_in, float carry,
                   float* mass, cudaStream_t stream) {
   if (!smem_limit_once<em_pass_kernel<D, 1>>(em_smem<D>(), pool->device) ||
-      !smem_limit_once<em_pass_kernel<D, 2>>(em_smem<D>(), pool->device))
+      !smem_limit_once<em_pass_kernel<D, 2>>(em_smem<D>(), pool->device) ||
+      !smem_limit_once<em_keys_kernel<D>>(em_smem<D>(), pool->device))
     return fail(KVS_ERR_CUDA, "extend_mass: cannot raise the shared-memory limit");
   const CUtensorMap& tk = D == 128 ? pool->tk1[layer] : pool->tk[layer];
   const dim3 grid((unsigned)pool->num_sms);
@@ -780,7 +1137,7 @@ kvs_status em_run(const kvs_pool* pool, int layer, const EmParams& p, const CUte
   if (p.n_tokens > 0)
     ok = em_launch(em_pass_kernel<D, 1>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess &&
          em_launch(em_join_kernel, dim3((unsigned)(((long long)p.n_tokens * p.hq + 255) / 256)), dim3(256), 0, stream, p) == cudaSuccess &&
-         em_launch(em_pass_kernel<D, 2>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess;
+         em_launch(p.few ? em_keys_kernel<D> : em_pass_kernel<D, 2>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess;
   if (ok && p.n_tokens > 0) count_launch(3);
   if (ok && em_launch(em_add_kernel, dim3((unsigned)((p.most + 255) / 256), (unsigned)p.n_seq), dim3(256), 0, stream, p, mass_in, carry,
                       mass) == cudaSuccess)
@@ -851,6 +1208,7 @@ extern "C" kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void*
   p.cuts1 = l.cuts1;
   p.cuts2 = l.cuts2;
   p.sms = pool->num_sms;
+  p.few = l.few;
   p.scale_log2 = scale_log2;
   CUtensorMap tq{};
   if (n_tokens > 0 && !ex_query_map(&tq, q_dev, n_tokens, p.g, p.hkv, d.head_dim, q_stride))
