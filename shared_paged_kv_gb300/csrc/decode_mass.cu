@@ -157,11 +157,16 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
   pdl_enter();
 
   // ---- this CTA's stretch of the line
-  int per_head = 0;
+  int per_head = 0, mine = 0, mine_before = 0;   // of the sequences tid, tid + T, ...: the first one's units, and those before it
   for (int a0 = 0; a0 < p.n_seq; a0 += T) {
     const int a = a0 + tid;
+    const int n = a < p.n_seq ? dm_span<UT>(p, a).units : 0;
     int total;
-    block_exclusive_scan(a < p.n_seq ? dm_span<UT>(p, a).units : 0, sh.warp_sums, total);
+    const int before = block_exclusive_scan(n, sh.warp_sums, total);
+    if (a0 == 0) {
+      mine = n;
+      mine_before = before;
+    }
     per_head += total;
   }
   for (int a = blockIdx.x; a < p.n_seq; a += gridDim.x) {
@@ -175,8 +180,12 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
   const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
   if (u0 >= u1) return;
   const int h0 = (int)(u0 / per_head), r0 = (int)(u0 - (long long)h0 * per_head);
+  if (mine_before <= r0 && r0 < mine_before + mine) {
+    sh.a = tid;
+    sh.b = r0 - mine_before;
+  }
   int carry = 0;
-  for (int a0 = 0; a0 < p.n_seq; a0 += T) {
+  for (int a0 = 0; p.n_seq > T && a0 < p.n_seq; a0 += T) {   // more sequences than threads: once more
     const int a = a0 + tid, n = a < p.n_seq ? dm_span<UT>(p, a).units : 0;
     int total;
     const int before = carry + block_exclusive_scan(n, sh.warp_sums, total);
@@ -381,14 +390,20 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
         } else {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) s[0][nt][0] = s[0][nt][1] = s[0][nt][2] = s[0][nt][3] = 0.f;
+          // two chains of products, so that a warp waits half as long for its scores
+          float s2[NT][4] = {};
           const uint32_t ka = smem_u32(kc);
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
             uint32_t x[4];
             ldsm_x4(ka + kv_tile_off<D>(lane & 15, j * 16 + (lane >> 4) * 8), x[0], x[1], x[2], x[3]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_bf16(s[0][nt], x, qb[nt][j][0], qb[nt][j][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_bf16(j & 1 ? s2[nt] : s[0][nt], x, qb[nt][j][0], qb[nt][j][1]);
           }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[0][nt][e] += s2[nt][e];
         }
         if (nv < UT) {   // the sequence ends here
 #pragma unroll
