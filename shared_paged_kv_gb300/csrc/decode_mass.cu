@@ -45,7 +45,7 @@ namespace {
 
 enum { kFmtBf16x64, kFmtBf16x128, kFmtMx };
 
-constexpr int kDmMaxGroup = 16, kDmMaxStages = 6;
+constexpr int kDmMaxGroup = 16, kDmMaxStages = 6, kDmMaxCtas = 3;
 
 template <int FMT, int NT>
 struct Dm {   // what a format and the number of 8-column tiles fix
@@ -53,14 +53,19 @@ struct Dm {   // what a format and the number of 8-column tiles fix
   static constexpr int D = FMT == kFmtBf16x64 ? 64 : 128;
   static constexpr int UT = mx ? 32 : 16;                 // tokens of a unit
   static constexpr int kBlockTokens = mx ? 64 : 16;
-  static constexpr int W = mx || NT == 2 ? 8 : 4;         // warps of a CTA
-  static constexpr int kCtas = NT == 1 ? 2 : 1;           // per SM
+  static constexpr int W = !mx && NT == 2 ? 8 : 4;        // warps of a CTA
+  static constexpr int kCtas = mx ? (NT == 1 ? 3 : 2) : NT == 1 ? 2 : 1;   // per SM (kDmMaxCtas at most)
   static constexpr int kCodes = mx ? UT * D / 2 : UT * D * 2;   // bytes of a unit's K or V
   static constexpr int kScales = mx ? UT * 4 : 0;
   static constexpr int kStage = 2 * kCodes + (mx ? 512 : 0);    // scales in the last 512 bytes
-  static constexpr int ST = mx || NT == 2 ? 2 : FMT == kFmtBf16x64 ? 6 : 3;
+  static constexpr int ST = FMT == kFmtBf16x64 && NT == 1 ? 4 : 2;   // three or four of 128 channels were slower (below)
   static constexpr int kHead = W == 4 ? 1024 : 2048;      // barriers and the warps' sums, in front of the ring
-  // two CTAs with three stages of 128 channels and eight heads fill the SM's shared memory to the byte
+  // Measured for bf16, one n-tile, 128 channels (8 x 13,000 tokens of 32 / 32 heads,
+  // 16 x 8,000 of 32 / 8, us): four warps, two CTAs an SM, two stages 266, 94; three
+  // stages 281, 99; five or six warps 272, 96; three CTAs 274, 98; two warps and
+  // four CTAs 337, 125.  Microscaled (8 x 24,000 of 32 / 8, 64 x 4,000 of 32 / 8):
+  // four warps, three CTAs 69.8, 78.9; two CTAs of eight warps, with 128 registers a
+  // thread, 77.3, 83.9; two of four 74.2, 83.7; four of three 74.4, 78.8.
   static constexpr int kPrep = mx ? UT * 16 + 4 * UT * 2 : 0;   // a warp's prepared scales
   static constexpr int kSmem = kHead + W * (ST * kStage + NT * 8 * D * 4 + kPrep);
   static constexpr float kBias = mx ? 11.f : 0.f;         // weights reach 2^(kBias + kLag)
@@ -154,7 +159,7 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     for (int s = 0; s < ST; ++s) mbar_init(&sh.full[warp][s], 1);
     fence_barrier_init();
   }
-  pdl_enter();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
   // ---- this CTA's stretch of the line
   int per_head = 0, mine = 0, mine_before = 0;   // of the sequences tid, tid + T, ...: the first one's units, and those before it
@@ -665,6 +670,10 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     done += n_seg;
     if (done < n_mine) dm_advance<UT>(p, seg, n_seg);
   }
+  // Only now may the next kernel's CTAs come: sooner, they would crowd where this
+  // grid's first CTAs end (eight sequences of 16,384 to 32,768 tokens in 4 bits: 85 us
+  // with the call at the start, 73 here).
+  asm volatile("griddepcontrol.launch_dependents;");
   if (dead)   // copies in flight land before the shared memory goes away
     for (int i = 0; i < ST; ++i) {
       const int use = uses + i;
@@ -755,7 +764,7 @@ DmLayout dm_layout(const kvs_pool* pool, int n_seq, int max_blocks, int g) {
     o += (b + 255) & ~size_t{255};
     return at;
   };
-  const size_t pairs = (size_t)n_seq * d.num_kv_heads, parts = (size_t)pool->num_sms * 2 + pairs;
+  const size_t pairs = (size_t)n_seq * d.num_kv_heads, parts = (size_t)pool->num_sms * kDmMaxCtas + pairs;
   l.part = take(parts * g * d.head_dim * 4);
   l.ml = take(parts * g * 8);
   l.fin = take(pairs * g * 8);

@@ -277,7 +277,6 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   const int tt = kEmTile / p.g;
   auto stop = [&]() { return __any_sync(0xffffffffu, s_abort != 0); };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -675,6 +674,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     }
     if (!ok) s_abort = 1;
   }
+  asm volatile("griddepcontrol.launch_dependents;");   // not sooner: small CTAs would crowd where this grid's first ones end
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
@@ -758,7 +758,6 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("griddepcontrol.launch_dependents;");
   const int tt = kEmTile / p.g;
   auto stop = [&]() { return __any_sync(0xffffffffu, s_abort != 0); };
   auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -1008,6 +1007,7 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     }
     if (!ok) s_abort = 1;
   }
+  asm volatile("griddepcontrol.launch_dependents;");   // not sooner: small CTAs would crowd where this grid's first ones end
   tc_fence_before();
   __syncthreads();
   if (warp == 0) {
