@@ -530,10 +530,9 @@ kvs_status kvs_append(kvs_pool* pool, int32_t layer, const void* k_dev, int64_t 
 /* Gather, the way back: k_out / v_out bf16 [n_tokens][num_kv_heads][head_dim]
  * receive the pool's values of the tokens that kvs_append with the same
  * tok_off and seq_len would write (the last n of the first seq_len[a]); Q4G64
- * pools give scale * code + bias, rounded to bf16, MX4 pools code * scale, which is
- * exact.  This is the k_cached of
- * kvs_select_critical.  Rows whose token has no valid place (device errors as
- * for kvs_append) are left as they were. */
+ * pools give scale * code + bias, rounded to bf16, MX4 pools code * scale, which
+ * is exact.  This is the k_cached of kvs_select_critical.  Rows whose token has
+ * no valid place (device errors as for kvs_append) are left as they were. */
 kvs_status kvs_gather(kvs_pool* pool, int32_t layer, const int32_t* tok_off_dev, int32_t n_tokens,
                       const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev, int32_t n_seq,
                       void* k_out_dev, void* v_out_dev, cudaStream_t stream);
@@ -625,7 +624,9 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  * kvs_extend_attn (weights of rows that see nothing are 0, bad block ids count as
  * zero keys; with bad offsets nothing is written).  A window of observation is
  * given as the last rows of every sequence.  Values are not read; BF16 pools.
- * ws: kvs_extend_mass_workspace_size bytes, for calls with these arguments.
+ * ws: kvs_extend_mass_workspace_size bytes, of one stream at a time; enough as
+ * well for every call with the same heads and no more tokens, sequences and
+ * blocks.
  *
  * A step of an eviction: the masses are gathered while the model runs,
  * kvs_keep_heavy lists the tokens to keep, kvs_compact closes the gaps.  Keys

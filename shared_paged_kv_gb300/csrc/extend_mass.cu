@@ -1102,9 +1102,15 @@ EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks
   l.seq = take((size_t)n_seq * 16);
   l.off1 = take((size_t)(n_seq + 1) * 4);
   l.off2 = take((size_t)(n_seq + 1) * 4);
-  l.parts = take((size_t)2 * l.cuts1 * n_tokens * hq * 8);
+  // Fewer rows or keys may take more cuts, so the two buffers of cuts are given
+  // what any smaller call takes: cuts <= sms4 / units + 1, units > n_tokens / (2 tt)
+  // hkv and units >= max_blocks * 16 / 256 hkv.
+  const long long most = (long long)max_blocks * 16;
+  const long long rows1 = std::min(std::clamp<long long>(key_tiles, 1, kEmMaxCuts) * n_tokens, 2 * tt * (sms4 / hkv + 1) + n_tokens);
+  const long long keys2 = std::min(std::clamp<long long>(row_tiles, 1, kEmMaxCuts) * most, 256 * (sms4 / hkv + 1) + most);
+  l.parts = take((size_t)2 * rows1 * hq * 8);
   l.nlse = take((size_t)n_tokens * hq * 4);
-  l.sums = take((size_t)2 * (l.few ? (size_t)(row_tiles + n_seq) : (size_t)l.cuts2 * n_seq) * hkv * max_blocks * 16 * 4);
+  l.sums = take((size_t)2 * std::max(n_seq * keys2, (std::min<long long>(row_tiles, n_seq) + n_seq) * most) * hkv * 4);
   l.total = o;
   return l;
 }

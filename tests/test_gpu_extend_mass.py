@@ -157,6 +157,23 @@ def test_captured_and_replayed():
     check(s, mass, True)
 
 
+@pytest.mark.parametrize("hkv, hq", [(32, 32), (8, 40), (2, 16), (1, 12), (8, 8)])
+def test_a_larger_step_needs_no_less_workspace(hkv, hq):
+    slab = [torch.zeros(2, hkv, 16, 64, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    p = K.kvs_pool_create(1, hkv, 64, 16, K.KVS_DTYPE_BF16, 2, 4096, [slab[0]], [slab[1]])
+    tokens, seqs, blocks = [0, 1, 2, 15, 33, 100, 255, 257, 1000, 4096, 8192, 30000, 200000], [1, 2, 3, 32, 33, 600, 4096], [1, 8, 9, 96, 500, 4096]
+    size = np.array([[[K.kvs_extend_mass_workspace_size(p, t, n, b, hq) for b in blocks] for n in seqs] for t in tokens])
+    for axis in range(3):
+        assert (np.diff(size, axis=axis) >= 0).all(), "tokens sequences blocks".split()[axis]
+
+
+def test_one_workspace_for_every_step():
+    big = chunk([2500, 300, 40], [1500, 300, 40], 8, 2, 64, seed=1)
+    ws = workspace(K.kvs_extend_mass_workspace_size(big["pool"], big["T"], 3, big["mb"], 8)).fill_(0xC3)
+    for s in (big, chunk([2400, 290, 30], [20, 7, 1], 8, 2, 64, seed=2), chunk([2300], [200], 8, 2, 64, seed=3), chunk([17], [1], 8, 2, 64, seed=4)):
+        check(s, call(s, True, ws=ws), True)
+
+
 def test_bad_blocks_lengths_and_offsets():
     s = chunk([300, 200], [300, 9], 8, 2, 64)
     s["table"][0, 1] = s["cap"]
