@@ -159,6 +159,27 @@ def test_microscaled_scales_of_every_size():
         check(s, *call(s))
 
 
+def test_microscaled_smallest_scales():
+    """Byte 0 is 2^-127, not 0: keys of that size count where the scale brings them up."""
+    s = make("mx4", [200, 64, 515], 8, 2, 128, seed=5, scales=(0, 3))
+    s["scale"] = 0.05 * 2.0 ** 125
+    out, mass = call(s)
+    check(s, out, mass)
+    zero = [x.clone() for x in s["ksc"]]
+    for x in s["ksc"]:
+        x[x < 255] = 0
+    s["values"][0] = s["values"][0] * np.repeat(np.exp2(-np.where(zero[0].cpu().numpy() < 255, zero[0].cpu().numpy(), 0).astype(np.float64)), 32, -1)
+    check(s, *call(s))
+
+
+def test_workspaces_for_a_step_serve_smaller_ones():
+    s = make("mx4", [64], 8, 2, 128)
+    many = K.kvs_pool_create(1, 2, 128, 64, K.KVS_DTYPE_MX4, s["cap"], 4096, s["k"], s["v"], s["ksc"], s["vsc"])
+    for op in (K.KVS_OP_DECODE_MASS, K.KVS_OP_COMPACT):
+        size = np.array([[K.kvs_workspace_size(many, op, n, b, 8) for b in (1, 2, 30, 500, 4096)] for n in (1, 2, 33, 600, 4096)])
+        assert (np.diff(size, axis=0) >= 0).all() and (np.diff(size, axis=1) >= 0).all()
+
+
 def test_scores_far_apart():
     """A maximum that keeps moving, and weights below every other's rounding."""
     for kind in ("bf16", "mx4"):
