@@ -63,6 +63,7 @@ struct EmParams {
   float* sums;        // pass 2: [cut][column half][hkv][n_seq][most], few rows: [row tile][column half][hkv][most]
   int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2, sms, few;   // cuts: the most there is room for; few: em_keys_kernel is pass 2
   float scale_log2;
+  int* tickets;       // calls without a plan: the claims of pass 1, zero between calls
 };
 
 // Cuts of every unit's Y tiles (1 to `most`, a lane each).  Items of about one
@@ -86,11 +87,37 @@ __device__ __forceinline__ int em_cuts(float units, float tiles, float longest, 
   return best + 1;
 }
 
+// What a sequence brings.
+struct EmCount {
+  int t0, rows, keys, units1, units2, longest1, longest2, bad;
+  unsigned long long tiles1, tiles2;   // twice the Y tiles of all units
+};
+__device__ __forceinline__ EmCount em_count(const EmParams& p, int a) {
+  const int tt = kEmTile / p.g, tu = 2 * tt;
+  const int t0 = __ldg(p.tok_off + a), t1 = __ldg(p.tok_off + a + 1), raw = __ldg(p.seq_len + a);
+  if (raw < 0 || raw > p.most) set_err(p.status, KVS_DEVERR_SEQ_LEN);
+  EmCount c{};
+  c.bad = t0 < 0 || t1 < t0 || t1 > p.n_tokens;
+  c.t0 = t0;
+  c.rows = t1 - t0;
+  c.keys = min(max(raw, 0), p.most);
+  if (c.bad || c.rows == 0) return c;
+  const int k = (c.keys + kEmTile - 1) / kEmTile, t = (c.rows - 1) / tt + 1;   // key tiles, row tiles
+  c.units1 = (c.rows - 1) / tu + 1;
+  c.units2 = p.few ? t : (c.keys + 2 * kEmTile - 1) / (2 * kEmTile);
+  // causal: the new tokens' share of either range is half full on the mean
+  c.tiles1 = (unsigned long long)c.units1 * (2 * k - (p.causal ? min(k, c.rows / kEmTile) : 0));
+  c.tiles2 = p.few ? (unsigned long long)c.units2 * (2 * k) : (unsigned long long)t * (2 * c.units2 - (p.causal ? min(c.units2, c.rows / (2 * kEmTile)) : 0));
+  c.longest1 = k;
+  c.longest2 = p.few ? k : t;
+  return c;
+}
+
 __global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ EmParams p) {
   __shared__ int warp_sums[32];
-  __shared__ unsigned long long s_tiles[2];   // twice the Y tiles of all units
+  __shared__ unsigned long long s_tiles[2];
   __shared__ int s_longest[2];
-  const int tid = threadIdx.x, tt = kEmTile / p.g, tu = 2 * tt;
+  const int tid = threadIdx.x;
   if (tid < 2) {
     s_tiles[tid] = 0;
     s_longest[tid] = 0;
@@ -101,28 +128,21 @@ __global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ E
   int longest1 = 0, longest2 = 0;
   for (int a0 = 0; a0 < p.n_seq; a0 += 1024) {
     const int a = a0 + tid;
-    int u1 = 0, u2 = 0;
+    EmCount c{};
     if (a < p.n_seq) {
-      const int t0 = __ldg(p.tok_off + a), t1 = __ldg(p.tok_off + a + 1), raw = __ldg(p.seq_len + a);
-      bad |= t0 < 0 || t1 < t0 || t1 > p.n_tokens;
-      if (raw < 0 || raw > p.most) set_err(p.status, KVS_DEVERR_SEQ_LEN);
-      const int keys = min(max(raw, 0), p.most), rows = t1 - t0;
-      p.seq[a] = make_int4(t0, rows, keys, 0);
-      u1 = rows > 0 ? (rows - 1) / tu + 1 : 0;
-      u2 = rows <= 0 ? 0 : p.few ? (rows - 1) / tt + 1 : (keys + 2 * kEmTile - 1) / (2 * kEmTile);
-      if (rows > 0) {   // causal: the new tokens' share of either range is half full on the mean
-        const int t1 = (keys + kEmTile - 1) / kEmTile, t2 = (rows - 1) / tt + 1;
-        tiles1 += (unsigned long long)u1 * (2 * t1 - (p.causal ? min(t1, rows / kEmTile) : 0));
-        tiles2 += p.few ? (unsigned long long)u2 * (2 * t1) : (unsigned long long)t2 * (2 * u2 - (p.causal ? min(u2, rows / (2 * kEmTile)) : 0));
-        longest1 = max(longest1, t1);
-        longest2 = max(longest2, p.few ? t1 : t2);
-      }
+      c = em_count(p, a);
+      p.seq[a] = make_int4(c.t0, c.rows, c.keys, 0);
     }
+    bad |= c.bad;
+    tiles1 += c.tiles1;
+    tiles2 += c.tiles2;
+    longest1 = max(longest1, c.longest1);
+    longest2 = max(longest2, c.longest2);
     int total;
-    const int b1 = block_exclusive_scan(u1, warp_sums, total);
+    const int b1 = block_exclusive_scan(c.units1, warp_sums, total);
     if (a < p.n_seq) p.off1[a] = n1 + b1;
     n1 += total;
-    const int b2 = block_exclusive_scan(u2, warp_sums, total);
+    const int b2 = block_exclusive_scan(c.units2, warp_sums, total);
     if (a < p.n_seq) p.off2[a] = n2 + b2;
     n2 += total;
   }
@@ -182,6 +202,46 @@ __device__ __forceinline__ int em_find(const int* off, int n, int v, int lane) {
   }
   const bool le = lane < n && __ldg(off + lo + lane + 1) <= v;
   return lo + __popc(__ballot_sync(0xffffffffu, le));
+}
+
+// Whole warp, at most 32 sequences: what the plan kernel finds.  Returns the cuts of
+// pass 1; the first CTA leaves what the kernels behind it need.
+__device__ __forceinline__ int em_count_all(const EmParams& p, int lane, EmCount& c, int& end, int& units) {
+  constexpr unsigned kAll = 0xffffffffu;
+  c = EmCount{};
+  if (lane < p.n_seq) c = em_count(p, lane);
+  const bool bad = __any_sync(kAll, c.bad);
+  end = c.units1;
+  int end2 = c.units2;
+  float tiles1 = (float)c.tiles1, tiles2 = (float)c.tiles2;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(kAll, end, o), y = __shfl_up_sync(kAll, end2, o);
+    end += lane >= o ? x : 0;
+    end2 += lane >= o ? y : 0;
+    tiles1 += __shfl_xor_sync(kAll, tiles1, o);
+    tiles2 += __shfl_xor_sync(kAll, tiles2, o);
+  }
+  const int n1 = __shfl_sync(kAll, end, 31), n2 = __shfl_sync(kAll, end2, 31);
+  const float h = (float)p.hkv, sms = (float)p.sms;
+  const int cuts1 = em_cuts((float)n1 * h, 0.5f * tiles1 * h, (float)__reduce_max_sync(kAll, c.longest1), p.cuts1, sms, lane);
+  if (blockIdx.x == 0) {
+    const int cuts2 = em_cuts((float)n2 * h, 0.5f * tiles2 * h, (float)__reduce_max_sync(kAll, c.longest2), p.cuts2, sms, lane);
+    if (lane < p.n_seq) {
+      p.seq[lane] = make_int4(c.t0, c.rows, c.keys, 0);
+      p.off2[lane] = end2 - c.units2;
+    }
+    if (lane == 0) {
+      if (bad) set_err(p.status, KVS_DEVERR_JOB);
+      p.off2[p.n_seq] = bad ? 0 : n2;
+      p.hdr[kMCuts1] = cuts1;
+      p.hdr[kMCuts2] = cuts2;
+      p.hdr[kMClaim2] = 0;
+      p.hdr[kMBad] = bad;
+    }
+  }
+  units = bad ? 0 : n1;
+  return cuts1;
 }
 
 // Blocks of key tiles j .. j + 3 of sequence a, eight lanes a tile; -1 where there is none.
@@ -269,9 +329,8 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   auto sX = [&](int x) { return base + kTile * x; };
   auto ring = [&](int i) { return base + kTile * (2 + i); };
-  // rows of a query tile behind its last whole token are never copied to
-  for (int i = threadIdx.x; i < (2 + ST) * kTile / 16; i += kEmThreads) reinterpret_cast<uint4*>(base)[i] = make_uint4(0u, 0u, 0u, 0u);
-  fence_proxy_async_smem();
+  // Rows of a query tile behind its last whole token are never copied to; what they
+  // hold stays in their own rows (pass 1) or columns (pass 2, masked) of S.
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -292,10 +351,9 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
   if (warp >= kEmSumWarps) {
     if (warp == kEmTma) {
       // --------------------------------------------- claims and TMA copies
+      const bool own = PASS == 1 && p.tickets;   // no plan: this warp counts for itself, a lane a sequence
       const int* off = PASS == 1 ? p.off1 : p.off2;
-      const int cuts = __ldg(p.hdr + (PASS == 1 ? kMCuts1 : kMCuts2));
-      const long long claims = (long long)__ldg(off + p.n_seq) * p.hkv * cuts;
-      int* counter = p.hdr + (PASS == 1 ? kMClaim1 : kMClaim2);
+      int* counter = own ? p.tickets : p.hdr + (PASS == 1 ? kMClaim1 : kMClaim2);
       int n = 0, nx = 0, ni = 0, armed = -1;
       bool ok = true;
       auto claim_next = [&]() {
@@ -303,11 +361,20 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         if (lane == 0) c = atomicAdd(counter, 1);
         return (long long)(unsigned)__shfl_sync(0xffffffffu, c, 0);
       };
+      long long claim = claim_next();
+      EmCount mine{};
+      int cuts, units, end = 0;                  // end: units up to this lane's sequence, its own among them
+      if (own) {
+        cuts = em_count_all(p, lane, mine, end, units);
+      } else {
+        cuts = __ldg(p.hdr + (PASS == 1 ? kMCuts1 : kMCuts2));
+        units = __ldg(off + p.n_seq);
+      }
+      const long long claims = (long long)units * p.hkv * cuts;
       auto copy_rows = [&](uint8_t* dst, int tok, int head, uint64_t* bar) {  // one lane
         for (int hf = 0; hf < HF; ++hf) tma_load_5d(dst + hf * kHalf, &tq, 0, 0, tok, head, hf, bar);
       };
       const uint32_t row_bytes = (uint32_t)(HF * tt * p.g * 128);
-      long long claim = claim_next();
       while (true) {
         if (stop()) { ok = false; break; }
         const int slot = ni & 1;
@@ -320,18 +387,29 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
           it.cut = (int)(claim - u * cuts);
           const int unit = (int)(u / p.hkv);
           it.head = (int)(u - (long long)unit * p.hkv);
-          it.seq = em_find(off, p.n_seq, unit, lane);
-          const int4 s = __ldg(p.seq + it.seq);
-          const int first = __ldg(off + it.seq), count = __ldg(off + it.seq + 1) - first;
-          it.t0 = s.x;
-          it.rows = s.y;
-          it.keys = s.z;
-          const int before = s.z - s.y;   // row j sees keys up to before + j (causal)
+          int first, count;
+          if (own) {
+            it.seq = __popc(__ballot_sync(0xffffffffu, lane < p.n_seq && end <= unit));
+            it.t0 = __shfl_sync(0xffffffffu, mine.t0, it.seq);
+            it.rows = __shfl_sync(0xffffffffu, mine.rows, it.seq);
+            it.keys = __shfl_sync(0xffffffffu, mine.keys, it.seq);
+            count = __shfl_sync(0xffffffffu, mine.units1, it.seq);
+            first = __shfl_sync(0xffffffffu, end, it.seq) - count;
+          } else {
+            it.seq = em_find(off, p.n_seq, unit, lane);
+            const int4 s = __ldg(p.seq + it.seq);
+            it.t0 = s.x;
+            it.rows = s.y;
+            it.keys = s.z;
+            first = __ldg(off + it.seq);
+            count = __ldg(off + it.seq + 1) - first;
+          }
+          const int before = it.keys - it.rows;   // row j sees keys up to before + j (causal)
           if constexpr (PASS == 1) {
             it.x0 = (count - 1 - (unit - first)) * 2 * tt;   // the last rows, which see most, first
             for (int x = 0; x < 2; ++x) {
               const int j0 = it.x0 + x * tt, j1 = min(it.rows, j0 + tt);
-              const int lim = p.causal ? min(max(before + j1, 0), s.z) : s.z;
+              const int lim = p.causal ? min(max(before + j1, 0), it.keys) : it.keys;
               nt_x[x] = j0 < it.rows ? (lim + kEmTile - 1) / kEmTile : 0;
             }
             const int nt = max(nt_x[0], nt_x[1]);
@@ -407,6 +485,11 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         // copies in flight land before the shared memory goes away
         for (int m = max(0, armed - ST + 1); m <= armed; ++m) mbar_drain(&bars.full[m % ST], (m / ST) & 1);
         if (nx) mbar_drain(&bars.x_full, (nx - 1) & 1);
+      }
+      if (own) {
+        // every CTA claims once in vain; who does so last leaves the counter at zero
+        while (claim < claims) claim = claim_next();
+        if (lane == 0 && claim == claims + gridDim.x - 1) *reinterpret_cast<volatile int*>(p.tickets) = 0;
       }
     } else if (warp < kEmTma) {
       // ------------------------------------------- products of one X tile
@@ -750,9 +833,6 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
   }
   uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
   auto ring = [&](int i) { return base + kTile * (2 + i); };
-  // rows of a query tile behind its last whole token are never copied to
-  for (int i = threadIdx.x; i < 2 * kTile / 16; i += kEmThreads) reinterpret_cast<uint4*>(base)[i] = make_uint4(0u, 0u, 0u, 0u);
-  fence_proxy_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -773,15 +853,15 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     bool ok = true;
     if (warp == kEmTma) {
       // ----------------------------------- claims, rows, half of every key tile
-      const int cuts = __ldg(p.hdr + kMCuts2);
-      const long long claims = (long long)__ldg(p.off2 + p.n_seq) * p.hkv * cuts;
       auto claim_next = [&]() {
         int c = 0;
         if (lane == 0) c = atomicAdd(p.hdr + kMClaim2, 1);
         return (long long)(unsigned)__shfl_sync(0xffffffffu, c, 0);
       };
-      int n = 0, nx = 0, armed = -1;
       long long claim = claim_next();
+      const int cuts = __ldg(p.hdr + kMCuts2);
+      const long long claims = (long long)__ldg(p.off2 + p.n_seq) * p.hkv * cuts;
+      int n = 0, nx = 0, armed = -1;
       for (int ni = 0;; ++ni) {
         if (stop()) { ok = false; break; }
         const int slot = ni & 1;
@@ -1026,15 +1106,21 @@ __global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ Em
   if (i >= rows || t < p.tok_off[0] || t >= p.tok_off[p.n_seq]) return;   // rows of no sequence have no parts
   const int n = 2 * p.hdr[kMCuts1];
   float m = -INFINITY, l = 0.f;
-#pragma unroll 8
-  for (int k = 0; k < n; ++k) {
-    const float2 v = p.parts[k * rows + i];
-    if (v.y > 0.f) m = fmaxf(m, v.x);
-  }
-#pragma unroll 8
-  for (int k = 0; k < n; ++k) {
-    const float2 v = p.parts[k * rows + i];
-    if (v.y > 0.f) l += v.y * fast_exp2(v.x - m);
+  for (int k0 = 0; k0 < n; k0 += 8) {   // eight loads under way
+    float2 v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = k0 + k < n ? p.parts[(k0 + k) * rows + i] : make_float2(0.f, 0.f);
+    float top = m;
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (v[k].y > 0.f) top = fmaxf(top, v[k].x);
+    if (top > m) {
+      l *= fast_exp2(m - top);
+      m = top;
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (v[k].y > 0.f) l += v[k].y * fast_exp2(v[k].x - m);
   }
   p.nlse[((size_t)(h / p.g) * p.n_tokens + t) * p.g + h % p.g] = l > 0.f ? -(m + log2f(l)) : -INFINITY;
 }
@@ -1219,8 +1305,14 @@ extern "C" kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void*
   CUtensorMap tq{};
   if (n_tokens > 0 && !ex_query_map(&tq, q_dev, n_tokens, p.g, p.hkv, d.head_dim, q_stride))
     return fail(KVS_ERR_CUDA, "extend_mass: cuTensorMapEncodeTiled failed for q");
-  if (launch_pdl(em_plan_kernel, dim3(1), dim3(1024), stream, p) != cudaSuccess) return check_launch("extend_mass");
-  count_launch();
+  // a warp of pass 1 counts up to 32 sequences for itself (1 row after 1,000 tokens
+  // 19.0 us with a plan, 17.1 without; 16 x 4 after 1,000, 40 / 8 heads: 31.9, 27.3)
+  if (n_seq <= 32 && n_tokens > 0) {
+    p.tickets = pool->tickets;
+  } else {
+    if (launch_pdl(em_plan_kernel, dim3(1), dim3(1024), stream, p) != cudaSuccess) return check_launch("extend_mass");
+    count_launch();
+  }
   return d.head_dim == 128 ? em_run<128>(pool, layer, p, tq, mass_in_dev, carry, mass_dev, stream)
                            : em_run<64>(pool, layer, p, tq, mass_in_dev, carry, mass_dev, stream);
 }
