@@ -37,7 +37,6 @@
 
 #include "common.cuh"
 #include "internal.h"
-#include "merge.cuh"
 
 namespace kvs {
 
@@ -45,7 +44,7 @@ namespace {
 
 enum { kFmtBf16x64, kFmtBf16x128, kFmtMx };
 
-constexpr int kDmMaxGroup = 16, kDmMaxStages = 6, kDmMaxCtas = 3;
+constexpr int kDmMaxGroup = 16, kDmMaxStages = 6, kDmMaxCtas = 3, kDmJoin = 8;
 
 template <int FMT, int NT>
 struct Dm {   // what a format and the number of 8-column tiles fix
@@ -76,9 +75,13 @@ template <int W>
 struct DmShared {
   uint64_t full[W][kDmMaxStages];
   float2 ml[W][kDmMaxGroup];
-  float m[kDmMaxGroup], l[kDmMaxGroup];
   int warp_sums[32];
-  int a, b, last;
+  int a, b, cuts;
+  long long per, u0;            // places of a CTA on the line, this CTA's first
+  struct Cut {                  // a pair that other CTAs share: this CTA's first and last
+    int seq, head, parts, last;
+    size_t slot;                // of its first part
+  } cut[2];
 };
 
 struct DmParams {
@@ -154,55 +157,123 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
   if (tid == 0) {
     prefetch_tmap(&tk);
     prefetch_tmap(&tv);
+    sh.cuts = 0;
   }
   if (lane == 0) {
     for (int s = 0; s < ST; ++s) mbar_init(&sh.full[warp][s], 1);
     fence_barrier_init();
   }
+  __syncwarp();
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  auto empty_sequences = [&]() {
+    for (int a = blockIdx.x; a < p.n_seq; a += gridDim.x) {
+      const int raw = p.seq_len[a];
+      if (tid == 0 && (raw < 0 || raw > p.most)) set_err(p.status, KVS_DEVERR_SEQ_LEN);
+      if (raw <= 0)
+        for (int i = tid; i < p.hq * D; i += T) p.out[(size_t)a * p.hq * D + i] = 0.f;
+    }
+  };
+
   // ---- this CTA's stretch of the line
-  int per_head = 0, mine = 0, mine_before = 0;   // of the sequences tid, tid + T, ...: the first one's units, and those before it
-  for (int a0 = 0; a0 < p.n_seq; a0 += T) {
-    const int a = a0 + tid;
-    const int n = a < p.n_seq ? dm_span<UT>(p, a).units : 0;
-    int total;
-    const int before = block_exclusive_scan(n, sh.warp_sums, total);
-    if (a0 == 0) {
-      mine = n;
-      mine_before = before;
+  long long per, u0;
+  int n_mine;   // units of this CTA
+  DmAt seg;
+  // units of a CTA: an even share, but no more parts of a pair than are worth their
+  // joining (a sequence of 32,000 tokens, eight heads on one KV head: 45 us evenly,
+  // 23 with fewer CTAs; in 4 bits 39 and 26)
+  auto share = [&](int total) {
+    const int least = (int)sqrtf((F::mx ? 0.03f : 0.06f) * (float)p.g * (float)total / (float)p.n_seq);
+    return max((long long)max(W, least), ((long long)total * p.hkv + gridDim.x - 1) / gridDim.x);
+  };
+  if (p.n_seq <= 32) {
+    // every warp for itself, a lane a sequence
+    const int real = lane < p.n_seq ? dm_span<UT>(p, lane).units : 0;
+    per = share(__reduce_add_sync(0xffffffffu, real));
+    // Where they fit, every pair begins a CTA (its units are rounded up to whole
+    // CTAs): a second pair costs a CTA more than a unit or two of every warp (four
+    // sequences of 300 tokens, 8 / 2 heads of 64 channels, with the masses: 8.4 us,
+    // 10.1 evenly).
+    const int whole = (int)((per + W - 1) / W) * W;
+    int n = real;
+    bool rounded = false;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int m = whole + k * W, up = (real + m - 1) / m;
+      if ((long long)__reduce_add_sync(0xffffffffu, up) * p.hkv <= gridDim.x) {
+        n = up * m;
+        per = m;
+        rounded = true;
+        break;
+      }
     }
-    per_head += total;
-  }
-  for (int a = blockIdx.x; a < p.n_seq; a += gridDim.x) {
-    const int raw = p.seq_len[a];
-    if (tid == 0 && (raw < 0 || raw > p.most)) set_err(p.status, KVS_DEVERR_SEQ_LEN);
-    if (raw <= 0)
-      for (int i = tid; i < p.hq * D; i += T) p.out[(size_t)a * p.hq * D + i] = 0.f;
-  }
-  const long long units = (long long)per_head * p.hkv;
-  const long long per = max((long long)W, (units + gridDim.x - 1) / gridDim.x);
-  const long long u0 = per * blockIdx.x, u1 = min(units, u0 + per);
-  if (u0 >= u1) return;
-  const int h0 = (int)(u0 / per_head), r0 = (int)(u0 - (long long)h0 * per_head);
-  if (mine_before <= r0 && r0 < mine_before + mine) {
-    sh.a = tid;
-    sh.b = r0 - mine_before;
-  }
-  int carry = 0;
-  for (int a0 = 0; p.n_seq > T && a0 < p.n_seq; a0 += T) {   // more sequences than threads: once more
-    const int a = a0 + tid, n = a < p.n_seq ? dm_span<UT>(p, a).units : 0;
-    int total;
-    const int before = carry + block_exclusive_scan(n, sh.warp_sums, total);
-    if (before <= r0 && r0 < before + n) {
-      sh.a = a;
-      sh.b = r0 - before;
+    int end = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, end, o);
+      end += lane >= o ? x : 0;
     }
-    carry += total;
+    const int per_head = __shfl_sync(0xffffffffu, end, 31);
+    u0 = per * blockIdx.x;
+    const long long u1 = min((long long)per_head * p.hkv, u0 + per);
+    if (u0 >= u1) {
+      empty_sequences();
+      return;
+    }
+    seg.h = (int)(u0 / per_head);
+    const int r0 = (int)(u0 - (long long)seg.h * per_head);
+    seg.a = __popc(__ballot_sync(0xffffffffu, lane < p.n_seq && end <= r0));
+    seg.b = r0 - __shfl_sync(0xffffffffu, end - n, seg.a);
+    seg.units = __shfl_sync(0xffffffffu, real, seg.a);
+    n_mine = rounded ? min((int)per, seg.units - seg.b) : (int)(u1 - u0);
+  } else {
+    int per_head = 0, mine = 0, mine_before = 0;   // of the sequences tid, tid + T, ...: the first one's units, and those before it
+    for (int a0 = 0; a0 < p.n_seq; a0 += T) {
+      const int a = a0 + tid;
+      const int n = a < p.n_seq ? dm_span<UT>(p, a).units : 0;
+      int total;
+      const int before = block_exclusive_scan(n, sh.warp_sums, total);
+      if (a0 == 0) {
+        mine = n;
+        mine_before = before;
+      }
+      per_head += total;
+    }
+    per = share(per_head);
+    u0 = per * blockIdx.x;
+    const long long u1 = min((long long)per_head * p.hkv, u0 + per);
+    if (u0 >= u1) {
+      empty_sequences();
+      return;
+    }
+    seg.h = (int)(u0 / per_head);
+    const int r0 = (int)(u0 - (long long)seg.h * per_head);
+    if (mine_before <= r0 && r0 < mine_before + mine) {
+      sh.a = tid;
+      sh.b = r0 - mine_before;
+    }
+    int carry = 0;
+    for (int a0 = 0; p.n_seq > T && a0 < p.n_seq; a0 += T) {   // more sequences than threads: once more
+      const int a = a0 + tid, n = a < p.n_seq ? dm_span<UT>(p, a).units : 0;
+      int total;
+      const int before = carry + block_exclusive_scan(n, sh.warp_sums, total);
+      if (before <= r0 && r0 < before + n) {
+        sh.a = a;
+        sh.b = r0 - before;
+      }
+      carry += total;
+    }
+    __syncthreads();
+    seg.a = sh.a;
+    seg.b = sh.b;
+    seg.units = dm_span<UT>(p, sh.a).units;
+    n_mine = (int)(u1 - u0);
   }
-  __syncthreads();
-  const int n_mine = (int)(u1 - u0);
-  DmAt seg{h0, sh.a, sh.b, dm_span<UT>(p, sh.a).units};
+
+  if (tid == 0) {
+    sh.per = per;
+    sh.u0 = u0;
+  }
 
   // ---- copies of this warp's units k = warp, warp + W, ...
   DmAt ahead = seg;
@@ -246,11 +317,13 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     id_ahead = look_up();
   };
   for (int i = 0; i < ST; ++i) issue();
+  empty_sequences();
 
   int k = warp;                    // this warp's next unit, relative to u0
   int stage = 0, uses = 0;
   uint32_t phase = 0;
   bool dead = false;
+  int got0 = 0, got1 = 0;   // thread 0: arrivals
   for (int done = 0; done < n_mine;) {
     // ---- one (sequence, KV head): units [seg.b, seg.units) as far as the stretch goes
     const int n_seg = min(seg.units - seg.b, n_mine - done);
@@ -602,8 +675,8 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
         }
       }
     __syncthreads();
-    const long long first = u0 + done - seg.b;    // the pair's first unit on the line
-    const int cta0 = (int)(first / per), n_parts = (int)((first + seg.units - 1) / per) - cta0 + 1;
+    const long long first = sh.u0 + done - seg.b;    // the pair's first unit on the line
+    const int cta0 = (int)(first / sh.per), n_parts = (int)((first + seg.units - 1) / sh.per) - cta0 + 1;
     const int order = seg.h * p.n_seq + seg.a, pair = seg.a * p.hkv + seg.h;
     const size_t slot = (size_t)blockIdx.x + order;
     for (int i = tid; i < p.g * (D / 4); i += T) {
@@ -631,48 +704,105 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
         if (col == 0) __stcg(reinterpret_cast<float2*>(p.part_ml + (slot * p.g + row) * 2), make_float2(M, L));
       }
     }
-    if (n_parts > 1 && arrive_last(p.tickets + pair, n_parts, &sh.last)) {
-      // the last CTA of the pair joins the parts in their order
-      const size_t s0 = (size_t)cta0 + order;
-      for (int row = warp; row < p.g; row += W) {
-        float M = -INFINITY, L = 0.f;
-        for (int s = lane; s < n_parts; s += 32) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((s0 + s) * p.g + row) * 2));
-          if (ml.y > 0.f) M = fmaxf(M, ml.x);
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-        for (int s = lane; s < n_parts; s += 32) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((s0 + s) * p.g + row) * 2));
-          L += ml.y > 0.f ? fast_exp2(ml.x - M) * ml.y : 0.f;
-        }
-#pragma unroll
-        for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        if (lane == 0) {
-          sh.m[row] = M;
-          sh.l[row] = L > 0.f ? 1.f / L : 0.f;
-          if (p.scores) p.fin[(size_t)pair * p.g + row] = make_float2(L > 0.f ? M : 0.f, sh.l[row]);
-        }
-      }
-      __syncthreads();
-      for (int i = tid; i < p.g * (D / 4); i += T) {
-        const int row = i / (D / 4), col = (i - row * (D / 4)) * 4;
-        const float M = sh.m[row], inv = sh.l[row];
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-        for (int s = 0; s < n_parts; ++s) {
-          const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + ((s0 + s) * p.g + row) * 2));
-          const float4 x = __ldcg(reinterpret_cast<const float4*>(p.part + ((s0 + s) * p.g + row) * D + col));
-          const float f = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
-          o.x += f * x.x; o.y += f * x.y; o.z += f * x.z; o.w += f * x.w;
-        }
-        *reinterpret_cast<float4*>(p.out + ((size_t)seg.a * p.hq + seg.h * p.g + row) * D + col) =
-            make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
-      }
-    }
+    if (n_parts > 1) __threadfence();
     __syncthreads();   // the states are read: the next pair's may be written
+    if (n_parts > 1 && tid == 0) {
+      // the parts are there; whether they were the last ones is looked at when
+      // this CTA has nothing else to do
+      sh.cut[sh.cuts] = {seg.a, seg.h, n_parts, 0, (size_t)cta0 + order};
+      if (sh.cuts++ == 0) got0 = atomicAdd(p.tickets + pair, 1);
+      else got1 = atomicAdd(p.tickets + pair, 1);
+    }
     done += n_seg;
     if (done < n_mine) dm_advance<UT>(p, seg, n_seg);
+  }
+  // Only a stretch's first and last pair can have parts of other CTAs; the last CTA
+  // of a pair joins its parts in their order.
+  if (tid == 0)
+    for (int k = 0; k < sh.cuts; ++k) {
+      const bool last = (k ? got1 : got0) == sh.cut[k].parts - 1;
+      if (last) p.tickets[(size_t)sh.cut[k].seq * p.hkv + sh.cut[k].head] = 0;
+      sh.cut[k].last = last;
+    }
+  __syncthreads();
+  const int cuts = sh.cuts;
+  if (cuts > 0) {
+    for (int k = 0; k < cuts; ++k) {
+      const auto cut = sh.cut[k];
+      if (!cut.last) continue;
+      __threadfence();
+      // four channels of a row a thread; where these are fewer than the threads,
+      // several groups of them share the parts
+      struct State {
+        float M, L;
+        float4 o;
+        __device__ void add(const float2* m, const float4* x) {   // kDmJoin states
+          float top = M;
+#pragma unroll
+          for (int u = 0; u < kDmJoin; ++u)
+            if (m[u].y > 0.f) top = fmaxf(top, m[u].x);
+          const float f = top > M ? fast_exp2(M - top) : 1.f;
+          M = top;
+          L *= f;
+          o.x *= f; o.y *= f; o.z *= f; o.w *= f;
+#pragma unroll
+          for (int u = 0; u < kDmJoin; ++u) {
+            const float w = m[u].y > 0.f ? fast_exp2(m[u].x - M) : 0.f;
+            L += w * m[u].y;
+            o.x += w * x[u].x; o.y += w * x[u].y; o.z += w * x[u].z; o.w += w * x[u].w;
+          }
+        }
+      };
+      const int items = p.g * (D / 4), groups = min(kDmJoin, max(1, T / items)), group = tid / items;
+      float2 m[kDmJoin];
+      float4 x[kDmJoin];
+      auto join = [&](int i, int first) {   // parts first, first + groups, ...; kDmJoin of them under way
+        const float2* ml = reinterpret_cast<const float2*>(p.part_ml) + cut.slot * p.g + i / (D / 4);
+        const float4* part = reinterpret_cast<const float4*>(p.part + cut.slot * p.g * D) + i;
+        State st{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        for (int s0 = first; s0 < cut.parts; s0 += kDmJoin * groups) {
+#pragma unroll
+          for (int u = 0; u < kDmJoin; ++u) {
+            const int s = s0 + u * groups, at = min(s, cut.parts - 1);
+            m[u] = __ldcg(ml + (size_t)at * p.g);
+            x[u] = __ldcg(part + (size_t)at * items);
+            if (s >= cut.parts) m[u].y = 0.f;
+          }
+          st.add(m, x);
+        }
+        return st;
+      };
+      auto finish = [&](int i, const State& st) {
+        const float inv = st.L > 0.f ? 1.f / st.L : 0.f;
+        reinterpret_cast<float4*>(p.out + ((size_t)cut.seq * p.hq + cut.head * p.g) * D)[i] =
+            make_float4(st.o.x * inv, st.o.y * inv, st.o.z * inv, st.o.w * inv);
+        if (i % (D / 4) == 0 && p.scores)
+          p.fin[((size_t)cut.seq * p.hkv + cut.head) * p.g + i / (D / 4)] = make_float2(st.L > 0.f ? st.M : 0.f, inv);
+      };
+      if (groups == 1) {
+        for (int i = tid; i < items; i += T) finish(i, join(i, 0));
+        continue;
+      }
+      float4* s_o = reinterpret_cast<float4*>(s_acc);
+      float2* s_ml = reinterpret_cast<float2*>(s_acc + T * 4);
+      if (group < groups) {
+        const State st = join(tid - group * items, group);
+        s_o[tid] = st.o;
+        s_ml[tid] = make_float2(st.M, st.L);
+      }
+      __syncthreads();
+      if (group == 0) {
+        State st{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll
+        for (int u = 0; u < kDmJoin; ++u) {
+          m[u] = u < groups ? s_ml[u * items + tid] : make_float2(0.f, 0.f);
+          x[u] = u < groups ? s_o[u * items + tid] : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        st.add(m, x);
+        finish(tid, st);
+      }
+      __syncthreads();   // s_acc may be written again
+    }
   }
   // Only now may the next kernel's CTAs come: sooner, they would crowd where this
   // grid's first CTAs end (eight sequences of 16,384 to 32,768 tokens in 4 bits: 85 us
