@@ -204,29 +204,35 @@ __device__ __forceinline__ int em_find(const int* off, int n, int v, int lane) {
   return lo + __popc(__ballot_sync(0xffffffffu, le));
 }
 
-// Whole warp, at most 32 sequences: what the plan kernel finds.  Returns the cuts of
-// pass 1; the first CTA leaves what the kernels behind it need.
-__device__ __forceinline__ int em_count_all(const EmParams& p, int lane, EmCount& c, int& end, int& units) {
+// At most 32 sequences, a lane each.
+struct EmLine {
+  int t0, rows, keys, units;   // of this lane's sequence
+  int end;                     // units up to it, its own among them
+  int all, cuts;
+};
+// Whole warp, pass 1: what the plan kernel finds otherwise; the first CTA leaves what
+// the kernels behind it need.
+__device__ __forceinline__ EmLine em_line1(const EmParams& p, int lane) {
   constexpr unsigned kAll = 0xffffffffu;
-  c = EmCount{};
+  EmCount c{};
   if (lane < p.n_seq) c = em_count(p, lane);
   const bool bad = __any_sync(kAll, c.bad);
-  end = c.units1;
-  int end2 = c.units2;
-  float tiles1 = (float)c.tiles1, tiles2 = (float)c.tiles2;
+  auto scan = [&](int end, float tiles, int longest, int most, int& last, int& cuts) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(kAll, end, o), y = __shfl_up_sync(kAll, end2, o);
-    end += lane >= o ? x : 0;
-    end2 += lane >= o ? y : 0;
-    tiles1 += __shfl_xor_sync(kAll, tiles1, o);
-    tiles2 += __shfl_xor_sync(kAll, tiles2, o);
-  }
-  const int n1 = __shfl_sync(kAll, end, 31), n2 = __shfl_sync(kAll, end2, 31);
-  const float h = (float)p.hkv, sms = (float)p.sms;
-  const int cuts1 = em_cuts((float)n1 * h, 0.5f * tiles1 * h, (float)__reduce_max_sync(kAll, c.longest1), p.cuts1, sms, lane);
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kAll, end, o);
+      end += lane >= o ? x : 0;
+      tiles += __shfl_xor_sync(kAll, tiles, o);
+    }
+    last = __shfl_sync(kAll, end, 31);
+    cuts = em_cuts((float)last * (float)p.hkv, 0.5f * tiles * (float)p.hkv, (float)__reduce_max_sync(kAll, longest), most, (float)p.sms, lane);
+    return end;
+  };
+  EmLine r{c.t0, c.rows, c.keys, c.units1, 0, 0, 0};
+  r.end = scan(c.units1, (float)c.tiles1, c.longest1, p.cuts1, r.all, r.cuts);
   if (blockIdx.x == 0) {
-    const int cuts2 = em_cuts((float)n2 * h, 0.5f * tiles2 * h, (float)__reduce_max_sync(kAll, c.longest2), p.cuts2, sms, lane);
+    int n2, cuts2;
+    const int end2 = scan(c.units2, (float)c.tiles2, c.longest2, p.cuts2, n2, cuts2);
     if (lane < p.n_seq) {
       p.seq[lane] = make_int4(c.t0, c.rows, c.keys, 0);
       p.off2[lane] = end2 - c.units2;
@@ -234,14 +240,56 @@ __device__ __forceinline__ int em_count_all(const EmParams& p, int lane, EmCount
     if (lane == 0) {
       if (bad) set_err(p.status, KVS_DEVERR_JOB);
       p.off2[p.n_seq] = bad ? 0 : n2;
-      p.hdr[kMCuts1] = cuts1;
+      p.hdr[kMCuts1] = r.cuts;
       p.hdr[kMCuts2] = cuts2;
       p.hdr[kMClaim2] = 0;
       p.hdr[kMBad] = bad;
     }
   }
-  units = bad ? 0 : n1;
-  return cuts1;
+  if (bad) r.all = 0;
+  return r;
+}
+// Pass 2: what that CTA or the plan kernel left.
+__device__ __forceinline__ EmLine em_line2(const EmParams& p, int lane) {
+  EmLine r{};
+  r.cuts = __ldg(p.hdr + kMCuts2);
+  r.all = __ldg(p.off2 + p.n_seq);
+  if (lane < p.n_seq) {
+    const int4 s = __ldg(p.seq + lane);
+    const int first = __ldg(p.off2 + lane);
+    r.t0 = s.x;
+    r.rows = s.y;
+    r.keys = s.z;
+    r.end = __ldg(p.off2 + lane + 1);
+    r.units = r.end - first;
+  }
+  return r;
+}
+
+// Whole warp: the sequence of a unit, with its rows and units.
+struct EmPlace {
+  int seq, t0, rows, keys, first, count;
+};
+__device__ __forceinline__ EmPlace em_place(const EmParams& p, const EmLine& line, const int* off, int unit, int lane) {
+  constexpr unsigned kAll = 0xffffffffu;
+  EmPlace r;
+  if (p.n_seq <= 32) {
+    r.seq = __popc(__ballot_sync(kAll, lane < p.n_seq && line.end <= unit));
+    r.t0 = __shfl_sync(kAll, line.t0, r.seq);
+    r.rows = __shfl_sync(kAll, line.rows, r.seq);
+    r.keys = __shfl_sync(kAll, line.keys, r.seq);
+    r.count = __shfl_sync(kAll, line.units, r.seq);
+    r.first = __shfl_sync(kAll, line.end, r.seq) - r.count;
+  } else {
+    r.seq = em_find(off, p.n_seq, unit, lane);
+    const int4 s = __ldg(p.seq + r.seq);
+    r.t0 = s.x;
+    r.rows = s.y;
+    r.keys = s.z;
+    r.first = __ldg(off + r.seq);
+    r.count = __ldg(off + r.seq + 1) - r.first;
+  }
+  return r;
 }
 
 // Blocks of key tiles j .. j + 3 of sequence a, eight lanes a tile; -1 where there is none.
@@ -351,31 +399,34 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
   if (warp >= kEmSumWarps) {
     if (warp == kEmTma) {
       // --------------------------------------------- claims and TMA copies
-      const bool own = PASS == 1 && p.tickets;   // no plan: this warp counts for itself, a lane a sequence
       const int* off = PASS == 1 ? p.off1 : p.off2;
-      int* counter = own ? p.tickets : p.hdr + (PASS == 1 ? kMClaim1 : kMClaim2);
+      int* counter = PASS == 1 && p.tickets ? p.tickets : p.hdr + (PASS == 1 ? kMClaim1 : kMClaim2);
       int n = 0, nx = 0, ni = 0, armed = -1;
       bool ok = true;
+      // a claim is under way while other loads are
+      int claimed = 0;
       auto claim_next = [&]() {
-        int c = 0;
-        if (lane == 0) c = atomicAdd(counter, 1);
-        return (long long)(unsigned)__shfl_sync(0xffffffffu, c, 0);
+        if (lane == 0) claimed = atomicAdd(counter, 1);
       };
-      long long claim = claim_next();
-      EmCount mine{};
-      int cuts, units, end = 0;                  // end: units up to this lane's sequence, its own among them
-      if (own) {
-        cuts = em_count_all(p, lane, mine, end, units);
+      auto claim_there = [&]() { return (unsigned)__shfl_sync(0xffffffffu, claimed, 0); };
+      claim_next();
+      EmLine line{};
+      if (PASS == 2) {
+        line = em_line2(p, lane);
+      } else if (p.tickets) {   // no plan: this warp counts for itself
+        line = em_line1(p, lane);
       } else {
-        cuts = __ldg(p.hdr + (PASS == 1 ? kMCuts1 : kMCuts2));
-        units = __ldg(off + p.n_seq);
+        line.cuts = __ldg(p.hdr + kMCuts1);
+        line.all = __ldg(off + p.n_seq);
       }
-      const long long claims = (long long)units * p.hkv * cuts;
+      const int cuts = line.cuts;
+      const unsigned claims = (unsigned)line.all * p.hkv * cuts;
+      unsigned claim = claim_there();
       auto copy_rows = [&](uint8_t* dst, int tok, int head, uint64_t* bar) {  // one lane
         for (int hf = 0; hf < HF; ++hf) tma_load_5d(dst + hf * kHalf, &tq, 0, 0, tok, head, hf, bar);
       };
       const uint32_t row_bytes = (uint32_t)(HF * tt * p.g * 128);
-      while (true) {
+      for (;; claim = claim_there()) {
         if (stop()) { ok = false; break; }
         const int slot = ni & 1;
         if (ni >= 2 && !wait(&bars.it_empty[slot], ((ni - 2) >> 1) & 1)) { ok = false; break; }
@@ -383,52 +434,40 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         it.done = claim >= claims;
         int nt_x[2] = {0, 0};
         if (!it.done) {
-          const long long u = claim / cuts;
+          const unsigned u = claim / (unsigned)cuts, unit = u / (unsigned)p.hkv;
           it.cut = (int)(claim - u * cuts);
-          const int unit = (int)(u / p.hkv);
-          it.head = (int)(u - (long long)unit * p.hkv);
-          int first, count;
-          if (own) {
-            it.seq = __popc(__ballot_sync(0xffffffffu, lane < p.n_seq && end <= unit));
-            it.t0 = __shfl_sync(0xffffffffu, mine.t0, it.seq);
-            it.rows = __shfl_sync(0xffffffffu, mine.rows, it.seq);
-            it.keys = __shfl_sync(0xffffffffu, mine.keys, it.seq);
-            count = __shfl_sync(0xffffffffu, mine.units1, it.seq);
-            first = __shfl_sync(0xffffffffu, end, it.seq) - count;
-          } else {
-            it.seq = em_find(off, p.n_seq, unit, lane);
-            const int4 s = __ldg(p.seq + it.seq);
-            it.t0 = s.x;
-            it.rows = s.y;
-            it.keys = s.z;
-            first = __ldg(off + it.seq);
-            count = __ldg(off + it.seq + 1) - first;
-          }
+          it.head = (int)(u - unit * p.hkv);
+          const EmPlace at = em_place(p, line, off, (int)unit, lane);
+          it.seq = at.seq;
+          it.t0 = at.t0;
+          it.rows = at.rows;
+          it.keys = at.keys;
+          const int first = at.first, count = at.count;
           const int before = it.keys - it.rows;   // row j sees keys up to before + j (causal)
           if constexpr (PASS == 1) {
-            it.x0 = (count - 1 - (unit - first)) * 2 * tt;   // the last rows, which see most, first
+            it.x0 = (count - 1 - ((int)unit - first)) * 2 * tt;   // the last rows, which see most, first
             for (int x = 0; x < 2; ++x) {
               const int j0 = it.x0 + x * tt, j1 = min(it.rows, j0 + tt);
               const int lim = p.causal ? min(max(before + j1, 0), it.keys) : it.keys;
               nt_x[x] = j0 < it.rows ? (lim + kEmTile - 1) / kEmTile : 0;
             }
             const int nt = max(nt_x[0], nt_x[1]);
-            it.y0 = (int)((long long)nt * it.cut / cuts);
-            it.y1 = (int)((long long)nt * (it.cut + 1) / cuts);
+            it.y0 = nt * it.cut / cuts;
+            it.y1 = nt * (it.cut + 1) / cuts;
             for (int x = 0; x < 2; ++x) {
               it.xs[x] = it.y0;
               it.xe[x] = min(it.y1, nt_x[x]);
             }
           } else {
-            it.x0 = (unit - first) * 2 * kEmTile;
+            it.x0 = ((int)unit - first) * 2 * kEmTile;
             const int tiles = (it.rows + tt - 1) / tt;
             for (int x = 0; x < 2; ++x) {
               const int key = it.x0 + x * kEmTile;
               nt_x[x] = key < it.keys ? min(tiles, p.causal ? max(0, key - before) / tt : 0) : tiles;   // first tile that sees the key
             }
             const int n_y = tiles - nt_x[0];
-            it.y0 = nt_x[0] + (int)((long long)n_y * it.cut / cuts);
-            it.y1 = nt_x[0] + (int)((long long)n_y * (it.cut + 1) / cuts);
+            it.y0 = nt_x[0] + n_y * it.cut / cuts;
+            it.y1 = nt_x[0] + n_y * (it.cut + 1) / cuts;
             for (int x = 0; x < 2; ++x) {
               it.xs[x] = max(it.y0, nt_x[x]);
               it.xe[x] = it.y1;
@@ -442,7 +481,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         __syncwarp();
         ++ni;
         if (it.done) break;
-        claim = claim_next();
+        claim_next();
         if (it.y0 >= it.y1) continue;
         int ids = PASS == 1 ? key_blocks(it.seq, it.y0, it.keys) : key_blocks(it.seq, it.x0 / kEmTile, it.keys);
         int ids_next = PASS == 1 ? key_blocks(it.seq, it.y0 + 4, it.keys) : 0;
@@ -486,9 +525,9 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         for (int m = max(0, armed - ST + 1); m <= armed; ++m) mbar_drain(&bars.full[m % ST], (m / ST) & 1);
         if (nx) mbar_drain(&bars.x_full, (nx - 1) & 1);
       }
-      if (own) {
+      if (PASS == 1 && p.tickets) {
         // every CTA claims once in vain; who does so last leaves the counter at zero
-        while (claim < claims) claim = claim_next();
+        for (claim = claim_there(); claim < claims; claim = claim_there()) claim_next();
         if (lane == 0 && claim == claims + gridDim.x - 1) *reinterpret_cast<volatile int*>(p.tickets) = 0;
       }
     } else if (warp < kEmTma) {
@@ -853,35 +892,37 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
     bool ok = true;
     if (warp == kEmTma) {
       // ----------------------------------- claims, rows, half of every key tile
+      int claimed = 0;
       auto claim_next = [&]() {
-        int c = 0;
-        if (lane == 0) c = atomicAdd(p.hdr + kMClaim2, 1);
-        return (long long)(unsigned)__shfl_sync(0xffffffffu, c, 0);
+        if (lane == 0) claimed = atomicAdd(p.hdr + kMClaim2, 1);
       };
-      long long claim = claim_next();
-      const int cuts = __ldg(p.hdr + kMCuts2);
-      const long long claims = (long long)__ldg(p.off2 + p.n_seq) * p.hkv * cuts;
+      auto claim_there = [&]() { return (unsigned)__shfl_sync(0xffffffffu, claimed, 0); };
+      claim_next();
+      const EmLine line = em_line2(p, lane);
+      const int cuts = line.cuts;
+      const unsigned claims = (unsigned)line.all * p.hkv * cuts;
+      unsigned claim = claim_there();
       int n = 0, nx = 0, armed = -1;
-      for (int ni = 0;; ++ni) {
+      for (int ni = 0;; ++ni, claim = claim_there()) {
         if (stop()) { ok = false; break; }
         const int slot = ni & 1;
         if (ni >= 2 && !wait(&bars.it_empty[slot], ((ni - 2) >> 1) & 1)) { ok = false; break; }
         EkItem it{};
         it.done = claim >= claims;
         if (!it.done) {
-          const long long u = claim / cuts;
-          const int cut = (int)(claim - u * cuts), unit = (int)(u / p.hkv);
-          it.head = (int)(u - (long long)unit * p.hkv);
-          it.seq = em_find(p.off2, p.n_seq, unit, lane);
-          const int4 s = __ldg(p.seq + it.seq);
-          it.unit = unit;
-          it.tile = unit - __ldg(p.off2 + it.seq);
-          it.t0 = s.x;
-          it.rows = s.y;
-          it.keys = s.z;
+          const unsigned u = claim / (unsigned)cuts, unit = u / (unsigned)p.hkv;
+          const int cut = (int)(claim - u * cuts);
+          it.head = (int)(u - unit * p.hkv);
+          const EmPlace at = em_place(p, line, p.off2, (int)unit, lane);
+          it.seq = at.seq;
+          it.unit = (int)unit;
+          it.tile = it.unit - at.first;
+          it.t0 = at.t0;
+          it.rows = at.rows;
+          it.keys = at.keys;
           const int nt = ek_tiles(p, it.rows, it.keys, it.tile, tt);
-          it.y0 = (int)((long long)nt * cut / cuts);
-          it.y1 = (int)((long long)nt * (cut + 1) / cuts);
+          it.y0 = nt * cut / cuts;
+          it.y1 = nt * (cut + 1) / cuts;
         }
         if (lane == 0) {
           work[slot] = it;
@@ -889,7 +930,7 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         }
         __syncwarp();
         if (it.done) break;
-        claim = claim_next();
+        claim_next();
         if (it.y0 >= it.y1) continue;
         int ids = key_blocks(it.seq, it.y0, it.keys), ids_next = key_blocks(it.seq, it.y0 + 4, it.keys);
         const int xs = nx & 1;
@@ -1099,27 +1140,27 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
 // Joins the parts of every row: -log2 of its whole sum, -inf where it has none.
 __global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ EmParams p) {
   pdl_enter();
-  if (p.hdr[kMBad]) return;
+  const int bad = p.hdr[kMBad], n = 2 * p.hdr[kMCuts1], t0 = p.tok_off[0], t1 = p.tok_off[p.n_seq];
   const size_t rows = (size_t)p.n_tokens * p.hq;
   const size_t i = (size_t)blockIdx.x * 256 + threadIdx.x;
   const int t = (int)(i / p.hq), h = (int)(i - (size_t)t * p.hq);
-  if (i >= rows || t < p.tok_off[0] || t >= p.tok_off[p.n_seq]) return;   // rows of no sequence have no parts
-  const int n = 2 * p.hdr[kMCuts1];
+  if (bad || i >= rows || t < t0 || t >= t1) return;   // rows of no sequence have no parts
+  constexpr int U = 16;
   float m = -INFINITY, l = 0.f;
-  for (int k0 = 0; k0 < n; k0 += 8) {   // eight loads under way
-    float2 v[8];
+  for (int k0 = 0; k0 < n; k0 += U) {   // as many loads under way
+    float2 v[U];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = k0 + k < n ? p.parts[(k0 + k) * rows + i] : make_float2(0.f, 0.f);
+    for (int k = 0; k < U; ++k) v[k] = k0 + k < n ? p.parts[(k0 + k) * rows + i] : make_float2(0.f, 0.f);
     float top = m;
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < U; ++k)
       if (v[k].y > 0.f) top = fmaxf(top, v[k].x);
     if (top > m) {
       l *= fast_exp2(m - top);
       m = top;
     }
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
+    for (int k = 0; k < U; ++k)
       if (v[k].y > 0.f) l += v[k].y * fast_exp2(v[k].x - m);
   }
   p.nlse[((size_t)(h / p.g) * p.n_tokens + t) * p.g + h % p.g] = l > 0.f ? -(m + log2f(l)) : -INFINITY;
@@ -1128,30 +1169,31 @@ __global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ Em
 // Adds the cuts' and heads' sums in their order.
 __global__ void __launch_bounds__(256) em_add_kernel(const __grid_constant__ EmParams p, const float* mass_in, float carry, float* mass) {
   pdl_enter();
-  if (p.hdr[kMBad]) return;
   const int a = blockIdx.y, t = blockIdx.x * 256 + threadIdx.x;
+  const int bad = p.hdr[kMBad], cuts = p.hdr[kMCuts2], first = p.off2[a];
   const int4 s = p.seq[a];
-  if (t >= s.z) return;
+  if (bad || t >= s.z) return;
   float sum = 0.f;
   const float* v = p.sums + (size_t)a * p.most + t;
   const size_t step = (size_t)p.n_seq * p.most;
   const size_t o = (size_t)a * p.most + t;
+  const float before = mass_in ? mass_in[o] : 0.f;
   if (s.y > 0 && p.few) {
     // of every row tile that sees the key, and of its halves that hold rows
     const int tt = kEmTile / p.g;
-    v = p.sums + (size_t)p.off2[a] * 2 * p.hkv * p.most + t;
+    v = p.sums + (size_t)first * 2 * p.hkv * p.most + t;
     for (int i = 0; i * tt < s.y; ++i) {
       if (t / kEmTile >= ek_tiles(p, s.y, s.z, i, tt)) continue;
       const int halves = min(tt, s.y - i * tt) * p.g > 64 ? 2 : 1;
-#pragma unroll 8
+#pragma unroll 16
       for (int k = 0; k < halves * p.hkv; ++k) sum += v[(size_t)(2 * i * p.hkv + k) * p.most];
     }
   } else if (s.y > 0) {
-    const int n = 2 * p.hdr[kMCuts2] * p.hkv;
-#pragma unroll 8
+    const int n = 2 * cuts * p.hkv;
+#pragma unroll 16
     for (int i = 0; i < n; ++i) sum += v[i * step];
   }
-  mass[o] = mass_in ? fmaf(carry, mass_in[o], sum) : sum;
+  mass[o] = mass_in ? fmaf(carry, before, sum) : sum;
 }
 
 struct EmLayout {
