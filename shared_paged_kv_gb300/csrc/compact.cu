@@ -80,7 +80,8 @@ __device__ __forceinline__ unsigned mass_key(float x) {
 // RANKS CTAs take a sequence, a thread holds KEYS masses at a time.
 template <int RANKS, int KEYS>
 __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_constant__ KeepParams p) {
-  __shared__ unsigned hist4[kKhCopies * kKhStride], hist[kKhBins];
+  __shared__ unsigned hist4[kKhCopies * kKhStride];
+  __shared__ __align__(8) unsigned hist[kKhBins];
   __shared__ int wsum[32];
   __shared__ long long wlong[32];
   __shared__ unsigned s_prefix;
@@ -164,8 +165,13 @@ __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_con
 #pragma unroll
     for (int q = 0; q < ranks; ++q) {
       const unsigned* h = RANKS > 1 ? cluster.map_shared_rank(hist, q) : hist;
-      c[0] += h[bins - 1 - tid * per];
-      if (per > 1) c[1] += h[bins - 2 - tid * per];
+      if (per > 1) {   // a pair as one load: distributed shared memory takes its time by the load
+        const uint2 v = reinterpret_cast<const uint2*>(h)[bins / 2 - 1 - tid];
+        c[0] += v.y;
+        c[1] += v.x;
+      } else {
+        c[0] += h[bins - 1 - tid];
+      }
     }
     int total;
     const int mine = (int)(c[0] + c[1]);
