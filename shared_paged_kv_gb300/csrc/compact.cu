@@ -577,6 +577,12 @@ __device__ __forceinline__ uint32_t load_row(const uint32_t* p) {
   return v;
 }
 
+__device__ __forceinline__ bool flag_set(const uint8_t* p) {
+  uint32_t v;
+  asm volatile("ld.acquire.gpu.u8 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
+  return v != 0;
+}
+
 // 16-byte pieces of an item's rows: thread v of the k-th hundred and twenty-eight
 // has piece v % VECS of row v / VECS.
 template <int VECS>
@@ -586,8 +592,14 @@ struct CpRows {
 #pragma unroll
     for (int k = 0; k < kCpVecs; ++k) {
       const int v = k * kCpThreads + threadIdx.x, r = v / VECS;
-      if (r < n) x[k] = load_row(reinterpret_cast<const uint4*>(slab + (size_t)(src[r] + at) * (VECS * 16)) + v % VECS);
+      x[k] = r < n ? load_row(reinterpret_cast<const uint4*>(slab + (size_t)(src[r] + at) * (VECS * 16)) + v % VECS) : make_uint4(0u, 0u, 0u, 0u);
     }
+  }
+  __device__ __forceinline__ uint32_t any() const {
+    uint32_t a = 0;
+#pragma unroll
+    for (int k = 0; k < kCpVecs; ++k) a |= x[k].x | x[k].y | x[k].z | x[k].w;
+    return a;
   }
   __device__ __forceinline__ void store(uint8_t* slab, int n, const int* dst, int at) const {
 #pragma unroll
@@ -669,7 +681,7 @@ __global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_cons
     auto step = [&](CpRows<VECS>& x, CpRows<VECS>& y, int c) {
       const int at = c % p.hkv * p.B;
       // a 4-bit row's scales go along, as words
-      uint32_t w[4];
+      uint32_t w[4] = {};
       const int words = p.sb_bytes / 4;   // 0, 1 or 2
       if (VECS == 4) {
         const uint8_t* slab = slab_of(c, 2);
@@ -679,26 +691,34 @@ __global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_cons
           if (r < s.n) w[k] = load_row(reinterpret_cast<const uint32_t*>(slab + (size_t)(s_src[r] + at) * p.sb_bytes) + v % words);
         }
       }
+      auto next = [&]() {
+        if (c + 1 < c1) y.load(slab_of(c + 1, 0), s.n, s_src, (c + 1) % p.hkv * p.B);
+      };
       if (in_place) {
-        // every row of this chain is read: said once the loads of all threads are done
-        __threadfence();
-        __syncthreads();
-        if (tid == 0) *const_cast<volatile uint8_t*>(p.flags + (size_t)sg * p.chains + c) = 1;
+        // Every row of this chain is read: said once the loads of all threads have
+        // returned, which the barrier's predicate needs.
+        uint32_t any = x.any();
+        if (VECS == 4) any |= w[0] | w[1] | w[2] | w[3];
+        __syncthreads_or(any == 1u);
+        if (tid == 0) {
+          __threadfence();
+          *const_cast<volatile uint8_t*>(p.flags + (size_t)sg * p.chains + c) = 1;
+        }
+        next();   // on their way while this chain waits and is written
         for (int q = wait0 + tid; q < wait1; q += kCpThreads) {
-          const volatile uint8_t* f = p.flags + (size_t)(s.first + q) * p.chains + c;
+          const uint8_t* f = p.flags + (size_t)(s.first + q) * p.chains + c;
           const long long t0 = clock64();
-          while (!*f) {
+          while (!flag_set(f)) {
             if (clock64() - t0 > (1ll << 31)) {
               set_err(p.status, KVS_DEVERR_WAIT_TIMEOUT);
               break;
             }
           }
         }
-        __threadfence();
         __syncthreads();
+      } else {
+        next();
       }
-      // the next chain's rows are on their way while this one's are written
-      if (c + 1 < c1) y.load(slab_of(c + 1, 0), s.n, s_src, (c + 1) % p.hkv * p.B);
       x.store(slab_of(c, 0), s.n, s_dst, at);
       if (VECS == 4) {
         uint8_t* slab = slab_of(c, 2);
