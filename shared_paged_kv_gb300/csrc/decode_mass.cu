@@ -77,7 +77,8 @@ struct DmShared {
   float2 ml[W][kDmMaxGroup];
   int warp_sums[32];
   int a, b, cuts;
-  long long per, u0;            // places of a CTA on the line, this CTA's first
+  long long per, first;         // places of a CTA on the line, that of the first unit of the pair at work
+  int gap;                      // places between two pairs
   struct Cut {                  // a pair that other CTAs share: this CTA's first and last
     int seq, head, parts, last;
     size_t slot;                // of its first part
@@ -123,6 +124,11 @@ template <int UT>
 __device__ __forceinline__ DmSpan dm_span(const DmParams& p, int a) {
   const int len = min(max(__ldg(p.seq_len + a), 0), p.most);
   return DmSpan{len, (len + UT - 1) / UT};
+}
+
+// a / b; 64-bit division takes some hundred instructions
+__device__ __forceinline__ int quotient(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? (int)(a / b) : (int)((unsigned)a / (unsigned)b);
 }
 
 // A place on the line of units.
@@ -176,15 +182,15 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
   };
 
   // ---- this CTA's stretch of the line
-  long long per, u0;
-  int n_mine;   // units of this CTA
+  long long per, first;
+  int n_mine, gap = 0;   // units of this CTA
   DmAt seg;
   // units of a CTA: an even share, but no more parts of a pair than are worth their
   // joining (a sequence of 32,000 tokens, eight heads on one KV head: 45 us evenly,
   // 23 with fewer CTAs; in 4 bits 39 and 26)
   auto share = [&](int total) {
     const int least = (int)sqrtf((F::mx ? 0.03f : 0.06f) * (float)p.g * (float)total / (float)p.n_seq);
-    return max((long long)max(W, least), ((long long)total * p.hkv + gridDim.x - 1) / gridDim.x);
+    return (long long)max(max(W, least), quotient((long long)total * p.hkv + gridDim.x - 1, gridDim.x));
   };
   if (p.n_seq <= 32) {
     // every warp for itself, a lane a sequence
@@ -207,25 +213,44 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
         break;
       }
     }
-    int end = n;
+    // Elsewhere a gap in front of every pair stands for what beginning it costs (32
+    // sequences that share 4,096 of 5,400 tokens, 16 / 2 heads: 26.2 us, 28.1 without).
+    if (!rounded) {
+      gap = 4 * W;
+      n = real ? real + gap : 0;
+    }
+    int end = n, units = real;   // places and units up to this lane's sequence
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int x = __shfl_up_sync(0xffffffffu, end, o);
+      const int x = __shfl_up_sync(0xffffffffu, end, o), y = __shfl_up_sync(0xffffffffu, units, o);
       end += lane >= o ? x : 0;
+      units += lane >= o ? y : 0;
     }
-    const int per_head = __shfl_sync(0xffffffffu, end, 31);
-    u0 = per * blockIdx.x;
-    const long long u1 = min((long long)per_head * p.hkv, u0 + per);
-    if (u0 >= u1) {
+    const int per_head = __shfl_sync(0xffffffffu, end, 31), units_head = __shfl_sync(0xffffffffu, units, 31);
+    const long long places = (long long)per_head * p.hkv;
+    if (!rounded) per = max(per, (long long)quotient(places + gridDim.x - 1, gridDim.x));
+    // the pair of a place, and the units before the place
+    auto locate = [&](long long u, DmAt& at, int& place) {
+      at.h = quotient(u, per_head);
+      const int r = (int)(u - (long long)at.h * per_head);
+      at.a = __popc(__ballot_sync(0xffffffffu, lane < p.n_seq && end <= r)) & 31;
+      place = r - __shfl_sync(0xffffffffu, end - n, at.a) - gap;
+      at.units = __shfl_sync(0xffffffffu, real, at.a);
+      at.b = min(max(place, 0), at.units);
+      return (long long)at.h * units_head + __shfl_sync(0xffffffffu, units - real, at.a) + at.b;
+    };
+    const long long u0 = per * blockIdx.x, u1 = min(places, u0 + per);
+    if (u0 < u1) {
+      int place, unused;
+      DmAt behind;
+      const long long before = locate(u0, seg, place);
+      n_mine = (int)((u1 < places ? locate(u1, behind, unused) : (long long)units_head * p.hkv) - before);
+      first = u0 - place;
+    }
+    if (u0 >= u1 || n_mine == 0) {
       empty_sequences();
       return;
     }
-    seg.h = (int)(u0 / per_head);
-    const int r0 = (int)(u0 - (long long)seg.h * per_head);
-    seg.a = __popc(__ballot_sync(0xffffffffu, lane < p.n_seq && end <= r0));
-    seg.b = r0 - __shfl_sync(0xffffffffu, end - n, seg.a);
-    seg.units = __shfl_sync(0xffffffffu, real, seg.a);
-    n_mine = rounded ? min((int)per, seg.units - seg.b) : (int)(u1 - u0);
   } else {
     int per_head = 0, mine = 0, mine_before = 0;   // of the sequences tid, tid + T, ...: the first one's units, and those before it
     for (int a0 = 0; a0 < p.n_seq; a0 += T) {
@@ -240,13 +265,12 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
       per_head += total;
     }
     per = share(per_head);
-    u0 = per * blockIdx.x;
-    const long long u1 = min((long long)per_head * p.hkv, u0 + per);
+    const long long u0 = per * blockIdx.x, u1 = min((long long)per_head * p.hkv, u0 + per);
     if (u0 >= u1) {
       empty_sequences();
       return;
     }
-    seg.h = (int)(u0 / per_head);
+    seg.h = quotient(u0, per_head);
     const int r0 = (int)(u0 - (long long)seg.h * per_head);
     if (mine_before <= r0 && r0 < mine_before + mine) {
       sh.a = tid;
@@ -268,11 +292,13 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     seg.b = sh.b;
     seg.units = dm_span<UT>(p, sh.a).units;
     n_mine = (int)(u1 - u0);
+    first = u0 - seg.b;
   }
 
   if (tid == 0) {
     sh.per = per;
-    sh.u0 = u0;
+    sh.first = first;
+    sh.gap = gap;
   }
 
   // ---- copies of this warp's units k = warp, warp + W, ...
@@ -675,8 +701,7 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
         }
       }
     __syncthreads();
-    const long long first = sh.u0 + done - seg.b;    // the pair's first unit on the line
-    const int cta0 = (int)(first / sh.per), n_parts = (int)((first + seg.units - 1) / sh.per) - cta0 + 1;
+    const int cta0 = quotient(sh.first, sh.per), n_parts = quotient(sh.first + seg.units - 1, sh.per) - cta0 + 1;
     const int order = seg.h * p.n_seq + seg.a, pair = seg.a * p.hkv + seg.h;
     const size_t slot = (size_t)blockIdx.x + order;
     for (int i = tid; i < p.g * (D / 4); i += T) {
@@ -706,12 +731,15 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     }
     if (n_parts > 1) __threadfence();
     __syncthreads();   // the states are read: the next pair's may be written
-    if (n_parts > 1 && tid == 0) {
-      // the parts are there; whether they were the last ones is looked at when
-      // this CTA has nothing else to do
-      sh.cut[sh.cuts] = {seg.a, seg.h, n_parts, 0, (size_t)cta0 + order};
-      if (sh.cuts++ == 0) got0 = atomicAdd(p.tickets + pair, 1);
-      else got1 = atomicAdd(p.tickets + pair, 1);
+    if (tid == 0) {
+      sh.first += seg.units + sh.gap;
+      if (n_parts > 1) {
+        // the parts are there; whether they were the last ones is looked at when
+        // this CTA has nothing else to do
+        sh.cut[sh.cuts] = {seg.a, seg.h, n_parts, 0, (size_t)cta0 + order};
+        if (sh.cuts++ == 0) got0 = atomicAdd(p.tickets + pair, 1);
+        else got1 = atomicAdd(p.tickets + pair, 1);
+      }
     }
     done += n_seg;
     if (done < n_mine) dm_advance<UT>(p, seg, n_seg);
