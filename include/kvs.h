@@ -613,7 +613,7 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  * id outside the pool (KVS_DEVERR_BLOCK_ID) takes its tokens out of the
  * sequence (weight 0); seq_len outside the table's row (KVS_DEVERR_SEQ_LEN) is
  * clamped; an empty context yields zeros.  Scores, sums and masses are float32,
- * a weight that multiplies values keeps 16 bits or more.  MX4 values below 2^-27
+ * a weight that multiplies values keeps 22 bits or more.  MX4 values below 2^-27
  * of the largest scale that their 32 channels have in the sequence count as 0.
  * The result is the same to the bit for the same call.
  * ws: kvs_workspace_size(KVS_OP_DECODE_MASS, n_seq, max_blocks, n_q_heads).

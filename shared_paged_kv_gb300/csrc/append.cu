@@ -243,7 +243,18 @@ __global__ void __launch_bounds__(kApThreads, kApCtas) append_kernel(const __gri
       const int pos = p.pos ? __ldg(p.pos + (size_t)axis * p.at.n_tokens + tt) : where[s].pos;
       const unsigned long long ph = (unsigned long long)(long long)pos * f;
       float sn, c;
-      sincospif(static_cast<float>(static_cast<int>(ph >> 32)) * 0x1p-31f, &sn, &c);
+      const int top = static_cast<int>(ph >> 32);
+      const float half_turns = static_cast<float>(top) * 0x1p-31f;
+      sincospif(half_turns, &sn, &c);
+      if constexpr (MODE == kApMx) {
+        // what the conversion cut off, up to 2^-25 half turns: a key near the border of
+        // two codes falls on the wrong side less often
+        const float rest = (static_cast<float>(top - static_cast<long long>(static_cast<float>(top))) + static_cast<float>(static_cast<uint32_t>(ph)) * 0x1p-32f) *
+                           (0x1p-31f * 3.14159265f);
+        const float s1 = fmaf(c, rest, sn);
+        c = fmaf(-sn, rest, c);
+        sn = s1;
+      }
       cs[s][i] = make_float2(c, p.inverse ? -sn : sn);
     }
   }

@@ -9,16 +9,18 @@
 // keys and values) and the second turns them into weights with the final
 // maximum and sum.
 //
-// Work: the blocks of all sequences, KV head by KV head, form one line that the
-// CTAs of one wave share evenly, whatever the lengths; a CTA's stretch may
-// cover the ends of several (sequence, KV head) pairs, and a pair several CTAs,
-// whose parts the last one to arrive joins in their order.  A warp takes every
-// W-th unit of its CTA's stretch and brings it with its own ring of TMA copies,
-// which run on across the pairs' borders.
+// Work: the units of all sequences, KV head by KV head, form one line that the CTAs
+// of one wave share evenly, whatever the lengths; a CTA's stretch may cover the
+// ends of several (sequence, KV head) pairs, and a pair several CTAs, whose parts
+// the last one to arrive joins in their order.  A warp takes every W-th unit of
+// its CTA's stretch and brings it with its own ring of TMA copies, which run on
+// across the pairs' borders.  Up to 32 sequences are placed by every warp for
+// itself; there, where all pairs fit, each begins a CTA.
 //
 // Tokens are the 16 rows of the products, query heads the 8 (or twice 8)
 // columns: S^T = K q^T, O^T += V^T P^T.  P^T is the transposed accumulator of S^T
-// (movmatrix) in two 16-bit parts, so that a weight keeps 16 bits or more.  The
+// (movmatrix) in three bf16 parts, which hold a weight's 24 bits (in two, 2e-6 of
+// the result were lost, in three 3e-7, at 1 us of 26), or in two fp16 parts.  The
 // reference of the exponentials moves only when a score exceeds it by more than
 // 2^4, so that a unit needs no exchange between lanes.
 //
@@ -32,6 +34,15 @@
 // accumulators follow E when it grows.  Row r of a product is token
 // r ^ (r >> 1 & 1) of its 16, with which all shared loads (64-byte swizzle) are
 // free of bank conflicts.
+//
+// Measured, graph replays with the masses (without for *): eight sequences of
+// 9,830 to 16,384 tokens, 32 heads of their own: 262 us, 6.4 TB/s, bound by HBM; 32
+// that share 4,096 of 5,400, 16 / 2 heads: 27 us, every sequence reads the common
+// part from L2 (6.5 TB/s), bound by a unit's chain of products and exponentials;
+// four of 350, 8 / 2 of 64 channels: 8.7 us, start, four units, arrival, join and the
+// second kernel, each a trip to memory.  In 4 bits: twelve of 4,000 to 16,384, 32 / 8
+// (*): 29 us; eight of 16,384 to 32,768: 72 us, 2.7 TB/s, bound by issue slots (52 %)
+// and the conversions.
 #include <algorithm>
 #include <cmath>
 
@@ -577,7 +588,7 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
           }
         }
         // ---- weights, transposed into the B operand
-        uint32_t ph[MT][NT][2], pl[MT][NT][2];
+        uint32_t ph[MT][NT][2], pl[MT][NT][2], pm[MT][NT][2];   // pm: bf16, between the two
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -590,24 +601,31 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               uint32_t hi, lo;
-              if constexpr (F::mx) split_f16(w[2 * i], w[2 * i + 1], hi, lo);
-              else split_bf16(w[2 * i], w[2 * i + 1], hi, lo);
+              if constexpr (F::mx) {
+                split_f16(w[2 * i], w[2 * i + 1], hi, lo);
+              } else {
+                hi = pack_bf16(w[2 * i], w[2 * i + 1]);
+                uint32_t mid;
+                split_bf16(w[2 * i] - bf16_lo(hi), w[2 * i + 1] - bf16_hi(hi), mid, lo);
+                pm[mt][nt][i] = movm_t(mid);
+              }
               ph[mt][nt][i] = movm_t(hi);
               pl[mt][nt][i] = movm_t(lo);
             }
           }
         // ---- O^T += V^T P^T.  Each unit's products are added in plain fp32: the
         // tensor cores cut their sums, which over a long context is a bias (16,384
-        // tokens: 5.5e-6 of the result, added here 2.2e-6; in 4 bits 1.3e-6 and
-        // 2.6e-7).
+        // tokens: 5.5e-6 of the result, added here 2.2e-6, with weights of two parts; in
+        // 4 bits 1.3e-6 and 2.6e-7).
         auto values = [&](int nt, int j, const uint32_t* x, int mt) {
           float y[4] = {0.f, 0.f, 0.f, 0.f};
           if constexpr (F::mx) {
             mma_f16(y, x[0], x[1], x[2], x[3], ph[mt][nt][0], ph[mt][nt][1]);
             mma_f16(y, x[0], x[1], x[2], x[3], pl[mt][nt][0], pl[mt][nt][1]);
           } else {
-            mma_bf16(y, x, ph[mt][nt][0], ph[mt][nt][1]);
             mma_bf16(y, x, pl[mt][nt][0], pl[mt][nt][1]);
+            mma_bf16(y, x, pm[mt][nt][0], pm[mt][nt][1]);
+            mma_bf16(y, x, ph[mt][nt][0], ph[mt][nt][1]);
           }
           float* a = acc[nt][j];
           const float2 u = __fadd2_rn(make_float2(a[0], a[1]), make_float2(y[0], y[1]));
