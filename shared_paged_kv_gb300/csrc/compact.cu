@@ -14,7 +14,7 @@
 // kvs_compact: row i of a sequence's kept tokens moves from place idx[i] to
 // place i, in every layer's slabs.  Places only fall (idx[i] >= i), blocks in
 // front of the first change stay, and a block that others reference is replaced
-// by a free one.  Three launches:
+// by a free one.  Three launches (two for few short sequences):
 //  cp_check  a CTA per sequence: the list's order, the first change, which
 //            blocks have to be replaced;
 //  cp_apply  a CTA per sequence: tables, counts, lengths, masses;
@@ -343,10 +343,9 @@ __device__ __forceinline__ int2 cp_share(int n) {
 }
 
 // A CTA per sequence, and some more to copy long rows of masses.
-__global__ void __launch_bounds__(kCpSeqThreads) cp_check(const __grid_constant__ CompactParams p) {
+__device__ __forceinline__ void check_sequence(const CompactParams& p) {
   __shared__ int s_same, s_bad;
   const int a = blockIdx.x, tid = threadIdx.x;
-  pdl_enter();
   for (long long w = (long long)(blockIdx.y * p.n_seq + a) * kCpSeqThreads + tid; w < (p.capacity + 31) / 32;
        w += (long long)p.n_seq * gridDim.y * kCpSeqThreads)
     p.freed[w] = 0;
@@ -441,11 +440,10 @@ __device__ __forceinline__ int cp_segments(const CompactParams& p, const CpSeq& 
 
 // A CTA per sequence (and some more for long rows of masses): every CTA adds up
 // what the sequences before it take.
-__global__ void __launch_bounds__(kCpSeqThreads) cp_apply(const __grid_constant__ CompactParams p) {
+__device__ __forceinline__ void apply_sequence(const CompactParams& p) {
   __shared__ int warp_sums[32];
   __shared__ int s_base, s_seg, s_drop, s_taken;
   const int a = blockIdx.x, tid = threadIdx.x;
-  pdl_enter();
   const CpSeq s = p.seq[a];
   const int avail = min(max(*p.n_free, 0), p.capacity);
   {
@@ -554,6 +552,29 @@ __global__ void __launch_bounds__(kCpSeqThreads) cp_apply(const __grid_constant_
     }
   }
   if (tid == 0) p.seq_len[a] = s.kept;
+}
+
+__global__ void __launch_bounds__(kCpSeqThreads) cp_check(const __grid_constant__ CompactParams p) {
+  pdl_enter();
+  check_sequence(p);
+}
+
+__global__ void __launch_bounds__(kCpSeqThreads) cp_apply(const __grid_constant__ CompactParams p) {
+  pdl_enter();
+  apply_sequence(p);
+}
+
+// Both, by one cluster: up to eight sequences with short rows of masses (four of some
+// hundred tokens: the choice and this call take the host 18 us, 21.5 with two
+// launches; in a graph they take the same).
+constexpr int kCpCluster = 8;
+__global__ void __cluster_dims__(kCpCluster) __launch_bounds__(kCpSeqThreads) cp_both(const __grid_constant__ CompactParams p) {
+  pdl_enter();
+  const bool there = (int)blockIdx.x < p.n_seq;
+  if (there) check_sequence(p);
+  __threadfence();
+  cg::this_cluster().sync();
+  if (there) apply_sequence(p);
 }
 
 __device__ __forceinline__ int lower_bound(const int32_t* x, int n, int v) {   // first i with x[i] >= v
@@ -854,9 +875,11 @@ extern "C" kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int3
   const dim3 per_seq((unsigned)n_seq, (unsigned)(mass_dev ? std::clamp<long long>(most / 8192, 1, 16) : 1));
   const unsigned grid = (unsigned)std::max(1ll, std::min(p.max_segs * p.chains, (long long)pool->num_sms * kCpCtas));
   auto move = p.row_bytes == 256 ? cp_move<16> : p.row_bytes == 128 ? cp_move<8> : cp_move<4>;
-  const bool ok = launch_pdl(cp_check, per_seq, dim3(kCpSeqThreads), stream, p) == cudaSuccess &&
-                  launch_pdl(cp_apply, per_seq, dim3(kCpSeqThreads), stream, p) == cudaSuccess &&
+  const bool both = n_seq <= kCpCluster && per_seq.y == 1;
+  const bool ok = (both ? launch_pdl(cp_both, dim3(kCpCluster), dim3(kCpSeqThreads), stream, p) == cudaSuccess
+                        : launch_pdl(cp_check, per_seq, dim3(kCpSeqThreads), stream, p) == cudaSuccess &&
+                              launch_pdl(cp_apply, per_seq, dim3(kCpSeqThreads), stream, p) == cudaSuccess) &&
                   launch_pdl(move, dim3(grid), dim3(kCpThreads), stream, p) == cudaSuccess;
-  if (ok) count_launch(3);
+  if (ok) count_launch(both ? 2 : 3);
   return check_launch("compact");
 }
