@@ -18,7 +18,8 @@
 // a tile of rows at most, pass 2 is em_keys_kernel: the rows stay and the keys stream.
 //
 // Items (a pair of X tiles, a range of Y tiles) are claimed in order, the longest
-// first.  Calls with few of them cut the Y ranges: pass 1 leaves (reference, sum) of
+// first; with few rows and many keys, every CTA takes an even stretch of key tiles
+// instead.  Calls with few of them cut the Y ranges: pass 1 leaves (reference, sum) of
 // each cut, which em_join_kernel joins; pass 2 leaves a sum for each cut and KV head,
 // which the last kernel adds in a fixed order.  A plan kernel counts the units of
 // every sequence; up to 32 sequences are counted by a warp of pass 1.
@@ -28,9 +29,8 @@
 // of what cuBLAS reaches.  A pair of tiles takes 1,024 cycles of
 // products and 1,024 of exponentials (8 lanes a cycle and scheduler); without any
 // exponentials the passes take 172 and 150.  Eight times 32 rows after 3,500 to 8,192
-// tokens 54 us: the keys are read twice at 5.8 TB/s (15 us each), the rest is starts (3
-// us until the first copy), uneven ends (CTAs stop after 17 to 24 us) and the two
-// small kernels.
+// tokens 47 us: the keys are read twice at 5.8 TB/s (15 us each), the rest is starts (3
+// us until the first copy of each pass) and the two small kernels.
 #include <algorithm>
 #include <cmath>
 
@@ -50,6 +50,7 @@ constexpr int kEmSumWarps = 16, kEmThreads = (kEmSumWarps + 4) * 32;
 constexpr int kEmMma = kEmSumWarps, kEmTma = kEmSumWarps + 2;   // and one more
 constexpr int kEmTile = 128;
 constexpr int kEmMaxCuts = 16;
+constexpr int kEmEven = 10;   // tiles a CTA from which on stretches are even
 constexpr uint32_t kEmCols = 512, kEmX = 384;   // scores in three buffers of 128 columns, behind them the X tiles
 
 template <int D>
@@ -59,7 +60,7 @@ __host__ __device__ constexpr int em_stages() { return D == 128 ? 4 : 8; }
 template <int D>
 __host__ __device__ constexpr int em_smem() { return 1024 + em_tile_bytes<D>() * (2 + em_stages<D>()); }
 
-enum { kMClaim1, kMClaim2, kMBad, kMCuts1, kMCuts2, kMTotal = 16 };
+enum { kMClaim1, kMClaim2, kMBad, kMCuts1, kMCuts2, kMPer, kMTotal = 16 };
 
 struct EmParams {
   const int32_t *table, *tok_off, *seq_len;
@@ -172,7 +173,7 @@ __global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ E
     if (bad) set_err(p.status, KVS_DEVERR_JOB);
     p.off1[p.n_seq] = bad ? 0 : n1;
     p.off2[p.n_seq] = bad ? 0 : n2;
-    p.hdr[kMClaim1] = p.hdr[kMClaim2] = 0;
+    p.hdr[kMClaim1] = p.hdr[kMClaim2] = p.hdr[kMPer] = 0;
     p.hdr[kMBad] = bad;
   }
 }
@@ -180,7 +181,7 @@ __global__ void __launch_bounds__(1024) em_plan_kernel(const __grid_constant__ E
 struct __align__(16) EmItem {
   int seq, head, cut, done;
   int t0, rows, keys, x0;       // of the sequence; x0: first token (pass 1) or key (pass 2) of the X tiles
-  int y0, y1, pad[2];           // Y tiles of the item
+  int y0, y1, behind, pad;      // Y tiles of the item; cuts behind this one that are empty
   int xs[2], xe[2];             // of them, those that X tile 0 / 1 takes
 };
 
@@ -213,12 +214,52 @@ __device__ __forceinline__ int em_find(const int* off, int n, int v, int lane) {
   return lo + __popc(__ballot_sync(0xffffffffu, le));
 }
 
+// Key tiles that row tile i of a sequence sees.
+__device__ __forceinline__ int ek_tiles(const EmParams& p, int rows, int keys, int i, int tt) {
+  const int lim = p.causal ? min(max(keys - rows + min(rows, (i + 1) * tt), 0), keys) : keys;
+  return (lim + kEmTile - 1) / kEmTile;
+}
+
 // At most 32 sequences, a lane each.
 struct EmLine {
   int t0, rows, keys, units;   // of this lane's sequence
   int end;                     // units up to it, its own among them
   int all, cuts;
+  // Even stretches: where every sequence has one row tile at most, the key tiles of all
+  // of them, KV head by KV head, form a line of which each CTA takes `per` (0: items
+  // are claimed).  Eight times 32 rows after 3,500 to 8,192 tokens, 18 tiles a CTA: 47
+  // us, 54 with claimed items; but 16 x 4 after 1,000, 40 / 8 heads, 7 tiles: 29.6
+  // and 27.7, 4 x 16 after 500, 2 tiles: 21 and 16.5 (a second pair costs its start).
+  int tiles, tiles_end, line, per;   // of this lane's sequence, up to it, of a KV head
 };
+// Whole warp: the lanes' tiles on the line.
+__device__ __forceinline__ void em_even_line(const EmParams& p, EmLine& r, int lane) {
+  r.tiles = r.rows > 0 ? ek_tiles(p, r.rows, r.keys, 0, kEmTile / p.g) : 0;
+  r.tiles_end = r.tiles;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, r.tiles_end, o);
+    r.tiles_end += lane >= o ? x : 0;
+  }
+  r.line = __shfl_sync(0xffffffffu, r.tiles_end, 31);
+}
+// Whole warp: what the stretch [place, stop) has of the pair at `place`.
+struct EmStretch {
+  int seq, head, y0, y1, cut, behind;   // behind: cuts that the pair does not have
+};
+__device__ __forceinline__ EmStretch em_stretch(const EmParams& p, const EmLine& r, int place, int stop, int lane) {
+  constexpr unsigned kAll = 0xffffffffu;
+  EmStretch e;
+  e.head = place / r.line;
+  const int at = place - e.head * r.line;
+  e.seq = __popc(__ballot_sync(kAll, lane < p.n_seq && r.tiles_end <= at));
+  const int tiles = __shfl_sync(kAll, r.tiles, e.seq);
+  e.y0 = at - (__shfl_sync(kAll, r.tiles_end, e.seq) - tiles);
+  e.y1 = min(tiles, e.y0 + stop - place);
+  e.cut = (int)blockIdx.x - (place - e.y0) / r.per;
+  e.behind = e.y1 == tiles ? r.cuts - 1 - e.cut : 0;
+  return e;
+}
 // Whole warp, pass 1: what the plan kernel finds otherwise; the first CTA leaves what
 // the kernels behind it need.
 __device__ __forceinline__ EmLine em_line1(const EmParams& p, int lane) {
@@ -237,8 +278,17 @@ __device__ __forceinline__ EmLine em_line1(const EmParams& p, int lane) {
     cuts = em_cuts((float)last * (float)p.hkv, 0.5f * tiles * (float)p.hkv, (float)__reduce_max_sync(kAll, longest), most, (float)p.sms, lane);
     return end;
   };
-  EmLine r{c.t0, c.rows, c.keys, c.units1, 0, 0, 0};
+  EmLine r{c.t0, c.rows, c.keys, c.units1};
   r.end = scan(c.units1, (float)c.tiles1, c.longest1, p.cuts1, r.all, r.cuts);
+  if (p.few && p.cuts1 > 1 && !bad) {
+    em_even_line(p, r, lane);
+    const long long line = (long long)r.line * p.hkv;
+    if (!__any_sync(kAll, r.rows > kEmTile / p.g || (r.rows > 0 && r.tiles == 0)) && line >= kEmEven * p.sms && line <= 0x3fffffff) {
+      const int longest = __reduce_max_sync(kAll, r.tiles), most = p.cuts1 - 1;
+      r.per = max(((int)line + p.sms - 1) / p.sms, (longest + most - 1) / most);
+      r.cuts = (longest + r.per - 2) / r.per + 1;
+    }
+  }
   if (blockIdx.x == 0) {
     int n2, cuts2;
     const int end2 = scan(c.units2, (float)c.tiles2, c.longest2, p.cuts2, n2, cuts2);
@@ -252,6 +302,7 @@ __device__ __forceinline__ EmLine em_line1(const EmParams& p, int lane) {
       p.hdr[kMCuts1] = r.cuts;
       p.hdr[kMCuts2] = cuts2;
       p.hdr[kMClaim2] = 0;
+      p.hdr[kMPer] = r.per;
       p.hdr[kMBad] = bad;
     }
   }
@@ -272,6 +323,8 @@ __device__ __forceinline__ EmLine em_line2(const EmParams& p, int lane) {
     r.end = __ldg(p.off2 + lane + 1);
     r.units = r.end - first;
   }
+  r.per = p.n_seq <= 32 ? __ldg(p.hdr + kMPer) : 0;
+  if (r.per) em_even_line(p, r, lane);
   return r;
 }
 
@@ -429,8 +482,11 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         line.all = __ldg(off + p.n_seq);
       }
       const int cuts = line.cuts;
-      const unsigned claims = (unsigned)line.all * p.hkv * cuts;
+      const bool even = PASS == 1 && line.per;
+      const unsigned claims = even ? 0u : (unsigned)line.all * p.hkv * cuts;
       unsigned claim = claim_there();
+      int place = (int)blockIdx.x * line.per;   // even stretches
+      const int stop_at = min(line.line * p.hkv, place + line.per);
       auto copy_rows = [&](uint8_t* dst, int tok, int head, uint64_t* bar) {  // one lane
         for (int hf = 0; hf < HF; ++hf) tma_load_5d(dst + hf * kHalf, &tq, 0, 0, tok, head, hf, bar);
       };
@@ -440,9 +496,21 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         const int slot = ni & 1;
         if (ni >= 2 && !wait(&bars.it_empty[slot], ((ni - 2) >> 1) & 1)) { ok = false; break; }
         EmItem it{};
-        it.done = claim >= claims;
+        it.done = even ? place >= stop_at : claim >= claims;
         int nt_x[2] = {0, 0};
-        if (!it.done) {
+        if (even && !it.done) {
+          const EmStretch e = em_stretch(p, line, place, stop_at, lane);
+          it.seq = e.seq;
+          it.head = e.head;
+          it.cut = e.cut;
+          it.behind = e.behind;
+          it.t0 = __shfl_sync(0xffffffffu, line.t0, e.seq);
+          it.rows = __shfl_sync(0xffffffffu, line.rows, e.seq);
+          it.keys = __shfl_sync(0xffffffffu, line.keys, e.seq);
+          it.y0 = it.xs[0] = it.xs[1] = e.y0;
+          it.y1 = it.xe[0] = e.y1;   // rows of the second X tile: none
+          place += e.y1 - e.y0;
+        } else if (!it.done) {
           const unsigned u = claim / (unsigned)cuts, unit = u / (unsigned)p.hkv;
           it.cut = (int)(claim - u * cuts);
           it.head = (int)(u - unit * p.hkv);
@@ -490,7 +558,7 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         __syncwarp();
         ++ni;
         if (it.done) break;
-        claim_next();
+        if (!even) claim_next();
         if (it.y0 >= it.y1) continue;
         int ids = PASS == 1 ? key_blocks(it.seq, it.y0, it.keys) : key_blocks(it.seq, it.x0 / kEmTile, it.keys);
         int ids_next = PASS == 1 ? key_blocks(it.seq, it.y0 + 4, it.keys) : 0;
@@ -600,10 +668,14 @@ em_pass_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         const int slot = ni & 1;
         if (stop() || !wait(&bars.it_full[slot], (ni >> 1) & 1)) { ok = false; break; }
         const int seq = work[slot].seq, head = work[slot].head, keys = work[slot].keys, y0 = work[slot].y0, y1 = work[slot].y1;
-        const int done = work[slot].done;
+        const int done = work[slot].done, behind = work[slot].behind, cut = work[slot].cut, t0 = work[slot].t0, rows = work[slot].rows;
         __syncwarp();
         if (lane == 0) mbar_arrive(&bars.it_empty[slot]);
         if (done) break;
+        for (int i = lane; behind > 0 && i < rows * p.g; i += 32) {   // even stretches: one row tile
+          const size_t at = (size_t)(t0 + i / p.g) * p.hq + head * p.g + i % p.g;
+          for (int k = 2 * (cut + 1); k < 2 * (cut + 1 + behind); ++k) p.parts[(size_t)k * p.n_tokens * p.hq + at] = make_float2(0.f, 0.f);
+        }
         if (y0 >= y1) continue;
         int ids = key_blocks(seq, y0, keys), ids_next = key_blocks(seq, y0 + 4, keys);
         for (int j = y0; j < y1; ++j) {
@@ -835,12 +907,6 @@ struct EkItem {
   int y0, y1, pad[2];           // key tiles
 };
 
-// Key tiles that row tile i of a sequence sees.
-__device__ __forceinline__ int ek_tiles(const EmParams& p, int rows, int keys, int i, int tt) {
-  const int lim = p.causal ? min(max(keys - rows + min(rows, (i + 1) * tt), 0), keys) : keys;
-  return (lim + kEmTile - 1) / kEmTile;
-}
-
 template <int D>
 __global__ void __launch_bounds__(kEmThreads, 1)
 em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk) {
@@ -909,16 +975,30 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
       claim_next();
       const EmLine line = em_line2(p, lane);
       const int cuts = line.cuts;
+      const bool even = line.per != 0;
       const unsigned claims = (unsigned)line.all * p.hkv * cuts;
       unsigned claim = claim_there();
+      int place = (int)blockIdx.x * line.per;
+      const int stop_at = min(line.line * p.hkv, place + line.per);
       int n = 0, nx = 0, armed = -1;
       for (int ni = 0;; ++ni, claim = claim_there()) {
         if (stop()) { ok = false; break; }
         const int slot = ni & 1;
         if (ni >= 2 && !wait(&bars.it_empty[slot], ((ni - 2) >> 1) & 1)) { ok = false; break; }
         EkItem it{};
-        it.done = claim >= claims;
-        if (!it.done) {
+        it.done = even ? place >= stop_at : claim >= claims;
+        if (even && !it.done) {
+          const EmStretch e = em_stretch(p, line, place, stop_at, lane);
+          it.seq = e.seq;
+          it.head = e.head;
+          it.unit = __shfl_sync(0xffffffffu, line.end - line.units, e.seq);
+          it.t0 = __shfl_sync(0xffffffffu, line.t0, e.seq);
+          it.rows = __shfl_sync(0xffffffffu, line.rows, e.seq);
+          it.keys = __shfl_sync(0xffffffffu, line.keys, e.seq);
+          it.y0 = e.y0;
+          it.y1 = e.y1;
+          place += e.y1 - e.y0;
+        } else if (!it.done) {
           const unsigned u = claim / (unsigned)cuts, unit = u / (unsigned)p.hkv;
           const int cut = (int)(claim - u * cuts);
           it.head = (int)(u - unit * p.hkv);
@@ -939,7 +1019,7 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
         }
         __syncwarp();
         if (it.done) break;
-        claim_next();
+        if (!even) claim_next();
         if (it.y0 >= it.y1) continue;
         int ids = key_blocks(it.seq, it.y0, it.keys), ids_next = key_blocks(it.seq, it.y0 + 4, it.keys);
         const int xs = nx & 1;

@@ -88,6 +88,19 @@ def test_key_tiles_that_rows_pass_by():
     check(s, call(s, True), True)
 
 
+@pytest.mark.parametrize("lens, new, hq, hkv, d", [
+    ([30000, 1, 12000], [32, 0, 5], 16, 8, 64),           # a pair's tiles over more CTAs than the others'
+    ([6100, 900, 0, 2000, 129], [4, 1, 0, 3, 4], 32, 32, 64),
+    ([5000, 8000, 128], [7, 1, 12], 20, 20, 128),
+    ([6100, 900, 0, 2000], [4, 1, 2, 3], 32, 32, 64),     # a row that sees nothing: items instead of stretches
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_even_stretches(lens, new, hq, hkv, d, causal):
+    """Enough key tiles for few rows that every CTA takes an even stretch of them."""
+    s = chunk(lens, new, hq, hkv, d, seed=len(lens), pad=1)
+    check(s, call(s, causal), causal)
+
+
 def test_scores_out_of_the_reference():
     """The first keys of a row say nothing about the later ones: scores that jump by hundreds, up and down."""
     s = chunk([900, 640], [200, 3], 4, 2, 64)
