@@ -7,9 +7,9 @@
 // over the order-preserving bits of the masses, three digits of 11, 11 and 10
 // bits, each CTA with the histogram of its own slice, added up through
 // distributed shared memory.  A thread's masses stay in registers, so a sequence is
-// read once (up to 131,072 tokens on eight CTAs).  131,072 tokens: 31 us, a chain of
-// loads (5), for each digit a histogram, an exchange and a scan (18), and the
-// writing in order (6); 32 sequences of some thousand tokens: 12 us.
+// read once (up to 131,072 tokens on eight CTAs).  131,072 tokens: 25 us, a chain of
+// loads (5), for each digit a histogram, an exchange and a scan, and the writing in
+// order (6); 32 sequences of 6,144 tokens: 9 us.
 //
 // kvs_compact: row i of a sequence's kept tokens moves from place idx[i] to
 // place i, in every layer's slabs.  Places only fall (idx[i] >= i), blocks in
@@ -797,13 +797,18 @@ extern "C" kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, cons
     return fail(KVS_ERR_INVALID_ARG, "keep_heavy: null pointer");
   if (kvs_status st = check_pool_device(pool, "keep_heavy"); st != KVS_OK) return st;
   KeepParams p{mass_dev, seq_len_dev, budget_dev, idx_out_dev, idx_off_dev, pool->status, n_seq, (int)most, n_first, n_recent};
-  // a CTA for every 4,096 tokens of the table row, eight at most
-  int ranks = 1;
-  while (ranks < 8 && most > 4096ll * ranks) ranks *= 2;
-  auto kern = ranks == 1   ? keep_heavy_kernel<1, 4>
-              : ranks == 2 ? keep_heavy_kernel<2, 4>
-              : ranks == 4 ? keep_heavy_kernel<4, 4>
-                           : keep_heavy_kernel<8, 16>;
+  // Few CTAs with their masses in registers: exchanges between CTAs cost more than
+  // longer slices.  (32 sequences of 6,144 tokens: one CTA 9.4 us, two 11.1; 16 of
+  // 32,000: four 15.9, eight, which no longer are resident together, 44; one of 65,000:
+  // four with sixteen masses a thread 20.2, eight 23.2; but one of 16,000: two 13.5,
+  // four 12.7.)
+  const int ranks = most <= 8192 ? 1 : most <= 16384 ? 2 : most <= 65536 ? 4 : 8;
+  auto kern = most <= 4096    ? keep_heavy_kernel<1, 4>
+              : most <= 8192  ? keep_heavy_kernel<1, 8>
+              : most <= 16384 ? keep_heavy_kernel<2, 8>
+              : most <= 32768 ? keep_heavy_kernel<4, 8>
+              : most <= 65536 ? keep_heavy_kernel<4, 16>
+                              : keep_heavy_kernel<8, 16>;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)n_seq * ranks);
   cfg.blockDim = dim3(kKhThreads);

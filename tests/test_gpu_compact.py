@@ -41,6 +41,9 @@ def keep(pool, mass, lens, budget, first, recent, max_blocks):
     ("bf16", [1024, 1025, 4096, 4095], [1, 1024, 4000, 100], 7, 0),
     ("bf16", [20000, 131, 16385, 9000], [1234, 0, 16384, 8999], 3, 77),
     ("q4", [1500, 256, 700], [600, 256, 699], 0, 31),
+    ("bf16", [8000, 5000], [2000, 4999], 16, 256),
+    ("bf16", [12000, 8193, 30], [3000, 8192, 1], 16, 256),
+    ("bf16", [50000, 40000], [1000, 39999], 64, 1024),
     ("bf16", [150000], [70000], 11, 13),           # beyond what eight CTAs hold in registers
 ])
 @pytest.mark.parametrize("values", ["spread", "ties", "signed"])
