@@ -15,7 +15,8 @@
 // Both are em_pass_kernel: two tiles of 128 rows (X) go to tensor memory, tiles of the
 // other operand (Y) stream through a TMA ring past both, and four warpgroups turn S,
 // in tensor memory too, into sums.  Scores and sums are float32.  Where a sequence has
-// a tile of rows at most, pass 2 is em_keys_kernel: the rows stay and the keys stream.
+// a tile of rows at most, pass 2 is em_keys_kernel: the rows stay and the keys stream;
+// short calls of that kind are one kernel (em_whole_kernel).
 //
 // Items (a pair of X tiles, a range of Y tiles) are claimed in order, the longest
 // first; with few rows and many keys, every CTA takes an even stretch of key tiles
@@ -71,7 +72,7 @@ struct EmParams {
   float2* parts;      // pass 1: [cut][column half][n_tokens][hq] {reference, sum}
   float* nlse;        // [hkv][n_tokens][g] -log2 of the rows' sums
   float* sums;        // pass 2: [cut][column half][hkv][n_seq][most], few rows: [row tile][column half][hkv][most]
-  int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2, sms, few;   // cuts: the most there is room for; few: em_keys_kernel is pass 2
+  int n_tokens, n_seq, max_blocks, capacity, g, hkv, hq, causal, slab_rows, most, cuts1, cuts2, sms, few, whole;   // cuts: the most there is room for; few: em_keys_kernel is pass 2; whole: CTAs of em_whole_kernel
   float scale_log2;
   int* tickets;       // calls without a plan: the claims of pass 1, zero between calls
 };
@@ -1226,6 +1227,283 @@ em_keys_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUten
   }
 }
 
+// --------------------------------------------------- short calls: one kernel
+// A row tile of one KV head a CTA, for both passes: S = Q K^T over the key tiles, the
+// row sums of two halves and of every other tile joined in shared memory, then S^T =
+// K Q^T over the same key tiles again, whose key sums the last kernel adds up.
+struct EwBars {
+  uint64_t full[8], empty[8], x_full;
+  uint64_t s_full[2][2], s_empty[2][2];
+  uint64_t fin[2];
+};
+
+template <int D>
+__global__ void __launch_bounds__(kEmThreads, 1)
+em_whole_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk) {
+  constexpr int HF = D / 64, ST = em_stages<D>(), kTile = em_tile_bytes<D>(), kHalf = kEmTile * 128;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ EwBars bars;
+  __shared__ EkItem work;
+  __shared__ float2 states[4][kEmTile];
+  __shared__ __align__(16) EmCols cl;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_abort;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    prefetch_tmap(&tq);
+    prefetch_tmap(&tk);
+    for (int i = 0; i < ST; ++i) {
+      mbar_init(&bars.full[i], 1);
+      mbar_init(&bars.empty[i], 2);      // both product warps
+    }
+    mbar_init(&bars.x_full, 1);
+    for (int i = 0; i < 2; ++i) {
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&bars.s_full[i][b], 1);
+        mbar_init(&bars.s_empty[i][b], kEmSumWarps / 2);
+      }
+      mbar_init(&bars.fin[i], 1);
+    }
+    s_abort = 0;
+    cl.least = 0x7fffffff;
+    fence_barrier_init();
+  }
+  if (warp == 0) {
+    tmem_alloc(&s_tmem, kEmCols);
+    tmem_relinquish();
+  }
+  uint8_t* base = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  auto ring = [&](int i) { return base + kTile * (2 + i); };
+  tc_fence_before();
+  const int tt = kEmTile / p.g;
+  if (warp == 1) {
+    // this CTA's row tile, a lane a sequence
+    constexpr unsigned kAll = 0xffffffffu;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    EmCount c{};
+    if (lane < p.n_seq) c = em_count(p, lane);
+    const bool bad = __any_sync(kAll, c.bad);
+    int end = c.units2;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kAll, end, o);
+      end += lane >= o ? x : 0;
+    }
+    const int units = __shfl_sync(kAll, end, 31), unit = (int)blockIdx.x / p.hkv;
+    const int seq = __popc(__ballot_sync(kAll, lane < p.n_seq && end <= unit)) & 31;
+    EkItem it{};
+    it.seq = seq;
+    it.head = (int)blockIdx.x - unit * p.hkv;
+    it.unit = unit;
+    it.tile = unit - __shfl_sync(kAll, end - c.units2, seq);
+    it.t0 = __shfl_sync(kAll, c.t0, seq);
+    it.rows = __shfl_sync(kAll, c.rows, seq);
+    it.keys = __shfl_sync(kAll, c.keys, seq);
+    it.y1 = bad || unit >= units ? 0 : ek_tiles(p, it.rows, it.keys, it.tile, tt);
+    if (lane == 0) work = it;
+    if (blockIdx.x == 0) {
+      if (lane < p.n_seq) {
+        p.seq[lane] = make_int4(c.t0, c.rows, c.keys, 0);
+        p.off2[lane] = end - c.units2;
+      }
+      if (lane == 0) {
+        if (bad) set_err(p.status, KVS_DEVERR_JOB);
+        p.hdr[kMBad] = bad;
+        p.hdr[kMCuts2] = 1;
+      }
+    }
+  }
+  __syncthreads();
+  tc_fence_after();
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const uint32_t tmem = s_tmem;
+  const EkItem it = work;
+  const int nt = it.y1;
+  auto stop = [&]() { return __any_sync(0xffffffffu, s_abort != 0); };
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    const bool ok = mbar_wait_bounded(bar, parity, p.status);
+    return __all_sync(0xffffffffu, ok);
+  };
+
+  if (nt == 0) {
+    // nothing to do
+  } else if (warp >= kEmSumWarps) {
+    bool ok = true;
+    if (warp == kEmTma || warp == kEmTma + 1) {
+      // ----------------------------- the rows, and half of every key tile each
+      const bool first = warp == kEmTma;
+      int armed = -1;
+      if (first && lane == 0) {
+        mbar_arrive_expect_tx(&bars.x_full, (uint32_t)(HF * tt * p.g * 128));
+        for (int hf = 0; hf < HF; ++hf) tma_load_5d(base + hf * kHalf, &tq, 0, 0, it.t0 + it.tile * tt, it.head, hf, &bars.x_full);
+      }
+      __syncwarp();
+      int ids = 0;
+      for (int n = 0; n < 2 * nt; ++n) {
+        const int j = n < nt ? n : n - nt, s = n % ST;
+        if ((j & 3) == 0) ids = em_blocks(p, it.seq, j, it.keys, lane);
+        if (n >= ST && !wait(&bars.empty[s], ((n - ST) / ST) & 1)) { ok = false; break; }
+        if (first && lane == 0) mbar_arrive_expect_tx(&bars.full[s], kTile);
+        __syncwarp();
+        // (the barrier counts the copies of both warps, before or after it is armed)
+        em_copy_keys<HF>(p, tk, ring(s), __shfl_sync(0xffffffffu, ids, (lane & 7) + 8 * (j & 3)), it.head, &bars.full[s], lane, first ? 0 : 4,
+                         first ? 4 : 8);
+        armed = n;
+      }
+      if (!ok) {   // copies in flight land before the shared memory goes away
+        if (first) {
+          for (int m = max(0, armed - ST + 1); m <= armed; ++m) mbar_drain(&bars.full[m % ST], (m / ST) & 1);
+          mbar_drain(&bars.x_full, 0);
+        } else {
+          const long long t0 = clock64();
+          while (clock64() - t0 < (1ll << 24)) {
+          }
+        }
+      }
+    } else {
+      // ------------------------------- products of every other tile
+      const int x = warp - kEmMma;
+      constexpr uint32_t idS = umma_idesc_bf16(128, 128, false, false);
+      constexpr uint32_t kHi = ex_desc_hi(1024);
+      const uint32_t xa = ex_desc_lo(smem_u32(base), 16), y_lo = ex_desc_lo(smem_u32(ring(0)), 16);
+      int b = 0, s = 0;
+      uint32_t full_par = 0, free_par = 1;   // a fresh buffer counts as handed back
+      ok = wait(&bars.x_full, 0);
+      for (int n = 0; ok && n < 2 * nt; ++n) {
+        if (stop() || !wait(&bars.full[s], full_par)) { ok = false; break; }
+        if ((n & 1) == x) {
+          if (!wait(&bars.s_empty[x][b], free_par)) { ok = false; break; }
+          tc_fence_after();
+          if (elect_one()) {
+            const uint32_t ya = y_lo + s * (kTile / 16), d = tmem + 128u * (2 * x + b);
+            const uint32_t ra = n < nt ? xa : ya, rb = n < nt ? ya : xa;   // rows and columns of the product
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t o = ((kk >> 2) * kHalf + (kk & 3) * 32) / 16;
+              ex_mma_ss(d, ra + o, rb + o, kHi, idS, kk > 0);
+            }
+            umma_commit(&bars.s_full[x][b]);
+            umma_commit(&bars.empty[s]);
+          }
+          __syncwarp();
+          if (b) free_par ^= 1u;
+          b ^= 1;
+        } else {
+          if (lane == 0) mbar_arrive(&bars.empty[s]);
+          __syncwarp();
+        }
+        if (++s == ST) {
+          s = 0;
+          full_par ^= 1u;
+        }
+      }
+      // every product issued has completed before the tensor memory is released
+      if (elect_one()) umma_commit(&bars.fin[x]);
+      __syncwarp();
+      mbar_wait_bounded(&bars.fin[x], 0, p.status);
+    }
+    if (!ok) s_abort = 1;
+  } else {
+    // ------------------------------------------------------------ sums
+    const int x = (warp >> 2) & 1, half = warp >> 3, r = (warp & 3) * 32 + lane;
+    const uint32_t tS = tmem + ((uint32_t)((warp & 3) * 32) << 16) + 256u * x + 64u * half;
+    const float2 sc2 = make_float2(p.scale_log2, p.scale_log2);
+    int b = 0;
+    uint32_t s_par = 0;
+    uint32_t v[64];
+    auto scores = [&](bool wanted) {
+      if (stop() || !wait(&bars.s_full[x][b], s_par)) return false;
+      tc_fence_after();
+      if (wanted) {
+        tmem_ld32_issue(tS + 128u * b, v);
+        tmem_ld32_issue(tS + 128u * b + 32, v + 32);
+        tmem_ld32x2_wait(v, v + 32);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bars.s_empty[x][b]);
+      if (b) s_par ^= 1u;
+      b ^= 1;
+      return true;
+    };
+    const int tok = it.tile * tt + r / p.g;               // this row's token
+    const bool live = r / p.g < tt && tok < it.rows;
+    const int lim = !live ? 0 : p.causal ? min(it.keys - it.rows + tok + 1, it.keys) : it.keys;   // keys that it sees
+    const bool any_live = __any_sync(0xffffffffu, live);
+    bool ok = true;
+    float m = 0.f, l = 0.f;
+    for (int n = x; n < nt; n += 2) {
+      if (!scores(any_live)) { ok = false; break; }
+      if (!any_live) continue;
+      const int key0 = n * kEmTile + 64 * half;
+#pragma unroll
+      for (int i = 0; i < 64; ++i)
+        if (key0 + i >= lim) v[i] = 0xff800000u;
+      const bool fresh = n == x;
+      float sum = fresh ? INFINITY : em_sum_up(v, sc2, [&](int) { return make_float2(-m, -m); });
+      if (__any_sync(0xffffffffu, !(sum < 0x1p60f))) {   // as in em_pass_kernel
+        float top = __uint_as_float(v[0]);
+#pragma unroll
+        for (int i = 1; i < 64; ++i) top = fmaxf(top, __uint_as_float(v[i]));
+        top *= p.scale_log2;
+        if (!(sum < 0x1p60f)) {
+          if (!fresh) l *= fast_exp2(m - top);
+          m = top == -INFINITY ? 0.f : top;
+        }
+        sum = em_sum_up(v, sc2, [&](int) { return make_float2(-m, -m); });
+      }
+      l += sum;
+    }
+    states[2 * x + half][r] = make_float2(m, l);
+    asm volatile("bar.sync 1, %0;" ::"n"(kEmSumWarps * 32) : "memory");
+    if (warp < 4) {
+      float top = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (states[i][r].y > 0.f) top = fmaxf(top, states[i][r].x);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (states[i][r].y > 0.f) sum += states[i][r].y * fast_exp2(states[i][r].x - top);
+      const bool seen = live && sum > 0.f;
+      cl.nlse[r] = seen ? -(top + log2f(sum)) : -INFINITY;
+      const int to = seen ? max(lim, 0) : 0, least = __reduce_min_sync(0xffffffffu, to);
+      cl.lim[r] = to;
+      if (lane == 0) atomicMin(&cl.least, least);
+    }
+    asm volatile("bar.sync 1, %0;" ::"n"(kEmSumWarps * 32) : "memory");
+    // columns behind the tile's last row hold nothing: whole halves are passed by
+    const bool any = 64 * half < min(tt, it.rows - it.tile * tt) * p.g;
+    float* out = p.sums + ((size_t)(2 * it.unit + half) * p.hkv + it.head) * p.most;
+    for (int n = nt + ((nt ^ x) & 1); ok && n < 2 * nt; n += 2) {
+      if (!scores(any)) { ok = false; break; }
+      const int key = (n - nt) * kEmTile + r;
+      float sum = 0.f;
+      if (any) {
+        if ((n - nt) * kEmTile + (warp & 3) * 32 + 31 >= cl.least) {
+#pragma unroll
+          for (int i = 0; i < 64; i += 4) {
+            const int4 u = *reinterpret_cast<const int4*>(cl.lim + 64 * half + i);
+            if (key >= u.x) v[i] = 0xff800000u;
+            if (key >= u.y) v[i + 1] = 0xff800000u;
+            if (key >= u.z) v[i + 2] = 0xff800000u;
+            if (key >= u.w) v[i + 3] = 0xff800000u;
+          }
+        }
+        sum = em_sum_up(v, sc2, [&](int i) { return *reinterpret_cast<const float2*>(cl.nlse + 64 * half + i); });
+      }
+      if (key < it.keys) out[key] = sum;
+    }
+    if (!ok) s_abort = 1;
+  }
+  asm volatile("griddepcontrol.launch_dependents;");
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) {
+    tc_fence_after();
+    tmem_dealloc(tmem, kEmCols);
+  }
+}
+
 // Joins the parts of every row: -log2 of its whole sum, -inf where it has none.
 __global__ void __launch_bounds__(256) em_join_kernel(const __grid_constant__ EmParams p) {
   pdl_enter();
@@ -1352,16 +1630,19 @@ kvs_status em_run(const kvs_pool* pool, int layer, const EmParams& p, const CUte
                   float* mass, cudaStream_t stream) {
   if (!smem_limit_once<em_pass_kernel<D, 1>>(em_smem<D>(), pool->device) ||
       !smem_limit_once<em_pass_kernel<D, 2>>(em_smem<D>(), pool->device) ||
-      !smem_limit_once<em_keys_kernel<D>>(em_smem<D>(), pool->device))
+      !smem_limit_once<em_keys_kernel<D>>(em_smem<D>(), pool->device) ||
+      !smem_limit_once<em_whole_kernel<D>>(em_smem<D>(), pool->device))
     return fail(KVS_ERR_CUDA, "extend_mass: cannot raise the shared-memory limit");
   const CUtensorMap& tk = D == 128 ? pool->tk1[layer] : pool->tk[layer];
   const dim3 grid((unsigned)pool->num_sms);
   bool ok = true;
-  if (p.n_tokens > 0)
+  if (p.whole)
+    ok = em_launch(em_whole_kernel<D>, dim3((unsigned)p.whole), dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess;
+  else if (p.n_tokens > 0)
     ok = em_launch(em_pass_kernel<D, 1>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess &&
          em_launch(em_join_kernel, dim3((unsigned)(((long long)p.n_tokens * p.hq + 255) / 256)), dim3(256), 0, stream, p) == cudaSuccess &&
          em_launch(p.few ? em_keys_kernel<D> : em_pass_kernel<D, 2>, grid, dim3(kEmThreads), em_smem<D>(), stream, p, tq, tk) == cudaSuccess;
-  if (ok && p.n_tokens > 0) count_launch(3);
+  if (ok && p.n_tokens > 0) count_launch(p.whole ? 1 : 3);
   if (ok && em_launch(em_add_kernel, dim3((unsigned)((p.most + 255) / 256), (unsigned)p.n_seq), dim3(256), 0, stream, p, mass_in, carry,
                       mass) == cudaSuccess)
     count_launch();
@@ -1438,7 +1719,15 @@ extern "C" kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void*
     return fail(KVS_ERR_CUDA, "extend_mass: cuTensorMapEncodeTiled failed for q");
   // a warp of pass 1 counts up to 32 sequences for itself (1 row after 1,000 tokens
   // 19.0 us with a plan, 17.1 without; 16 x 4 after 1,000, 40 / 8 heads: 31.9, 27.3)
-  if (n_seq <= 32 && n_tokens > 0) {
+  // One kernel for both passes where keys are few, or rows and heads enough for as many
+  // CTAs as make up for them (us, whole and in two passes: 16 x 4 rows after 1,000
+  // tokens, 40 / 8 heads, 17.2 and 28.1; 4 x 16 after 500, 16 / 2, 12.3 and 17.9; 16 x 4
+  // after 4,000, 40 / 8, 52.8 and 62.9; but 4 x 16 after 2,000, 32 / 8 of 64 channels,
+  // 25.2 and 21.9; after 4,000 of 128 channels 45 and 28).
+  const long long ctas = ((long long)n_tokens / (kEmTile / p.g) + n_seq) * p.hkv, tiles = (p.most + kEmTile - 1) / kEmTile;
+  if (p.few && n_tokens > 0 && n_seq <= 32 && ctas <= 4ll * p.sms && (tiles <= 8 || (tiles <= 32 && ctas >= 4 * tiles))) {
+    p.whole = (int)ctas;
+  } else if (n_seq <= 32 && n_tokens > 0) {
     p.tickets = pool->tickets;
   } else {
     if (launch_pdl(em_plan_kernel, dim3(1), dim3(1024), stream, p) != cudaSuccess) return check_launch("extend_mass");

@@ -101,6 +101,56 @@ def test_even_stretches(lens, new, hq, hkv, d, causal):
     check(s, call(s, causal), causal)
 
 
+@pytest.mark.parametrize("lens, new, hq, hkv, d", [
+    ([300, 40, 7, 0], [20, 1, 1, 0], 16, 2, 128),         # two row tiles beside shorter sequences
+    ([1, 16, 128, 129, 127], [1, 16, 3, 2, 1], 8, 8, 64),
+    ([900, 10, 1000], [9, 12, 1], 12, 1, 64),             # rows in front of the first key
+    ([3900, 4000, 1, 257], [4, 2, 1, 4], 40, 8, 128),     # more tiles than stages, both passes
+    ([500] * 30, [4] * 30, 40, 8, 64),                    # more CTAs than SMs
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_short_calls(lens, new, hq, hkv, d, causal):
+    """Few rows and short tables: both passes in one kernel."""
+    s = chunk(lens, new, hq, hkv, d, seed=len(lens), pad=1)
+    mass = call(s, causal)
+    check(s, mass, causal)
+    assert torch.equal(call(s, causal), mass)
+
+
+def test_short_calls_far_scores_bad_blocks_offsets_and_graphs():
+    s = chunk([900, 640, 30], [3, 3, 3], 4, 2, 64)
+    for b in range(s["k"][0].shape[0]):
+        s["k"][0][b] *= 30 if b % 3 == 0 else 0.1 if b % 3 == 1 else 1
+    s["values"][0] = np.nan_to_num(f64(s["k"][0]))
+    check(s, call(s, True), True)
+    ws = workspace(K.kvs_extend_mass_workspace_size(s["pool"], s["T"], 3, s["mb"], 4)).fill_(0xC3)
+    off, table, lens, mass, q = i32(s["off"]), i32(s["table"]), i32(s["lens"]), torch.full_like(s["mass_in"], -3.0), s["q"].contiguous()
+    run = lambda: K.kvs_extend_mass(s["pool"], 0, q, s["T"], off, 4, table, s["mb"], lens, 3, True, s["scale"], s["mass_in"], 0.75, mass, ws)  # noqa: E731
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        run()
+        side.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            run()
+        q.neg_()
+        for _ in range(3):
+            graph.replay()
+        side.synchronize()
+    s["q"] = q
+    check(s, mass, True)
+    values = s["values"][0]
+    s["table"][0, 1] = -7
+    bad = call(s, True)
+    assert K.kvs_pool_check(s["pool"]) == K.KVS_DEVERR_BLOCK_ID
+    s["table"][0, 1] = s["cap"]
+    s["values"][0] = np.concatenate([values, np.zeros((1,) + values.shape[1:])])   # zero keys
+    check(s, bad, True)
+    s["off"] = np.array([0, 3, 2, 9])
+    mass = call(s, True)
+    assert K.kvs_pool_check(s["pool"]) & K.KVS_DEVERR_JOB and (mass == -3).all()
+
+
 def test_scores_out_of_the_reference():
     """The first keys of a row say nothing about the later ones: scores that jump by hundreds, up and down."""
     s = chunk([900, 640], [200, 3], 4, 2, 64)
