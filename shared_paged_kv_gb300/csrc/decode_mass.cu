@@ -14,7 +14,7 @@
 // ends of several (sequence, KV head) pairs, and a pair several CTAs, whose parts
 // the last one to arrive joins in their order.  A warp takes every W-th unit of
 // its CTA's stretch and brings it with its own ring of TMA copies, which run on
-// across the pairs' borders.  Up to 32 sequences are placed by every warp for
+// across the pairs' borders.  Up to 64 sequences are placed by every warp for
 // itself; there, where all pairs fit, each begins a CTA.
 //
 // Tokens are the 16 rows of the products, query heads the 8 (or twice 8)
@@ -203,22 +203,25 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     const int least = (int)sqrtf((F::mx ? 0.03f : 0.06f) * (float)p.g * (float)total / (float)p.n_seq);
     return (long long)max(max(W, least), quotient((long long)total * p.hkv + gridDim.x - 1, gridDim.x));
   };
-  if (p.n_seq <= 32) {
-    // every warp for itself, a lane a sequence
-    const int real = lane < p.n_seq ? dm_span<UT>(p, lane).units : 0;
-    per = share(__reduce_add_sync(0xffffffffu, real));
+  if (p.n_seq <= 64) {
+    // every warp for itself, a lane two sequences (64 of 500 tokens, 16 / 2 heads: 13.8 us,
+    // 16.1 by the whole CTA)
+    const int a0 = 2 * lane;
+    const int real0 = a0 < p.n_seq ? dm_span<UT>(p, a0).units : 0, real1 = a0 + 1 < p.n_seq ? dm_span<UT>(p, a0 + 1).units : 0;
+    per = share(__reduce_add_sync(0xffffffffu, real0 + real1));
     // Where they fit, every pair begins a CTA (its units are rounded up to whole
     // CTAs): a second pair costs a CTA more than a unit or two of every warp (four
     // sequences of 300 tokens, 8 / 2 heads of 64 channels, with the masses: 8.4 us,
     // 10.1 evenly).
     const int whole = (int)((per + W - 1) / W) * W;
-    int n = real;
+    int n0 = real0, n1 = real1;
     bool rounded = false;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
-      const int m = whole + k * W, up = (real + m - 1) / m;
-      if ((long long)__reduce_add_sync(0xffffffffu, up) * p.hkv <= gridDim.x) {
-        n = up * m;
+      const int m = whole + k * W, up0 = (real0 + m - 1) / m, up1 = (real1 + m - 1) / m;
+      if ((long long)__reduce_add_sync(0xffffffffu, up0 + up1) * p.hkv <= gridDim.x) {
+        n0 = up0 * m;
+        n1 = up1 * m;
         per = m;
         rounded = true;
         break;
@@ -228,9 +231,10 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     // sequences that share 4,096 of 5,400 tokens, 16 / 2 heads: 26.2 us, 28.1 without).
     if (!rounded) {
       gap = 4 * W;
-      n = real ? real + gap : 0;
+      n0 = real0 ? real0 + gap : 0;
+      n1 = real1 ? real1 + gap : 0;
     }
-    int end = n, units = real;   // places and units up to this lane's sequence
+    int end = n0 + n1, units = real0 + real1;   // places and units up to this lane's sequences, both among them
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(0xffffffffu, end, o), y = __shfl_up_sync(0xffffffffu, units, o);
@@ -244,11 +248,15 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
     auto locate = [&](long long u, DmAt& at, int& place) {
       at.h = quotient(u, per_head);
       const int r = (int)(u - (long long)at.h * per_head);
-      at.a = __popc(__ballot_sync(0xffffffffu, lane < p.n_seq && end <= r)) & 31;
-      place = r - __shfl_sync(0xffffffffu, end - n, at.a) - gap;
-      at.units = __shfl_sync(0xffffffffu, real, at.a);
+      const int l = __popc(__ballot_sync(0xffffffffu, end <= r)) & 31;
+      const int from = __shfl_sync(0xffffffffu, end - n0 - n1, l), size = __shfl_sync(0xffffffffu, n0, l);
+      const int u_0 = __shfl_sync(0xffffffffu, real0, l), u_1 = __shfl_sync(0xffffffffu, real1, l);
+      const bool second = r >= from + size;
+      at.a = 2 * l + second;
+      place = r - from - (second ? size : 0) - gap;
+      at.units = second ? u_1 : u_0;
       at.b = min(max(place, 0), at.units);
-      return (long long)at.h * units_head + __shfl_sync(0xffffffffu, units - real, at.a) + at.b;
+      return (long long)at.h * units_head + __shfl_sync(0xffffffffu, units - real0 - real1, l) + (second ? u_0 : 0) + at.b;
     };
     const long long u0 = per * blockIdx.x, u1 = min(places, u0 + per);
     if (u0 < u1) {

@@ -130,6 +130,15 @@ def test_many_short_sequences(kind):
 
 
 @pytest.mark.parametrize("kind", ["bf16", "mx4"])
+@pytest.mark.parametrize("n, most", [(31, 900), (32, 300), (33, 700), (63, 200), (64, 1500), (65, 400)])
+def test_sequences_around_what_a_warp_places(kind, n, most):
+    lens = np.random.default_rng(n).integers(0, most, n)
+    lens[[0, n // 2, n - 1]] = 0, 1, most
+    s = make(kind, lens.tolist(), 8, 2, 128 if kind == "mx4" else 64, seed=n)
+    check(s, *call(s))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "mx4"])
 def test_mass_forms(kind):
     """No earlier masses, in place, carried whole; no masses at all (microscaled); twice the same to the bit."""
     s = make(kind, [700, 33], 8, 2, 128)
