@@ -55,7 +55,7 @@ namespace {
 
 enum { kFmtBf16x64, kFmtBf16x128, kFmtMx };
 
-constexpr int kDmMaxGroup = 16, kDmMaxStages = 6, kDmMaxCtas = 3, kDmJoin = 8;
+constexpr int kDmMaxGroup = 16, kDmMaxStages = 4, kDmMaxCtas = 3, kDmJoin = 8;
 
 template <int FMT, int NT>
 struct Dm {   // what a format and the number of 8-column tiles fix
