@@ -41,7 +41,7 @@
 // part from L2 (6.5 TB/s), bound by a unit's chain of products and exponentials;
 // four of 350, 8 / 2 of 64 channels: 8.7 us, start, four units, arrival, join and the
 // second kernel, each a trip to memory.  In 4 bits: twelve of 4,000 to 8,191, 32 / 8
-// (*): 29 us; eight of 16,384 to 32,768: 72 us, 2.7 TB/s, bound by issue slots (52 %)
+// (*): 29 us; eight of 16,384 to 32,768: 72 us, 3.1 TB/s, bound by issue slots (52 %)
 // and the conversions.
 #include <algorithm>
 #include <cmath>

@@ -1277,34 +1277,47 @@ em_whole_kernel(const __grid_constant__ EmParams p, const __grid_constant__ CUte
   tc_fence_before();
   const int tt = kEmTile / p.g;
   if (warp == 1) {
-    // this CTA's row tile, a lane a sequence
+    // this CTA's row tile, a lane two sequences
     constexpr unsigned kAll = 0xffffffffu;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    EmCount c{};
-    if (lane < p.n_seq) c = em_count(p, lane);
-    const bool bad = __any_sync(kAll, c.bad);
-    int end = c.units2;
+    const int a = 2 * lane;
+    EmCount c0{}, c1{};
+    if (a < p.n_seq) c0 = em_count(p, a);
+    if (a + 1 < p.n_seq) c1 = em_count(p, a + 1);
+    const bool bad = __any_sync(kAll, c0.bad | c1.bad);
+    int end = c0.units2 + c1.units2;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int x = __shfl_up_sync(kAll, end, o);
       end += lane >= o ? x : 0;
     }
+    const int begin = end - c0.units2 - c1.units2, middle = begin + c0.units2;   // units before these sequences, before the second
     const int units = __shfl_sync(kAll, end, 31), unit = (int)blockIdx.x / p.hkv;
-    const int seq = __popc(__ballot_sync(kAll, lane < p.n_seq && end <= unit)) & 31;
+    const int l = __popc(__ballot_sync(kAll, end <= unit)) & 31;
+    const bool second = unit >= __shfl_sync(kAll, middle, l);
+    auto of = [&](int x0, int x1) {   // of the unit's sequence
+      x0 = __shfl_sync(kAll, x0, l);
+      x1 = __shfl_sync(kAll, x1, l);
+      return second ? x1 : x0;
+    };
     EkItem it{};
-    it.seq = seq;
+    it.seq = 2 * l + second;
     it.head = (int)blockIdx.x - unit * p.hkv;
     it.unit = unit;
-    it.tile = unit - __shfl_sync(kAll, end - c.units2, seq);
-    it.t0 = __shfl_sync(kAll, c.t0, seq);
-    it.rows = __shfl_sync(kAll, c.rows, seq);
-    it.keys = __shfl_sync(kAll, c.keys, seq);
+    it.tile = unit - of(begin, middle);
+    it.t0 = of(c0.t0, c1.t0);
+    it.rows = of(c0.rows, c1.rows);
+    it.keys = of(c0.keys, c1.keys);
     it.y1 = bad || unit >= units ? 0 : ek_tiles(p, it.rows, it.keys, it.tile, tt);
     if (lane == 0) work = it;
     if (blockIdx.x == 0) {
-      if (lane < p.n_seq) {
-        p.seq[lane] = make_int4(c.t0, c.rows, c.keys, 0);
-        p.off2[lane] = end - c.units2;
+      if (a < p.n_seq) {
+        p.seq[a] = make_int4(c0.t0, c0.rows, c0.keys, 0);
+        p.off2[a] = begin;
+      }
+      if (a + 1 < p.n_seq) {
+        p.seq[a + 1] = make_int4(c1.t0, c1.rows, c1.keys, 0);
+        p.off2[a + 1] = middle;
       }
       if (lane == 0) {
         if (bad) set_err(p.status, KVS_DEVERR_JOB);
@@ -1725,7 +1738,7 @@ extern "C" kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void*
   // after 4,000, 40 / 8, 52.8 and 62.9; but 4 x 16 after 2,000, 32 / 8 of 64 channels,
   // 25.2 and 21.9; after 4,000 of 128 channels 45 and 28).
   const long long ctas = ((long long)n_tokens / (kEmTile / p.g) + n_seq) * p.hkv, tiles = (p.most + kEmTile - 1) / kEmTile;
-  if (p.few && n_tokens > 0 && n_seq <= 32 && ctas <= 4ll * p.sms && (tiles <= 8 || (tiles <= 32 && ctas >= 4 * tiles))) {
+  if (p.few && n_tokens > 0 && n_seq <= 64 && ctas <= 4ll * p.sms && (tiles <= 8 || (tiles <= 32 && ctas >= 4 * tiles))) {
     p.whole = (int)ctas;
   } else if (n_seq <= 32 && n_tokens > 0) {
     p.tickets = pool->tickets;

@@ -107,6 +107,9 @@ def test_even_stretches(lens, new, hq, hkv, d, causal):
     ([900, 10, 1000], [9, 12, 1], 12, 1, 64),             # rows in front of the first key
     ([3900, 4000, 1, 257], [4, 2, 1, 4], 40, 8, 128),     # more tiles than stages, both passes
     ([500] * 30, [4] * 30, 40, 8, 64),                    # more CTAs than SMs
+    ([90, 0, 17] * 21 + [128], [1, 0, 2] * 21 + [3], 8, 4, 64),   # 64 sequences
+    ([33] * 32 + [700], [1] * 32 + [40], 16, 2, 128),     # 33, the last of several row tiles
+    ([33] * 65, [1] * 65, 8, 2, 64),                      # one more than a warp counts
 ])
 @pytest.mark.parametrize("causal", [True, False])
 def test_short_calls(lens, new, hq, hkv, d, causal):
