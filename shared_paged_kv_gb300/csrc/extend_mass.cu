@@ -1564,9 +1564,18 @@ __global__ void __launch_bounds__(256) em_add_kernel(const __grid_constant__ EmP
     v = p.sums + (size_t)first * 2 * p.hkv * p.most + t;
     for (int i = 0; i * tt < s.y; ++i) {
       if (t / kEmTile >= ek_tiles(p, s.y, s.z, i, tt)) continue;
-      const int halves = min(tt, s.y - i * tt) * p.g > 64 ? 2 : 1;
+      const int n = (min(tt, s.y - i * tt) * p.g > 64 ? 2 : 1) * p.hkv;
+      const float* w = v + (size_t)2 * i * p.hkv * p.most;
+      if (n % 16 == 0) {   // as many loads under way as divide their number
 #pragma unroll 16
-      for (int k = 0; k < halves * p.hkv; ++k) sum += v[(size_t)(2 * i * p.hkv + k) * p.most];
+        for (int k = 0; k < n; ++k) sum += w[(size_t)k * p.most];
+      } else if (n % 4 == 0) {
+#pragma unroll 4
+        for (int k = 0; k < n; ++k) sum += w[(size_t)k * p.most];
+      } else {
+#pragma unroll 2
+        for (int k = 0; k < n; ++k) sum += w[(size_t)k * p.most];
+      }
     }
   } else if (s.y > 0) {
     const int n = 2 * cuts * p.hkv;
@@ -1618,7 +1627,10 @@ EmLayout em_layout(const kvs_pool* pool, int n_tokens, int n_seq, int max_blocks
   const long long keys2 = std::min(std::clamp<long long>(row_tiles, 1, kEmMaxCuts) * most, 256 * (sms4 / hkv + 1) + most);
   l.parts = take((size_t)2 * rows1 * hq * 8);
   l.nlse = take((size_t)n_tokens * hq * 4);
-  l.sums = take((size_t)2 * std::max(n_seq * keys2, (std::min<long long>(row_tiles, n_seq) + n_seq) * most) * hkv * 4);
+  // sums by row tile: few rows, and short calls of some more (em_whole)
+  const long long by_rows = (std::min<long long>(row_tiles, n_seq) + n_seq) * most;
+  const long long by_rows_whole = (std::min<long long>(row_tiles, 2ll * n_seq + 6) + n_seq) * std::min<long long>(most, 8 * kEmTile);
+  l.sums = take((size_t)2 * std::max({n_seq * keys2, by_rows, by_rows_whole}) * hkv * 4);
   l.total = o;
   return l;
 }
@@ -1737,8 +1749,14 @@ extern "C" kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void*
   // tokens, 40 / 8 heads, 17.2 and 28.1; 4 x 16 after 500, 16 / 2, 12.3 and 17.9; 16 x 4
   // after 4,000, 40 / 8, 52.8 and 62.9; but 4 x 16 after 2,000, 32 / 8 of 64 channels,
   // 25.2 and 21.9; after 4,000 of 128 channels 45 and 28).
-  const long long ctas = ((long long)n_tokens / (kEmTile / p.g) + n_seq) * p.hkv, tiles = (p.most + kEmTile - 1) / kEmTile;
-  if (p.few && n_tokens > 0 && n_seq <= 64 && ctas <= 4ll * p.sms && (tiles <= 8 || (tiles <= 32 && ctas >= 4 * tiles))) {
+  // Over tables of eight key tiles also where sequences have a few row tiles (1 x 64
+  // rows after 300, 8 / 2: 10.1 and 17.3; 8 x 64 after 300, 32 / 8: 12.5 and 21.1; 1 x 256
+  // after 200: 18.9 and 21.7; but after 700: 24.1 and 22.2).
+  const int tt = kEmTile / p.g;
+  const long long ctas = ((long long)n_tokens / tt + n_seq) * p.hkv, tiles = (p.most + kEmTile - 1) / kEmTile;
+  if (n_tokens > 0 && n_seq <= 64 && ctas <= 4ll * p.sms &&
+      (tiles <= 8 ? p.few || ((long long)n_tokens + tt - 1) / tt <= 2ll * n_seq + (tiles <= 4 ? 6 : 2) : p.few && tiles <= 32 && ctas >= 4 * tiles)) {
+    p.few = 1;
     p.whole = (int)ctas;
   } else if (n_seq <= 32 && n_tokens > 0) {
     p.tickets = pool->tickets;

@@ -108,6 +108,9 @@ def test_even_stretches(lens, new, hq, hkv, d, causal):
     ([3900, 4000, 1, 257], [4, 2, 1, 4], 40, 8, 128),     # more tiles than stages, both passes
     ([500] * 30, [4] * 30, 40, 8, 64),                    # more CTAs than SMs
     ([90, 0, 17] * 21 + [128], [1, 0, 2] * 21 + [3], 8, 4, 64),   # 64 sequences
+    ([364], [64], 8, 2, 128),                             # more row tiles than sequences
+    ([305], [182], 20, 4, 64),
+    ([450, 20, 700], [150, 20, 40], 16, 4, 128),
     ([33] * 32 + [700], [1] * 32 + [40], 16, 2, 128),     # 33, the last of several row tiles
     ([33] * 65, [1] * 65, 8, 2, 64),                      # one more than a warp counts
 ])
