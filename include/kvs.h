@@ -67,7 +67,7 @@ typedef enum {
 #define KVS_DEVERR_ROPE_RANGE   0x20u /* |position shift| >= 2^18 */
 #define KVS_DEVERR_JOB          0x40u /* a RoPE job addresses tokens outside its table row */
 #define KVS_DEVERR_PLAN         0x80u /* kvs_decode_attn_planned saw no matching plan in ws */
-#define KVS_DEVERR_REFCOUNT     0x100u /* a release took a reference count below zero */
+#define KVS_DEVERR_REFCOUNT     0x100u /* a release took a reference count below zero, or counts miss references */
 
 typedef enum { KVS_DTYPE_BF16 = 0, KVS_DTYPE_Q4G64 = 1, KVS_DTYPE_MX4 = 2 } kvs_dtype;
 
@@ -676,8 +676,10 @@ kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* 
  * sequence's kept tokens, in its last block, are left as they were.
  * A sequence is left as it was where its list is not ascending or leaves it
  * (KVS_DEVERR_JOB), its seq_len lies outside its table row (KVS_DEVERR_SEQ_LEN),
- * a block id outside the pool (KVS_DEVERR_BLOCK_ID), or the free stack does not
- * hold enough blocks (KVS_DEVERR_CAPACITY).  Each sequence is listed once.
+ * a block id outside the pool (KVS_DEVERR_BLOCK_ID), the free stack does not
+ * hold enough blocks (KVS_DEVERR_CAPACITY), or the rows to write, those of the
+ * sequences before it among them, are more than the pool holds, as where blocks of
+ * two sequences are counted once (KVS_DEVERR_REFCOUNT).  Each sequence is listed once.
  * Mirror diffs are not moved: a sequence with diffs is not compacted.
  * Any pool.  ws: kvs_workspace_size(KVS_OP_COMPACT, n_seq, max_blocks) bytes. */
 kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blocks, int32_t* seq_len_dev,

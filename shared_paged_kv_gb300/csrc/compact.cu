@@ -434,32 +434,42 @@ __device__ __forceinline__ void check_sequence(const CompactParams& p) {
   }
 }
 
-__device__ __forceinline__ int cp_segments(const CompactParams& p, const CpSeq& s) {
-  return s.need < 0 ? 0 : (s.kept - s.start + p.rows - 1) / p.rows;
+__device__ __forceinline__ int cp_moved(const CpSeq& s) { return s.need < 0 ? 0 : s.kept - s.start; }   // rows
+__device__ __forceinline__ int cp_segments(const CompactParams& p, const CpSeq& s) { return (cp_moved(s) + p.rows - 1) / p.rows; }
+
+// The sum over the CTA's threads, in 64 bits; *total is 0 before and read after it.
+__device__ __forceinline__ void cp_add_up(long long x, unsigned long long* total) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  if ((threadIdx.x & 31) == 0 && x) atomicAdd(total, (unsigned long long)x);
 }
 
 // A CTA per sequence (and some more for long rows of masses): every CTA adds up
 // what the sequences before it take.
 __device__ __forceinline__ void apply_sequence(const CompactParams& p) {
   __shared__ int warp_sums[32];
+  __shared__ unsigned long long s_need, s_moved;
   __shared__ int s_base, s_seg, s_drop, s_taken;
   const int a = blockIdx.x, tid = threadIdx.x;
   const CpSeq s = p.seq[a];
   const int avail = min(max(*p.n_free, 0), p.capacity);
+  if (tid == 0) s_need = s_moved = 0;
+  __syncthreads();
   {
-    long long need = 0;
-    int before = 0, segs = 0, bad = 0;
+    long long need = 0, moved = 0;
+    int before = 0, segs = 0;
     for (int c = tid; c < p.n_seq; c += kCpSeqThreads) {
       const CpSeq q = p.seq[c];
       need += max(q.need, 0);
+      moved += cp_moved(q);
       if (c < a) {
         before += max(q.need, 0);
         segs += cp_segments(p, q);
       }
     }
-    bad = __syncthreads_or(need > avail);   // one thread's sum alone
-    int total, b0, g0;
-    block_exclusive_scan((int)min(need, (long long)avail + 1), warp_sums, total);
+    cp_add_up(need, &s_need);
+    cp_add_up(moved, &s_moved);
+    int b0, g0;
     block_exclusive_scan(before, warp_sums, b0);
     block_exclusive_scan(segs, warp_sums, g0);
     if (tid == 0) {
@@ -467,40 +477,44 @@ __device__ __forceinline__ void apply_sequence(const CompactParams& p) {
       s_base = b0;
       s_seg = g0;
       s_taken = b0 + max(s.need, 0);
-      if (bad || total > avail || total < 0) {
-        // the stack is short: a sequence gets its blocks if those before it left enough
+      const long long room = (long long)p.capacity * p.B;   // what a pool holds, and the segments are laid out for
+      if (s_need > (unsigned long long)avail || s_moved > (unsigned long long)room) {
+        // The stack is short, or more rows are to be written than there are (a block of two
+        // sequences that is counted once): a sequence is served if those before it left
+        // enough of both.
         int left = avail, seg = 0;
+        long long rows = room;
         for (int c = 0; c <= a; ++c) {
           const CpSeq q = p.seq[c];
-          s_base = avail - left;
-          s_seg = seg;
-          if (c == a) s_drop = q.need < 0 || q.need > left;
-          if (q.need >= 0 && q.need <= left) {
+          const bool blocks = q.need <= left, fits = blocks && cp_moved(q) <= rows;
+          if (c == a) {
+            s_base = avail - left;
+            s_seg = seg;
+            s_drop = q.need < 0 || !fits;
+            if (q.need >= 0 && !fits) set_err(p.status, blocks ? KVS_DEVERR_REFCOUNT : KVS_DEVERR_CAPACITY);
+          }
+          if (q.need >= 0 && fits) {
             left -= q.need;
+            rows -= cp_moved(q);
             seg += cp_segments(p, q);
           }
         }
         s_taken = avail - left;
-        if (s_drop && s.need >= 0) set_err(p.status, KVS_DEVERR_CAPACITY);
       }
     }
   }
   __syncthreads();
   const int base = s_base, seg0 = s_seg;
   const int segs = s_drop ? 0 : cp_segments(p, s);
-  const bool fits = seg0 + segs <= p.max_segs;   // otherwise the counts belong to no real pool
-  if (tid == 0 && blockIdx.y == 0) {
-    if (!fits) set_err(p.status, KVS_DEVERR_REFCOUNT);
-    if (a == p.n_seq - 1) {
-      const int total = (int)min((long long)(seg0 + segs), p.max_segs);
-      p.hdr[kCpSegs] = total;
-      p.hdr[kCpTaken] = s_taken;
-      p.hdr[kCpTicket] = p.hdr[kCpDone] = 0;
-      // chains that an item takes one after the other: its places are looked up
-      // once; as many as leave sixteen items to an SM
-      const long long items = (long long)total * p.chains;
-      p.hdr[kCpGroup] = (int)min(max(items / (kCpItemsPerSm * (long long)p.sms), 1ll), (long long)kCpMaxGroup);
-    }
+  if (tid == 0 && blockIdx.y == 0 && a == p.n_seq - 1) {
+    const int total = seg0 + segs;   // all of them are written below
+    p.hdr[kCpSegs] = total;
+    p.hdr[kCpTaken] = s_taken;
+    p.hdr[kCpTicket] = p.hdr[kCpDone] = 0;
+    // chains that an item takes one after the other: its places are looked up
+    // once; as many as leave sixteen items to an SM
+    const long long items = (long long)total * p.chains;
+    p.hdr[kCpGroup] = (int)min(max(items / (kCpItemsPerSm * (long long)p.sms), 1ll), (long long)kCpMaxGroup);
   }
   if (s_drop) return;
   const size_t row = (size_t)a * p.max_blocks;
@@ -513,16 +527,14 @@ __device__ __forceinline__ void apply_sequence(const CompactParams& p) {
     for (int i = mine.x + tid; i < mine.y; i += kCpSeqThreads) to[i] = i < s.kept ? from[idx[i]] : 0.f;
   }
   if (blockIdx.y > 0) return;
-  if (fits) {
-    const long long idx0 = p.idx_off[a];
-    const int all_new = s.need == (s.kept + p.B - 1) / p.B - s.start / p.B;
-    for (int i = tid; i < segs; i += kCpSeqThreads) {
-      const int i0 = s.start + i * p.rows;
-      p.segs[seg0 + i] = CpSeg{a, i0, min(p.rows, s.kept - i0), all_new ? -1 - s.start : s.start, idx0, seg0, 0};
-    }
-    if (!all_new)
-      for (long long i = (long long)seg0 * p.chains + tid; i < (long long)(seg0 + segs) * p.chains; i += kCpSeqThreads) p.flags[i] = 0;
+  const long long idx0 = p.idx_off[a];
+  const int all_new = s.need == (s.kept + p.B - 1) / p.B - s.start / p.B;
+  for (int i = tid; i < segs; i += kCpSeqThreads) {
+    const int i0 = s.start + i * p.rows;
+    p.segs[seg0 + i] = CpSeg{a, i0, min(p.rows, s.kept - i0), all_new ? -1 - s.start : s.start, idx0, seg0, 0};
   }
+  if (!all_new)
+    for (long long i = (long long)seg0 * p.chains + tid; i < (long long)(seg0 + segs) * p.chains; i += kCpSeqThreads) p.flags[i] = 0;
   const int nb_old = (s.len + p.B - 1) / p.B;
   int carry = base;
   for (int b0 = 0; b0 < nb_old; b0 += kCpSeqThreads) {
