@@ -680,6 +680,8 @@ kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* 
  * hold enough blocks (KVS_DEVERR_CAPACITY), or the rows to write, those of the
  * sequences before it among them, are more than the pool holds, as where blocks of
  * two sequences are counted once (KVS_DEVERR_REFCOUNT).  Each sequence is listed once.
+ * Rows whose place others have not read after a bounded wait (KVS_DEVERR_WAIT_TIMEOUT)
+ * are not written; their sequence's rows are incomplete then.
  * Mirror diffs are not moved: a sequence with diffs is not compacted.
  * Any pool.  ws: kvs_workspace_size(KVS_OP_COMPACT, n_seq, max_blocks) bytes. */
 kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blocks, int32_t* seq_len_dev,
@@ -705,6 +707,11 @@ kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blo
 /* KVS_TEST_EXTEND_PLANNED: while set, kvs_extend_attn and its two steps take
  * the planned path also for calls that would be a single launch. */
 #define KVS_TEST_EXTEND_PLANNED 0x4u
+/* KVS_TEST_STALL_COMPACT: in the next kvs_compact the first rows that move never
+ * count as read, so a write in place that waits for them runs out (about a second):
+ * it records KVS_DEVERR_WAIT_TIMEOUT and leaves its rows unwritten, the others move.
+ * The flag is consumed by that call. */
+#define KVS_TEST_STALL_COMPACT 0x8u
 kvs_status kvs_pool_set_test_flags(kvs_pool* pool, uint32_t flags);
 
 /* Workspace bytes for an operation with the given call shape. */

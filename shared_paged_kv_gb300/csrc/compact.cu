@@ -298,6 +298,7 @@ struct CompactParams {
   long long max_segs;
   int n_seq, max_blocks, B, hkv, capacity, chains, per_layer, row_bytes, sb_bytes, rows;   // chain: a layer's K or V of one head
   int sms;
+  int stall_first;         // test-only (KVS_TEST_STALL_COMPACT): the first item does not say that it has read its first chain
 };
 
 struct CpLayout {
@@ -734,13 +735,14 @@ __global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_cons
       auto next = [&]() {
         if (c + 1 < c1) y.load(slab_of(c + 1, 0), s.n, s_src, (c + 1) % p.hkv * p.B);
       };
+      bool late = false;
       if (in_place) {
         // Every row of this chain is read: said once the loads of all threads have
         // returned, which the barrier's predicate needs.
         uint32_t any = x.any();
         if (VECS == 4) any |= w[0] | w[1] | w[2] | w[3];
         __syncthreads_or(any == 1u);
-        if (tid == 0) {
+        if (tid == 0 && !(p.stall_first && sg == 0 && c == 0)) {
           __threadfence();
           *const_cast<volatile uint8_t*>(p.flags + (size_t)sg * p.chains + c) = 1;
         }
@@ -751,14 +753,16 @@ __global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_cons
           while (!flag_set(f)) {
             if (clock64() - t0 > (1ll << 31)) {
               set_err(p.status, KVS_DEVERR_WAIT_TIMEOUT);
+              late = true;
               break;
             }
           }
         }
-        __syncthreads();
+        late = __syncthreads_or(late);
       } else {
         next();
       }
+      if (late) return;   // rows that others still have to read are not written over
       x.store(slab_of(c, 0), s.n, s_dst, at);
       if (VECS == 4) {
         uint8_t* slab = slab_of(c, 2);
@@ -887,6 +891,8 @@ extern "C" kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int3
   p.sb_bytes = d.dtype == KVS_DTYPE_BF16 ? 0 : d.dtype == KVS_DTYPE_Q4G64 ? d.head_dim / 16 : d.head_dim / 32;
   p.rows = cp_rows(d);
   p.sms = pool->num_sms;
+  p.stall_first = (pool->test_flags & KVS_TEST_STALL_COMPACT) ? 1 : 0;
+  pool->test_flags &= ~KVS_TEST_STALL_COMPACT;   // one launch only
   // more CTAs for the masses of a sequence whose table holds more than 8,192
   const long long most = (long long)max_blocks * d.block_tokens;
   const dim3 per_seq((unsigned)n_seq, (unsigned)(mass_dev ? std::clamp<long long>(most / 8192, 1, 16) : 1));

@@ -52,3 +52,37 @@ def test_blocks_with_references_elsewhere(kind, d, lens):
         used = table[table >= 0]
         refs[used[np.random.default_rng(len(used)).random(len(used)) < 0.3]] += 1
     run_compact(kind, 2, 2, d, lens, 0.5, [0] * len(lens), True, cap_extra=200, refs_change=more)
+
+
+@pytest.mark.parametrize("kind, hkv", [("bf16", 2), ("mx4", 1)])
+def test_a_wait_that_runs_out_writes_nothing(kind, hkv):
+    """The first item never says that it has read its first chain: the one item that writes where those rows lay leaves
+    them, everything else moves, and the next call is whole."""
+    d, rows = (64, 128) if kind == "bf16" else (128, 256)     # places of an item
+    pool, slabs, block = make_pool(kind, 2, hkv, d, 8 * rows // 16, 1)
+    cap, n, mb = 8 * rows // 16, 8 * rows, 8 * rows // block
+    ids = np.random.default_rng(3).permutation(cap)
+    table, refs, free = ids[None, :mb], np.zeros(cap, np.int64), [int(x) for x in ids[mb:]]
+    refs[table] = 1
+    lists = np.arange(rows, n)                                # item i reads where item i + 1 writes
+    want = OC.compact([s.cpu().numpy() for s in slabs], table, [n], lists, [0, len(lists)], None, refs, free, block)
+    was = [s.cpu().numpy() for s in slabs]
+    args = (i32(lists), i64([0, len(lists)]))
+    state = lambda: (i32(refs), i32(np.concatenate([free, np.zeros(cap - len(free))])), i32([len(free)]))  # noqa: E731
+    ws = workspace(K.kvs_workspace_size(pool, K.KVS_OP_COMPACT, 1, mb)).fill_(0xAB)
+    start = [s.clone() for s in slabs]
+    K.kvs_pool_set_test_flags(pool, K.KVS_TEST_STALL_COMPACT)
+    K.kvs_compact(pool, i32(table), mb, i32([n]), 1, *args, *state(), ws)
+    assert K.kvs_pool_check(pool) == K.KVS_DEVERR_WAIT_TIMEOUT
+    places = np.arange(rows, 2 * rows)
+    for i, (x, exp) in enumerate(zip(slabs, want[0])):
+        if i in ((0,) if kind == "bf16" else (0, 2)):         # the first chain: layer 0, keys (and their scales), head 0
+            exp = exp.copy()
+            exp[table[0, places // block], 0, places % block] = was[i][table[0, places // block], 0, places % block]
+        np.testing.assert_array_equal(x.cpu().numpy(), exp)
+    for x, y in zip(slabs, start):
+        x.copy_(y)
+    K.kvs_compact(pool, i32(table), mb, i32([n]), 1, *args, *state(), ws)
+    assert K.kvs_pool_check(pool) == 0
+    for x, exp in zip(slabs, want[0]):
+        np.testing.assert_array_equal(x.cpu().numpy(), exp)
