@@ -641,7 +641,11 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  * [idx_off[a] .. idx_off[a + 1]), idx_off_dev int64 [n_seq + 1]; idx_out holds
  * their number, at most n_seq * max_blocks * block_tokens.  budget_dev int32
  * [n_seq].  seq_len outside the table's row (KVS_DEVERR_SEQ_LEN) is clamped.
- * The masses are not changed.  Any pool. */
+ * The masses are not changed.  Any pool.
+ * kvs_keep_heavy_bounded: the same into a list of idx_capacity entries.  The number
+ * of kept tokens is known on the device alone; a sequence whose indices do not all
+ * fit sets KVS_DEVERR_CAPACITY, its part of the list is left as it was, and idx_off
+ * tells what was wanted. */
 kvs_status kvs_decode_attn_mass(kvs_pool* pool, int32_t layer, const void* q_dev, int32_t n_q_heads,
                                 const int32_t* block_table_dev, int32_t max_blocks, const int32_t* seq_len_dev,
                                 int32_t n_seq, float scale, float* out_dev, const float* mass_in_dev, float carry,
@@ -660,6 +664,9 @@ kvs_status kvs_extend_mass(kvs_pool* pool, int32_t layer, const void* q_dev, int
 kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* seq_len_dev, int32_t n_seq,
                           int32_t max_blocks, const int32_t* budget_dev, int32_t n_first, int32_t n_recent,
                           int32_t* idx_out_dev, int64_t* idx_off_dev, cudaStream_t stream);
+kvs_status kvs_keep_heavy_bounded(kvs_pool* pool, const float* mass_dev, const int32_t* seq_len_dev, int32_t n_seq,
+                                  int32_t max_blocks, const int32_t* budget_dev, int32_t n_first, int32_t n_recent,
+                                  int32_t* idx_out_dev, int64_t idx_capacity, int64_t* idx_off_dev, cudaStream_t stream);
 
 /* Compaction: in every layer, row idx[i] of a sequence moves to place i, for
  * the list idx_dev [idx_off[a] .. idx_off[a + 1]) of kvs_keep_heavy or of the
@@ -683,11 +690,18 @@ kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* 
  * Rows whose place others have not read after a bounded wait (KVS_DEVERR_WAIT_TIMEOUT)
  * are not written; their sequence's rows are incomplete then.
  * Mirror diffs are not moved: a sequence with diffs is not compacted.
- * Any pool.  ws: kvs_workspace_size(KVS_OP_COMPACT, n_seq, max_blocks) bytes. */
+ * Any pool.  ws: kvs_workspace_size(KVS_OP_COMPACT, n_seq, max_blocks) bytes.
+ * kvs_compact_bounded: the same with a list of idx_capacity entries; a sequence
+ * whose offsets lead out of it is left as it was (KVS_DEVERR_JOB), so that what
+ * kvs_keep_heavy_bounded could not write is not read either. */
 kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blocks, int32_t* seq_len_dev,
                        int32_t n_seq, const int32_t* idx_dev, const int64_t* idx_off_dev, float* mass_dev,
                        int32_t* refcount_dev, int32_t* free_ids_dev, int32_t* n_free_dev, void* ws, size_t ws_bytes,
                        cudaStream_t stream);
+kvs_status kvs_compact_bounded(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blocks, int32_t* seq_len_dev,
+                               int32_t n_seq, const int32_t* idx_dev, int64_t idx_capacity, const int64_t* idx_off_dev,
+                               float* mass_dev, int32_t* refcount_dev, int32_t* free_ids_dev, int32_t* n_free_dev,
+                               void* ws, size_t ws_bytes, cudaStream_t stream);
 
 /* Test-only switches.  KVS_TEST_STALL_ONE_STAGE: the next kvs_decode_attn /
  * kvs_decode_attn_planned launch with a query group <= 8 leaves one ring

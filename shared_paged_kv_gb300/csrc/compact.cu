@@ -59,6 +59,7 @@ struct KeepParams {
   int32_t* idx;
   int64_t* idx_off;
   uint32_t* status;
+  long long cap;                        // entries of idx
   int n_seq, most, n_first, n_recent;   // most: tokens a table row holds
 };
 
@@ -120,7 +121,9 @@ __global__ void __launch_bounds__(kKhThreads) keep_heavy_kernel(const __grid_con
     if (raw < 0 || raw > p.most) set_err(p.status, KVS_DEVERR_SEQ_LEN);
     p.idx_off[a] = out0;
     if (a == p.n_seq - 1) p.idx_off[p.n_seq] = out0 + r.kept();
+    if (out0 + r.kept() > p.cap) set_err(p.status, KVS_DEVERR_CAPACITY);
   }
+  if (out0 + r.kept() > p.cap) return;            // the same for the whole cluster
   int32_t* out = p.idx + out0;
   const int who = rank * kKhThreads + tid, all = ranks * kKhThreads;
   for (int t = who; t < r.lo; t += all) out[t] = t;
@@ -284,6 +287,7 @@ struct CompactParams {
   int32_t *table, *seq_len;
   const int32_t* idx;
   const int64_t* idx_off;
+  long long idx_cap;       // entries of idx
   float* mass;
   int32_t *refcount, *free_ids, *n_free;
   uint32_t* status;
@@ -360,7 +364,7 @@ __device__ __forceinline__ void check_sequence(const CompactParams& p) {
   if (blockIdx.y > 0) return;
   const long long o0 = p.idx_off[a], o1 = p.idx_off[a + 1];
   const int len = p.seq_len[a];
-  const bool ok = len >= 0 && len <= p.max_blocks * p.B && o0 >= 0 && o1 >= o0 && o1 - o0 <= len;
+  const bool ok = len >= 0 && len <= p.max_blocks * p.B && o0 >= 0 && o1 >= o0 && o1 - o0 <= len && o1 <= p.idx_cap;
   const int kept = ok ? (int)(o1 - o0) : 0;
   if (tid == 0) {
     s_same = kept;
@@ -799,20 +803,21 @@ size_t compact_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks) 
 
 using namespace kvs;
 
-extern "C" kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* seq_len_dev, int32_t n_seq,
-                                     int32_t max_blocks, const int32_t* budget_dev, int32_t n_first, int32_t n_recent,
-                                     int32_t* idx_out_dev, int64_t* idx_off_dev, cudaStream_t stream) {
+extern "C" kvs_status kvs_keep_heavy_bounded(kvs_pool* pool, const float* mass_dev, const int32_t* seq_len_dev, int32_t n_seq,
+                                             int32_t max_blocks, const int32_t* budget_dev, int32_t n_first, int32_t n_recent,
+                                             int32_t* idx_out_dev, int64_t idx_capacity, int64_t* idx_off_dev, cudaStream_t stream) {
   if (!pool) return fail(KVS_ERR_INVALID_ARG, "keep_heavy: null pool");
   const kvs_pool_desc& d = pool->desc;
-  if (n_seq < 0 || max_blocks < 1 || n_first < 0 || n_recent < 0) return fail(KVS_ERR_INVALID_ARG, "keep_heavy: bad sizes");
+  if (n_seq < 0 || max_blocks < 1 || n_first < 0 || n_recent < 0 || idx_capacity < 0)
+    return fail(KVS_ERR_INVALID_ARG, "keep_heavy: bad sizes");
   if (n_seq > d.max_seqs) return fail(KVS_ERR_CAPACITY, "keep_heavy: n_seq exceeds the pool's max_seqs");
   const long long most = (long long)max_blocks * d.block_tokens;
   if (most > 0x40000000ll) return fail(KVS_ERR_CAPACITY, "keep_heavy: more than 2^30 tokens in a table row");
   if (n_seq == 0) return KVS_OK;
-  if (!mass_dev || !seq_len_dev || !budget_dev || !idx_out_dev || !idx_off_dev)
+  if (!mass_dev || !seq_len_dev || !budget_dev || (!idx_out_dev && idx_capacity > 0) || !idx_off_dev)
     return fail(KVS_ERR_INVALID_ARG, "keep_heavy: null pointer");
   if (kvs_status st = check_pool_device(pool, "keep_heavy"); st != KVS_OK) return st;
-  KeepParams p{mass_dev, seq_len_dev, budget_dev, idx_out_dev, idx_off_dev, pool->status, n_seq, (int)most, n_first, n_recent};
+  KeepParams p{mass_dev, seq_len_dev, budget_dev, idx_out_dev, idx_off_dev, pool->status, idx_capacity, n_seq, (int)most, n_first, n_recent};
   // Few CTAs with their masses in registers: exchanges between CTAs cost more than
   // longer slices.  (32 sequences of 6,144 tokens: one CTA 9.4 us, two 11.1; 16 of
   // 32,000: four 15.9, eight, which no longer are resident together, 44; one of 65,000:
@@ -842,18 +847,26 @@ extern "C" kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, cons
   return check_launch("keep_heavy");
 }
 
-extern "C" kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blocks, int32_t* seq_len_dev,
-                                  int32_t n_seq, const int32_t* idx_dev, const int64_t* idx_off_dev, float* mass_dev,
-                                  int32_t* refcount_dev, int32_t* free_ids_dev, int32_t* n_free_dev, void* ws,
-                                  size_t ws_bytes, cudaStream_t stream) {
+extern "C" kvs_status kvs_keep_heavy(kvs_pool* pool, const float* mass_dev, const int32_t* seq_len_dev, int32_t n_seq,
+                                     int32_t max_blocks, const int32_t* budget_dev, int32_t n_first, int32_t n_recent,
+                                     int32_t* idx_out_dev, int64_t* idx_off_dev, cudaStream_t stream) {
+  return kvs_keep_heavy_bounded(pool, mass_dev, seq_len_dev, n_seq, max_blocks, budget_dev, n_first, n_recent, idx_out_dev,
+                                INT64_MAX, idx_off_dev, stream);
+}
+
+extern "C" kvs_status kvs_compact_bounded(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blocks, int32_t* seq_len_dev,
+                                          int32_t n_seq, const int32_t* idx_dev, int64_t idx_capacity, const int64_t* idx_off_dev,
+                                          float* mass_dev, int32_t* refcount_dev, int32_t* free_ids_dev, int32_t* n_free_dev,
+                                          void* ws, size_t ws_bytes, cudaStream_t stream) {
   if (!pool) return fail(KVS_ERR_INVALID_ARG, "compact: null pool");
   const kvs_pool_desc& d = pool->desc;
-  if (n_seq < 0 || max_blocks < 1) return fail(KVS_ERR_INVALID_ARG, "compact: bad sizes");
+  if (n_seq < 0 || max_blocks < 1 || idx_capacity < 0) return fail(KVS_ERR_INVALID_ARG, "compact: bad sizes");
   if (n_seq > d.max_seqs) return fail(KVS_ERR_CAPACITY, "compact: n_seq exceeds the pool's max_seqs");
   if ((long long)max_blocks * d.block_tokens > 0x40000000ll)
     return fail(KVS_ERR_CAPACITY, "compact: more than 2^30 tokens in a table row");
   if (n_seq == 0) return KVS_OK;
-  if (!block_table_dev || !seq_len_dev || !idx_dev || !idx_off_dev || !refcount_dev || !free_ids_dev || !n_free_dev || !ws)
+  if (!block_table_dev || !seq_len_dev || (!idx_dev && idx_capacity > 0) || !idx_off_dev || !refcount_dev || !free_ids_dev ||
+      !n_free_dev || !ws)
     return fail(KVS_ERR_INVALID_ARG, "compact: null pointer");
   if (!aligned16(ws)) return fail(KVS_ERR_INVALID_ARG, "compact: ws must be 16-byte aligned");
   const CpLayout l = cp_layout(pool, n_seq, max_blocks);
@@ -865,6 +878,7 @@ extern "C" kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int3
   p.seq_len = seq_len_dev;
   p.idx = idx_dev;
   p.idx_off = idx_off_dev;
+  p.idx_cap = idx_capacity;
   p.mass = mass_dev;
   p.refcount = refcount_dev;
   p.free_ids = free_ids_dev;
@@ -905,4 +919,12 @@ extern "C" kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int3
                   launch_pdl(move, dim3(grid), dim3(kCpThreads), stream, p) == cudaSuccess;
   if (ok) count_launch(both ? 2 : 3);
   return check_launch("compact");
+}
+
+extern "C" kvs_status kvs_compact(kvs_pool* pool, int32_t* block_table_dev, int32_t max_blocks, int32_t* seq_len_dev,
+                                  int32_t n_seq, const int32_t* idx_dev, const int64_t* idx_off_dev, float* mass_dev,
+                                  int32_t* refcount_dev, int32_t* free_ids_dev, int32_t* n_free_dev, void* ws,
+                                  size_t ws_bytes, cudaStream_t stream) {
+  return kvs_compact_bounded(pool, block_table_dev, max_blocks, seq_len_dev, n_seq, idx_dev, INT64_MAX, idx_off_dev, mass_dev,
+                             refcount_dev, free_ids_dev, n_free_dev, ws, ws_bytes, stream);
 }

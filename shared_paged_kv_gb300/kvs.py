@@ -56,6 +56,7 @@ EXPORTED = [
     "kvs_workspace_size", "kvs_pool_check", "kvs_pool_stats", "kvs_last_error_string",
     "kvs_launch_count", "kvs_rope_apply", "kvs_append", "kvs_gather", "kvs_extend_workspace_size",
     "kvs_extend_plan", "kvs_extend_attn_planned", "kvs_extend_attn", "kvs_keep_heavy", "kvs_compact",
+    "kvs_keep_heavy_bounded", "kvs_compact_bounded",
     "kvs_decode_attn_mass", "kvs_decode_attn_mx4",
     "kvs_extend_mass_workspace_size", "kvs_extend_mass",
 ]
@@ -138,7 +139,9 @@ def load(path: str = LIB_PATH):
         "kvs_extend_mass_workspace_size": [P, I32, I32, I32, I32, ctypes.POINTER(SZ)],
         "kvs_extend_mass": [P, I32, P, I64, P, I32, I32, P, I32, P, I32, I32, F32, P, F32, P, P, SZ, P],
         "kvs_keep_heavy": [P, P, P, I32, I32, P, I32, I32, P, P, P],
+        "kvs_keep_heavy_bounded": [P, P, P, I32, I32, P, I32, I32, P, I64, P, P],
         "kvs_compact": [P, P, I32, P, I32, P, P, P, P, P, P, P, SZ, P],
+        "kvs_compact_bounded": [P, P, I32, P, I32, P, I64, P, P, P, P, P, P, SZ, P],
         "kvs_pool_check": [P, P, ctypes.POINTER(U32)],
         "kvs_pool_stats": [P, P, P, P, ctypes.POINTER(Stats)],
     }
@@ -408,6 +411,10 @@ def _ints(t, n: int, what: str, dev=None):
     return t.data_ptr()
 
 
+def _length(t) -> int:
+    return 0 if t is None else t.numel()
+
+
 def _positions(pos, n_axes: int, n_tokens: int, dev=None):
     """Positions [n_axes][n_tokens].  One axis may go on behind n_tokens; with
     several, that would put the second one elsewhere."""
@@ -597,12 +604,13 @@ def kvs_extend_mass(pool: Pool, layer, q, n_tokens, tok_off, n_q_heads, block_ta
 
 def kvs_keep_heavy(pool: Pool, mass, seq_len, n_seq, max_blocks, budget, n_first, n_recent, idx, idx_off, stream=None):
     """List the tokens worth keeping: the first, the last, and of the others
-    those of largest mass, budget[a] in all.  idx holds as many values."""
+    those of largest mass, budget[a] in all.  idx holds as many values; a
+    sequence whose indices it does not hold sets KVS_DEVERR_CAPACITY."""
     dev = _device()
-    _check(load().kvs_keep_heavy(pool.handle, _mass(mass, pool, n_seq, max_blocks, "mass", dev),
-                                 _ints(seq_len, n_seq, "seq_len", dev), n_seq, max_blocks,
-                                 _ints(budget, n_seq, "budget", dev), n_first, n_recent, _ints(idx, 0, "idx", dev),
-                                 _offsets(idx_off, n_seq + 1, "idx_off", dev), _stream(stream)))
+    _check(load().kvs_keep_heavy_bounded(pool.handle, _mass(mass, pool, n_seq, max_blocks, "mass", dev),
+                                         _ints(seq_len, n_seq, "seq_len", dev), n_seq, max_blocks,
+                                         _ints(budget, n_seq, "budget", dev), n_first, n_recent, _ints(idx, 0, "idx", dev),
+                                         _length(idx), _offsets(idx_off, n_seq + 1, "idx_off", dev), _stream(stream)))
 
 
 def kvs_compact(pool: Pool, block_table, max_blocks, seq_len, n_seq, idx, idx_off, refcount, free_ids, n_free, ws, mass=None,
@@ -610,12 +618,12 @@ def kvs_compact(pool: Pool, block_table, max_blocks, seq_len, n_seq, idx, idx_of
     """Move the listed tokens' rows of every layer to the front of their
     sequences, with tables, lengths, counts, the free stack and the masses."""
     dev, cap = _device(), pool.desc.capacity_blocks
-    _check(load().kvs_compact(pool.handle, _table(block_table, n_seq, max_blocks, dev), max_blocks,
-                              _ints(seq_len, n_seq, "seq_len", dev), n_seq, _ints(idx, 0, "idx", dev),
-                              _offsets(idx_off, n_seq + 1, "idx_off", dev),
-                              _mass(mass, pool, n_seq, max_blocks, "mass", dev), _ints(refcount, cap, "refcount", dev),
-                              _ints(free_ids, cap, "free_ids", dev), _ints(n_free, 1, "n_free", dev), *_ws(ws, dev),
-                              _stream(stream)))
+    _check(load().kvs_compact_bounded(pool.handle, _table(block_table, n_seq, max_blocks, dev), max_blocks,
+                                      _ints(seq_len, n_seq, "seq_len", dev), n_seq, _ints(idx, 0, "idx", dev), _length(idx),
+                                      _offsets(idx_off, n_seq + 1, "idx_off", dev),
+                                      _mass(mass, pool, n_seq, max_blocks, "mass", dev), _ints(refcount, cap, "refcount", dev),
+                                      _ints(free_ids, cap, "free_ids", dev), _ints(n_free, 1, "n_free", dev), *_ws(ws, dev),
+                                      _stream(stream)))
 
 
 def kvs_pool_check(pool: Pool, stream=None) -> int:

@@ -86,3 +86,50 @@ def test_a_wait_that_runs_out_writes_nothing(kind, hkv):
     assert K.kvs_pool_check(pool) == 0
     for x, exp in zip(slabs, want[0]):
         np.testing.assert_array_equal(x.cpu().numpy(), exp)
+
+
+@pytest.mark.parametrize("lens, budget, cap, whole", [
+    ([100, 333, 5, 64], [50, 100, 2, 63], 150, 2),      # the third does not fit
+    ([100, 333, 5, 64], [50, 100, 2, 63], 151, 2),
+    ([300], [-7], 20, 1),                                # protected tokens alone, as many as fit
+    ([300], [-7], 19, 0),                                # they are more than a list of the budgets' sum
+    ([64, 40], [64, 40], 64, 1),                         # everything is kept
+    ([20000, 40], [1000, 40], 999, 0),                   # several CTAs a sequence
+    ([20, 0], [0, 5], 0, 2),                             # an empty list, and no list
+])
+def test_a_list_that_is_too_short(lens, budget, cap, whole):
+    """No index is written past the list; the compaction that gets it leaves those sequences as they were."""
+    first, recent, n = (4, 16, len(lens)) if cap else (0, 0, len(lens))
+    block, hkv, d = 16, 1, 64
+    nb = [-(-x // block) for x in lens]
+    mb, used = max(nb) + 1, sum(nb)
+    pool, slabs, _ = make_pool("bf16", 1, hkv, d, used + 1, n)
+    table, at = np.full((n, mb), -1), 0
+    for a in range(n):
+        table[a, :nb[a]] = np.arange(at, at + nb[a])
+        at += nb[a]
+    refs = (np.arange(used + 1) < used).astype(np.int64)
+    mass = np.random.default_rng(sum(lens)).random((n, mb * block)).astype(np.float32)
+    lists, off = OC.keep_heavy(mass, lens, budget, first, recent)
+    memory = torch.full((len(lists) + 64,), -7, dtype=torch.int32, device=DEV)
+    idx, do, md = memory[:cap], torch.full((n + 1,), -7, dtype=torch.int64, device=DEV), torch.as_tensor(mass, device=DEV)
+    K.kvs_keep_heavy(pool, md, i32(lens), n, mb, i32(budget), first, recent, idx, do)
+    fits = off[1:] <= cap
+    assert K.kvs_pool_check(pool) == (0 if fits.all() else K.KVS_DEVERR_CAPACITY)
+    assert do.tolist() == off.tolist() and fits[:whole].all() and not fits[whole:whole + 1].any()
+    want = np.full(len(memory), -7)
+    for a in np.nonzero(fits)[0]:
+        want[off[a]:off[a + 1]] = lists[off[a]:off[a + 1]]
+    np.testing.assert_array_equal(memory.cpu().numpy(), want)
+    # and on: sequences whose offsets lead out of the list keep everything
+    rule = [lists[off[a]:off[a + 1]] if fits[a] else np.array([1, 1]) for a in range(n)]
+    roff = np.concatenate([[0], np.cumsum([len(x) for x in rule])])
+    exp = OC.compact([s.cpu().numpy() for s in slabs], table, lens, np.concatenate(rule), roff, mass, refs, [used], block)
+    t, ln, rc, free, nf = i32(table), i32(lens), i32(refs), i32([used] + [0] * used), i32([1])
+    ws = workspace(K.kvs_workspace_size(pool, K.KVS_OP_COMPACT, n, mb)).fill_(0xAB)
+    K.kvs_compact(pool, t, mb, ln, n, idx, do, rc, free, nf, ws, mass=md)
+    assert K.kvs_pool_check(pool) == (0 if fits.all() else K.KVS_DEVERR_JOB)
+    for got, x in zip((t, ln, md, rc), exp[1:5]):
+        np.testing.assert_array_equal(got.cpu().numpy(), x)
+    for x, y in zip(slabs, exp[0]):
+        np.testing.assert_array_equal(x.cpu().numpy(), y)
