@@ -616,7 +616,9 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  * a weight that multiplies values keeps 22 bits or more.  MX4 values below 2^-27
  * of the largest scale that their 32 channels have in the sequence count as 0.
  * The result is the same to the bit for the same call.
- * ws: kvs_workspace_size(KVS_OP_DECODE_MASS, n_seq, max_blocks, n_q_heads).
+ * ws: kvs_workspace_size(KVS_OP_DECODE_MASS, n_seq, max_blocks, n_q_heads), of which
+ * the scores of all tokens and heads are the most; attention alone leaves none and
+ * takes KVS_OP_DECODE_MX4.
  *
  * kvs_extend_mass: the same sum over the rows of query chunks,
  *   mass[a][t] = carry * mass_in[a][t] + sum over rows j and heads of w(t),
@@ -737,6 +739,7 @@ kvs_status kvs_pool_set_test_flags(kvs_pool* pool, uint32_t flags);
 #define KVS_OP_BLOCKS 5   /* n_seq = n_items = max(n_writes, n_seq); max_blocks unused */
 #define KVS_OP_COMPACT 6
 #define KVS_OP_DECODE_MASS 7   /* kvs_decode_attn_mass, kvs_decode_attn_mx4 */
+#define KVS_OP_DECODE_MX4 8    /* kvs_decode_attn_mx4 without masses */
 kvs_status kvs_workspace_size(const kvs_pool* pool, int32_t op, int32_t n_seq,
                               int32_t max_blocks, int32_t n_q_heads, size_t* bytes);
 

@@ -942,6 +942,7 @@ __global__ void __launch_bounds__(kMassThreads) add_mass_kernel(const __grid_con
 
 struct DmLayout {
   size_t part, ml, fin, scores, total;
+  size_t bytes(bool masses) const { return masses ? total : scores; }   // the scores are for the masses alone
 };
 DmLayout dm_layout(const kvs_pool* pool, int n_seq, int max_blocks, int g) {
   const kvs_pool_desc& d = pool->desc;
@@ -1000,7 +1001,7 @@ kvs_status decode_mass(kvs_pool* pool, int32_t layer, const void* q, int32_t n_q
   if (!q || !table || !seq_len || !out || !ws) return fail(KVS_ERR_INVALID_ARG, what + ": null pointer");
   if (!aligned16(q) || !aligned16(out) || !aligned16(ws)) return fail(KVS_ERR_INVALID_ARG, what + ": q, out and ws must be 16-byte aligned");
   const DmLayout l = dm_layout(pool, n_seq, max_blocks, g);
-  if (ws_bytes < l.total) return fail(KVS_ERR_CAPACITY, what + ": workspace too small");
+  if (ws_bytes < l.bytes(mass != nullptr)) return fail(KVS_ERR_CAPACITY, what + ": workspace too small");
   if (kvs_status st = check_pool_device(pool, what.c_str()); st != KVS_OK) return st;
   uint8_t* w = static_cast<uint8_t*>(ws);
   DmParams p{};
@@ -1057,8 +1058,8 @@ kvs_status decode_mass(kvs_pool* pool, int32_t layer, const void* q, int32_t n_q
 
 }  // namespace
 
-size_t decode_mass_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks, int g) {
-  return dm_layout(pool, n_seq, max_blocks, g).total;
+size_t decode_mass_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks, int g, bool masses) {
+  return dm_layout(pool, n_seq, max_blocks, g).bytes(masses);
 }
 
 }  // namespace kvs

@@ -142,7 +142,7 @@ bool ex_query_map(CUtensorMap* m, const void* q, int n_tokens, int g, int hkv, i
 size_t mirror_workspace_bytes(int n_seq, int max_blocks);
 
 // Decode attention with the tokens' weights (decode_mass.cu).
-size_t decode_mass_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks, int g);
+size_t decode_mass_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks, int g, bool masses);
 
 // Compaction behind an eviction (compact.cu).
 size_t compact_workspace_bytes(const kvs_pool* pool, int n_seq, int max_blocks);

@@ -333,9 +333,12 @@ kvs_status kvs_workspace_size(const kvs_pool* p, int32_t op, int32_t n_seq, int3
     case KVS_OP_BLOCKS:
       b = blocks_workspace_bytes(p->desc.capacity_blocks, n_seq);
       break;
+    case KVS_OP_DECODE_MX4:
+      if (p->desc.dtype != KVS_DTYPE_MX4) return fail(KVS_ERR_INVALID_ARG, "workspace_size: pool is not MX4");
+      [[fallthrough]];
     case KVS_OP_DECODE_MASS: {
       if (n_q_heads < 1 || n_q_heads % p->desc.num_kv_heads) return fail(KVS_ERR_INVALID_ARG, "workspace_size: n_q_heads");
-      b = decode_mass_workspace_bytes(p, n_seq, max_blocks, n_q_heads / p->desc.num_kv_heads);
+      b = decode_mass_workspace_bytes(p, n_seq, max_blocks, n_q_heads / p->desc.num_kv_heads, op == KVS_OP_DECODE_MASS);
       break;
     }
     case KVS_OP_COMPACT:

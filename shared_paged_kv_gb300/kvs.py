@@ -45,7 +45,7 @@ KVS_DTYPE_Q4G64 = 1
 KVS_DTYPE_MX4 = 2
 KVS_DEDUP_TEST_WEAK_KEYS = 0x1
 KVS_OP_DEDUP, KVS_OP_DECODE_ATTN, KVS_OP_DECODE_ATTN_Q4, KVS_OP_SELECT, KVS_OP_MIRROR, KVS_OP_BLOCKS = 0, 1, 2, 3, 4, 5
-KVS_OP_COMPACT, KVS_OP_DECODE_MASS = 6, 7
+KVS_OP_COMPACT, KVS_OP_DECODE_MASS, KVS_OP_DECODE_MX4 = 6, 7, 8
 
 EXPORTED = [
     "kvs_pool_create", "kvs_pool_destroy", "kvs_fingerprint_dedup", "kvs_rope_rerotate",
