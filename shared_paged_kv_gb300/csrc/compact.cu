@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_cons
       auto next = [&]() {
         if (c + 1 < c1) y.load(slab_of(c + 1, 0), s.n, s_src, (c + 1) % p.hkv * p.B);
       };
-      bool late = false;
+      int n = s.n;
       if (in_place) {
         // Every row of this chain is read: said once the loads of all threads have
         // returned, which the barrier's predicate needs.
@@ -751,6 +751,7 @@ __global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_cons
           *const_cast<volatile uint8_t*>(p.flags + (size_t)sg * p.chains + c) = 1;
         }
         next();   // on their way while this chain waits and is written
+        bool late = false;
         for (int q = wait0 + tid; q < wait1; q += kCpThreads) {
           const uint8_t* f = p.flags + (size_t)(s.first + q) * p.chains + c;
           const long long t0 = clock64();
@@ -762,18 +763,17 @@ __global__ void __launch_bounds__(kCpThreads, kCpCtas) cp_move(const __grid_cons
             }
           }
         }
-        late = __syncthreads_or(late);
+        if (__syncthreads_or(late)) n = 0;   // rows that others still have to read are not written over
       } else {
         next();
       }
-      if (late) return;   // rows that others still have to read are not written over
-      x.store(slab_of(c, 0), s.n, s_dst, at);
+      x.store(slab_of(c, 0), n, s_dst, at);
       if (VECS == 4) {
         uint8_t* slab = slab_of(c, 2);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           const int v = k * kCpThreads + tid, r = v / words;
-          if (r < s.n && s_dst[r] >= 0) *(reinterpret_cast<uint32_t*>(slab + (size_t)(s_dst[r] + at) * p.sb_bytes) + v % words) = w[k];
+          if (r < n && s_dst[r] >= 0) *(reinterpret_cast<uint32_t*>(slab + (size_t)(s_dst[r] + at) * p.sb_bytes) + v % words) = w[k];
         }
       }
     };
