@@ -612,9 +612,12 @@ kvs_status kvs_extend_attn(kvs_pool* pool, int32_t layer, const void* q_dev, int
  * seq_len are finite, and what the pool holds behind them is never used.  A block
  * id outside the pool (KVS_DEVERR_BLOCK_ID) takes its tokens out of the
  * sequence (weight 0); seq_len outside the table's row (KVS_DEVERR_SEQ_LEN) is
- * clamped; an empty context yields zeros.  Scores, sums and masses are float32,
- * a weight that multiplies values keeps 22 bits or more.  MX4 values below 2^-27
- * of the largest scale that their 32 channels have in the sequence count as 0.
+ * clamped; an empty context yields zeros.  Scores, sums and masses are float32.
+ * A weight that multiplies values keeps 24 bits over BF16 pools; over MX4 pools it
+ * is off by at most 2^-22 of itself and 2^-36 of the largest weight of its query
+ * head.  There a value may count as 0 where its scale is less than 2^-27 of the
+ * largest one that its 32 channels have in the sequence, whatever the weight of
+ * the token with that one.
  * The result is the same to the bit for the same call.
  * ws: kvs_workspace_size(KVS_OP_DECODE_MASS, n_seq, max_blocks, n_q_heads), of which
  * the scores of all tokens and heads are the most; attention alone leaves none and

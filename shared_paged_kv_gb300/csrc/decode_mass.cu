@@ -30,7 +30,10 @@
 // channels are scaled by the group's power of two in fp32, exactly.  Values: a
 // token's scale multiplies the fp16 pairs, relative to the largest one that this
 // warp has met in the group (E): 2^(e - E + 13), exact for e >= E - 27 and zero
-// below, which is 2^-24 of nothing that a sum in fp32 would keep; the
+// below.  E goes by the scales alone: next to weights of one size a value lost is
+// 2^-27 of a sum that fp32 holds to 2^-24, but a token of a huge scale hides the others
+// even where its own weight is small.  Weights are two fp16 parts at 2^11 and more of the
+// largest one met, so 2^-36 of that is the least that they hold.  The
 // accumulators follow E when it grows.  Row r of a product is token
 // r ^ (r >> 1 & 1) of its 16, with which all shared loads (64-byte swizzle) are
 // free of bank conflicts.
