@@ -1379,11 +1379,11 @@ PFN_cuTensorMapEncodeTiled_v12000 ex_encoder() {
   return fn;
 }
 
+}  // namespace
+
 // Queries [tokens][hkv][G][D] as {64 elements, G heads, tokens, KV heads, D/64
 // halves}: a box {64, G, 128/G, 1, 1} is one half of a row tile, row = token *
 // G + head.  Tokens behind the last one arrive as zeros.
-}  // namespace
-
 bool ex_query_map(CUtensorMap* m, const void* q, int n_tokens, int g, int hkv, int d, long long stride) {
   auto enc = ex_encoder();
   if (!enc) return false;
