@@ -5,7 +5,7 @@ import torch
 from shared_paged_kv_gb300 import kvs as K
 
 from harness import DEV, i32, workspace
-from test_gpu_decode_mass import call, make
+from test_gpu_decode_mass import call, check, make
 
 pytestmark = pytest.mark.gpu
 
@@ -36,3 +36,16 @@ def test_of_pools_in_4_bits_alone():
     s = make("bf16", [20], 4, 2, 64)
     with pytest.raises(K.KvsError):
         K.kvs_workspace_size(s["pool"], K.KVS_OP_DECODE_MX4, 1, 2, 4)
+
+
+@pytest.mark.parametrize("up", [100, 110])
+def test_sums_of_large_values_stay_finite(up):
+    """Values of up to 6 * 2^(1 + up): what they add up to over 2,000 tokens lies below 2^127, and so does every step."""
+    s = make("mx4", [2000, 64, 700], 8, 2, 128, seed=up)
+    s["scale"] /= 8                                  # weights of about one size
+    for e in s["vsc"]:
+        e[e < 255] += up
+    s["values"][1] = s["values"][1] * 2.0 ** up
+    out, mass = call(s)
+    assert torch.isfinite(out).all()
+    check(s, out, mass)
