@@ -30,9 +30,10 @@
 //            more onto the free stack.
 // Bound by HBM where rows are long (32 sequences, 4 layers of 256-byte rows: 473 MB in
 // 88 us, 5.4 TB/s), by a chain's two trips to memory and its barriers where they
-// are 64 bytes and lie apart (one sequence of 131,072 tokens in 4 bits, 8 layers: 558
-// MB in 131 us); small calls by the three launches' chains (4 sequences of some hundred
-// tokens: 14 us with the choice).
+// are 64 bytes and lie apart (one sequence of 131,072 tokens in 4 bits, 8 layers: 581
+// MB in 124 us); small calls by the three launches' chains (4 sequences of some hundred
+// tokens: 14 us with the choice).  These are copies into new blocks; in place the flags
+// and waits come on top (32 sequences, the whole eviction: 253 us instead of 114).
 #include <algorithm>
 #include <cooperative_groups.h>
 
@@ -610,7 +611,7 @@ __device__ __forceinline__ int lower_bound(const int32_t* x, int n, int v) {   /
 
 // Kept rows lie apart, and 4-bit ones are 64 bytes: L2 fetches no more than that
 // (one sequence of 131,072 tokens, 32,768 kept: 336 MB read instead of 519, the whole
-// eviction 193 -> 177 us).
+// eviction 193 -> 177 us then).
 __device__ __forceinline__ uint4 load_row(const uint4* p) {
   uint4 v;
   asm volatile("ld.global.L2::64B.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");

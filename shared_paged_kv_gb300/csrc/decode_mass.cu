@@ -44,8 +44,10 @@
 // part from L2 (6.5 TB/s), bound by a unit's chain of products and exponentials;
 // four of 350, 8 / 2 of 64 channels: 8.7 us, start, four units, arrival, join and the
 // second kernel, each a trip to memory.  In 4 bits: twelve of 4,000 to 8,191, 32 / 8
-// (*): 29 us; eight of 16,384 to 32,768: 72 us, 3.1 TB/s, bound by issue slots (52 %)
-// and the conversions.
+// (*): 29 us; eight of 16,384 to 32,768: 72 us, 3.1 TB/s.  There three warps a scheduler
+// (168 registers) wait for one another's results: of 5.3 cycles a warp takes for an
+// instruction, 1.8 are the latency of the one before, 0.4 a busy pipe, 0.7 memory and
+// shared memory; 52 % of the issue slots are used.
 #include <algorithm>
 #include <cmath>
 
