@@ -709,7 +709,9 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
 
     // ---- the warps' states become one
     // microscaled: times 2^(E - 127 - 13 - kBias), as two factors that float32 holds; kBias
-    // goes out of the sums here, so that those of large values stay finite as over bf16 pools
+    // goes out of the sums here, so that those of large values stay finite as over bf16 pools.
+    // What the weights were taken against is ref - kBias as float32 rounds it; adding kBias to
+    // that is exact
     constexpr float kUnbias = F::mx ? 0x1p-11f : 1.f;
     static_assert(F::kBias == (F::mx ? 11.f : 0.f), "kUnbias is 2^-kBias");
     const int e_up = (int)((top_e >> (8 * (g >> 1))) & 255u) - 151;
@@ -722,7 +724,7 @@ decode_mass_kernel(const __grid_constant__ DmParams p, const __grid_constant__ C
         for (int o = 4; o < 32; o <<= 1) l[nt][i] += __shfl_xor_sync(0xffffffffu, l[nt][i], o);
         const int row = nt * 8 + 2 * c + i;
         if (row >= p.g) continue;
-        if (g == 0) sh.ml[warp][row] = make_float2(ref[nt][i], l[nt][i] * kUnbias);
+        if (g == 0) sh.ml[warp][row] = make_float2(__fadd_rn(__fsub_rn(ref[nt][i], F::kBias), F::kBias), l[nt][i] * kUnbias);
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) {
           float* o = s_acc + ((size_t)warp * p.g + row) * D;

@@ -1,11 +1,14 @@
 """Attention over a pool of microscaled 4-bit values without masses: no memory for scores is wanted."""
+import numpy as np
 import pytest
 import torch
 
+from oracle import mass as OM
+from oracle import mx4 as O4
 from shared_paged_kv_gb300 import kvs as K
 
 from harness import DEV, i32, workspace
-from test_gpu_decode_mass import call, check, make
+from test_gpu_decode_mass import call, check, f64, make
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +52,29 @@ def test_sums_of_large_values_stay_finite(up):
     out, mass = call(s)
     assert torch.isfinite(out).all()
     check(s, out, mass)
+
+
+def test_warps_states_agree_on_their_references():
+    """Sequences of two units, a warp each, whose tokens all have one score, values 1 in one and 0 in the other: the output
+    is 1 / (1 + 2^(x1 - x0)).  The scores (base 2) lie between -64 and -32 and are exact products; what a warp's weights
+    were taken against has to be what it is joined by, to the bit: half a last place at 64 is 2^-19, 1.3e-6 of a weight.
+    Otherwise a warp's weights are off by 2^-22 (the exponential) and 2^-21 ln 2 (its argument, about 11, rounded): (1 - w) of
+    twice 5.7e-7; the parts of a weight and their sum by 2^-23 each, the division by 2^-23, the factor of the join by 2^-22:
+    1.2e-6 where 1 - w is at most 0.55."""
+    n, hq = 60, 8
+    s = make("mx4", [64] * n, hq, 1, 128, scales=(127, 128))
+    kc, vc = s["k"][0], s["v"][0]
+    kc.zero_(), vc.zero_()
+    kc[..., 0] = 0x07                              # channel 0: 6, everywhere
+    kc[:, :, 32:, 1] = 0x01                        # channel 2: 0.5 in the second half of a block
+    vc[:, :, :32, :] = 0x22                        # values: 1 in the first half
+    s["values"] = [np.where(np.isnan(x), 0, O4.dequantize(c.cpu().numpy(), np.full(x.shape[:3] + (4,), 127))) for x, c in zip(s["values"], (kc, vc))]
+    q = np.zeros((n, hq, 128), np.float32)
+    r = np.random.default_rng(0)
+    q[..., 0] = -r.uniform(4.0, 7.0, (n, hq))      # 6 q log2(e) from -60 to -35
+    q[..., 2] = r.uniform(-0.25, 0.25, (n, hq))    # half of it between the two scores
+    s["q"], s["scale"] = torch.as_tensor(q).to(torch.bfloat16).to(DEV), 1.0
+    out, mass = call(s, mass_in=None)
+    want, _, w, _ = OM.attend(f64(s["q"]), *s["values"], s["table"], range(n + 1), s["lens"], 64, 1.0, False)
+    assert 0.45 <= want.min() and want.max() <= 0.55
+    assert np.abs(f64(out) / want - 1).max() <= 1.2e-6
